@@ -255,7 +255,8 @@ def prepare(case, seed):
         rng.shuffle(order)
         s["dst_ids"], s["src_ids"] = i32(order), i32([i % B for i in range(B * C)])
         s["zeros"] = torch.zeros(B * C, dtype=torch.int32, device=dev)
-        s["rows"] = B + B * C
+        s["pages"] = torch.empty(B * C, dtype=torch.int32, device=dev)
+        s["work"] = torch.empty(2 * B * C, dtype=torch.int32, device=dev)
     else:
         g = case["grow"]
         s["stride"] = -(-(max(ctx) + g) // P)
@@ -269,7 +270,8 @@ def prepare(case, seed):
             first, then = [0] * len(ids), [ctx[i] for i in ids]
         else:
             first, then = [ctx[i] + g for i in ids], [ctx[i] for i in ids]
-        s["ids"], s["first"], s["then"], s["rows"] = i32(ids), i32(first), i32(then), B
+        s["ids"], s["first"], s["then"] = i32(ids), i32(first), i32(then)
+        s["work"] = torch.empty(2 * len(ids), dtype=torch.int32, device=dev)
     s["refs"] = torch.zeros(s["pool"], dtype=torch.int32, device=dev)
     s["refs"][perm[:used].long()] = 1
     s["free"] = torch.full((s["pool"],), -1, dtype=torch.int32, device=dev)
@@ -398,6 +400,7 @@ def _fork_plain(s, src, dst):
     page = free[pos].long()
     last = (k == full[:, None]) & (need > 0)[:, None]
     s["table"][dst] = torch.where(shared, rows, torch.where(last, page[:, None], -1)).int()
+    s["pages"].copy_(torch.where(need > 0, page, -1))
     refs = torch.cat([s["refs"], s["refs"].new_zeros(1)])
     refs.index_add_(0, torch.where(shared, rows, s["pool"]).reshape(-1), shared.reshape(-1).int())
     refs.index_add_(0, torch.where(need > 0, page, s["pool"]), need.int())
@@ -443,11 +446,14 @@ def run(s):
             smla.cache_compact(d, s["table"], s["starts"], s["cu"], s["keep"], s["kv"], s["lens"], s["err"])
             return {"kv": s["kv"], "lens": s["lens"]}
         if op == "fork":
-            smla.cache_resize(d, s["table"], s["lens"], s["refs"], s["free"], s["nfree"], s["dst_ids"], s["zeros"], s["err"])
-            smla.cache_fork(d, s["table"], s["lens"], s["refs"], s["free"], s["nfree"], s["src_ids"], s["dst_ids"], s["kv"], s["err"])
-            return {"kv": s["kv"], **_pages(s)}
-        smla.cache_resize(d, s["table"], s["lens"], s["refs"], s["free"], s["nfree"], s["ids"], s["first"], s["err"])
-        smla.cache_resize(d, s["table"], s["lens"], s["refs"], s["free"], s["nfree"], s["ids"], s["then"], s["err"])
+            smla.cache_resize(d, s["table"], s["lens"], s["refs"], s["free"], s["nfree"], s["dst_ids"], s["zeros"], s["work"],
+                              s["err"])
+            smla.cache_fork(d, s["table"], s["lens"], s["refs"], s["free"], s["nfree"], s["src_ids"], s["dst_ids"],
+                            s["pages"], s["kv"], s["err"])
+            return {"kv": s["kv"], "pages": s["pages"], **_pages(s)}
+        smla.cache_resize(d, s["table"], s["lens"], s["refs"], s["free"], s["nfree"], s["ids"], s["first"], s["work"],
+                          s["err"])
+        smla.cache_resize(d, s["table"], s["lens"], s["refs"], s["free"], s["nfree"], s["ids"], s["then"], s["work"], s["err"])
         return _pages(s)
     if op == "tree":
         return _tree_plain(s)
@@ -459,7 +465,7 @@ def run(s):
     if op == "fork":
         _resize_plain(s, s["dst_ids"], s["zeros"])
         _fork_plain(s, s["src_ids"], s["dst_ids"])
-        return {"kv": s["kv"], **_pages(s)}
+        return {"kv": s["kv"], "pages": s["pages"], **_pages(s)}
     _resize_plain(s, s["ids"], s["first"])
     _resize_plain(s, s["ids"], s["then"])
     return _pages(s)
