@@ -110,10 +110,11 @@ typedef struct smla_desc {
 /* Human-readable name of a status (static string). */
 const char* smla_status_string(int32_t status);
 
-/* ABI version of this header (increments whenever the interface changes; 2 added kv_scale,
+/* ABI version of this header (increments whenever the interface that was there changes; 2 added kv_scale,
  * 3 added SMLA_ERR_TIMEOUT, SMLA_ERR_OPERAND_RANGE, SMLA_DEVERR_RANGE,
  * smla_noalloc_read_error, the indexer calls and smla_store_kv_normed; 4 added q_format and
- * q_scale in place of two reserved words; 5 added smla_plan_launches). */
+ * q_scale in place of two reserved words; 5 added smla_plan_launches). The tree and cache page
+ * calls came later and change nothing that version 5 had: look their symbols up. */
 int32_t smla_abi_version(void);
 
 /*
@@ -394,6 +395,183 @@ smla_status smla_indexer_logits(const smla_indexer_desc* d, const void* q, const
  */
 smla_status smla_indexer_topk(const smla_indexer_desc* d, const float* logits,
                               const int32_t* context_lens, int32_t* topk, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * Tree attention: the attention that verifies drafted tokens. Every request has a context in
+ * the paged cache and a few nodes (drafted tokens) whose keys stand behind it; a node attends
+ * the whole context and the nodes it sees, its ancestors in the tree and itself. One node per
+ * request is dense single-token decode, and a chain (no mask) is the usual causal decode of
+ * several tokens. The pages name the multi-token decode of the drafts (vLLM PR #52164,
+ * "功能与动机": next_n query rows of a request handled natively); the tree's mask is this
+ * library's own.
+ * ---------------------------------------------------------------------------------------
+ */
+typedef struct smla_tree_desc {
+  int32_t num_tokens;        /* T >= 1: rows of q and out; cu_nodes[B] may be smaller */
+  int32_t num_heads;         /* H: 1..128 */
+  int32_t num_requests;      /* B: 1..65536 rows of page_table */
+  int32_t page_size;         /* P: power of two, 1..4096 */
+  int64_t num_pages;         /* pages in kv_cache; num_pages * P < 2^31 - 1 */
+  int32_t page_table_stride; /* entries per page_table row (>= 1) */
+  int32_t kv_format;         /* SMLA_KV_* */
+  float sm_scale;            /* softmax scale multiplying q.k */
+  float kv_scale;            /* SMLA_KV_FP8_TENSOR: the cache's scale (finite, > 0) */
+  int32_t mask_words;        /* W: 32-bit words of a mask row; 0 without a mask; at most 2048 */
+  int32_t reserved[3];       /* must be zero */
+} smla_tree_desc;
+
+/*
+ * Bytes of device workspace smla_tree_decode needs for `d` on the current device: the device
+ * error word and the partial results of work that several SMs share (about 40 MB, whatever the
+ * batch's size). The caller allocates it (256-byte aligned) and zeroes it once before first
+ * use; smla_read_error reads and clears the error word. Writes 0 into *bytes on error.
+ */
+smla_status smla_tree_workspace_size(const smla_tree_desc* d, size_t* bytes);
+
+/*
+ * Attention of all nodes over their contexts and the nodes they see.
+ *   q            [T, H, 576] bf16, 16-byte aligned: node i of request r is row cu_nodes[r] + i.
+ *   kv_cache     as in smla_decode. Slot s < context_lens[r] is context; the key of node i
+ *                is at slot context_lens[r] + i (smla_pack_kv or smla_store_kv_normed wrote it).
+ *   page_table   [B, page_table_stride] int32: request-local page -> physical page.
+ *   context_lens [B] int32, >= 0.
+ *   cu_nodes     [B + 1] int32, ascending from cu_nodes[0] >= 0: request r has n_r =
+ *                cu_nodes[r + 1] - cu_nodes[r] nodes (0: none). Rows of out that belong to no
+ *                node (before cu_nodes[0], from cu_nodes[B] on) are left as they were.
+ *   tree_mask    [T, W] 32-bit words, or NULL with mask_words = 0. Bit j % 32 of word j / 32 of
+ *                row cu_nodes[r] + i: node i sees node j (bits at or past n_r are ignored; a
+ *                node that does not see itself is allowed). NULL: node i sees nodes j <= i.
+ *   sink         [H] fp32 or NULL, as in smla_decode.
+ *   out          [T, H, 512] bf16, 16-byte aligned: sum_j e^{s_j} v_j / (sum_j e^{s_j} +
+ *                [sink] e^{sigma_h}), s_j = sm_scale <q, k_j>; 0 where a node sees nothing.
+ *   lse          [T, H] fp32 or NULL: natural log of the denominator (-inf where it is empty).
+ *   workspace    smla_tree_workspace_size(d) bytes, 256-byte aligned; calls that may overlap
+ *                (two streams, two graphs) need one each.
+ * The lengths are read on the device: a captured call serves any batch that fits `d`.
+ *
+ * Slots whose page entry lies outside [0, num_pages) are skipped like hidden ones
+ * (SMLA_DEVERR_PAGE). A request whose context is negative, whose nodes are not within
+ * [0, T] or more than 32 W with a mask, or whose slots do not fit the page table is left out
+ * (SMLA_DEVERR_INDEX): its rows of out and lse are not written. What a node does not see never
+ * reaches its result, whatever the bytes there: rows past the last node are not used, and a
+ * key with a NaN among its latent values makes the results of the nodes that see it NaN (with
+ * an infinity they are unspecified) and leaves the other nodes' as they are.
+ *
+ * Precision. Scores, softmax statistics and sums are fp32. With the FP8 formats q and the keys
+ * enter the tensor cores as f16: q exactly, brought into range by a power of two a row, and
+ * the keys within the operand range that smla_decode documents for SMLA_KV_FP8_DS
+ * (SMLA_DEVERR_RANGE); probabilities enter PV as f16. With SMLA_KV_BF16 q, keys and
+ * probabilities enter as bf16.
+ */
+smla_status smla_tree_decode(const smla_tree_desc* d, const void* q, const void* kv_cache,
+                             const int32_t* page_table, const int32_t* context_lens,
+                             const int32_t* cu_nodes, const uint32_t* tree_mask, const float* sink,
+                             void* out, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * Pages of the cache: copied, compacted, forked, and handed out and taken back. All calls work
+ * on every layer of a model at once: the cache of layer l starts at kv_cache + l * layer_stride
+ * and all layers share the page table. They move bytes and whole numbers only, and their
+ * results do not depend on how the GPU schedules them.
+ * ---------------------------------------------------------------------------------------
+ */
+enum {
+  /* smla_cache_desc.kv_format: besides SMLA_KV_*, the key pages of smla_indexer_logits
+   * (P x 128 codes, then P fp32 scales; P = 16, 32, 64 or 128). */
+  SMLA_CACHE_INDEX_KEYS = 3
+};
+
+typedef struct smla_cache_desc {
+  int32_t kv_format;         /* SMLA_KV_* or SMLA_CACHE_INDEX_KEYS */
+  int32_t num_layers;        /* L >= 1 */
+  int32_t page_size;         /* P: power of two, 1..4096 */
+  int32_t num_requests;      /* B: 1..65536 rows of page_table */
+  int32_t page_table_stride; /* entries per page_table row (>= 1) */
+  int32_t reserved;          /* must be zero */
+  int64_t num_pages;         /* pages of a layer (1 .. 2^31 - 1) */
+  int64_t layer_stride;      /* bytes from one layer's cache to the next: a multiple of 16, at
+                                least num_pages pages (ignored with one layer) */
+} smla_cache_desc;
+
+/*
+ * Copy pages: in every layer, page dst_pages[i] receives the bytes of page src_pages[i], i < n
+ * (int32 each). A pair with -1 on either side, or with both sides equal, is skipped; one outside
+ * [0, num_pages) is skipped and sets SMLA_DEVERR_PAGE. The pages of dst_pages must be distinct
+ * and must not stand in src_pages: their bytes are unspecified otherwise.
+ * Status of this and the calls below (before any launch): SMLA_ERR_UNSUPPORTED for another
+ * kv_format, SMLA_ERR_SHAPE for a size or a reserved word, SMLA_ERR_NULL or SMLA_ERR_ALIGN for a
+ * pointer (kv_cache 16-byte, the rest 4-byte aligned); n == 0 launches nothing. error_word:
+ * device int32 receiving SMLA_DEVERR_* bits, or NULL.
+ */
+smla_status smla_cache_copy_pages(const smla_cache_desc* d, const int32_t* src_pages,
+                                  const int32_t* dst_pages, int64_t n, void* kv_cache,
+                                  int32_t* error_word, void* stream);
+
+/*
+ * Compact kept rows in place: in every layer, slot starts[r] + k of request r receives the row
+ * of slot starts[r] + keep[cu_keep[r] + k], for k < count_r = cu_keep[r + 1] - cu_keep[r].
+ * The accepted path of a drafted tree becomes context with starts = the context lengths and
+ * keep = the accepted nodes; evicted slots close up with starts = 0 and keep = the others.
+ *   page_table [B, page_table_stride], starts [B], cu_keep [B + 1], keep [n_keep] int32. The kept
+ *   offsets of a request are strictly ascending and not negative. new_lens [B] int32 or NULL
+ *   receives starts[r] + count_r; it must not overlap the other arguments.
+ * Rows of other slots stay as they were. A request whose start or count is negative or reaches
+ * past n_keep is left out (SMLA_DEVERR_INDEX, its new_lens not written). A kept row that breaks
+ * the ascending order, or has a slot outside the page table (SMLA_DEVERR_INDEX) or a page
+ * outside the cache (SMLA_DEVERR_PAGE), is not moved. Pages that several requests hold must be
+ * made private first (smla_cache_copy_pages): the rows of both would move.
+ */
+smla_status smla_cache_compact(const smla_cache_desc* d, const int32_t* page_table,
+                               const int32_t* starts, const int32_t* cu_keep, const int32_t* keep,
+                               int64_t n_keep, void* kv_cache, int32_t* new_lens,
+                               int32_t* error_word, void* stream);
+
+/*
+ * The tables of the two calls below:
+ *   page_table [B, page_table_stride] int32: request r holds entries [0, ceil(lens[r] / P)).
+ *   lens       [B] int32: slots of each request.
+ *   refcounts  [num_pages] int32: requests that hold a page (below 2^30); 0 for a free page.
+ *   free_list  [num_pages] int32: its first free_count[0] entries are the free pages; pages are
+ *              taken off its end and the entries they leave become -1.
+ *   free_count [1] int32.
+ *
+ * Fork requests: for i < n, request dst_requests[i] (which holds no slots) gets the slots of
+ * src_requests[i]. Full pages are shared (refcount + 1). The used rows of a partly filled last
+ * page are copied, in every layer, to a page off the free list (i in ascending order). lens
+ * follows.
+ *   fork_pages [n] int32 receives the page taken, -1 where none was needed, -2 where the fork
+ *   was refused and changed nothing: SMLA_DEVERR_INDEX for a request outside [0, B), a target
+ *   that is listed twice or is also a source, a target that holds slots, or a source whose
+ *   length does not fit the table; SMLA_DEVERR_PAGE for a free list that is too short for this
+ *   fork and those before it, or whose entry is no page.
+ * n is at most num_requests (SMLA_ERR_SHAPE).
+ */
+smla_status smla_cache_fork(const smla_cache_desc* d, int32_t* page_table, int32_t* lens,
+                            int32_t* refcounts, int32_t* free_list, int32_t* free_count,
+                            const int32_t* src_requests, const int32_t* dst_requests, int32_t n,
+                            int32_t* fork_pages, void* kv_cache, int32_t* error_word,
+                            void* stream);
+
+/*
+ * Resize requests: for i < n, request requests[i] gets length new_lens[i] (0 frees all of it).
+ * First the pages past the new lengths leave the table (their entries become -1) and lose a
+ * holder; those without a holder go to the end of the free list in ascending order. Then the
+ * requests that grow take pages off its end, in the order of the call. No cache row is touched.
+ *   work [2 n] int32: scratch of this call.
+ * A request outside [0, B), listed twice, or with a length outside [0, page_table_stride * P] is
+ * left as it was (SMLA_DEVERR_INDEX). A request grows only if the pages that it and those before
+ * it ask for are free; otherwise it stays as it was (SMLA_DEVERR_PAGE). A released entry that is
+ * no page, or a page released more often than it was held, sets SMLA_DEVERR_PAGE and is not
+ * listed. n is at most num_requests (SMLA_ERR_SHAPE). kv_format, num_layers and layer_stride
+ * are checked and not used.
+ */
+smla_status smla_cache_resize(const smla_cache_desc* d, int32_t* page_table, int32_t* lens,
+                              int32_t* refcounts, int32_t* free_list, int32_t* free_count,
+                              const int32_t* requests, const int32_t* new_lens, int32_t n,
+                              int32_t* work, int32_t* error_word, void* stream);
 
 /*
  * Size of the library-owned scratch array used by smla_decode_noalloc (16 MiB per device).

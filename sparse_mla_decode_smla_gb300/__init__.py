@@ -15,6 +15,7 @@ from ._build import LIB as LIB_PATH
 SMLA_KV_BF16 = 0
 SMLA_KV_FP8_DS = 1
 SMLA_KV_FP8_TENSOR = 2
+SMLA_CACHE_INDEX_KEYS = 3
 SMLA_SCALE_POW2 = 0
 SMLA_SCALE_FP32 = 1
 SMLA_Q_BF16 = 0
@@ -39,7 +40,8 @@ EXPORTS = ["smla_status_string", "smla_abi_version", "smla_workspace_size", "sml
            "smla_pack_kv", "smla_gather_dequant", "smla_read_error", "smla_decode_noalloc",
            "smla_set_kernel_events", "smla_pack_kv_fp8_tensor", "smla_selftest_wait_timeout",
            "smla_noalloc_read_error", "smla_indexer_logits", "smla_indexer_topk", "smla_store_kv_normed",
-           "smla_plan_launches"]
+           "smla_plan_launches", "smla_tree_workspace_size", "smla_tree_decode", "smla_cache_copy_pages",
+           "smla_cache_compact", "smla_cache_fork", "smla_cache_resize"]
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -80,6 +82,22 @@ class smla_store_desc(ctypes.Structure):
                 ("kv_scale", ctypes.c_float), ("rms_eps", ctypes.c_float), ("n", ctypes.c_int64),
                 ("num_slots", ctypes.c_int64), ("max_position", ctypes.c_int64),
                 ("reserved", ctypes.c_int32 * 2)]
+
+
+class smla_tree_desc(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("num_requests", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64), ("page_table_stride", ctypes.c_int32),
+                ("kv_format", ctypes.c_int32), ("sm_scale", ctypes.c_float),
+                ("kv_scale", ctypes.c_float), ("mask_words", ctypes.c_int32),
+                ("reserved", ctypes.c_int32 * 3)]
+
+
+class smla_cache_desc(ctypes.Structure):
+    _fields_ = [("kv_format", ctypes.c_int32), ("num_layers", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_requests", ctypes.c_int32),
+                ("page_table_stride", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64), ("layer_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -127,6 +145,19 @@ def lib() -> ctypes.CDLL:
         L.smla_indexer_topk.argtypes = [XD, P, P, P, P]
         L.smla_store_kv_normed.restype = I32
         L.smla_store_kv_normed.argtypes = [ctypes.POINTER(smla_store_desc), P, P, P, P, P, P, P, P, P]
+        TD, CD = ctypes.POINTER(smla_tree_desc), ctypes.POINTER(smla_cache_desc)
+        L.smla_tree_workspace_size.restype = I32
+        L.smla_tree_workspace_size.argtypes = [TD, ctypes.POINTER(SZ)]
+        L.smla_tree_decode.restype = I32
+        L.smla_tree_decode.argtypes = [TD, P, P, P, P, P, P, P, P, P, P, SZ, P]
+        L.smla_cache_copy_pages.restype = I32
+        L.smla_cache_copy_pages.argtypes = [CD, P, P, I64, P, P, P]
+        L.smla_cache_compact.restype = I32
+        L.smla_cache_compact.argtypes = [CD, P, P, P, P, I64, P, P, P, P]
+        L.smla_cache_fork.restype = I32
+        L.smla_cache_fork.argtypes = [CD, P, P, P, P, P, P, P, I32, P, P, P, P]
+        L.smla_cache_resize.restype = I32
+        L.smla_cache_resize.argtypes = [CD, P, P, P, P, P, P, P, I32, P, P, P]
         _lib = L
     return _lib
 
@@ -237,9 +268,11 @@ def selftest_wait_timeout(error_word, limit_us: int, stream=None):
 
 
 def read_error(desc, workspace, stream=None) -> int:
-    """Synchronises, returns and clears the device error word (SMLA_DEVERR_* bits)."""
+    """Synchronises, returns and clears the device error word (SMLA_DEVERR_* bits) of a decode or
+    tree decode workspace. desc is not read: None, or the descriptor the workspace was made for."""
     v = ctypes.c_int32(0)
-    st = lib().smla_read_error(ctypes.byref(desc), _ptr(workspace),
+    d = ctypes.byref(desc) if isinstance(desc, smla_desc) else None
+    st = lib().smla_read_error(d, _ptr(workspace),
                                workspace.numel() * workspace.element_size(), ctypes.byref(v),
                                _stream(stream))
     if st not in DEVICE_ERROR_STATUSES:
@@ -288,3 +321,69 @@ def store_kv_normed(kv_format, latent, rope, norm_weight, eps, positions, cos_si
     _check("smla_store_kv_normed", lib().smla_store_kv_normed(
         ctypes.byref(d), _ptr(latent), _ptr(rope), _ptr(norm_weight), _ptr(positions), _ptr(cos_sin),
         _ptr(slot_mapping), _ptr(kv_cache), _ptr(error_word), _stream(stream)))
+
+
+def make_tree_desc(num_tokens, num_heads, num_requests, page_size, num_pages, page_table_stride, kv_format,
+                   sm_scale, mask_words=0, kv_scale=1.0) -> smla_tree_desc:
+    d = smla_tree_desc()
+    d.num_tokens, d.num_heads, d.num_requests = num_tokens, num_heads, num_requests
+    d.page_size, d.num_pages, d.page_table_stride = page_size, num_pages, page_table_stride
+    d.kv_format, d.sm_scale, d.kv_scale, d.mask_words = kv_format, sm_scale, kv_scale, mask_words
+    return d
+
+
+def tree_workspace_size(desc: smla_tree_desc) -> int:
+    n = ctypes.c_size_t(0)
+    _check("smla_tree_workspace_size", lib().smla_tree_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def tree_decode(desc, q, kv_cache, page_table, context_lens, cu_nodes, tree_mask, sink, out, lse, workspace,
+                stream=None):
+    """Attention of drafted nodes over their contexts and the nodes they see (smla_tree_decode)."""
+    _check("smla_tree_decode", lib().smla_tree_decode(
+        ctypes.byref(desc), _ptr(q), _ptr(kv_cache), _ptr(page_table), _ptr(context_lens), _ptr(cu_nodes),
+        _ptr(tree_mask), _ptr(sink), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def make_cache_desc(kv_format, num_layers, page_size, num_pages, num_requests, page_table_stride,
+                    layer_stride=None) -> smla_cache_desc:
+    """layer_stride: bytes between layers; None: the layers' pages follow one another."""
+    row = {SMLA_KV_BF16: 1152, SMLA_KV_FP8_DS: 656, SMLA_KV_FP8_TENSOR: 576, SMLA_CACHE_INDEX_KEYS: 132}
+    d = smla_cache_desc()
+    d.kv_format, d.num_layers, d.page_size = kv_format, num_layers, page_size
+    d.num_requests, d.page_table_stride, d.num_pages = num_requests, page_table_stride, num_pages
+    d.layer_stride = num_pages * page_size * row.get(kv_format, 0) if layer_stride is None else layer_stride
+    return d
+
+
+def cache_copy_pages(desc, src_pages, dst_pages, kv_cache, error_word=None, stream=None):
+    """Copy pages in every layer (smla_cache_copy_pages)."""
+    _check("smla_cache_copy_pages", lib().smla_cache_copy_pages(
+        ctypes.byref(desc), _ptr(src_pages), _ptr(dst_pages), src_pages.shape[0], _ptr(kv_cache),
+        _ptr(error_word), _stream(stream)))
+
+
+def cache_compact(desc, page_table, starts, cu_keep, keep, kv_cache, new_lens=None, error_word=None, stream=None):
+    """Move kept rows together, in place, in every layer (smla_cache_compact)."""
+    _check("smla_cache_compact", lib().smla_cache_compact(
+        ctypes.byref(desc), _ptr(page_table), _ptr(starts), _ptr(cu_keep), _ptr(keep), keep.shape[0],
+        _ptr(kv_cache), _ptr(new_lens), _ptr(error_word), _stream(stream)))
+
+
+def cache_fork(desc, page_table, lens, refcounts, free_list, free_count, src_requests, dst_requests, fork_pages,
+               kv_cache, error_word=None, stream=None):
+    """Fork requests: full pages shared, the partly filled last one copied (smla_cache_fork)."""
+    _check("smla_cache_fork", lib().smla_cache_fork(
+        ctypes.byref(desc), _ptr(page_table), _ptr(lens), _ptr(refcounts), _ptr(free_list), _ptr(free_count),
+        _ptr(src_requests), _ptr(dst_requests), src_requests.shape[0], _ptr(fork_pages), _ptr(kv_cache),
+        _ptr(error_word), _stream(stream)))
+
+
+def cache_resize(desc, page_table, lens, refcounts, free_list, free_count, requests, new_lens, work,
+                 error_word=None, stream=None):
+    """Grow and shrink requests over the free list (smla_cache_resize); work: int32 [2 n] scratch."""
+    _check("smla_cache_resize", lib().smla_cache_resize(
+        ctypes.byref(desc), _ptr(page_table), _ptr(lens), _ptr(refcounts), _ptr(free_list), _ptr(free_count),
+        _ptr(requests), _ptr(new_lens), requests.shape[0], _ptr(work), _ptr(error_word), _stream(stream)))

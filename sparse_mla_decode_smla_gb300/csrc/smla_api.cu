@@ -8,8 +8,10 @@
 #include <atomic>
 
 #include "../../include/smla.h"
+#include "cache_pages.h"
 #include "indexer.h"
 #include "kernels.h"
+#include "tree_decode.h"
 
 namespace {
 
@@ -224,6 +226,51 @@ smla::IndexerArgs make_indexer_args(const smla_indexer_desc* d, const int32_t* c
   a.K = d->topk;
   a.num_pages = d->num_pages;
   return a;
+}
+
+smla_status check_tree_desc(const smla_tree_desc* d) {
+  if (!d) return SMLA_ERR_NULL;
+  if (d->num_tokens < 1 || d->num_requests < 1 || d->num_requests > smla::kTreeMaxRequests) return SMLA_ERR_SHAPE;
+  if (d->num_heads < 1 || d->num_heads > 128) return SMLA_ERR_SHAPE;
+  if (int64_t(d->num_tokens) * d->num_heads >= (int64_t(1) << 31)) return SMLA_ERR_SHAPE;
+  if (!is_pow2(d->page_size) || d->page_size > 4096) return SMLA_ERR_SHAPE;
+  if (d->num_pages < 1 || d->num_pages >= smla::kMaxGatherSlots || d->num_pages * d->page_size >= smla::kMaxGatherSlots)
+    return SMLA_ERR_SHAPE;
+  if (d->page_table_stride < 1) return SMLA_ERR_SHAPE;
+  if (d->kv_format != SMLA_KV_BF16 && d->kv_format != SMLA_KV_FP8_DS && d->kv_format != SMLA_KV_FP8_TENSOR)
+    return SMLA_ERR_UNSUPPORTED;
+  if (!isfinite(d->sm_scale)) return SMLA_ERR_SHAPE;
+  if (d->kv_format == SMLA_KV_FP8_TENSOR && !(isfinite(d->kv_scale) && d->kv_scale > 0.f)) return SMLA_ERR_SHAPE;
+  if (d->mask_words < 0 || d->mask_words > 2048) return SMLA_ERR_SHAPE;
+  for (int i = 0; i < 3; ++i)
+    if (d->reserved[i] != 0) return SMLA_ERR_SHAPE;
+  return SMLA_OK;
+}
+
+// Checks a cache description and fills the launchers' arguments from it.
+smla_status make_cache_pages(const smla_cache_desc* d, void* kv, int32_t* err, smla::CachePages* c) {
+  if (!d) return SMLA_ERR_NULL;
+  const bool keys = d->kv_format == SMLA_CACHE_INDEX_KEYS;
+  if (!keys && d->kv_format != SMLA_KV_BF16 && d->kv_format != SMLA_KV_FP8_DS && d->kv_format != SMLA_KV_FP8_TENSOR)
+    return SMLA_ERR_UNSUPPORTED;
+  if (!is_pow2(d->page_size) || d->page_size > 4096) return SMLA_ERR_SHAPE;
+  if (keys && (d->page_size < 16 || d->page_size > 128)) return SMLA_ERR_SHAPE;
+  if (d->num_layers < 1 || d->num_requests < 1 || d->num_requests > smla::kCacheMaxRequests) return SMLA_ERR_SHAPE;
+  if (d->page_table_stride < 1 || d->reserved != 0) return SMLA_ERR_SHAPE;
+  if (d->num_pages < 1 || d->num_pages >= (int64_t(1) << 31)) return SMLA_ERR_SHAPE;
+  c->kv = static_cast<uint8_t*>(kv);
+  c->L = d->num_layers;
+  c->B = d->num_requests;
+  c->stride = d->page_table_stride;
+  c->log2_page = ilog2(d->page_size);
+  c->index_keys = keys ? 1 : 0;
+  c->row_bytes = keys ? 128 : smla::kv_row_bytes(d->kv_format);
+  c->page_bytes = int64_t(d->page_size) * (keys ? 132 : c->row_bytes);
+  c->num_pages = d->num_pages;
+  c->layer_stride = d->num_layers > 1 ? d->layer_stride : 0;
+  c->err = err;
+  if (d->num_layers > 1 && (d->layer_stride % 16 != 0 || d->layer_stride < d->num_pages * c->page_bytes)) return SMLA_ERR_SHAPE;
+  return SMLA_OK;
 }
 
 // The status smla_read_error reports for a device error word: a timeout first (every
@@ -503,6 +550,147 @@ smla_status smla_indexer_topk(const smla_indexer_desc* d, const float* logits, c
   // one CTA a token and an SM: with more tokens than SMs, the longest rows go first
   a.longest_first = d->num_tokens > sms && d->num_tokens <= smla::kTkRankMax ? 1 : 0;
   if (smla::launch_indexer_topk(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return SMLA_ERR_CUDA;
+  return SMLA_OK;
+}
+
+smla_status smla_tree_workspace_size(const smla_tree_desc* d, size_t* bytes) {
+  if (!bytes) return SMLA_ERR_NULL;
+  *bytes = 0;
+  smla_status st = check_tree_desc(d);
+  if (st != SMLA_OK) return st;
+  int sms = 0;
+  st = current_device(&sms);
+  if (st != SMLA_OK) return st;
+  *bytes = smla::tree_workspace_bytes(sms);
+  return SMLA_OK;
+}
+
+smla_status smla_tree_decode(const smla_tree_desc* d, const void* q, const void* kv_cache, const int32_t* page_table,
+                             const int32_t* context_lens, const int32_t* cu_nodes, const uint32_t* tree_mask,
+                             const float* sink, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  smla_status st = check_tree_desc(d);
+  if (st != SMLA_OK) return st;
+  if (!q || !kv_cache || !page_table || !context_lens || !cu_nodes || !out || !workspace) return SMLA_ERR_NULL;
+  if ((tree_mask != nullptr) != (d->mask_words > 0)) return SMLA_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(page_table, 4) ||
+      !aligned(context_lens, 4) || !aligned(cu_nodes, 4) || !aligned(tree_mask, 4) || !aligned(sink, 4) ||
+      !aligned(lse, 4) || !aligned(workspace, kWsAlign))
+    return SMLA_ERR_ALIGN;
+  int sms = 0;
+  st = current_device(&sms);
+  if (st != SMLA_OK) return st;
+  if (workspace_bytes < smla::tree_workspace_bytes(sms)) return SMLA_ERR_WORKSPACE;
+  smla::TreeArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.kv = static_cast<const uint8_t*>(kv_cache);
+  a.page_table = page_table;
+  a.ctx = context_lens;
+  a.cu = cu_nodes;
+  a.mask = tree_mask;
+  a.sink = sink;
+  a.out = out;
+  a.lse = lse;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.T = d->num_tokens;
+  a.H = d->num_heads;
+  a.B = d->num_requests;
+  a.W = d->mask_words;
+  a.stride = d->page_table_stride;
+  a.log2_page = ilog2(d->page_size);
+  a.kv_format = d->kv_format;
+  a.num_pages = d->num_pages;
+  a.c2 = d->sm_scale * 1.4426950408889634f;
+  a.kv_scale = d->kv_format == SMLA_KV_FP8_TENSOR ? d->kv_scale : 1.f;
+  if (smla::launch_tree_decode(a, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) return SMLA_ERR_CUDA;
+  return SMLA_OK;
+}
+
+smla_status smla_cache_copy_pages(const smla_cache_desc* d, const int32_t* src_pages, const int32_t* dst_pages, int64_t n,
+                                  void* kv_cache, int32_t* error_word, void* stream) {
+  smla::CachePages c;
+  smla_status st = make_cache_pages(d, kv_cache, error_word, &c);
+  if (st != SMLA_OK) return st;
+  if (n < 0 || n > d->num_pages) return SMLA_ERR_SHAPE;
+  if (n == 0) return SMLA_OK;
+  if (!src_pages || !dst_pages || !kv_cache) return SMLA_ERR_NULL;
+  if (!aligned(src_pages, 4) || !aligned(dst_pages, 4) || !aligned(kv_cache, 16) || !aligned(error_word, 4))
+    return SMLA_ERR_ALIGN;
+  int sms = 0;
+  st = current_device(&sms);
+  if (st != SMLA_OK) return st;
+  if (smla::launch_cache_copy_pages(c, src_pages, dst_pages, n, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return SMLA_ERR_CUDA;
+  return SMLA_OK;
+}
+
+smla_status smla_cache_compact(const smla_cache_desc* d, const int32_t* page_table, const int32_t* starts,
+                               const int32_t* cu_keep, const int32_t* keep, int64_t n_keep, void* kv_cache,
+                               int32_t* new_lens, int32_t* error_word, void* stream) {
+  smla::CachePages c;
+  smla_status st = make_cache_pages(d, kv_cache, error_word, &c);
+  if (st != SMLA_OK) return st;
+  if (n_keep < 0 || n_keep >= (int64_t(1) << 31)) return SMLA_ERR_SHAPE;
+  if (!page_table || !starts || !cu_keep || (!keep && n_keep > 0) || !kv_cache) return SMLA_ERR_NULL;
+  if (!aligned(page_table, 4) || !aligned(starts, 4) || !aligned(cu_keep, 4) || !aligned(keep, 4) ||
+      !aligned(kv_cache, 16) || !aligned(new_lens, 4) || !aligned(error_word, 4))
+    return SMLA_ERR_ALIGN;
+  int sms = 0;
+  st = current_device(&sms);
+  if (st != SMLA_OK) return st;
+  if (smla::launch_cache_compact(c, page_table, starts, cu_keep, keep, n_keep, new_lens, sms,
+                                 static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return SMLA_ERR_CUDA;
+  return SMLA_OK;
+}
+
+smla_status smla_cache_fork(const smla_cache_desc* d, int32_t* page_table, int32_t* lens, int32_t* refcounts,
+                            int32_t* free_list, int32_t* free_count, const int32_t* src_requests,
+                            const int32_t* dst_requests, int32_t n, int32_t* fork_pages, void* kv_cache,
+                            int32_t* error_word, void* stream) {
+  smla::CachePages c;
+  smla_status st = make_cache_pages(d, kv_cache, error_word, &c);
+  if (st != SMLA_OK) return st;
+  if (n < 0 || n > d->num_requests) return SMLA_ERR_SHAPE;
+  if (n == 0) return SMLA_OK;
+  if (!page_table || !lens || !refcounts || !free_list || !free_count || !src_requests || !dst_requests || !fork_pages ||
+      !kv_cache)
+    return SMLA_ERR_NULL;
+  if (!aligned(page_table, 4) || !aligned(lens, 4) || !aligned(refcounts, 4) || !aligned(free_list, 4) ||
+      !aligned(free_count, 4) || !aligned(src_requests, 4) || !aligned(dst_requests, 4) || !aligned(fork_pages, 4) ||
+      !aligned(kv_cache, 16) || !aligned(error_word, 4))
+    return SMLA_ERR_ALIGN;
+  int sms = 0;
+  st = current_device(&sms);
+  if (st != SMLA_OK) return st;
+  const smla::CacheTables t = {page_table, lens, refcounts, free_list, free_count};
+  if (smla::launch_cache_fork(c, t, src_requests, dst_requests, n, fork_pages, sms, static_cast<cudaStream_t>(stream)) !=
+      cudaSuccess)
+    return SMLA_ERR_CUDA;
+  return SMLA_OK;
+}
+
+smla_status smla_cache_resize(const smla_cache_desc* d, int32_t* page_table, int32_t* lens, int32_t* refcounts,
+                              int32_t* free_list, int32_t* free_count, const int32_t* requests, const int32_t* new_lens,
+                              int32_t n, int32_t* work, int32_t* error_word, void* stream) {
+  smla::CachePages c;
+  smla_status st = make_cache_pages(d, nullptr, error_word, &c);
+  if (st != SMLA_OK) return st;
+  if (n < 0 || n > d->num_requests) return SMLA_ERR_SHAPE;
+  if (n == 0) return SMLA_OK;
+  if (!page_table || !lens || !refcounts || !free_list || !free_count || !requests || !new_lens || !work)
+    return SMLA_ERR_NULL;
+  if (!aligned(page_table, 4) || !aligned(lens, 4) || !aligned(refcounts, 4) || !aligned(free_list, 4) ||
+      !aligned(free_count, 4) || !aligned(requests, 4) || !aligned(new_lens, 4) || !aligned(work, 4) ||
+      !aligned(error_word, 4))
+    return SMLA_ERR_ALIGN;
+  int sms = 0;
+  st = current_device(&sms);
+  if (st != SMLA_OK) return st;
+  const smla::CacheTables t = {page_table, lens, refcounts, free_list, free_count};
+  if (smla::launch_cache_resize(c, t, requests, new_lens, n, work, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return SMLA_ERR_CUDA;
   return SMLA_OK;
 }
 

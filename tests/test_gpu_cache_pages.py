@@ -1,0 +1,281 @@
+"""The cache's page operators on the GPU against their plain models, bit for bit: whole caches and
+tables are compared, so a byte moved too much is found as well."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.cache_pages_oracle as C
+import sparse_mla_decode_smla_gb300 as smla
+
+pytestmark = pytest.mark.gpu
+
+FMT = {"bf16": 0, "fp8_ds": 1, "fp8_tensor": 2, "index_keys": 3}
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+
+
+class Pool:
+    """A cache of L layers with its tables, on the GPU and as numpy arrays."""
+
+    def __init__(self, fmt, L, page, lens, stride, pages, seed=0, gap=0):
+        g = np.random.default_rng(seed)
+        self.fmt, self.L, self.P, self.B, self.stride, self.pages = fmt, L, page, len(lens), stride, pages
+        self.cache = g.integers(0, 256, (L, pages, C.page_bytes(fmt, page)), dtype=np.uint8)
+        self.table = np.full((self.B, stride), -1, dtype=np.int32)
+        perm = g.permutation(pages).astype(np.int32)
+        self.lens, self.refs = np.array(lens, dtype=np.int32), np.zeros(pages, dtype=np.int32)
+        at = 0
+        for r, n in enumerate(lens):
+            k = -(-n // page)
+            self.table[r, :k] = perm[at:at + k]
+            at += k
+        self.refs[perm[:at]] = 1
+        self.free = np.full(pages, -1, dtype=np.int32)
+        self.free[:pages - at] = perm[at:]
+        self.count = pages - at
+        layer = pages * C.page_bytes(fmt, page)
+        self.raw = torch.zeros((L, layer + gap), dtype=torch.uint8, device="cuda")
+        self.raw[:, :layer] = torch.from_numpy(self.cache.reshape(L, -1)).cuda()
+        self.desc = smla.make_cache_desc(FMT[fmt], L, page, pages, self.B, stride, layer + gap)
+        self.d_table, self.d_lens, self.d_refs, self.d_free = (_dev(x) for x in (self.table, self.lens, self.refs, self.free))
+        self.d_count, self.err = _dev([self.count]), torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def tables(self):
+        return self.d_table, self.d_lens, self.d_refs, self.d_free, self.d_count
+
+    def fork(self, src, dst, stream=None):
+        s, d = _dev(src), _dev(dst)
+        got = torch.full((len(src),), -9, dtype=torch.int32, device="cuda")
+        smla.cache_fork(self.desc, *self.tables(), s, d, got, self.raw, self.err, stream)
+        e, self.count, pages = C.fork(self.cache, self.fmt, self.P, self.table, self.lens, self.refs, self.free, self.count, src, dst)
+        torch.cuda.synchronize()
+        assert got.tolist() == pages
+        return e
+
+    def resize(self, req, new, stream=None):
+        r, n = _dev(req), _dev(new)
+        work = torch.empty(2 * len(req), dtype=torch.int32, device="cuda")
+        smla.cache_resize(self.desc, *self.tables(), r, n, work, self.err, stream)
+        e, self.count = C.resize(self.P, self.table, self.lens, self.refs, self.free, self.count, req, new)
+        torch.cuda.synchronize()
+        return e
+
+    def check(self, err=0):
+        torch.cuda.synchronize()
+        layer = self.cache[0].size
+        assert np.array_equal(self.raw[:, :layer].cpu().numpy().reshape(self.cache.shape), self.cache)
+        assert not self.raw[:, layer:].any()
+        for name, d, a in (("table", self.d_table, self.table), ("lens", self.d_lens, self.lens), ("refs", self.d_refs, self.refs),
+                           ("free", self.d_free, self.free)):
+            assert np.array_equal(d.cpu().numpy(), a), name
+        assert self.d_count.item() == self.count
+        assert self.err.item() == err
+        self.err.zero_()
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("page", [1, 2, 16, 64, 512])
+def test_copy_pages(fmt, page):
+    if fmt == "index_keys" and not 16 <= page <= 128:
+        pytest.skip("index keys come in pages of 16 to 128 slots")
+    for L, n, gap in ((1, 1, 0), (3, 5, 48)):
+        p = Pool(fmt, L, page, [3], 4096, 14, seed=page, gap=gap)
+        ids = np.random.default_rng(n).permutation(14)
+        src, dst = ids[:n].tolist(), ids[n:2 * n].tolist()
+        smla.cache_copy_pages(p.desc, _dev(src), _dev(dst), p.raw, p.err)
+        C.copy_pages(p.cache, src, dst)
+        p.check()
+
+
+def test_copy_skips_and_flags():
+    p = Pool("fp8_ds", 2, 16, [3], 4, 9)
+    src, dst = [0, -1, 2, 5, 9, 3], [4, 1, -1, 5, 6, -7]
+    smla.cache_copy_pages(p.desc, _dev(src), _dev(dst), p.raw, p.err)
+    assert C.copy_pages(p.cache, src, dst) == C.ERR_PAGE
+    p.check(C.ERR_PAGE)
+    smla.cache_copy_pages(p.desc, _dev([8]), _dev([7]), p.raw)  # no error word
+    C.copy_pages(p.cache, [8], [7])
+    p.check()
+
+
+def test_copy_past_four_gigabytes():
+    # 32-bit offsets would wrap: the second layer starts past 4 GiB, and its last page past that
+    page, pages = 64, 110000
+    stride = pages * page * 656
+    assert stride > 1 << 32
+    raw = torch.zeros(2 * stride, dtype=torch.uint8, device="cuda")
+    d = smla.make_cache_desc(1, 2, page, pages, 1, 1, stride)
+    one = page * 656
+    a = torch.randint(0, 256, (2, one), dtype=torch.uint8, device="cuda")
+    for l in range(2):
+        raw[l * stride + 7 * one:l * stride + 8 * one] = a[l]
+    smla.cache_copy_pages(d, _dev([7]), _dev([pages - 1]), raw)
+    torch.cuda.synchronize()
+    for l in range(2):
+        assert torch.equal(raw[l * stride + (pages - 1) * one:(l + 1) * stride], a[l])
+    total = int(raw.view(torch.int64).ne(0).sum())
+    assert total <= 4 * one // 8
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("page", [1, 8, 16, 64])
+@pytest.mark.parametrize("L,gap", [(1, 0), (3, 16)])
+def test_compact(fmt, page, L, gap):
+    if fmt == "index_keys" and page < 16:
+        pytest.skip("index keys come in pages of 16 to 128 slots")
+    g = np.random.default_rng(page + L)
+    lens = [0, 1, 2, 70, 333, 1500, 64, 129]
+    p = Pool(fmt, L, page, lens, 1500 // page + 1, sum(-(-n // page) for n in lens) + 3, seed=5, gap=gap)
+    starts, keep = [], []
+    for n in lens:
+        st = int(g.integers(0, n + 1)) if n < 1000 else 3
+        rest = n - st
+        keep.append(sorted(g.choice(rest, int(g.integers(0, rest + 1)), replace=False).tolist()) if rest else [])
+        starts.append(st)
+    keep[4] = list(range(len(keep[4])))  # already in place
+    cu = np.concatenate([[0], np.cumsum([len(k) for k in keep])])
+    flat = [x for k in keep for x in k]
+    new = torch.full((len(lens),), -5, dtype=torch.int32, device="cuda")
+    smla.cache_compact(p.desc, p.d_table, _dev(starts), _dev(cu), _dev(flat), p.raw, new, p.err)
+    want = np.full(len(lens), -5)
+    assert C.compact(p.cache, fmt, page, p.table, starts, cu, flat, want) == 0
+    p.check()
+    assert new.tolist() == want.tolist()
+
+
+def test_compact_one_long_request_in_place():
+    # every chunk's targets are sources of rows before them: a wrong order shows
+    for fmt, keep in (("fp8_ds", list(range(1, 9000))), ("bf16", list(range(0, 9000, 2))), ("fp8_tensor", list(range(513, 9000)))):
+        p = Pool(fmt, 1, 64, [9000], 141, 150, seed=1)
+        smla.cache_compact(p.desc, p.d_table, _dev([0]), _dev([0, len(keep)]), _dev(keep), p.raw, None, p.err)
+        C.compact(p.cache, fmt, 64, p.table, [0], [0, len(keep)], keep)
+        p.check()
+
+
+def test_compact_refuses_what_it_cannot_move():
+    p = Pool("fp8_ds", 2, 4, [20, 20, 20, 20, 20], 5, 30, seed=3)
+    table = p.table.copy()
+    table[1, 2], table[2, 1] = 30, -1          # a page outside the cache, a page that is missing
+    starts, cu = [0, 0, 0, -1, 4], [0, 3, 6, 9, 10, 14]
+    keep = [5, 5, 7, 1, 8, 9, 2, 4, 5, 3, 1, 15, 16, 0]   # twice the same; bad pages; bad start; past the table; not ascending
+    new = torch.full((5,), -5, dtype=torch.int32, device="cuda")
+    smla.cache_compact(p.desc, _dev(table), _dev(starts), _dev(cu), _dev(keep), p.raw, new, p.err)
+    want = np.full(5, -5)
+    e = C.compact(p.cache, "fp8_ds", 4, table, starts, cu, keep, want)
+    assert e == C.ERR_INDEX | C.ERR_PAGE
+    p.check(e)
+    assert new.tolist() == want.tolist()
+    for bad in ([0, 3, 2, 3, 3, 3], [0, 99, 99, 99, 99, 99], [-1, 0, 0, 0, 0, 0]):
+        smla.cache_compact(p.desc, p.d_table, _dev([0] * 5), _dev(bad), _dev([1, 2, 3]), p.raw, None, p.err)
+        assert C.compact(p.cache, "fp8_ds", 4, p.table, [0] * 5, bad, [1, 2, 3]) == C.ERR_INDEX
+        p.check(C.ERR_INDEX)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("page", [1, 4, 16, 128])
+def test_fork(fmt, page):
+    if fmt == "index_keys" and page < 16:
+        pytest.skip("index keys come in pages of 16 to 128 slots")
+    lens = [0, 1, page, page + 1, 7 * page - 1, 300] + [0] * 8
+    p = Pool(fmt, 3, page, lens, 300 // page + 7, sum(-(-n // page) for n in lens) + 9, seed=page, gap=32)
+    assert p.fork([5, 1, 2, 0, 5, 3, 4, 5], [6, 7, 8, 9, 10, 11, 12, 13]) == 0
+    p.check()
+    # the copies let go, then the originals: the pages come back
+    assert p.resize([13, 6, 8, 10], [0, 0, 0, 0]) == 0
+    p.check()
+    assert p.resize([5, 4, 12, 11], [1, 0, page, 0]) == 0
+    p.check()
+
+
+def test_fork_refusals():
+    p = Pool("bf16", 2, 8, [9, 10, 16, 0, 0, 0, 0, 3], 2, 10, seed=4)  # two pages free
+    assert p.count == 3
+    e = p.fork([0, 0, 1, 99, 2, 3, 2], [3, 3, 7, 4, -1, 4, 5])
+    # 3 twice; 7 holds slots; no request 99; no request -1; 3 is a source and so no target; 2 -> 5 shares pages
+    assert e == C.ERR_INDEX
+    p.check(e)
+    e = p.fork([0, 1, 0, 7], [3, 4, 6, 99])
+    p.check(e)
+    assert p.resize([3, 4, 6, 5], [0, 0, 0, 0]) == 0
+    p.check()
+    q = Pool("bf16", 1, 8, [9, 16, 0, 0, 0, 0], 2, 5, seed=4)   # one page free, two forks that need one
+    assert q.fork([0, 0, 1], [2, 3, 4]) == C.ERR_PAGE
+    q.check(C.ERR_PAGE)
+
+
+def test_resize_random_walk():
+    g = np.random.default_rng(7)
+    p = Pool("fp8_tensor", 1, 4, [0] * 40, 30, 500, seed=1)
+    for _ in range(40):
+        if g.random() < 0.7:
+            n = int(g.integers(1, 41))
+            ids = g.permutation(40)[:n]
+            new = g.integers(0, 121, n) * (g.random(n) < 0.7)
+            e = p.resize(ids.tolist(), new.tolist())
+        else:
+            ids = g.permutation(40)[:20]
+            e = p.fork(ids[:10].tolist(), ids[10:].tolist())
+        p.check(e)
+
+
+def test_resize_refusals():
+    p = Pool("bf16", 1, 4, [10, 11, 12, 0], 4, 12, seed=2)
+    e = p.resize([0, 0, 1, 4], [0, 4, 17, 1])       # twice; too long; no such request
+    assert e == C.ERR_INDEX
+    p.check(e)
+    assert p.resize([3, 2, 0], [16, 13, 0]) == 0     # grows on what the same call frees
+    p.check()
+    e = p.resize([0, 2, 1], [16, 16, 5])             # not enough for the first: it stays, the last still shrinks
+    p.check(e)
+    # a page that no request holds, and a table entry that is no page
+    p.d_refs[int(p.table[1, 0])] = 0
+    p.refs[int(p.table[1, 0])] = 0
+    p.d_table[1, 1] = 77
+    p.table[1, 1] = 77
+    assert p.resize([1], [0]) == C.ERR_PAGE
+    p.check(C.ERR_PAGE)
+
+
+def test_resize_large_pool():
+    g = np.random.default_rng(3)
+    lens = g.integers(0, 40000, 96).tolist()
+    p = Pool("fp8_tensor", 1, 1, [0] * 96, 40000, 4096, seed=1)
+    del p
+    pages = sum(-(-n // 16) for n in lens) + 1234
+    B, stride = 96, 2500
+    perm = g.permutation(pages).astype(np.int32)
+    table, lens0 = np.full((B, stride), -1, dtype=np.int32), np.zeros(B, dtype=np.int32)
+    refs, free, count = np.zeros(pages, dtype=np.int32), perm.copy(), pages
+    d = smla.make_cache_desc(0, 1, 16, pages, B, stride)
+    dv = [_dev(x) for x in (table, lens0, refs, free, [count])]
+    err, work = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.empty(2 * B, dtype=torch.int32, device="cuda")
+    order = g.permutation(B)
+    for new in (np.array(lens)[order], np.where(g.random(B) < 0.5, 0, np.array(lens)[order] // 2), np.array(lens)[order]):
+        smla.cache_resize(d, *dv, _dev(order), _dev(new), work, err)
+        e, count = C.resize(16, table, lens0, refs, free, count, order.tolist(), new.tolist())
+        assert e == 0 and err.item() == 0 and dv[4].item() == count
+        for a, b in zip(dv, (table, lens0, refs, free)):
+            assert np.array_equal(a.cpu().numpy(), b)
+
+
+def test_streams_and_graphs():
+    # on a side stream, and captured once and replayed: the same results as the calls made in turn
+    p = Pool("fp8_ds", 2, 16, [40, 100, 0, 0], 8, 30, seed=9)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert p.fork([0, 1], [2, 3], stream=side) == 0
+    p.check()
+    ids, up, down = _dev([0, 1]), _dev([60, 100]), _dev([40, 100])
+    work = torch.empty(4, dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        smla.cache_resize(p.desc, *p.tables(), ids, up, work, p.err)
+        smla.cache_resize(p.desc, *p.tables(), ids, down, work, p.err)
+    for _ in range(3):
+        g.replay()
+        for new in ([60, 100], [40, 100]):
+            e, p.count = C.resize(p.P, p.table, p.lens, p.refs, p.free, p.count, [0, 1], new)
+            assert e == 0
+        p.check()
