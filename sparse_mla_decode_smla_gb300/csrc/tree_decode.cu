@@ -1,120 +1,1107 @@
-// Attention of drafted nodes over the paged latent cache: every node of a request attends the
-// request's context and the nodes it sees (a bit mask, or the chain j <= i).
+// Attention of drafted nodes over the paged latent cache, on the 5th-generation tensor cores:
+// every node of a request attends the request's context and the nodes it sees (a bit mask, or
+// the chain j <= i).
 //
 // out_h = sum_j e^{s_j} v_j / (sum_j e^{s_j} + e^{sink_h}), s_j = sm_scale <q_h, k_j>, v_j = k_j[0:512],
 // in one pass over the slots with a running maximum and sum.
+//
+// Work. The (node, head) rows of a request share its keys. 64 consecutive rows are a row tile, 64
+// consecutive slots a key tile; a unit is one of each. The units of the batch, in the order (request,
+// row tile, key tile), are cut into equal runs, one for each SM's CTA, from the lengths on the device: no
+// launch depends on them, SMs are equally loaded however ragged the batch, and row tiles of a request
+// run near one another, so that its keys are read from HBM once. A row tile that a run's end cuts leaves
+// its part, normalised, with its log-sum-exp, in the workspace; a second kernel joins the parts in the
+// order of the slots (equal results in every call). A CTA cuts at most two row tiles, so the workspace
+// holds two parts an SM whatever the batch.
+//
+// A unit on one SM. The fp32 output of 64 rows x 512 dims takes half of the tensor memory when the
+// halves of each row are stacked on its 128 lanes: lane l < 64 holds row l's dims [0, 256), lane 64 + l
+// its dims [256, 512). q is stacked the same way.
+//  * Scores: B stacks the 64 slots twice, their low dims over their high ones. Of the M128 N128 result,
+//    lanes l < 64, columns 0-63 are the low partial scores, lanes 64 + l, columns 64-127 the high ones;
+//    the two warps of a row exchange halves through shared memory and finish 32 slots each.
+//  * Values: A = [P; 0] against the low dims and [0; P] against the high ones, into the same columns.
+//  Half of every MMA is unused; in exchange nothing crosses between SMs and q stays in tensor memory.
+//
+// FP8 formats: rows come by bulk copies of up to 16 consecutive slots into a ring, eight warps turn them
+// into f16 key tiles (block scales applied, exact for powers of two). BF16: TMA boxes land in the key
+// tile itself, and the same warps only look after tiles with hidden or unused slots.
+//
+// What is hidden never counts: slots without a page or past the last node become zero rows with weight
+// zero, and in tiles that hold nodes a row with a non-finite latent value is zeroed and marked, so that
+// the scores of the nodes that see it become NaN and the others' sums never meet it.
+//
+// Per CTA (480 threads): warps 0-3 softmax and epilogue, 4-11 key tiles and q, 12 copies, 13 MMA issue,
+// 14 check of the block scales against the f16 window (fp8_ds). Every wait is bounded in time; one
+// that gives up sets SMLA_DEVERR_TIMEOUT.
 #include <math_constants.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tcgen05.cuh"
 #include "tree_decode.h"
 
 namespace smla {
 namespace {
 
-// One warp per (node, head). Lane l holds dims [16 l, 16 l + 16) of the latent and [2 l, 2 l + 2)
-// of the RoPE part.
-__global__ void __launch_bounds__(256) tree_simple_kernel(const TreeArgs p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (item >= int64_t(p.T) * p.H) return;
-  const int t = static_cast<int>(item / p.H), h = static_cast<int>(item % p.H);
-  int r = -1, cu0 = 0, n = 0;
-  for (int i = 0; i < p.B; ++i) {
-    const int a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1);
-    if (t >= a && t < b) { r = i; cu0 = a; n = b - a; }
+constexpr int kTrN = 64;   // slots of a key tile
+constexpr int kTrM = 64;   // rows of a row tile
+constexpr int kTrSub = 16; // slots of a raw stage
+constexpr int kTrFirstConv = 4, kTrConvWarps = 8;
+constexpr int kTrProducer = kTrFirstConv + kTrConvWarps, kTrMmaWarp = kTrProducer + 1, kTrCheckWarp = kTrMmaWarp + 1;
+constexpr int kTrThreads = 32 * (kTrCheckWarp + 1);
+constexpr int kTrBarConv = 11;  // named barrier of the key-tile warps (1-10: softmax warp pairs)
+// key tiles a CTA takes at least: shorter runs would spend more on their start and on joining
+// parts than they save
+constexpr int kTrMinUnits = 4;
+constexpr float kTrRescale = 8.f;  // the running maximum moves when it grows by more (log2 units)
+// weights are 2^(s - m + 7): at most 2^15 between moves of the maximum, within f16, and exact to
+// 2^-11 down to 2^-21 of the largest one
+constexpr float kTrShift = 7.f;
+
+constexpr int kTrPairBlk = 2 * kTrN * 128;  // 64 dims: [64 slots, low | the same slots, high]
+constexpr int kTrKLat = 4 * kTrPairBlk;
+constexpr int kTrPBlk = kTrM * kTrN * 2;
+constexpr int kTrXRow = 80;
+constexpr int kTrMeta = 8;  // key tiles between the copies' warp and the softmax at most: 5
+
+// TMEM columns
+constexpr uint32_t kTrTmO = 0, kTrTmQ = 256, kTrTmS = 384;
+
+template <int FMT>
+struct Lay {
+  static constexpr bool bf16 = FMT == SMLA_KV_BF16, tens = FMT == SMLA_KV_FP8_TENSOR;
+  static constexpr int row = bf16 ? kBf16RowBytes : tens ? kFp8TensorRowBytes : kFp8RowBytes;
+  // BF16: the 64 RoPE dims as loaded, and the same slots from dim 32 on (the high half), a buffer
+  static constexpr int rope_blk = bf16 ? 2 * kTrN * 128 : 2 * kTrN * 64;
+  static constexpr int rope_bufs = bf16 ? 2 : 1;
+  static constexpr int raw_stage = kTrSub * row;
+  static constexpr size_t K = 0;
+  static constexpr size_t rope = K + 2 * size_t(kTrKLat);
+  static constexpr size_t P = rope + size_t(rope_bufs) * rope_blk;  // [0 | P | 0]
+  static constexpr size_t qr = P + 3 * size_t(kTrPBlk);
+  static constexpr size_t raw = qr + 128 * 64;
+  static constexpr size_t xs = raw + (bf16 ? 0 : 4 * size_t(raw_stage));
+  static constexpr size_t xm = xs + 128 * size_t(kTrXRow);
+  static constexpr size_t qf = xm + 128 * 4;
+  static constexpr size_t pmax = qf + 128 * 4;
+  static constexpr size_t meta = pmax + 256 * 4;
+  static constexpr size_t bad = meta + kTrMeta * 8;
+  static constexpr size_t tmem = bad + kTrMeta * 8;
+  static constexpr size_t bars = tmem + 16;
+  static constexpr size_t bytes = bars + 32 * 8 + 1024;
+  static_assert(bytes <= 232448, "shared memory budget");
+  static_assert(rope % 1024 == 0 && P % 1024 == 0 && qr % 1024 == 0 && raw % 128 == 0 && bars % 8 == 0 && raw_stage % 16 == 0,
+                "swizzle atoms and copies");
+};
+enum {
+  R_RAW_FULL = 0,                  // [stage]; BF16: [buffer]
+  R_RAW_EMPTY = R_RAW_FULL + 4,    // [stage]
+  R_K_FULL = R_RAW_EMPTY + 4,      // [buffer]
+  R_K_FREE = R_K_FULL + 2,         // [buffer][16-slot chunk]
+  R_ROPE_FULL = R_K_FREE + 8,
+  R_S_FULL, R_S_FREE, R_P_READY, R_PV_DONE, R_Q, R_DRAIN, R_COUNT
+};
+static_assert(R_COUNT <= 32, "barriers");
+
+// ---------------------------------------------------------------- the schedule
+
+struct TreeReq {
+  int ctx, n, cu0, kt;  // context, nodes, first row of q, key tiles
+  int64_t units;        // row tiles x key tiles
+};
+
+// 1: a request with nodes, 0: without, -1: one that does not fit the description.
+__device__ __forceinline__ int tree_request(const TreeArgs& p, int r, TreeReq& q) {
+  const int a = __ldg(p.cu + r), b = __ldg(p.cu + r + 1), c = __ldg(p.ctx + r);
+  q.ctx = c;
+  q.cu0 = a;
+  q.n = 0;
+  q.kt = 0;
+  q.units = 0;
+  if (a == b) return 0;
+  const int64_t n = int64_t(b) - a;
+  if (a < 0 || n < 0 || b > p.T || c < 0 || (p.W > 0 && n > 32 * int64_t(p.W)) ||
+      c + n > (int64_t(p.stride) << p.log2_page))
+    return -1;
+  q.n = static_cast<int>(n);
+  q.kt = static_cast<int>((c + n + kTrN - 1) / kTrN);
+  q.units = (n * p.H + kTrM - 1) / kTrM * q.kt;
+  return 1;
+}
+
+struct TreeRun {  // the units [u0, u1) of one CTA
+  int64_t u0, u1, per;
+  int64_t base0, base1;  // first units of the requests of unit u0 and of unit u1 - 1
+  int r0, r1;            // those requests
+};
+
+// The run of CTA g of G, for a whole CTA of NT threads; ends with a barrier.
+template <int NT>
+__device__ void tree_schedule(const TreeArgs& p, int g, int G, TreeRun* run, int64_t* s_warp, int32_t* err) {
+  constexpr int kWarps = NT / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int each = (p.B + NT - 1) / NT;
+  const int ra = min(p.B, tid * each), rb = min(p.B, ra + each);
+  TreeReq q;
+  int64_t sum = 0;
+  for (int r = ra; r < rb; ++r) {
+    if (tree_request(p, r, q) < 0 && err) atomicOr(err, SMLA_DEVERR_INDEX);
+    sum += q.units;
   }
-  if (r < 0) return;
+  int64_t v = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    const int64_t x = s_warp[w];
+    if (w < warp) before += x;
+    total += x;
+  }
+  v += before - sum;  // units before this thread's requests
+  int64_t per = (total + G - 1) / G;
+  if (per < kTrMinUnits) per = kTrMinUnits;
+  const int64_t u0 = min(total, g * per), u1 = min(total, u0 + per);
+  if (tid == 0) {
+    run->u0 = u0;
+    run->u1 = u1;
+    run->per = per;
+    run->r0 = run->r1 = p.B;
+    run->base0 = run->base1 = total;
+  }
+  __syncthreads();
+  if (u0 < u1 && v < u1 && u0 < v + sum) {
+    for (int r = ra; r < rb; ++r) {
+      tree_request(p, r, q);
+      if (v <= u0 && u0 < v + q.units) { run->r0 = r; run->base0 = v; }
+      if (v <= u1 - 1 && u1 - 1 < v + q.units) { run->r1 = r; run->base1 = v; }
+      v += q.units;
+    }
+  }
+  __syncthreads();
+}
+
+struct TreeSeg {  // key tiles [k0, k1) of row tile m of a request
+  int r, m, k0, k1;
+  TreeReq q;
+  bool whole, first;  // all of the row tile's key tiles; the run starts here
+};
+
+// Walks a run's segments; every thread of a warp calls it together.
+struct TreeWalk {
+  int64_t u, u0, u1, base;
+  int r;
+  TreeReq q;
+  __device__ __forceinline__ TreeWalk(const TreeArgs& p, const TreeRun& run)
+      : u(run.u0), u0(run.u0), u1(run.u1), base(run.base0), r(run.r0) {
+    if (u < u1) tree_request(p, r, q);
+  }
+  __device__ __forceinline__ bool next(const TreeArgs& p, TreeSeg& s) {
+    if (u >= u1) return false;
+    if (u >= base + q.units) {  // the next request with nodes, 32 looked at together
+      base += q.units;
+      const int lane = threadIdx.x & 31;
+      for (int x = r + 1; x < p.B; x += 32) {
+        TreeReq c;
+        const bool has = x + lane < p.B && tree_request(p, x + lane, c) == 1;
+        const uint32_t b = __ballot_sync(0xffffffffu, has);
+        if (b) {
+          r = x + __ffs(b) - 1;
+          break;
+        }
+      }
+      tree_request(p, r, q);
+    }
+    const int64_t off = u - base;
+    s.r = r;
+    s.q = q;
+    s.m = static_cast<int>(off / q.kt);
+    s.k0 = static_cast<int>(off - int64_t(s.m) * q.kt);
+    s.k1 = static_cast<int>(min(int64_t(q.kt), s.k0 + (u1 - u)));
+    s.first = u == u0;
+    s.whole = s.k0 == 0 && s.k1 == q.kt;
+    u += s.k1 - s.k0;
+    return true;
+  }
+};
+
+// Part `slot` (0: of the row tile a run starts in, 1: of the one it ends in) of CTA g: 64 rows of 512
+// fp32 values, then their log-sum-exps.
+constexpr size_t kTrPart = size_t(kTrM) * (kLatent + 1) * 4;
+__device__ __forceinline__ float* tree_part(const TreeArgs& p, int64_t g, int slot) {
+  return reinterpret_cast<float*>(p.ws + 256 + size_t(2 * g + slot) * kTrPart);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Final factor of a row whose output is divided by its sum already, and its log-sum-exp, with the sink.
+__device__ __forceinline__ void apply_sink(const float* sink, int h, float& lse, float& f) {
+  if (!sink) return;
+  const float sg = __ldg(sink + h);
+  if (sg == -CUDART_INF_F) return;
+  const float both = fmaxf(lse, sg) + log1pf(expf(-fabsf(lse - sg)));
+  f *= expf(lse - both);
+  lse = both;
+}
+
+// The 64 visibility bits of key tile k for node i of a request: all context slots, and the nodes that
+// its mask row shows.
+__device__ __forceinline__ uint64_t tree_bits(const TreeArgs& p, const TreeReq& q, int i, int k) {
+  const int64_t base = int64_t(k) * kTrN - q.ctx;  // node of the tile's first slot
+  if (base + kTrN <= 0) return ~0ull;
+  if (p.W == 0) {
+    const int64_t last = i - base;  // the tile's last visible slot
+    return last >= 63 ? ~0ull : last < 0 ? 0ull : (2ull << last) - 1;
+  }
+  const uint32_t* row = p.mask + int64_t(q.cu0 + i) * p.W;
+  const int64_t from = base < 0 ? 0 : base;
+  const int w = static_cast<int>(from >> 5), sh = static_cast<int>(from & 31);
+  const uint64_t w0 = w < p.W ? __ldg(row + w) : 0u, w1 = w + 1 < p.W ? __ldg(row + w + 1) : 0u,
+                 w2 = w + 2 < p.W ? __ldg(row + w + 2) : 0u;
+  uint64_t b = (w0 | (w1 << 32)) >> sh;
+  if (sh) b |= w2 << (64 - sh);
+  if (base < 0) b = (b << -base) | ((1ull << -base) - 1);  // -base in 1..63
+  return b;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+// A pipeline wait of a whole warp: all lanes go on, or none does.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kTrThreads, 1)
+    tree_decode_kernel(const TreeArgs p, const __grid_constant__ CUtensorMap kv_map) {
+  using Y = Lay<FMT>;
+  constexpr bool BF = Y::bf16, tens = Y::tens;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TreeRun s_run;
+  __shared__ int64_t s_warp[32];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(sm);
+  auto bar = [&](int k) -> uint32_t { return sb + uint32_t(Y::bars) + 8u * k; };
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* err = reinterpret_cast<int32_t*>(p.ws);
-  const int ctx = __ldg(p.ctx + r), i = t - cu0;
-  if (cu0 < 0 || cu0 + n > p.T || ctx < 0 || (p.mask && n > 32 * p.W) ||
-      int64_t(ctx) + n > (int64_t(p.stride) << p.log2_page)) {
-    if (lane == 0) atomicOr(err, SMLA_DEVERR_INDEX);
-    return;
-  }
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + item * kDim;
-  float ql[16], qr[2], o[16];
-  for (int e = 0; e < 16; ++e) { ql[e] = __bfloat162float(q[16 * lane + e]); o[e] = 0.f; }
-  for (int e = 0; e < 2; ++e) qr[e] = __bfloat162float(q[kLatent + 2 * lane + e]);
-  float m = -CUDART_INF_F, l = 0.f;
-  for (int s = 0; s < ctx + n; ++s) {
-    if (s >= ctx) {
-      const int j = s - ctx;
-      const bool see = p.mask ? (p.mask[int64_t(t) * p.W + (j >> 5)] >> (j & 31)) & 1u : j <= i;
-      if (!see) continue;
-    }
-    const int32_t page = __ldg(p.page_table + int64_t(r) * p.stride + (s >> p.log2_page));
-    if (page < 0 || page >= p.num_pages) {
-      if (lane == 0) atomicOr(err, SMLA_DEVERR_PAGE);
-      continue;
-    }
-    const int64_t slot = (int64_t(page) << p.log2_page) + (s & ((1 << p.log2_page) - 1));
-    float k[16], kr[2];
-    if (p.kv_format == SMLA_KV_BF16) {
-      const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(p.kv + slot * kBf16RowBytes);
-      for (int e = 0; e < 16; ++e) k[e] = __bfloat162float(row[16 * lane + e]);
-      for (int e = 0; e < 2; ++e) kr[e] = __bfloat162float(row[kLatent + 2 * lane + e]);
-    } else {
-      const bool ds = p.kv_format == SMLA_KV_FP8_DS;
-      const uint8_t* row = p.kv + slot * (ds ? kFp8RowBytes : kFp8TensorRowBytes);
-      const float sc = ds ? reinterpret_cast<const float*>(row + kScaleOff)[lane >> 3] : p.kv_scale;
-      for (int e = 0; e < 16; e += 2) {
-        const uint32_t x = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(row + 16 * lane + e));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
-        k[e] = f.x * sc;
-        k[e + 1] = f.y * sc;
+  volatile uint64_t* meta = reinterpret_cast<volatile uint64_t*>(sm + Y::meta);  // slots with a row, per tile
+  uint32_t* bad = reinterpret_cast<uint32_t*>(sm + Y::bad);                     // non-finite rows, per tile
+
+  // ------------------------------------------------------------------ set-up
+  if (BF && tid == 0) prefetch_tensormap(&kv_map);
+  {
+    uint4* zp = reinterpret_cast<uint4*>(sm + Y::P);  // the zero blocks beside P stay zero
+    for (int k = tid; k < 3 * kTrPBlk / 16; k += kTrThreads) zp[k] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (tid == 0) {
+      for (int s = 0; s < 4; ++s) {
+        mbar_init(bar(R_RAW_FULL + s), 1);
+        mbar_init(bar(R_RAW_EMPTY + s), kTrConvWarps + (FMT == SMLA_KV_FP8_DS ? 1 : 0));
       }
-      if (ds) {
-        const uint32_t w = reinterpret_cast<const uint32_t*>(row + kRopeOffFp8)[lane];
-        kr[0] = bf16_lo(w);
-        kr[1] = bf16_hi(w);
+      for (int b = 0; b < 2; ++b) mbar_init(bar(R_K_FULL + b), kTrConvWarps);
+      for (int c = 0; c < 8; ++c) mbar_init(bar(R_K_FREE + c), 1);
+      mbar_init(bar(R_ROPE_FULL), kTrConvWarps);
+      mbar_init(bar(R_S_FULL), 1);
+      mbar_init(bar(R_S_FREE), 4);
+      mbar_init(bar(R_P_READY), 4);
+      mbar_init(bar(R_PV_DONE), 1);
+      mbar_init(bar(R_Q), kTrConvWarps);
+      mbar_init(bar(R_DRAIN), 1);
+      tc::fence_mbarrier_init_cluster();
+    }
+    if (warp == kTrMmaWarp) tc::alloc(sb + uint32_t(Y::tmem), 512);
+    tc::fence_before();
+    tree_schedule<kTrThreads>(p, blockIdx.x, gridDim.x, &s_run, s_warp, blockIdx.x == 0 ? err : nullptr);
+    tc::fence_after();
+  }
+  const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + Y::tmem);
+  TreeWalk walk(p, s_run);
+  TreeSeg seg;
+  bool ok = true;
+  int gi = 0;  // key tiles of this CTA so far: the barriers' phases follow it across segments
+
+  // ------------------------------------------------------------------ copies
+  if (warp == kTrProducer) {
+    auto entries = [&](const TreeSeg& s, int k, int32_t& e0, int32_t& e1) {
+      const int32_t* row = p.page_table + int64_t(s.r) * p.stride;
+      const int64_t a = int64_t(k) * kTrN + lane, end = int64_t(s.q.ctx) + s.q.n;
+      e0 = a < end ? __ldg(row + (a >> p.log2_page)) : -2;  // -2: no such slot
+      e1 = a + 32 < end ? __ldg(row + ((a + 32) >> p.log2_page)) : -2;
+    };
+    const int P = 1 << p.log2_page;
+    bool more = walk.next(p, seg);
+    int k = seg.k0;
+    int32_t e0 = -2, e1 = -2;
+    if (more) entries(seg, k, e0, e1);
+    while (more && ok) {
+      TreeSeg ns = seg;
+      int nk = k + 1;
+      bool nm = true;
+      if (nk == seg.k1) {
+        nm = walk.next(p, ns);
+        nk = ns.k0;
+      }
+      int32_t n0 = -2, n1 = -2;
+      if (nm) entries(ns, nk, n0, n1);  // a tile ahead: their latency is hidden
+      const bool ok0 = e0 >= 0 && e0 < p.num_pages, ok1 = e1 >= 0 && e1 < p.num_pages;
+      if ((!ok0 && e0 != -2) || (!ok1 && e1 != -2)) atomicOr(err, SMLA_DEVERR_PAGE);
+      const uint64_t v = uint64_t(__ballot_sync(0xffffffffu, ok0)) | uint64_t(__ballot_sync(0xffffffffu, ok1)) << 32;
+      if (lane == 0) {
+        meta[gi % kTrMeta] = v;
+        bad[2 * (gi % kTrMeta)] = bad[2 * (gi % kTrMeta) + 1] = 0;
+      }
+      if constexpr (BF) {
+        const int b = gi & 1;
+        if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * b + 3), ((gi >> 1) - 1) & 1)) { ok = false; break; }
+        const int rb = min(P, kTrN), runs = kTrN / rb;
+        // a run of slots of one page is loaded whole when its first slot counts; what lies past the
+        // last slot is cleared later
+        int nvalid = 0;
+        for (int x = 0; x < runs; ++x) nvalid += (v >> (x * rb)) & 1;
+        if (lane == 0) {
+          if (nvalid)
+            mbar_arrive_expect_tx(bar(R_RAW_FULL + b), uint32_t(nvalid) * 10u * rb * 128u);
+          else
+            mbar_arrive(bar(R_RAW_FULL + b));
+        }
+        __syncwarp();
+        const uint32_t kt = sb + uint32_t(Y::K) + uint32_t(b * kTrKLat);
+        const uint32_t rp = sb + uint32_t(Y::rope) + uint32_t(b * Y::rope_blk);
+        for (int x0 = 0; x0 < runs * 10; x0 += 32) {
+          const int x = x0 + lane, run = min(x / 10, runs - 1), bx = x - 10 * (x / 10), j = run * rb;
+          const int32_t ea = __shfl_sync(0xffffffffu, e0, j & 31), eb = __shfl_sync(0xffffffffu, e1, j & 31);
+          if (x < runs * 10 && ((v >> j) & 1)) {
+            const int64_t y = (int64_t(j < 32 ? ea : eb) << p.log2_page) + ((int64_t(k) * kTrN + j) & (P - 1));
+            const uint32_t dst = bx < 8 ? kt + (bx & 3) * kTrPairBlk + (bx >> 2) * (kTrN * 128) : rp + (bx - 8) * (kTrN * 128);
+            tma_load_2d(dst + j * 128, &kv_map, bx < 8 ? 64 * bx : kLatent + 32 * (bx - 8), static_cast<int32_t>(y),
+                        bar(R_RAW_FULL + b));
+          }
+        }
       } else {
-        const uint32_t x = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(row + kLatent + 2 * lane));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
-        kr[0] = f.x * sc;
-        kr[1] = f.y * sc;
+        const int run = min(P, kTrSub);
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          if (gi >= 1 && !warp_wait(bar(R_RAW_EMPTY + q), (gi - 1) & 1)) { ok = false; break; }
+          const uint32_t vq = uint32_t(v >> (kTrSub * q)) & 0xffffu;
+          if (lane == 0) {
+            if (vq)
+              mbar_arrive_expect_tx(bar(R_RAW_FULL + q), uint32_t(__popc(vq)) * Y::row);
+            else
+              mbar_arrive(bar(R_RAW_FULL + q));
+          }
+          __syncwarp();
+          const int j = kTrSub * q + lane;
+          const int32_t page = __shfl_sync(0xffffffffu, q < 2 ? e0 : e1, j & 31);
+          if (lane < kTrSub && (lane & (run - 1)) == 0) {
+            const int cnt = __popc((vq >> lane) & ((1u << run) - 1));  // the run's slots are its first cnt
+            if (cnt) {
+              const int64_t slot = (int64_t(page) << p.log2_page) + ((int64_t(k) * kTrN + j) & (P - 1));
+              bulk_g2s(sb + uint32_t(Y::raw) + uint32_t(q * Y::raw_stage + lane * Y::row), p.kv + slot * Y::row,
+                       uint32_t(cnt * Y::row), bar(R_RAW_FULL + q));
+            }
+          }
+        }
+        if (!ok) break;
+      }
+      seg = ns;
+      k = nk;
+      e0 = n0;
+      e1 = n1;
+      more = nm;
+      ++gi;
+    }
+    // no copy may land after the CTA has left
+    if constexpr (BF) {
+      for (int x = max(0, gi - 2); x < gi; ++x)
+        if (!mbar_wait(bar(R_RAW_FULL + (x & 1)), (x >> 1) & 1)) break;
+    } else if (gi > 0) {
+      for (int q = 0; q < 4; ++q)
+        if (!mbar_wait(bar(R_RAW_FULL + q), (gi - 1) & 1)) break;
+    }
+  }
+  // ------------------------------------------------------------------ MMA issuer
+  else if (warp == kTrMmaWarp) {
+    constexpr uint32_t kIdQK = BF ? tc::idesc_bf16_f32(128, 128, false, false) : tc::idesc_f16_f32(128, 128, false, false);
+    constexpr uint32_t kIdPV = BF ? tc::idesc_bf16_f32(128, 256, false, true) : tc::idesc_f16_f32(128, 256, false, true);
+    const uint32_t qr = sb + uint32_t(Y::qr);
+    const uint32_t d = tm + kTrTmS;
+    int nseg = 0;
+    while (ok && walk.next(p, seg)) {
+      const int nt = seg.k1 - seg.k0;
+      if (lane == 0) {
+        auto qk_ready = [&](int g) {
+          return mbar_test_wait(bar(R_K_FULL + (g & 1)), (g >> 1) & 1) && (g > gi || mbar_test_wait(bar(R_Q), nseg & 1)) &&
+                 (g == 0 || mbar_test_wait(bar(R_S_FREE), (g - 1) & 1)) && (BF || mbar_test_wait(bar(R_ROPE_FULL), g & 1));
+        };
+        auto qk = [&](int g) {
+          tc::fence_after();
+          const uint32_t kt = sb + uint32_t(Y::K) + uint32_t((g & 1) * kTrKLat);
+          const uint32_t rope = sb + uint32_t(Y::rope) + uint32_t(BF ? (g & 1) * Y::rope_blk : 0);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            tc::mma_ts(d, tm + kTrTmQ + 8 * j, tc::sdesc_sw128(kt + (j >> 2) * kTrPairBlk + (j & 3) * 32, 16, 1024), kIdQK, j > 0);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            tc::mma_ss(d, tc::sdesc_sw64(qr + 32 * j, 16, 512),
+                       BF ? tc::sdesc_sw128(rope + 32 * j, 16, 1024) : tc::sdesc_sw64(rope + 32 * j, 16, 512), kIdQK, 1);
+          tc::commit(bar(R_S_FULL));
+        };
+        auto pv = [&](int g) {
+          tc::fence_after();
+          const uint32_t kt = sb + uint32_t(Y::K) + uint32_t((g & 1) * kTrKLat);
+          const uint32_t pa = sb + uint32_t(Y::P) + uint32_t(kTrPBlk);
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            tc::mma_ss(tm + kTrTmO, tc::sdesc_sw128(pa + 32 * s, 16, 1024), tc::sdesc_sw128(kt + 2048 * s, kTrPairBlk, 1024), kIdPV,
+                       g > gi || s > 0);
+            tc::mma_ss(tm + kTrTmO, tc::sdesc_sw128(pa - kTrPBlk + 32 * s, 16, 1024),
+                       tc::sdesc_sw128(kt + kTrN * 128 + 2048 * s, kTrPairBlk, 1024), kIdPV, 1);
+            tc::commit(bar(R_K_FREE + 4 * (g & 1) + s));
+          }
+          tc::commit(bar(R_PV_DONE));
+        };
+        int nqk = 0, npv = 0;
+        uint64_t t0 = globaltimer_ns();
+        for (uint32_t it = 0; npv < nt; ++it) {
+          if (npv < nqk && mbar_test_wait(bar(R_P_READY), (gi + npv) & 1)) {
+            pv(gi + npv++);
+          } else if (nqk < nt && nqk <= npv + 1 && qk_ready(gi + nqk)) {
+            qk(gi + nqk++);
+          } else {
+            if ((it & 255u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
+              ok = false;
+              break;
+            }
+            continue;
+          }
+          t0 = globaltimer_ns();
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      gi += nt;
+      ++nseg;
+    }
+    if (lane == 0 && nseg > 0) {  // every MMA has completed before the tensor memory is released
+      tc::commit(bar(R_DRAIN));
+      if (!mbar_wait(bar(R_DRAIN), 0)) ok = false;
+    }
+    __syncwarp();
+  }
+  // ------------------------------------------------------------------ f16 window check
+  else if (warp == kTrCheckWarp) {
+    if constexpr (FMT == SMLA_KV_FP8_DS) {
+      // lane l looks at row l % 16 of each raw stage, scales 2h and 2h + 1 (h = l / 16): the largest, the
+      // smallest power of two and the smallest other one over all rows, compared with the window at
+      // the end
+      const int r = lane & 15, hh = lane >> 4;
+      uint32_t smax = 0, smin_p2 = ~0u, smin_other = ~0u;
+      while (ok && walk.next(p, seg)) {
+        for (int k = seg.k0; k < seg.k1 && ok; ++k, ++gi) {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            if (!warp_wait(bar(R_RAW_FULL + q), gi & 1)) { ok = false; break; }
+            if ((meta[gi % kTrMeta] >> (kTrSub * q + r)) & 1) {
+              const uint2 sc2 = lds64(sb + uint32_t(Y::raw) + uint32_t(q * Y::raw_stage + r * Y::row) + kScaleOff + 8 * hh);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t a = (e ? sc2.y : sc2.x) & 0x7fffffffu;
+                const bool p2 = (a & 0x7fffffu) == 0;
+                smax = max(smax, a);
+                smin_p2 = min(smin_p2, (p2 && a != 0) ? a : ~0u);
+                smin_other = min(smin_other, p2 ? ~0u : a);
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(R_RAW_EMPTY + q));
+          }
+        }
+      }
+      const bool out_of_window = smax > 0x43000000u || smin_p2 < 0x38000000u || smin_other < 0x38800000u;
+      if (__any_sync(0xffffffffu, out_of_window) && lane == 0) atomicOr(err, SMLA_DEVERR_RANGE);
+    }
+  }
+  // ------------------------------------------------------------------ key tiles and q
+  else if (warp >= kTrFirstConv) {
+    const int dtid = tid - 32 * kTrFirstConv, dw = dtid >> 5;
+    const int quarter = warp & 3, part = dw >> 2, half = quarter >> 1;
+    const int hl = 32 * (quarter & 1) + lane, row = 32 * quarter + lane;
+    const uint32_t lrow = tm + (uint32_t(32 * quarter) << 16);
+    while (ok && walk.next(p, seg)) {
+      // q of this row tile, once the softmax has taken the last scores of the previous one (and with them
+      // its factors of q): dims [256 half + 128 part, + 128) of
+      // a row by this thread, and its 32 RoPE dims by part 1. FP8 formats: f16, scaled by a power of two
+      // that brings the row's largest value into [1, 2); the factor goes back into the scores.
+      // PV two tiles back comes first: a barrier's parity tells its last phase from the one before only
+      if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * (gi & 1) + 3), ((gi >> 1) - 1) & 1)) { ok = false; break; }
+      if (gi > 0 && !warp_wait(bar(R_S_FREE), (gi - 1) & 1)) { ok = false; break; }
+      {
+        tc::fence_after();
+        const int64_t R = int64_t(seg.m) * kTrM + hl;
+        const bool have = R < int64_t(seg.q.n) * p.H;
+        const uint16_t* qrow = static_cast<const uint16_t*>(p.q) + (int64_t(seg.q.cu0) * p.H + (have ? R : 0)) * kDim;
+        const uint4* lat = reinterpret_cast<const uint4*>(qrow + 256 * half + 128 * part);
+        const uint4* rop = reinterpret_cast<const uint4*>(qrow + kLatent + 32 * half);
+        float qdown = 1.f;
+        if constexpr (!BF) {
+          uint32_t m4[4] = {0, 0, 0, 0};
+          if (have) {
+#pragma unroll 8
+            for (int c = 0; c < 16; ++c) {
+              const uint4 v = __ldg(lat + c);
+              m4[0] = bf16x2_max(m4[0], v.x & 0x7fff7fffu);
+              m4[1] = bf16x2_max(m4[1], v.y & 0x7fff7fffu);
+              m4[2] = bf16x2_max(m4[2], v.z & 0x7fff7fffu);
+              m4[3] = bf16x2_max(m4[3], v.w & 0x7fff7fffu);
+            }
+            if (part == 1) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint4 v = __ldg(rop + c);
+                m4[0] = bf16x2_max(m4[0], v.x & 0x7fff7fffu);
+                m4[1] = bf16x2_max(m4[1], v.y & 0x7fff7fffu);
+                m4[2] = bf16x2_max(m4[2], v.z & 0x7fff7fffu);
+                m4[3] = bf16x2_max(m4[3], v.w & 0x7fff7fffu);
+              }
+            }
+          }
+          const uint32_t mx = bf16x2_hmax_bits(bf16x2_max(bf16x2_max(m4[0], m4[1]), bf16x2_max(m4[2], m4[3])));
+          const uint32_t pm = sb + uint32_t(Y::pmax);
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(pm + uint32_t(128 * part + row) * 4), "r"(mx) : "memory");
+          named_bar(kTrBarConv, 32 * kTrConvWarps);
+          const int qe = pow2_exponent_of_bf16(max(lds_u32(pm + uint32_t(row) * 4), lds_u32(pm + uint32_t(128 + row) * 4)));
+          qdown = exp2_int(-qe);
+          if (part == 0)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + uint32_t(Y::qf) + uint32_t(row) * 4), "f"(exp2_int(qe)) : "memory");
+        }
+        auto cvt = [&](uint32_t w) -> uint32_t { return BF ? w : pack_f16x2(bf16_lo(w) * qdown, bf16_hi(w) * qdown); };
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t wv[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 v = have ? __ldg(lat + 4 * ch + k) : make_uint4(0, 0, 0, 0);
+            wv[4 * k] = cvt(v.x); wv[4 * k + 1] = cvt(v.y);
+            wv[4 * k + 2] = cvt(v.z); wv[4 * k + 3] = cvt(v.w);
+          }
+          tc::st16(lrow + kTrTmQ + 64 * part + 16 * ch, wv);
+        }
+        tc::wait_st();
+        if (part == 1) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 v = have ? __ldg(rop + c) : make_uint4(0, 0, 0, 0);
+            const uint32_t dst = sb + uint32_t(Y::qr) + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(cvt(v.x)), "r"(cvt(v.y)), "r"(cvt(v.z)),
+                         "r"(cvt(v.w)) : "memory");
+          }
+          fence_proxy_async_smem();
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(R_Q));
+      }
+      for (int k = seg.k0; k < seg.k1 && ok; ++k, ++gi) {
+        const int b = gi & 1;
+        const uint32_t kt = sb + uint32_t(Y::K) + uint32_t(b * kTrKLat);
+        const bool nodes = int64_t(k + 1) * kTrN > seg.q.ctx;  // the tile holds drafted nodes
+        uint32_t* badw = bad + 2 * (gi % kTrMeta);
+        if constexpr (BF) {
+          if (!warp_wait(bar(R_RAW_FULL + b), (gi >> 1) & 1)) { ok = false; break; }
+          const uint64_t v = meta[gi % kTrMeta];
+          if (v != ~0ull || nodes) {
+            const int sl = dtid & 63, grp = dtid >> 6;  // a slot's pieces [16 grp, 16 grp + 16) of 64
+            const bool has = (v >> sl) & 1;
+            bool odd = false;
+            for (int pc = 16 * grp; pc < 16 * grp + 16; ++pc) {
+              const int bx = pc >> 3;
+              const uint32_t at = kt + (bx & 3) * kTrPairBlk + (bx >> 2) * (kTrN * 128) + sl * 128 + (((pc & 7) ^ (sl & 7)) << 4);
+              bool clear = !has;
+              if (has && nodes) {
+                const uint4 x = lds128(at);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  clear |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+                odd |= clear;
+              }
+              if (clear) asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+            }
+            if (!has) {
+              const uint32_t rp = sb + uint32_t(Y::rope) + uint32_t(b * Y::rope_blk) + (grp >> 1) * (kTrN * 128) + sl * 128;
+              for (int c = 4 * (grp & 1); c < 4 * (grp & 1) + 4; ++c)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(rp + (c << 4)), "r"(0) : "memory");
+            }
+            if (odd) atomicOr(badw + (sl >> 5), 1u << (sl & 31));
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(R_K_FULL + b));
+        } else {
+          // Jobs are placed so that every access phase of a warp (8 lanes of 16 bytes) meets distinct
+          // banks. fp8_ds rows (656 bytes): 8 consecutive slots, one 16-byte piece. Per-tensor rows (576):
+          // two slots, four pieces. Either way the f16 stores, two 16-byte pieces, spread over the
+          // 128-byte swizzle.
+          int lslot, lch, rslot, rc;
+          if constexpr (tens) {
+            lslot = 2 * (lane >> 3) + ((lane >> 2) & 1);
+            lch = 4 * dw + (lane & 3);
+            rslot = 2 * ((dtid >> 4) & 7) + ((dtid >> 2) & 1);
+            rc = (dtid & 3) + 4 * ((dtid >> 3) & 1);
+          } else {
+            lslot = lane & 15;
+            lch = 4 * dw + 2 * (lane >> 4);
+            rslot = dtid & 15;
+            rc = (dtid >> 4) & 7;
+          }
+          const int rq0 = 2 * (dtid >> 7);
+          uint4 rv0 = make_uint4(0, 0, 0, 0), rv1 = rv0;
+#pragma unroll 1
+          for (int q = 0; q < 4 && ok; ++q) {
+            if (!warp_wait(bar(R_RAW_FULL + q), gi & 1)) { ok = false; break; }
+            const uint32_t vq = uint32_t(meta[gi % kTrMeta] >> (kTrSub * q));
+            const uint32_t raw = sb + uint32_t(Y::raw) + uint32_t(q * Y::raw_stage);
+            uint32_t o[2][8];
+            const float sc = tens ? 1.f : lds_f32(raw + lslot * Y::row + kScaleOff + 4 * (lch >> 3));
+            const __half2 s2 = __float2half2_rn(sc);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int slot = tens ? lslot + 8 * j : lslot, ch = tens ? lch : lch + j;
+              const uint4 v = lds128(raw + slot * Y::row + 16 * ch);
+              const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+              const bool has = (vq >> slot) & 1;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t lo, hi;
+                e4m3x4_to_f16x4(wv[e], lo, hi);  // exact
+                if constexpr (!tens) {  // code * scale in f16
+                  __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&lo), s2);
+                  __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&hi), s2);
+                  lo = *reinterpret_cast<uint32_t*>(&x);
+                  hi = *reinterpret_cast<uint32_t*>(&y);
+                }
+                o[j][2 * e] = has ? lo : 0u;
+                o[j][2 * e + 1] = has ? hi : 0u;
+              }
+              if (nodes) {
+                bool odd = false;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  odd |= (o[j][e] & 0x7c00u) == 0x7c00u || (o[j][e] & 0x7c000000u) == 0x7c000000u;
+                if (odd) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) o[j][e] = 0u;
+                  const int sl = kTrSub * q + slot;
+                  atomicOr(badw + (sl >> 5), 1u << (sl & 31));
+                }
+              }
+            }
+            if ((q & ~1) == rq0) {  // this thread's RoPE piece of the stage, kept in registers
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if ((vq >> rslot) & 1) {
+                if constexpr (tens) {
+                  const uint2 cw = lds64(raw + rslot * Y::row + kLatent + 8 * rc);
+                  e4m3x4_to_f16x4(cw.x, v.x, v.y);
+                  e4m3x4_to_f16x4(cw.y, v.z, v.w);
+                } else {
+                  const uint4 x = lds128(raw + rslot * Y::row + kRopeOffFp8 + 16 * rc);
+                  v = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
+                }
+              }
+              if (q & 1)
+                rv1 = v;
+              else
+                rv0 = v;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(R_RAW_EMPTY + q));
+            // rows [16q, 16q + 16) of the buffer are free once that chunk of PV, two tiles ago, is done
+            if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * b + q), ((gi >> 1) - 1) & 1)) { ok = false; break; }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int slot = tens ? lslot + 8 * j : lslot, ch = tens ? lch : lch + j;
+              const int rr = kTrN * (ch >> 4) + kTrSub * q + slot;
+              const uint32_t at = kt + ((ch >> 2) & 3) * kTrPairBlk + rr * 128;
+              const int c0 = 2 * (ch & 3);
+              const uint32_t sw = rr & 7;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((c0 ^ sw) << 4)), "r"(o[j][0]), "r"(o[j][1]),
+                           "r"(o[j][2]), "r"(o[j][3]) : "memory");
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((c0 + 1) ^ sw) << 4)), "r"(o[j][4]),
+                           "r"(o[j][5]), "r"(o[j][6]), "r"(o[j][7]) : "memory");
+            }
+          }
+          if (!ok) break;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(R_K_FULL + b));
+          // the one RoPE block is free once QK of the previous tile has completed
+          if (gi >= 1 && !warp_wait(bar(R_S_FULL), (gi - 1) & 1)) { ok = false; break; }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int rr = kTrN * (rc >> 2) + kTrSub * (rq0 + j) + rslot, c = rc & 3;
+            const uint32_t dst = sb + uint32_t(Y::rope) + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4);
+            const uint4 v = j ? rv1 : rv0;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(R_ROPE_FULL));
+        }
       }
     }
-    float d = qr[0] * kr[0] + qr[1] * kr[1];
-    for (int e = 0; e < 16; ++e) d = fmaf(ql[e], k[e], d);
-    for (int x = 16; x; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-    const float sc2 = d * p.c2;
-    if (sc2 > m) {
-      const float a = exp2f(m - sc2);
-      l *= a;
-      for (int e = 0; e < 16; ++e) o[e] *= a;
-      m = sc2;
-    }
-    const float w = exp2f(sc2 - (m == -CUDART_INF_F ? 0.f : m));
-    l += w;
-    for (int e = 0; e < 16; ++e) o[e] = fmaf(w, k[e], o[e]);
+    if (dtid == 0) pdl_trigger();  // the joining kernel may start launching
   }
-  float lse = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
-  float f = l == 0.f ? 0.f : 1.f / l;
-  if (p.sink) {
-    const float sg = __ldg(p.sink + h);
-    if (sg != -CUDART_INF_F) {
-      const float both = fmaxf(lse, sg) + log1pf(expf(-fabsf(lse - sg)));
-      f *= expf(lse - both);
-      lse = both;
+  // ------------------------------------------------------------------ softmax + epilogue
+  else {
+    const int half = warp >> 1, pr = warp & 1;
+    const int hl = 32 * pr + lane;
+    const uint32_t lrow = tm + (uint32_t(32 * warp) << 16);
+    const uint32_t xmine = sb + uint32_t(Y::xs) + uint32_t(32 * warp + lane) * kTrXRow;
+    const uint32_t xpart = sb + uint32_t(Y::xs) + uint32_t(32 * (warp ^ 2) + lane) * kTrXRow;
+    const uint32_t mmine = sb + uint32_t(Y::xm) + uint32_t(32 * warp + lane) * 4;
+    const uint32_t mpart = sb + uint32_t(Y::xm) + uint32_t(32 * (warp ^ 2) + lane) * 4;
+    const int bar_x = 1 + pr;                      // both warps of the pair have written
+    const int bar_mine = 3 + 2 * pr + half;        // the partner has read my row
+    const int bar_part = 3 + 2 * pr + (half ^ 1);  // I have read the partner's row
+    const int bar_max = 7 + pr;                    // both maxima are written
+    const int bar_x2 = 9 + pr;                     // both second halves are written
+    const float c2 = tens ? p.c2 * p.kv_scale : p.c2;
+    int nseg = 0;
+    while (ok && walk.next(p, seg)) {
+      const int64_t R = int64_t(seg.m) * kTrM + hl;
+      const bool real = R < int64_t(seg.q.n) * p.H;
+      const int node = real ? static_cast<int>(R / p.H) : 0;
+      const int h = real ? static_cast<int>(R - int64_t(node) * p.H) : 0;
+      const int nt = seg.k1 - seg.k0;
+      bool good = warp_wait(bar(R_Q), nseg & 1);
+      float c2m = c2, c2p = c2;
+      if constexpr (!BF) {
+        c2m *= lds_f32(sb + uint32_t(Y::qf) + uint32_t(32 * warp + lane) * 4);
+        c2p *= lds_f32(sb + uint32_t(Y::qf) + uint32_t(32 * (warp ^ 2) + lane) * 4);
+      }
+      float m = -CUDART_INF_F, l = 0.f;
+      auto correct_o = [&](float a) {  // warp-wide: the whole warp calls it when any lane needs it
+#pragma unroll 1
+        for (int k = 0; k < 16; ++k) {
+          uint32_t v[16];
+          tc::ld16(lrow + kTrTmO + 16 * k, v);
+          tc::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
+          tc::st16(lrow + kTrTmO + 16 * k, v);
+        }
+        tc::wait_st();
+      };
+      for (int i = 0; i < nt; ++i, ++gi) {
+        float v[64];
+        const bool got = good && warp_wait(bar(R_S_FULL), gi & 1);
+        if (got) {
+          tc::fence_after();
+          uint32_t w0[32], w1[32];
+          tc::ld32(lrow + kTrTmS + 64 * half, w0);
+          tc::ld32(lrow + kTrTmS + 64 * half + 32, w1);
+          tc::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            v[e] = __uint_as_float(w0[e]);
+            v[32 + e] = __uint_as_float(w1[e]);
+          }
+          tc::fence_before();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) v[e] = 0.f;
+        }
+        __syncwarp();
+        if (lane == 0 && got) mbar_arrive(bar(R_S_FREE));
+        // the low warp finishes slots 0-31 and sends its partials of slots 32-63, the high warp the other
+        // way round
+        float own[32], send[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          own[e] = half ? v[32 + e] : v[e];
+          send[e] = half ? v[e] : v[32 + e];
+        }
+        if (gi > 0) named_bar(bar_mine, 64);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(xmine + 16 * k), "r"(__float_as_uint(send[4 * k])),
+                       "r"(__float_as_uint(send[4 * k + 1])), "r"(__float_as_uint(send[4 * k + 2])),
+                       "r"(__float_as_uint(send[4 * k + 3])) : "memory");
+        if (!named_bar_and(bar_x, 64, got)) {
+          ok = false;
+          break;
+        }
+        float x[32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 xv = lds128(xpart + 16 * k);
+          x[4 * k] = __uint_as_float(xv.x); x[4 * k + 1] = __uint_as_float(xv.y);
+          x[4 * k + 2] = __uint_as_float(xv.z); x[4 * k + 3] = __uint_as_float(xv.w);
+        }
+        named_bar_arrive(bar_part, 64);
+        named_bar(bar_mine, 64);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(xmine + 16 * k), "r"(__float_as_uint(send[16 + 4 * k])),
+                       "r"(__float_as_uint(send[16 + 4 * k + 1])), "r"(__float_as_uint(send[16 + 4 * k + 2])),
+                       "r"(__float_as_uint(send[16 + 4 * k + 3])) : "memory");
+        named_bar(bar_x2, 64);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 xv = lds128(xpart + 16 * k);
+          x[16 + 4 * k] = __uint_as_float(xv.x); x[16 + 4 * k + 1] = __uint_as_float(xv.y);
+          x[16 + 4 * k + 2] = __uint_as_float(xv.z); x[16 + 4 * k + 3] = __uint_as_float(xv.w);
+        }
+        uint64_t vis = meta[gi % kTrMeta];
+        uint32_t oddm = 0;
+        if (int64_t(seg.k0 + i + 1) * kTrN > seg.q.ctx) {  // a tile with nodes
+          vis &= tree_bits(p, seg.q, node, seg.k0 + i);
+          oddm = reinterpret_cast<volatile uint32_t*>(bad)[2 * (gi % kTrMeta) + half];
+        }
+        const uint32_t msk = real ? uint32_t(vis >> (32 * half)) : 0u;
+        oddm &= msk;
+        float s[32];
+        float mx = -CUDART_INF_F;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float sv = ((msk >> j) & 1u) ? fmaf(own[j], c2m, x[j] * c2p) : -CUDART_INF_F;
+          s[j] = sv;
+          mx = fmaxf(mx, sv);
+        }
+        if (oddm) {  // a visible row with a non-finite value: NaN
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if ((oddm >> j) & 1u) s[j] = CUDART_NAN_F;
+        }
+        named_bar_arrive(bar_part, 64);
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(mmine), "f"(mx) : "memory");
+        named_bar(bar_max, 64);
+        mx = fmaxf(mx, lds_f32(mpart));
+        float a = 1.f;
+        const float mn = fmaxf(m, mx);
+        if (m == -CUDART_INF_F ? mn != -CUDART_INF_F : mn > m + kTrRescale) {
+          a = exp2_fast(m - mn);  // 0 when m was -inf
+          m = mn;
+        }
+        const float base = m == -CUDART_INF_F ? 0.f : m - kTrShift;
+        float sum = 0.f;
+        uint32_t pw2[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float p0 = exp2_fast(s[2 * j] - base), p1 = exp2_fast(s[2 * j + 1] - base);
+          sum += p0 + p1;
+          pw2[j] = BF ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+        }
+        l = l * a + sum;
+        // the P block and O are free once PV of the previous tile is complete
+        if (i >= 1 && !warp_wait(bar(R_PV_DONE), (gi - 1) & 1)) good = false;
+        tc::fence_after();
+        if (good && i > 0 && __any_sync(0xffffffffu, a != 1.f)) correct_o(a);
+        if (good) {
+          const uint32_t prow = sb + uint32_t(Y::P) + uint32_t(kTrPBlk) + uint32_t(hl) * 128;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int c = 4 * half + k;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(prow + ((c ^ (hl & 7)) << 4)), "r"(pw2[4 * k]),
+                         "r"(pw2[4 * k + 1]), "r"(pw2[4 * k + 2]), "r"(pw2[4 * k + 3]) : "memory");
+          }
+          fence_proxy_async_smem();
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0 && good) mbar_arrive(bar(R_P_READY));
+      }
+      if (!ok) break;
+      // ---- epilogue: both row halves' sums, then O lane -> output or part
+      named_bar(bar_mine, 64);  // the partner has read my last row
+      bool fin = good && warp_wait(bar(R_PV_DONE), (gi - 1) & 1);
+      tc::fence_after();
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(xmine), "f"(l) : "memory");
+      if (!named_bar_and(bar_x, 64, fin)) {
+        ok = false;
+        break;
+      }
+      l += lds_f32(xpart);
+      named_bar_arrive(bar_part, 64);
+      float lse = l == 0.f ? -CUDART_INF_F : (m - kTrShift + log2f(l)) * kLn2;
+      float f = l == 0.f ? 0.f : (tens ? p.kv_scale : 1.f) / l;
+      const int64_t orow = (int64_t(seg.q.cu0) + node) * p.H + h;
+      float* part = nullptr;
+      if (seg.whole) {
+        apply_sink(p.sink, h, lse, f);
+        if (p.lse && real && half == 0) p.lse[orow] = lse;
+      } else {
+        part = tree_part(p, blockIdx.x, seg.first ? 0 : 1);
+        if (half == 0) part[kTrM * kLatent + hl] = lse;
+      }
+#pragma unroll 1
+      for (int k4 = 0; k4 < 4; ++k4) {
+        uint32_t v4[4][16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tc::ld16(lrow + kTrTmO + 64 * k4 + 16 * j, v4[j]);
+        tc::wait_ld();
+        if (!real) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t* vv = v4[j];
+          const int col = 256 * half + 64 * k4 + 16 * j;
+          if (seg.whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * kLatent + col);
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = pack_bf16x2(__uint_as_float(vv[2 * e]) * f, __uint_as_float(vv[2 * e + 1]) * f);
+            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          } else {
+            float4* dst = reinterpret_cast<float4*>(part + hl * kLatent + col);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_float4(__uint_as_float(vv[4 * e]) * f, __uint_as_float(vv[4 * e + 1]) * f,
+                                   __uint_as_float(vv[4 * e + 2]) * f, __uint_as_float(vv[4 * e + 3]) * f);
+          }
+        }
+      }
+      tc::fence_before();  // the next row tile's PV comes after this one's loads
+      ++nseg;
+    }
+    if (ok && nseg > 0) named_bar(bar_mine, 64);  // the last arrival at the pair's barriers
+  }
+
+  // ------------------------------------------------------------------ teardown
+  if (!ok && lane == 0) atomicOr(err, SMLA_DEVERR_TIMEOUT);
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kTrMmaWarp) {
+    tc::fence_after();
+    tc::dealloc(tm, 512);
+  }
+}
+
+// ---------------------------------------------------------------- joining the parts
+
+constexpr int kTrJoinThreads = 256;
+
+// CTA g joins its share of the rows of the (at most two) row tiles that its run cuts: of a tile that k
+// runs share, the j-th joins rows [64 j / k, 64 (j + 1) / k). Four warps a row, one for each 128 dims:
+// out = sum_i w_i o_i / sum_i w_i with w_i = e^(lse_i - max), in the order of the slots.
+__global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeArgs p) {
+  __shared__ TreeRun s_run;
+  __shared__ int64_t s_warp[32];
+  tree_schedule<kTrJoinThreads>(p, blockIdx.x, gridDim.x, &s_run, s_warp, nullptr);
+  pdl_wait();
+  const TreeRun run = s_run;
+  if (run.u0 >= run.u1) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = 128 * (warp & 3) + 4 * lane;
+  for (int side = 0; side < 2; ++side) {
+    const int r = side ? run.r1 : run.r0;
+    const int64_t base = side ? run.base1 : run.base0, u = side ? run.u1 - 1 : run.u0;
+    TreeReq q;
+    tree_request(p, r, q);
+    const int64_t m = (u - base) / q.kt, ub = base + m * q.kt;
+    if (side && ub <= run.u0) return;  // the same row tile
+    const int64_t g0 = ub / run.per, g1 = (ub + q.kt - 1) / run.per;
+    if (g0 == g1) continue;
+    const int k = static_cast<int>(g1 - g0 + 1), j = static_cast<int>(blockIdx.x - g0);
+    const int first_slot = ub % run.per != 0 ? 1 : 0;
+    const int hi = kTrM * (j + 1) / k;
+    for (int row = kTrM * j / k + (warp >> 2); row < hi; row += 2) {
+      const int64_t R = m * kTrM + row;
+      if (R >= int64_t(q.n) * p.H) continue;
+      float M = -CUDART_INF_F;
+      for (int i = lane; i < k; i += 32) M = fmaxf(M, tree_part(p, g0 + i, i ? 0 : first_slot)[kTrM * kLatent + row]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float ref = M == -CUDART_INF_F ? 0.f : M;
+      float W = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int i = 0; i < k; ++i) {
+        const float* part = tree_part(p, g0 + i, i ? 0 : first_slot);
+        const float w = expf(part[kTrM * kLatent + row] - ref);
+        const float4 o = *reinterpret_cast<const float4*>(part + row * kLatent + col);
+        W += w;
+        acc.x = fmaf(w, o.x, acc.x);
+        acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z);
+        acc.w = fmaf(w, o.w, acc.w);
+      }
+      float lse = W == 0.f ? -CUDART_INF_F : ref + logf(W);
+      float f = W == 0.f ? 0.f : 1.f / W;
+      apply_sink(p.sink, static_cast<int>(R % p.H), lse, f);
+      const int64_t orow = int64_t(q.cu0) * p.H + R;
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * kLatent + col) =
+          make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+      if (p.lse && (warp & 3) == 0 && lane == 0) p.lse[orow] = lse;
     }
   }
-  if (p.lse && lane == 0) p.lse[item] = lse;
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + item * kLatent + 16 * lane);
-  uint32_t w[8];
-  for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e] * f, o[2 * e + 1] * f);
-  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// The cache as [slots, 576] bf16 with boxes of one page's slots (at most 64) x 64 dims.
+cudaError_t tree_bf16_map(const TreeArgs& a, CUtensorMap* out) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if (tensor_map_encoder(&encode) != cudaSuccess) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {cuuint64_t(kDim), cuuint64_t(a.num_pages << a.log2_page)};
+  const cuuint64_t strides[1] = {cuuint64_t(kBf16RowBytes)};
+  const cuuint32_t rows = a.log2_page >= 6 ? 64u : 1u << a.log2_page;
+  const cuuint32_t box[2] = {64, rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(a.kv), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const TreeArgs& a, int sms, const CUtensorMap& map, cudaStream_t s) {
+  // devices (below 64) whose kernel attribute is set; concurrent first calls set it twice
+  static std::atomic<uint64_t> configured{0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t(1) << dev) : 0;
+  if (!(configured.load(std::memory_order_acquire) & bit) || !bit) {
+    cudaError_t e = cudaFuncSetAttribute(tree_decode_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Lay<FMT>::bytes));
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_release);
+  }
+  tree_decode_kernel<FMT><<<sms, kTrThreads, Lay<FMT>::bytes, s>>>(a, map);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(sms));
+  cfg.blockDim = dim3(kTrJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel, a);
 }
 
 }  // namespace
 
-size_t tree_workspace_bytes(int) { return 256; }
+size_t tree_workspace_bytes(int num_sms) { return 256 + size_t(2) * num_sms * kTrPart; }
 
-cudaError_t launch_tree_decode(const TreeArgs& a, int, cudaStream_t s) {
-  const int64_t blocks = (int64_t(a.T) * a.H + 7) / 8;
-  tree_simple_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_tree_decode(const TreeArgs& a, int num_sms, cudaStream_t s) {
+  alignas(64) CUtensorMap map = {};
+  if (a.kv_format == SMLA_KV_BF16) {
+    const cudaError_t e = tree_bf16_map(a, &map);
+    if (e != cudaSuccess) return e;
+    return launch_fmt<SMLA_KV_BF16>(a, num_sms, map, s);
+  }
+  if (a.kv_format == SMLA_KV_FP8_TENSOR) return launch_fmt<SMLA_KV_FP8_TENSOR>(a, num_sms, map, s);
+  return launch_fmt<SMLA_KV_FP8_DS>(a, num_sms, map, s);
 }
 
 }  // namespace smla
