@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     if (tid == 0) {
       for (int s = 0; s < 4; ++s) {
         mbar_init(bar(R_RAW_FULL + s), 1);
-        mbar_init(bar(R_RAW_EMPTY + s), kTrConvWarps + (FMT == SMLA_KV_FP8_DS ? 1 : 0));
+        mbar_init(bar(R_RAW_EMPTY + s), 2 + (FMT == SMLA_KV_FP8_DS ? 1 : 0));
       }
       for (int b = 0; b < 2; ++b) mbar_init(bar(R_K_FULL + b), kTrConvWarps);
       for (int c = 0; c < 8; ++c) mbar_init(bar(R_K_FREE + c), 1);
@@ -648,99 +648,81 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(R_K_FULL + b));
         } else {
+          // A stage of 16 slots belongs to two warps, one for each half of the 512 dims: a tile's four
+          // stages are worked on at once, and a thread's loads are all in flight together. The stage
+          // goes back to the copies as soon as they are in registers.
           // Jobs are placed so that every access phase of a warp (8 lanes of 16 bytes) meets distinct
           // banks. fp8_ds rows (656 bytes): 8 consecutive slots, one 16-byte piece. Per-tensor rows (576):
           // two slots, four pieces. Either way the f16 stores, two 16-byte pieces, spread over the
           // 128-byte swizzle.
-          int lslot, lch, rslot, rc;
+          const int q = dw & 3, hw = dw >> 2;
+          auto slot_of = [&](int j) { return tens ? 2 * (lane >> 3) + ((lane >> 2) & 1) + 8 * (j & 1) : lane & 15; };
+          auto piece_of = [&](int j) { return 16 * hw + (tens ? 4 * (j >> 1) + (lane & 3) : 2 * j + (lane >> 4)); };
+          auto rslot_of = [&](int j) { return tens ? 8 * hw + 4 * j + (lane >> 3) : lane & 15; };
+          auto rpiece_of = [&](int j) { return tens ? lane & 7 : 4 * hw + 2 * j + (lane >> 4); };
+          if (!warp_wait(bar(R_RAW_FULL + q), gi & 1)) { ok = false; break; }
+          const uint32_t vq = uint32_t(meta[gi % kTrMeta] >> (kTrSub * q)) & 0xffffu;
+          const uint32_t raw = sb + uint32_t(Y::raw) + uint32_t(q * Y::raw_stage);
+          uint4 v[8], rv[2];
+          float2 sc = make_float2(1.f, 1.f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = lds128(raw + slot_of(j) * Y::row + 16 * piece_of(j));
           if constexpr (tens) {
-            lslot = 2 * (lane >> 3) + ((lane >> 2) & 1);
-            lch = 4 * dw + (lane & 3);
-            rslot = 2 * ((dtid >> 4) & 7) + ((dtid >> 2) & 1);
-            rc = (dtid & 3) + 4 * ((dtid >> 3) & 1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint2 cw = lds64(raw + rslot_of(j) * Y::row + kLatent + 8 * rpiece_of(j));
+              rv[j] = make_uint4(cw.x, cw.y, 0, 0);
+            }
           } else {
-            lslot = lane & 15;
-            lch = 4 * dw + 2 * (lane >> 4);
-            rslot = dtid & 15;
-            rc = (dtid >> 4) & 7;
+            const uint2 s2 = lds64(raw + (lane & 15) * Y::row + kScaleOff + 8 * hw);
+            sc = make_float2(__uint_as_float(s2.x), __uint_as_float(s2.y));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) rv[j] = lds128(raw + rslot_of(j) * Y::row + kRopeOffFp8 + 16 * rpiece_of(j));
           }
-          const int rq0 = 2 * (dtid >> 7);
-          uint4 rv0 = make_uint4(0, 0, 0, 0), rv1 = rv0;
-#pragma unroll 1
-          for (int q = 0; q < 4 && ok; ++q) {
-            if (!warp_wait(bar(R_RAW_FULL + q), gi & 1)) { ok = false; break; }
-            const uint32_t vq = uint32_t(meta[gi % kTrMeta] >> (kTrSub * q));
-            const uint32_t raw = sb + uint32_t(Y::raw) + uint32_t(q * Y::raw_stage);
-            uint32_t o[2][8];
-            const float sc = tens ? 1.f : lds_f32(raw + lslot * Y::row + kScaleOff + 4 * (lch >> 3));
-            const __half2 s2 = __float2half2_rn(sc);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(R_RAW_EMPTY + q));
+          // rows [16q, 16q + 16) of the buffer are free once that chunk of PV, two tiles ago, is done
+          if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * b + q), ((gi >> 1) - 1) & 1)) { ok = false; break; }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int slot = tens ? lslot + 8 * j : lslot, ch = tens ? lch : lch + j;
-              const uint4 v = lds128(raw + slot * Y::row + 16 * ch);
-              const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
-              const bool has = (vq >> slot) & 1;
+          for (int j = 0; j < 8; ++j) {
+            const int slot = slot_of(j), ch = piece_of(j);
+            const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            const __half2 s2 = __float2half2_rn(j < 4 ? sc.x : sc.y);
+            uint32_t o[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t lo, hi;
-                e4m3x4_to_f16x4(wv[e], lo, hi);  // exact
-                if constexpr (!tens) {  // code * scale in f16
-                  __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&lo), s2);
-                  __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&hi), s2);
-                  lo = *reinterpret_cast<uint32_t*>(&x);
-                  hi = *reinterpret_cast<uint32_t*>(&y);
-                }
-                o[j][2 * e] = has ? lo : 0u;
-                o[j][2 * e + 1] = has ? hi : 0u;
-              }
-              if (nodes) {
-                bool odd = false;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  odd |= (o[j][e] & 0x7c00u) == 0x7c00u || (o[j][e] & 0x7c000000u) == 0x7c000000u;
-                if (odd) {
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) o[j][e] = 0u;
-                  const int sl = kTrSub * q + slot;
-                  atomicOr(badw + (sl >> 5), 1u << (sl & 31));
-                }
+            for (int e = 0; e < 4; ++e) {
+              e4m3x4_to_f16x4(wv[e], o[2 * e], o[2 * e + 1]);  // exact
+              if constexpr (!tens) {  // code * scale in f16
+                __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&o[2 * e]), s2);
+                __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&o[2 * e + 1]), s2);
+                o[2 * e] = *reinterpret_cast<uint32_t*>(&x);
+                o[2 * e + 1] = *reinterpret_cast<uint32_t*>(&y);
               }
             }
-            if ((q & ~1) == rq0) {  // this thread's RoPE piece of the stage, kept in registers
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if ((vq >> rslot) & 1) {
-                if constexpr (tens) {
-                  const uint2 cw = lds64(raw + rslot * Y::row + kLatent + 8 * rc);
-                  e4m3x4_to_f16x4(cw.x, v.x, v.y);
-                  e4m3x4_to_f16x4(cw.y, v.z, v.w);
-                } else {
-                  const uint4 x = lds128(raw + rslot * Y::row + kRopeOffFp8 + 16 * rc);
-                  v = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
-                }
-              }
-              if (q & 1)
-                rv1 = v;
-              else
-                rv0 = v;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(R_RAW_EMPTY + q));
-            // rows [16q, 16q + 16) of the buffer are free once that chunk of PV, two tiles ago, is done
-            if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * b + q), ((gi >> 1) - 1) & 1)) { ok = false; break; }
+            if (vq != 0xffffu && !((vq >> slot) & 1)) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int slot = tens ? lslot + 8 * j : lslot, ch = tens ? lch : lch + j;
-              const int rr = kTrN * (ch >> 4) + kTrSub * q + slot;
-              const uint32_t at = kt + ((ch >> 2) & 3) * kTrPairBlk + rr * 128;
-              const int c0 = 2 * (ch & 3);
-              const uint32_t sw = rr & 7;
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((c0 ^ sw) << 4)), "r"(o[j][0]), "r"(o[j][1]),
-                           "r"(o[j][2]), "r"(o[j][3]) : "memory");
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((c0 + 1) ^ sw) << 4)), "r"(o[j][4]),
-                           "r"(o[j][5]), "r"(o[j][6]), "r"(o[j][7]) : "memory");
+              for (int e = 0; e < 8; ++e) o[e] = 0u;
             }
+            if (nodes) {
+              bool odd = false;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) odd |= (o[e] & 0x7c00u) == 0x7c00u || (o[e] & 0x7c000000u) == 0x7c000000u;
+              if (odd) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = 0u;
+                const int sl = kTrSub * q + slot;
+                atomicOr(badw + (sl >> 5), 1u << (sl & 31));
+              }
+            }
+            const int rr = kTrN * hw + kTrSub * q + slot;
+            const uint32_t at = kt + ((ch >> 2) & 3) * kTrPairBlk + rr * 128;
+            const int c0 = 2 * (ch & 3);
+            const uint32_t sw = rr & 7;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((c0 ^ sw) << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                         "r"(o[3]) : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((c0 + 1) ^ sw) << 4)), "r"(o[4]), "r"(o[5]),
+                         "r"(o[6]), "r"(o[7]) : "memory");
           }
-          if (!ok) break;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(R_K_FULL + b));
@@ -748,10 +730,18 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           if (gi >= 1 && !warp_wait(bar(R_S_FULL), (gi - 1) & 1)) { ok = false; break; }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int rr = kTrN * (rc >> 2) + kTrSub * (rq0 + j) + rslot, c = rc & 3;
+            const int rslot = rslot_of(j), rc = rpiece_of(j);
+            const int rr = kTrN * (rc >> 2) + kTrSub * q + rslot, c = rc & 3;
             const uint32_t dst = sb + uint32_t(Y::rope) + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4);
-            const uint4 v = j ? rv1 : rv0;
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+            uint4 x;
+            if constexpr (tens) {
+              e4m3x4_to_f16x4(rv[j].x, x.x, x.y);
+              e4m3x4_to_f16x4(rv[j].y, x.z, x.w);
+            } else {
+              x = make_uint4(bf16x2_to_f16x2(rv[j].x), bf16x2_to_f16x2(rv[j].y), bf16x2_to_f16x2(rv[j].z), bf16x2_to_f16x2(rv[j].w));
+            }
+            if (!((vq >> rslot) & 1)) x = make_uint4(0, 0, 0, 0);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -871,13 +861,16 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const uint32_t msk = real ? uint32_t(vis >> (32 * half)) : 0u;
         oddm &= msk;
         float s[32];
-        float mx = -CUDART_INF_F;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float sv = ((msk >> j) & 1u) ? fmaf(own[j], c2m, x[j] * c2p) : -CUDART_INF_F;
-          s[j] = sv;
-          mx = fmaxf(mx, sv);
+        for (int j = 0; j < 32; ++j) s[j] = fmaf(own[j], c2m, x[j] * c2p);
+        if (!__all_sync(0xffffffffu, msk == ~0u)) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[j] = ((msk >> j) & 1u) ? s[j] : -CUDART_INF_F;
         }
+        float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int j = 4; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], s[j]);
+        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         if (oddm) {  // a visible row with a non-finite value: NaN
 #pragma unroll
           for (int j = 0; j < 32; ++j)
@@ -894,15 +887,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           m = mn;
         }
         const float base = m == -CUDART_INF_F ? 0.f : m - kTrShift;
-        float sum = 0.f;
+        float sum4[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t pw2[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const float p0 = exp2_fast(s[2 * j] - base), p1 = exp2_fast(s[2 * j + 1] - base);
-          sum += p0 + p1;
+          sum4[j & 3] += p0 + p1;
           pw2[j] = BF ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
         }
-        l = l * a + sum;
+        l = l * a + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
         // the P block and O are free once PV of the previous tile is complete
         if (i >= 1 && !warp_wait(bar(R_PV_DONE), (gi - 1) & 1)) good = false;
         tc::fence_after();
