@@ -19,7 +19,7 @@
 // its dims [256, 512). q is stacked the same way.
 //  * Scores: B stacks the 64 slots twice, their low dims over their high ones. Of the M128 N128 result,
 //    lanes l < 64, columns 0-63 are the low partial scores, lanes 64 + l, columns 64-127 the high ones;
-//    the two warps of a row exchange halves through shared memory and finish 32 slots each.
+//    the four threads of a row exchange halves through shared memory and finish 16 slots each.
 //  * Values: A = [P; 0] against the low dims and [0; P] against the high ones, into the same columns.
 //  Half of every MMA is unused; in exchange nothing crosses between SMs and q stays in tensor memory.
 //
@@ -31,8 +31,8 @@
 // zero, and in tiles that hold nodes a row with a non-finite latent value is zeroed and marked, so that
 // the scores of the nodes that see it become NaN and the others' sums never meet it.
 //
-// Per CTA (480 threads): warps 0-3 softmax and epilogue, 4-11 key tiles and q, 12 copies, 13 MMA issue,
-// 14 check of the block scales against the f16 window (fp8_ds). Every wait is bounded in time; one
+// Per CTA (608 threads): warps 0-7 softmax and epilogue, 8-15 key tiles and q, 16 copies, 17 MMA issue,
+// 18 check of the block scales against the f16 window (fp8_ds). Every wait is bounded in time; one
 // that gives up sets SMLA_DEVERR_TIMEOUT.
 #include <math_constants.h>
 
@@ -49,10 +49,9 @@ namespace {
 constexpr int kTrN = 64;   // slots of a key tile
 constexpr int kTrM = 64;   // rows of a row tile
 constexpr int kTrSub = 16; // slots of a raw stage
-constexpr int kTrFirstConv = 4, kTrConvWarps = 8;
+constexpr int kTrSoftWarps = 8, kTrFirstConv = kTrSoftWarps, kTrConvWarps = 8;
 constexpr int kTrProducer = kTrFirstConv + kTrConvWarps, kTrMmaWarp = kTrProducer + 1, kTrCheckWarp = kTrMmaWarp + 1;
 constexpr int kTrThreads = 32 * (kTrCheckWarp + 1);
-constexpr int kTrBarConv = 11;  // named barrier of the key-tile warps (1-10: softmax warp pairs)
 // key tiles a CTA takes at least: shorter runs would spend more on their start and on joining
 // parts than they save
 constexpr int kTrMinUnits = 4;
@@ -64,11 +63,16 @@ constexpr float kTrShift = 7.f;
 constexpr int kTrPairBlk = 2 * kTrN * 128;  // 64 dims: [64 slots, low | the same slots, high]
 constexpr int kTrKLat = 4 * kTrPairBlk;
 constexpr int kTrPBlk = kTrM * kTrN * 2;
-constexpr int kTrXRow = 80;
 constexpr int kTrMeta = 8;  // key tiles between the copies' warp and the softmax at most: 5
 
 // TMEM columns
 constexpr uint32_t kTrTmO = 0, kTrTmQ = 256, kTrTmS = 384;
+
+struct TreeRun {  // the units [u0, u1) of one CTA
+  int64_t u0, u1, per;
+  int64_t base0, base1;  // first units of the requests of unit u0 and of unit u1 - 1
+  int r0, r1;            // those requests
+};
 
 template <int FMT>
 struct Lay {
@@ -84,14 +88,14 @@ struct Lay {
   static constexpr size_t qr = P + 3 * size_t(kTrPBlk);
   static constexpr size_t raw = qr + 128 * 64;
   static constexpr size_t xs = raw + (bf16 ? 0 : 4 * size_t(raw_stage));
-  static constexpr size_t xm = xs + 128 * size_t(kTrXRow);
-  static constexpr size_t qf = xm + 128 * 4;
-  static constexpr size_t pmax = qf + 128 * 4;
-  static constexpr size_t meta = pmax + 256 * 4;
+  static constexpr size_t xm = xs + 256 * 64;   // xs: 16 partial scores a softmax thread
+  static constexpr size_t qf = xm + 256 * 4;    // xm: a maximum a softmax thread
+  static constexpr size_t meta = qf + 128 * 4;
   static constexpr size_t bad = meta + kTrMeta * 8;
-  static constexpr size_t tmem = bad + kTrMeta * 8;
+  static constexpr size_t run = bad + kTrMeta * 8;
+  static constexpr size_t tmem = run + sizeof(TreeRun);
   static constexpr size_t bars = tmem + 16;
-  static constexpr size_t bytes = bars + 32 * 8 + 1024;
+  static constexpr size_t bytes = bars + 32 * 8;
   static_assert(bytes <= 232448, "shared memory budget");
   static_assert(rope % 1024 == 0 && P % 1024 == 0 && qr % 1024 == 0 && raw % 128 == 0 && bars % 8 == 0 && raw_stage % 16 == 0,
                 "swizzle atoms and copies");
@@ -131,12 +135,6 @@ __device__ __forceinline__ int tree_request(const TreeArgs& p, int r, TreeReq& q
   q.units = (n * p.H + kTrM - 1) / kTrM * q.kt;
   return 1;
 }
-
-struct TreeRun {  // the units [u0, u1) of one CTA
-  int64_t u0, u1, per;
-  int64_t base0, base1;  // first units of the requests of unit u0 and of unit u1 - 1
-  int r0, r1;            // those requests
-};
 
 // The run of CTA g of G, for a whole CTA of NT threads; ends with a barrier.
 template <int NT>
@@ -287,10 +285,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     tree_decode_kernel(const TreeArgs p, const __grid_constant__ CUtensorMap kv_map) {
   using Y = Lay<FMT>;
   constexpr bool BF = Y::bf16, tens = Y::tens;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ TreeRun s_run;
-  __shared__ int64_t s_warp[32];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];  // all of it: the swizzle atoms need its start
   const uint32_t sb = smem_u32(sm);
   auto bar = [&](int k) -> uint32_t { return sb + uint32_t(Y::bars) + 8u * k; };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -313,8 +308,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       for (int c = 0; c < 8; ++c) mbar_init(bar(R_K_FREE + c), 1);
       mbar_init(bar(R_ROPE_FULL), kTrConvWarps);
       mbar_init(bar(R_S_FULL), 1);
-      mbar_init(bar(R_S_FREE), 4);
-      mbar_init(bar(R_P_READY), 4);
+      mbar_init(bar(R_S_FREE), kTrSoftWarps);
+      mbar_init(bar(R_P_READY), kTrSoftWarps);
       mbar_init(bar(R_PV_DONE), 1);
       mbar_init(bar(R_Q), kTrConvWarps);
       mbar_init(bar(R_DRAIN), 1);
@@ -322,11 +317,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     }
     if (warp == kTrMmaWarp) tc::alloc(sb + uint32_t(Y::tmem), 512);
     tc::fence_before();
-    tree_schedule<kTrThreads>(p, blockIdx.x, gridDim.x, &s_run, s_warp, blockIdx.x == 0 ? err : nullptr);
+    tree_schedule<kTrThreads>(p, blockIdx.x, gridDim.x, reinterpret_cast<TreeRun*>(sm + Y::run),
+                              reinterpret_cast<int64_t*>(sm + Y::xs), blockIdx.x == 0 ? err : nullptr);
     tc::fence_after();
   }
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + Y::tmem);
-  TreeWalk walk(p, s_run);
+  TreeWalk walk(p, *reinterpret_cast<const TreeRun*>(sm + Y::run));
   TreeSeg seg;
   bool ok = true;
   int gi = 0;  // key tiles of this CTA so far: the barriers' phases follow it across segments
@@ -554,32 +550,21 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const uint4* rop = reinterpret_cast<const uint4*>(qrow + kLatent + 32 * half);
         float qdown = 1.f;
         if constexpr (!BF) {
+          // both warps of a row look at all of its dims: no exchange
           uint32_t m4[4] = {0, 0, 0, 0};
+          auto look = [&](const uint4 v) {
+            m4[0] = bf16x2_max(m4[0], v.x & 0x7fff7fffu);
+            m4[1] = bf16x2_max(m4[1], v.y & 0x7fff7fffu);
+            m4[2] = bf16x2_max(m4[2], v.z & 0x7fff7fffu);
+            m4[3] = bf16x2_max(m4[3], v.w & 0x7fff7fffu);
+          };
           if (have) {
 #pragma unroll 8
-            for (int c = 0; c < 16; ++c) {
-              const uint4 v = __ldg(lat + c);
-              m4[0] = bf16x2_max(m4[0], v.x & 0x7fff7fffu);
-              m4[1] = bf16x2_max(m4[1], v.y & 0x7fff7fffu);
-              m4[2] = bf16x2_max(m4[2], v.z & 0x7fff7fffu);
-              m4[3] = bf16x2_max(m4[3], v.w & 0x7fff7fffu);
-            }
-            if (part == 1) {
+            for (int c = 0; c < 32; ++c) look(__ldg(lat - 16 * part + c));
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint4 v = __ldg(rop + c);
-                m4[0] = bf16x2_max(m4[0], v.x & 0x7fff7fffu);
-                m4[1] = bf16x2_max(m4[1], v.y & 0x7fff7fffu);
-                m4[2] = bf16x2_max(m4[2], v.z & 0x7fff7fffu);
-                m4[3] = bf16x2_max(m4[3], v.w & 0x7fff7fffu);
-              }
-            }
+            for (int c = 0; c < 4; ++c) look(__ldg(rop + c));
           }
-          const uint32_t mx = bf16x2_hmax_bits(bf16x2_max(bf16x2_max(m4[0], m4[1]), bf16x2_max(m4[2], m4[3])));
-          const uint32_t pm = sb + uint32_t(Y::pmax);
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(pm + uint32_t(128 * part + row) * 4), "r"(mx) : "memory");
-          named_bar(kTrBarConv, 32 * kTrConvWarps);
-          const int qe = pow2_exponent_of_bf16(max(lds_u32(pm + uint32_t(row) * 4), lds_u32(pm + uint32_t(128 + row) * 4)));
+          const int qe = pow2_exponent_of_bf16(bf16x2_hmax_bits(bf16x2_max(bf16x2_max(m4[0], m4[1]), bf16x2_max(m4[2], m4[3]))));
           qdown = exp2_int(-qe);
           if (part == 0)
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + uint32_t(Y::qf) + uint32_t(row) * 4), "f"(exp2_int(qe)) : "memory");
@@ -753,18 +738,21 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   }
   // ------------------------------------------------------------------ softmax + epilogue
   else {
-    const int half = warp >> 1, pr = warp & 1;
+    // Four threads hold a row: half (low or high partial scores) and sub (16 of 32 slots). Thread (half,
+    // sub) finishes slots 32 half + 16 sub .. + 15: it takes the other half's partials of them from thread
+    // (1 - half, sub) and gives it its own of that thread's slots. The four warps of a row group meet at
+    // two named barriers a tile: partials written, maxima written.
+    const int quarter = warp & 3, sub = warp >> 2, half = quarter >> 1, pr = quarter & 1;
     const int hl = 32 * pr + lane;
-    const uint32_t lrow = tm + (uint32_t(32 * warp) << 16);
-    const uint32_t xmine = sb + uint32_t(Y::xs) + uint32_t(32 * warp + lane) * kTrXRow;
-    const uint32_t xpart = sb + uint32_t(Y::xs) + uint32_t(32 * (warp ^ 2) + lane) * kTrXRow;
-    const uint32_t mmine = sb + uint32_t(Y::xm) + uint32_t(32 * warp + lane) * 4;
-    const uint32_t mpart = sb + uint32_t(Y::xm) + uint32_t(32 * (warp ^ 2) + lane) * 4;
-    const int bar_x = 1 + pr;                      // both warps of the pair have written
-    const int bar_mine = 3 + 2 * pr + half;        // the partner has read my row
-    const int bar_part = 3 + 2 * pr + (half ^ 1);  // I have read the partner's row
-    const int bar_max = 7 + pr;                    // both maxima are written
-    const int bar_x2 = 9 + pr;                     // both second halves are written
+    const uint32_t lrow = tm + (uint32_t(32 * quarter) << 16);
+    // 16 partials of (quarter, sub, lane): 16-byte piece k at k ^ ((lane >> 1) & 3), no bank conflicts
+    const uint32_t xmine = sb + uint32_t(Y::xs) + uint32_t(32 * warp + lane) * 64;
+    const uint32_t xpart = sb + uint32_t(Y::xs) + uint32_t(32 * (warp ^ 2) + lane) * 64;
+    const uint32_t xsw = uint32_t((lane >> 1) & 3);
+    // maxima of a row: [(half, sub)][row]
+    const uint32_t mrow = sb + uint32_t(Y::xm) + uint32_t(hl) * 4;
+    const uint32_t mmine = mrow + uint32_t(2 * half + sub) * 256;
+    const int bar_x = 1 + pr, bar_m = 3 + pr;
     const float c2 = tens ? p.c2 * p.kv_scale : p.c2;
     int nseg = 0;
     while (ok && walk.next(p, seg)) {
@@ -776,126 +764,98 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       bool good = warp_wait(bar(R_Q), nseg & 1);
       float c2m = c2, c2p = c2;
       if constexpr (!BF) {
-        c2m *= lds_f32(sb + uint32_t(Y::qf) + uint32_t(32 * warp + lane) * 4);
-        c2p *= lds_f32(sb + uint32_t(Y::qf) + uint32_t(32 * (warp ^ 2) + lane) * 4);
+        c2m *= lds_f32(sb + uint32_t(Y::qf) + uint32_t(32 * quarter + lane) * 4);
+        c2p *= lds_f32(sb + uint32_t(Y::qf) + uint32_t(32 * (quarter ^ 2) + lane) * 4);
       }
       float m = -CUDART_INF_F, l = 0.f;
       auto correct_o = [&](float a) {  // warp-wide: the whole warp calls it when any lane needs it
 #pragma unroll 1
-        for (int k = 0; k < 16; ++k) {
-          uint32_t v[16];
-          tc::ld16(lrow + kTrTmO + 16 * k, v);
+        for (int k = 8 * sub; k < 8 * sub + 8; k += 2) {
+          uint32_t v0[16], v1[16];
+          tc::ld16(lrow + kTrTmO + 16 * k, v0);
+          tc::ld16(lrow + kTrTmO + 16 * k + 16, v1);
           tc::wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
-          tc::st16(lrow + kTrTmO + 16 * k, v);
+          for (int e = 0; e < 16; ++e) {
+            v0[e] = __float_as_uint(__uint_as_float(v0[e]) * a);
+            v1[e] = __float_as_uint(__uint_as_float(v1[e]) * a);
+          }
+          tc::st16(lrow + kTrTmO + 16 * k, v0);
+          tc::st16(lrow + kTrTmO + 16 * k + 16, v1);
         }
         tc::wait_st();
       };
       for (int i = 0; i < nt; ++i, ++gi) {
-        float v[64];
+        uint32_t own[16], send[16];
         const bool got = good && warp_wait(bar(R_S_FULL), gi & 1);
         if (got) {
           tc::fence_after();
-          uint32_t w0[32], w1[32];
-          tc::ld32(lrow + kTrTmS + 64 * half, w0);
-          tc::ld32(lrow + kTrTmS + 64 * half + 32, w1);
+          tc::ld16(lrow + kTrTmS + 64 * half + 32 * (half ^ 1) + 16 * sub, send);
+          tc::ld16(lrow + kTrTmS + 64 * half + 32 * half + 16 * sub, own);
           tc::wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            v[e] = __uint_as_float(w0[e]);
-            v[32 + e] = __uint_as_float(w1[e]);
-          }
           tc::fence_before();
         } else {
 #pragma unroll
-          for (int e = 0; e < 64; ++e) v[e] = 0.f;
+          for (int e = 0; e < 16; ++e) own[e] = send[e] = 0u;
         }
         __syncwarp();
         if (lane == 0 && got) mbar_arrive(bar(R_S_FREE));
-        // the low warp finishes slots 0-31 and sends its partials of slots 32-63, the high warp the other
-        // way round
-        float own[32], send[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          own[e] = half ? v[32 + e] : v[e];
-          send[e] = half ? v[e] : v[32 + e];
-        }
-        if (gi > 0) named_bar(bar_mine, 64);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(xmine + 16 * k), "r"(__float_as_uint(send[4 * k])),
-                       "r"(__float_as_uint(send[4 * k + 1])), "r"(__float_as_uint(send[4 * k + 2])),
-                       "r"(__float_as_uint(send[4 * k + 3])) : "memory");
-        if (!named_bar_and(bar_x, 64, got)) {
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(xmine + ((k ^ xsw) << 4)), "r"(send[4 * k]),
+                       "r"(send[4 * k + 1]), "r"(send[4 * k + 2]), "r"(send[4 * k + 3]) : "memory");
+        if (!named_bar_and(bar_x, 128, got)) {
           ok = false;
           break;
         }
-        float x[32];
+        float s[16];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint4 xv = lds128(xpart + 16 * k);
-          x[4 * k] = __uint_as_float(xv.x); x[4 * k + 1] = __uint_as_float(xv.y);
-          x[4 * k + 2] = __uint_as_float(xv.z); x[4 * k + 3] = __uint_as_float(xv.w);
-        }
-        named_bar_arrive(bar_part, 64);
-        named_bar(bar_mine, 64);
+          const uint4 xv = lds128(xpart + ((k ^ xsw) << 4));
+          const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(xmine + 16 * k), "r"(__float_as_uint(send[16 + 4 * k])),
-                       "r"(__float_as_uint(send[16 + 4 * k + 1])), "r"(__float_as_uint(send[16 + 4 * k + 2])),
-                       "r"(__float_as_uint(send[16 + 4 * k + 3])) : "memory");
-        named_bar(bar_x2, 64);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 xv = lds128(xpart + 16 * k);
-          x[16 + 4 * k] = __uint_as_float(xv.x); x[16 + 4 * k + 1] = __uint_as_float(xv.y);
-          x[16 + 4 * k + 2] = __uint_as_float(xv.z); x[16 + 4 * k + 3] = __uint_as_float(xv.w);
+          for (int e = 0; e < 4; ++e)
+            s[4 * k + e] = fmaf(__uint_as_float(own[4 * k + e]), c2m, __uint_as_float(xw[e]) * c2p);
         }
         uint64_t vis = meta[gi % kTrMeta];
         uint32_t oddm = 0;
         if (int64_t(seg.k0 + i + 1) * kTrN > seg.q.ctx) {  // a tile with nodes
           vis &= tree_bits(p, seg.q, node, seg.k0 + i);
-          oddm = reinterpret_cast<volatile uint32_t*>(bad)[2 * (gi % kTrMeta) + half];
+          oddm = reinterpret_cast<volatile uint32_t*>(bad)[2 * (gi % kTrMeta) + half] >> (16 * sub);
         }
-        const uint32_t msk = real ? uint32_t(vis >> (32 * half)) : 0u;
-        oddm &= msk;
-        float s[32];
+        const uint32_t msk = real ? uint32_t(vis >> (32 * half + 16 * sub)) & 0xffffu : 0u;
+        if (!__all_sync(0xffffffffu, msk == 0xffffu)) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s[j] = fmaf(own[j], c2m, x[j] * c2p);
-        if (!__all_sync(0xffffffffu, msk == ~0u)) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) s[j] = ((msk >> j) & 1u) ? s[j] : -CUDART_INF_F;
+          for (int j = 0; j < 16; ++j) s[j] = ((msk >> j) & 1u) ? s[j] : -CUDART_INF_F;
         }
         float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int j = 4; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], s[j]);
-        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        for (int j = 4; j < 16; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], s[j]);
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(mmine), "f"(mx) : "memory");
+        oddm &= msk;
         if (oddm) {  // a visible row with a non-finite value: NaN
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
+          for (int j = 0; j < 16; ++j)
             if ((oddm >> j) & 1u) s[j] = CUDART_NAN_F;
         }
-        named_bar_arrive(bar_part, 64);
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(mmine), "f"(mx) : "memory");
-        named_bar(bar_max, 64);
-        mx = fmaxf(mx, lds_f32(mpart));
+        named_bar(bar_m, 128);
+        const float mn = fmaxf(fmaxf(fmaxf(lds_f32(mrow), lds_f32(mrow + 256)), fmaxf(lds_f32(mrow + 512), lds_f32(mrow + 768))), m);
         float a = 1.f;
-        const float mn = fmaxf(m, mx);
         if (m == -CUDART_INF_F ? mn != -CUDART_INF_F : mn > m + kTrRescale) {
           a = exp2_fast(m - mn);  // 0 when m was -inf
           m = mn;
         }
         const float base = m == -CUDART_INF_F ? 0.f : m - kTrShift;
-        float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pw2[16];
+        float sum2[2] = {0.f, 0.f};
+        uint32_t pw2[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < 8; ++j) {
           const float p0 = exp2_fast(s[2 * j] - base), p1 = exp2_fast(s[2 * j + 1] - base);
-          sum4[j & 3] += p0 + p1;
+          sum2[j & 1] += p0 + p1;
           pw2[j] = BF ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
         }
-        l = l * a + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
+        l = l * a + (sum2[0] + sum2[1]);
         // the P block and O are free once PV of the previous tile is complete
         if (i >= 1 && !warp_wait(bar(R_PV_DONE), (gi - 1) & 1)) good = false;
         tc::fence_after();
@@ -903,8 +863,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         if (good) {
           const uint32_t prow = sb + uint32_t(Y::P) + uint32_t(kTrPBlk) + uint32_t(hl) * 128;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int c = 4 * half + k;
+          for (int k = 0; k < 2; ++k) {
+            const int c = 4 * half + 2 * sub + k;
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(prow + ((c ^ (hl & 7)) << 4)), "r"(pw2[4 * k]),
                          "r"(pw2[4 * k + 1]), "r"(pw2[4 * k + 2]), "r"(pw2[4 * k + 3]) : "memory");
           }
@@ -915,30 +875,31 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         if (lane == 0 && good) mbar_arrive(bar(R_P_READY));
       }
       if (!ok) break;
-      // ---- epilogue: both row halves' sums, then O lane -> output or part
-      named_bar(bar_mine, 64);  // the partner has read my last row
-      bool fin = good && warp_wait(bar(R_PV_DONE), (gi - 1) & 1);
+      // ---- epilogue: the four threads' sums of a row, then O lane -> output or part
+      const bool fin = good && warp_wait(bar(R_PV_DONE), (gi - 1) & 1);
       tc::fence_after();
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(xmine), "f"(l) : "memory");
-      if (!named_bar_and(bar_x, 64, fin)) {
+      // (the partials of the last tile have been read: every thread has passed its second barrier)
+      const uint32_t lsum = sb + uint32_t(Y::xs) + uint32_t(hl) * 4;
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(lsum + uint32_t(2 * half + sub) * 256), "f"(l) : "memory");
+      if (!named_bar_and(bar_x, 128, fin)) {
         ok = false;
         break;
       }
-      l += lds_f32(xpart);
-      named_bar_arrive(bar_part, 64);
+      l = (lds_f32(lsum) + lds_f32(lsum + 256)) + (lds_f32(lsum + 512) + lds_f32(lsum + 768));
+      named_bar(bar_m, 128);
       float lse = l == 0.f ? -CUDART_INF_F : (m - kTrShift + log2f(l)) * kLn2;
       float f = l == 0.f ? 0.f : (tens ? p.kv_scale : 1.f) / l;
       const int64_t orow = (int64_t(seg.q.cu0) + node) * p.H + h;
       float* part = nullptr;
       if (seg.whole) {
         apply_sink(p.sink, h, lse, f);
-        if (p.lse && real && half == 0) p.lse[orow] = lse;
+        if (p.lse && real && half == 0 && sub == 0) p.lse[orow] = lse;
       } else {
         part = tree_part(p, blockIdx.x, seg.first ? 0 : 1);
-        if (half == 0) part[kTrM * kLatent + hl] = lse;
+        if (half == 0 && sub == 0) part[kTrM * kLatent + hl] = lse;
       }
 #pragma unroll 1
-      for (int k4 = 0; k4 < 4; ++k4) {
+      for (int k4 = 2 * sub; k4 < 2 * sub + 2; ++k4) {
         uint32_t v4[4][16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) tc::ld16(lrow + kTrTmO + 64 * k4 + 16 * j, v4[j]);
@@ -967,7 +928,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       tc::fence_before();  // the next row tile's PV comes after this one's loads
       ++nseg;
     }
-    if (ok && nseg > 0) named_bar(bar_mine, 64);  // the last arrival at the pair's barriers
   }
 
   // ------------------------------------------------------------------ teardown
