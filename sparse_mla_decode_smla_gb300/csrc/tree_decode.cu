@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       if (lane == 0) {
         auto qk_ready = [&](int g) {
           return mbar_test_wait(bar(R_K_FULL + (g & 1)), (g >> 1) & 1) && (g > gi || mbar_test_wait(bar(R_Q), nseg & 1)) &&
-                 (g == 0 || mbar_test_wait(bar(R_S_FREE), (g - 1) & 1)) && (BF || mbar_test_wait(bar(R_ROPE_FULL), g & 1));
+                 (g == 0 || mbar_test_wait(bar(R_S_FREE), (g - 1) & 1));
         };
         auto qk = [&](int g) {
           tc::fence_after();
@@ -447,6 +447,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             tc::mma_ts(d, tm + kTrTmQ + 8 * j, tc::sdesc_sw128(kt + (j >> 2) * kTrPairBlk + (j & 3) * 32, 16, 1024), kIdQK, j > 0);
+          // the one RoPE block is rewritten once the previous tile's scores are complete: that hides behind
+          // the 16 MMAs above
+          if (!BF && !mbar_wait(bar(R_ROPE_FULL), g & 1)) ok = false;
+          tc::fence_after();
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             tc::mma_ss(d, tc::sdesc_sw64(qr + 32 * j, 16, 512),
@@ -469,7 +473,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         };
         int nqk = 0, npv = 0;
         uint64_t t0 = globaltimer_ns();
-        for (uint32_t it = 0; npv < nt; ++it) {
+        for (uint32_t it = 0; npv < nt && ok; ++it) {
           if (npv < nqk && mbar_test_wait(bar(R_P_READY), (gi + npv) & 1)) {
             pv(gi + npv++);
           } else if (nqk < nt && nqk <= npv + 1 && qk_ready(gi + nqk)) {
