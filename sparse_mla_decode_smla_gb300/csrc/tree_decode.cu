@@ -52,6 +52,7 @@ constexpr int kTrSub = 16; // slots of a raw stage
 constexpr int kTrSoftWarps = 8, kTrFirstConv = kTrSoftWarps, kTrConvWarps = 8;
 constexpr int kTrProducer = kTrFirstConv + kTrConvWarps, kTrMmaWarp = kTrProducer + 1, kTrCheckWarp = kTrMmaWarp + 1;
 constexpr int kTrThreads = 32 * (kTrCheckWarp + 1);
+constexpr int kTrBarConv = 11;  // named barrier of the key-tile warps (1-4: softmax row groups)
 // key tiles a CTA takes at least: shorter runs would spend more on their start and on joining
 // parts than they save
 constexpr int kTrMinUnits = 4;
@@ -186,6 +187,17 @@ __device__ void tree_schedule(const TreeArgs& p, int g, int G, TreeRun* run, int
   __syncthreads();
 }
 
+// What a run leaves for joining: the row tile it ends in, if later runs go on with it (a tile that several
+// runs share is the last one of the first of them, so a run has one at most).
+struct alignas(32) TreeJoin {
+  int row0, rows;   // first row of out (token x H + head), rows of the tile; 0: nothing to join
+  int parts, slot;  // runs that share it, from this one on; where this one's part is
+  int head0, pad[3];  // head of the first row
+};
+__device__ __forceinline__ TreeJoin* tree_join_of(const TreeArgs& p, int g) {
+  return reinterpret_cast<TreeJoin*>(p.ws + 256) + g;
+}
+
 struct TreeSeg {  // key tiles [k0, k1) of row tile m of a request
   int r, m, k0, k1;
   TreeReq q;
@@ -231,10 +243,11 @@ struct TreeWalk {
 };
 
 // Part `slot` (0: of the row tile a run starts in, 1: of the one it ends in) of CTA g: 64 rows of 512
-// fp32 values, then their log-sum-exps.
+// fp32 values, four dims of a row together, rows next to one another (a warp, a row a lane, stores 512
+// consecutive bytes); then their log-sum-exps.
 constexpr size_t kTrPart = size_t(kTrM) * (kLatent + 1) * 4;
-__device__ __forceinline__ float* tree_part(const TreeArgs& p, int64_t g, int slot) {
-  return reinterpret_cast<float*>(p.ws + 256 + size_t(2 * g + slot) * kTrPart);
+__device__ __forceinline__ float* tree_part(const TreeArgs& p, int64_t g, int slot, int G) {
+  return reinterpret_cast<float*>(p.ws + 256 + size_t(G) * sizeof(TreeJoin) + size_t(2 * g + slot) * kTrPart);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -322,7 +335,24 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     tc::fence_after();
   }
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + Y::tmem);
-  TreeWalk walk(p, *reinterpret_cast<const TreeRun*>(sm + Y::run));
+  const TreeRun run = *reinterpret_cast<const TreeRun*>(sm + Y::run);
+  TreeWalk walk(p, run);
+  if (tid == 32 * kTrCheckWarp) {  // the row tile this run ends in, for the joining kernel
+    TreeJoin jn = {};
+    if (run.u0 < run.u1) {
+      TreeReq q;
+      tree_request(p, run.r1, q);
+      const int64_t m = (run.u1 - 1 - run.base1) / q.kt, ub = run.base1 + m * q.kt;
+      if (ub >= run.u0 && ub + q.kt > run.u1) {
+        jn.row0 = q.cu0 * p.H + static_cast<int>(m) * kTrM;
+        jn.rows = static_cast<int>(min(int64_t(kTrM), int64_t(q.n) * p.H - m * kTrM));
+        jn.parts = static_cast<int>((ub + q.kt - 1) / run.per - blockIdx.x + 1);
+        jn.slot = ub > run.u0 ? 1 : 0;
+        jn.head0 = static_cast<int>(m * kTrM % p.H);
+      }
+    }
+    *tree_join_of(p, blockIdx.x) = jn;
+  }
   TreeSeg seg;
   bool ok = true;
   int gi = 0;  // key tiles of this CTA so far: the barriers' phases follow it across segments
@@ -552,9 +582,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const uint16_t* qrow = static_cast<const uint16_t*>(p.q) + (int64_t(seg.q.cu0) * p.H + (have ? R : 0)) * kDim;
         const uint4* lat = reinterpret_cast<const uint4*>(qrow + 256 * half + 128 * part);
         const uint4* rop = reinterpret_cast<const uint4*>(qrow + kLatent + 32 * half);
+        uint4 w[16], wr[4];  // all loads in flight together
+#pragma unroll
+        for (int c = 0; c < 16; ++c) w[c] = have ? __ldg(lat + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) wr[c] = have && part == 1 ? __ldg(rop + c) : make_uint4(0, 0, 0, 0);
         float qdown = 1.f;
         if constexpr (!BF) {
-          // both warps of a row look at all of its dims: no exchange
           uint32_t m4[4] = {0, 0, 0, 0};
           auto look = [&](const uint4 v) {
             m4[0] = bf16x2_max(m4[0], v.x & 0x7fff7fffu);
@@ -562,24 +596,28 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             m4[2] = bf16x2_max(m4[2], v.z & 0x7fff7fffu);
             m4[3] = bf16x2_max(m4[3], v.w & 0x7fff7fffu);
           };
-          if (have) {
-#pragma unroll 8
-            for (int c = 0; c < 32; ++c) look(__ldg(lat - 16 * part + c));
 #pragma unroll
-            for (int c = 0; c < 4; ++c) look(__ldg(rop + c));
-          }
-          const int qe = pow2_exponent_of_bf16(bf16x2_hmax_bits(bf16x2_max(bf16x2_max(m4[0], m4[1]), bf16x2_max(m4[2], m4[3]))));
+          for (int c = 0; c < 16; ++c) look(w[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) look(wr[c]);
+          const uint32_t mx = bf16x2_hmax_bits(bf16x2_max(bf16x2_max(m4[0], m4[1]), bf16x2_max(m4[2], m4[3])));
+          // the two warps of a row meet in the halves of its factor's word
+          const uint32_t at = sb + uint32_t(Y::qf) + uint32_t(row) * 4;
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 2 * part), "h"(uint16_t(mx)) : "memory");
+          named_bar(kTrBarConv, 32 * kTrConvWarps);
+          const uint32_t both = lds_u32(at);
+          named_bar(kTrBarConv, 32 * kTrConvWarps);
+          const int qe = pow2_exponent_of_bf16(max(both & 0xffffu, both >> 16));
           qdown = exp2_int(-qe);
-          if (part == 0)
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + uint32_t(Y::qf) + uint32_t(row) * 4), "f"(exp2_int(qe)) : "memory");
+          if (part == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(exp2_int(qe)) : "memory");
         }
-        auto cvt = [&](uint32_t w) -> uint32_t { return BF ? w : pack_f16x2(bf16_lo(w) * qdown, bf16_hi(w) * qdown); };
-#pragma unroll 1
+        auto cvt = [&](uint32_t x) -> uint32_t { return BF ? x : pack_f16x2(bf16_lo(x) * qdown, bf16_hi(x) * qdown); };
+#pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
           uint32_t wv[16];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 v = have ? __ldg(lat + 4 * ch + k) : make_uint4(0, 0, 0, 0);
+            const uint4 v = w[4 * ch + k];
             wv[4 * k] = cvt(v.x); wv[4 * k + 1] = cvt(v.y);
             wv[4 * k + 2] = cvt(v.z); wv[4 * k + 3] = cvt(v.w);
           }
@@ -589,10 +627,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         if (part == 1) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint4 v = have ? __ldg(rop + c) : make_uint4(0, 0, 0, 0);
             const uint32_t dst = sb + uint32_t(Y::qr) + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(cvt(v.x)), "r"(cvt(v.y)), "r"(cvt(v.z)),
-                         "r"(cvt(v.w)) : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(cvt(wr[c].x)), "r"(cvt(wr[c].y)),
+                         "r"(cvt(wr[c].z)), "r"(cvt(wr[c].w)) : "memory");
           }
           fence_proxy_async_smem();
         }
@@ -882,14 +919,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       // ---- epilogue: the four threads' sums of a row, then O lane -> output or part
       const bool fin = good && warp_wait(bar(R_PV_DONE), (gi - 1) & 1);
       tc::fence_after();
-      // (the partials of the last tile have been read: every thread has passed its second barrier)
-      const uint32_t lsum = sb + uint32_t(Y::xs) + uint32_t(hl) * 4;
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(lsum + uint32_t(2 * half + sub) * 256), "f"(l) : "memory");
+      // the sums meet in the partials' places, which this group of four warps alone uses: those of the last
+      // tile were read before its second barrier
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(xmine), "f"(l) : "memory");
       if (!named_bar_and(bar_x, 128, fin)) {
         ok = false;
         break;
       }
-      l = (lds_f32(lsum) + lds_f32(lsum + 256)) + (lds_f32(lsum + 512) + lds_f32(lsum + 768));
+      const uint32_t lsum = sb + uint32_t(Y::xs) + uint32_t(32 * pr + lane) * 64;  // warps pr, pr + 2, pr + 4, pr + 6
+      l = (lds_f32(lsum) + lds_f32(lsum + 64 * 64)) + (lds_f32(lsum + 128 * 64) + lds_f32(lsum + 192 * 64));
       named_bar(bar_m, 128);
       float lse = l == 0.f ? -CUDART_INF_F : (m - kTrShift + log2f(l)) * kLn2;
       float f = l == 0.f ? 0.f : (tens ? p.kv_scale : 1.f) / l;
@@ -899,7 +937,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         apply_sink(p.sink, h, lse, f);
         if (p.lse && real && half == 0 && sub == 0) p.lse[orow] = lse;
       } else {
-        part = tree_part(p, blockIdx.x, seg.first ? 0 : 1);
+        part = tree_part(p, blockIdx.x, seg.first ? 0 : 1, gridDim.x);
         if (half == 0 && sub == 0) part[kTrM * kLatent + hl] = lse;
       }
 #pragma unroll 1
@@ -921,10 +959,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
             dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
           } else {
-            float4* dst = reinterpret_cast<float4*>(part + hl * kLatent + col);
+            float4* dst = reinterpret_cast<float4*>(part) + (col >> 2) * kTrM + hl;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              dst[e] = make_float4(__uint_as_float(vv[4 * e]) * f, __uint_as_float(vv[4 * e + 1]) * f,
+              dst[e * kTrM] = make_float4(__uint_as_float(vv[4 * e]) * f, __uint_as_float(vv[4 * e + 1]) * f,
                                    __uint_as_float(vv[4 * e + 2]) * f, __uint_as_float(vv[4 * e + 3]) * f);
           }
         }
@@ -946,61 +984,86 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 
 // ---------------------------------------------------------------- joining the parts
 
-constexpr int kTrJoinThreads = 256;
+constexpr int kTrJoinThreads = 256, kTrJoinCtas = 4;  // CTAs an SM
+constexpr int kTrMaxRuns = 512;
 
-// CTA g joins its share of the rows of the (at most two) row tiles that its run cuts: of a tile that k
-// runs share, the j-th joins rows [64 j / k, 64 (j + 1) / k). Four warps a row, one for each 128 dims:
-// out = sum_i w_i o_i / sum_i w_i with w_i = e^(lse_i - max), in the order of the slots.
-__global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeArgs p) {
-  __shared__ TreeRun s_run;
-  __shared__ int64_t s_warp[32];
-  tree_schedule<kTrJoinThreads>(p, blockIdx.x, gridDim.x, &s_run, s_warp, nullptr);
+// The row tiles to join, 64 items each: four rows and 128 dims. out = sum_i w_i o_i / sum_i w_i with w_i =
+// e^(lse_i - max) over a tile's parts i: the weights of the four rows go to shared memory, then a thread
+// takes four dims of a row over the even or the odd parts, always in the same order. Bound by the latency of
+// a few dependent loads: spread over the whole GPU it takes a few microseconds, where one CTA a run,
+// two rows at a time, took 30-55 us.
+__global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeArgs p, int G) {
+  __shared__ int s_list[kTrMaxRuns], s_count;
+  __shared__ float s_w[4][kTrMaxRuns], s_lse[4], s_f[4];
+  __shared__ float4 s_acc[128];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
-  const TreeRun run = s_run;
-  if (run.u0 >= run.u1) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = 128 * (warp & 3) + 4 * lane;
-  for (int side = 0; side < 2; ++side) {
-    const int r = side ? run.r1 : run.r0;
-    const int64_t base = side ? run.base1 : run.base0, u = side ? run.u1 - 1 : run.u0;
-    TreeReq q;
-    tree_request(p, r, q);
-    const int64_t m = (u - base) / q.kt, ub = base + m * q.kt;
-    if (side && ub <= run.u0) return;  // the same row tile
-    const int64_t g0 = ub / run.per, g1 = (ub + q.kt - 1) / run.per;
-    if (g0 == g1) continue;
-    const int k = static_cast<int>(g1 - g0 + 1), j = static_cast<int>(blockIdx.x - g0);
-    const int first_slot = ub % run.per != 0 ? 1 : 0;
-    const int hi = kTrM * (j + 1) / k;
-    for (int row = kTrM * j / k + (warp >> 2); row < hi; row += 2) {
-      const int64_t R = m * kTrM + row;
-      if (R >= int64_t(q.n) * p.H) continue;
-      float M = -CUDART_INF_F;
-      for (int i = lane; i < k; i += 32) M = fmaxf(M, tree_part(p, g0 + i, i ? 0 : first_slot)[kTrM * kLatent + row]);
+  if (warp == 0) {  // the runs that leave a row tile to join
+    int n = 0;
+    for (int x = 0; x < G; x += 32) {
+      const bool has = x + lane < G && tree_join_of(p, x + lane)->rows > 0;
+      const uint32_t b = __ballot_sync(0xffffffffu, has);
+      if (has) s_list[n + __popc(b & ((1u << lane) - 1))] = x + lane;
+      n += __popc(b);
+    }
+    if (lane == 0) s_count = n;
+  }
+  __syncthreads();
+  const int items = 64 * s_count;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int g = s_list[item >> 6];
+    const TreeJoin jn = *tree_join_of(p, g);
+    const int row0 = 4 * ((item >> 2) & 15);
+    if (row0 >= jn.rows) continue;
+    if (warp < 4) {  // the weights of row row0 + warp
+      const int row = row0 + warp;
+      float M = -CUDART_INF_F, W = 0.f;
+      for (int i = lane; i < jn.parts; i += 32) {
+        const float v = tree_part(p, g + i, i ? 0 : jn.slot, G)[kTrM * kLatent + row];
+        s_w[warp][i] = v;
+        M = fmaxf(M, v);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       const float ref = M == -CUDART_INF_F ? 0.f : M;
-      float W = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int i = 0; i < k; ++i) {
-        const float* part = tree_part(p, g0 + i, i ? 0 : first_slot);
-        const float w = expf(part[kTrM * kLatent + row] - ref);
-        const float4 o = *reinterpret_cast<const float4*>(part + row * kLatent + col);
+      for (int i = lane; i < jn.parts; i += 32) {
+        const float w = expf(s_w[warp][i] - ref);
+        s_w[warp][i] = w;
         W += w;
-        acc.x = fmaf(w, o.x, acc.x);
-        acc.y = fmaf(w, o.y, acc.y);
-        acc.z = fmaf(w, o.z, acc.z);
-        acc.w = fmaf(w, o.w, acc.w);
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
       float lse = W == 0.f ? -CUDART_INF_F : ref + logf(W);
       float f = W == 0.f ? 0.f : 1.f / W;
-      apply_sink(p.sink, static_cast<int>(R % p.H), lse, f);
-      const int64_t orow = int64_t(q.cu0) * p.H + R;
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * kLatent + col) =
-          make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-      if (p.lse && (warp & 3) == 0 && lane == 0) p.lse[orow] = lse;
+      apply_sink(p.sink, (jn.head0 + row) % p.H, lse, f);
+      if (lane == 0) {
+        s_lse[warp] = lse;
+        s_f[warp] = f;
+      }
     }
+    __syncthreads();
+    const int r = tid & 3, quad = 32 * (item & 3) + ((tid >> 2) & 31), odd = tid >> 7;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = odd; i < jn.parts; i += 2) {
+      const float4 o = reinterpret_cast<const float4*>(tree_part(p, g + i, i ? 0 : jn.slot, G))[quad * kTrM + row0 + r];
+      const float w = s_w[r][i];
+      a.x = fmaf(w, o.x, a.x);
+      a.y = fmaf(w, o.y, a.y);
+      a.z = fmaf(w, o.z, a.z);
+      a.w = fmaf(w, o.w, a.w);
+    }
+    if (odd) s_acc[tid & 127] = a;
+    __syncthreads();
+    if (!odd && row0 + r < jn.rows) {
+      const float4 o = s_acc[tid];
+      const float f = s_f[r];
+      const int64_t orow = int64_t(jn.row0) + row0 + r;
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * kLatent + 4 * quad) =
+          make_uint2(pack_bf16x2((a.x + o.x) * f, (a.y + o.y) * f), pack_bf16x2((a.z + o.z) * f, (a.w + o.w) * f));
+      if (p.lse && quad == 0) p.lse[orow] = s_lse[r];
+    }
+    __syncthreads();
   }
 }
 
@@ -1035,7 +1098,7 @@ cudaError_t launch_fmt(const TreeArgs& a, int sms, const CUtensorMap& map, cudaS
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(sms));
+  cfg.gridDim = dim3(static_cast<unsigned>(sms * kTrJoinCtas));
   cfg.blockDim = dim3(kTrJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -1043,14 +1106,15 @@ cudaError_t launch_fmt(const TreeArgs& a, int sms, const CUtensorMap& map, cudaS
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_join_kernel, a);
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel, a, sms);
 }
 
 }  // namespace
 
-size_t tree_workspace_bytes(int num_sms) { return 256 + size_t(2) * num_sms * kTrPart; }
+size_t tree_workspace_bytes(int num_sms) { return 256 + num_sms * (sizeof(TreeJoin) + 2 * kTrPart); }
 
 cudaError_t launch_tree_decode(const TreeArgs& a, int num_sms, cudaStream_t s) {
+  if (num_sms > kTrMaxRuns) return cudaErrorInvalidConfiguration;
   alignas(64) CUtensorMap map = {};
   if (a.kv_format == SMLA_KV_BF16) {
     const cudaError_t e = tree_bf16_map(a, &map);
