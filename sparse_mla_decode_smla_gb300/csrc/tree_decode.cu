@@ -52,10 +52,9 @@ constexpr int kTrSub = 16; // slots of a raw stage
 constexpr int kTrSoftWarps = 8, kTrFirstConv = kTrSoftWarps, kTrConvWarps = 8;
 constexpr int kTrProducer = kTrFirstConv + kTrConvWarps, kTrMmaWarp = kTrProducer + 1, kTrCheckWarp = kTrMmaWarp + 1;
 constexpr int kTrThreads = 32 * (kTrCheckWarp + 1);
-constexpr int kTrBarConv = 11;  // named barrier of the key-tile warps (1-4: softmax row groups)
 // key tiles a CTA takes at least: shorter runs would spend more on their start and on joining
 // parts than they save
-constexpr int kTrMinUnits = 4;
+constexpr int kTrMinUnits = 2;
 constexpr float kTrRescale = 8.f;  // the running maximum moves when it grows by more (log2 units)
 // weights are 2^(s - m + 7): at most 2^15 between moves of the maximum, within f16, and exact to
 // 2^-11 down to 2^-21 of the largest one
@@ -107,7 +106,7 @@ enum {
   R_K_FULL = R_RAW_EMPTY + 4,      // [buffer]
   R_K_FREE = R_K_FULL + 2,         // [buffer][16-slot chunk]
   R_ROPE_FULL = R_K_FREE + 8,
-  R_S_FULL, R_S_FREE, R_P_READY, R_PV_DONE, R_Q, R_DRAIN, R_COUNT
+  R_S_FULL, R_S_FREE, R_P_READY, R_PV_DONE, R_Q, R_QRAW, R_QX, R_DRAIN, R_COUNT
 };
 static_assert(R_COUNT <= 32, "barriers");
 
@@ -137,19 +136,26 @@ __device__ __forceinline__ int tree_request(const TreeArgs& p, int r, TreeReq& q
   return 1;
 }
 
-// The run of CTA g of G, for a whole CTA of NT threads; ends with a barrier.
+// The run of CTA g of G, for a whole CTA of NT threads, in two steps: each thread's requests (their loads
+// pass behind what comes in between), then the run, which ends with a barrier.
 template <int NT>
-__device__ void tree_schedule(const TreeArgs& p, int g, int G, TreeRun* run, int64_t* s_warp, int32_t* err) {
-  constexpr int kWarps = NT / 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int each = (p.B + NT - 1) / NT;
-  const int ra = min(p.B, tid * each), rb = min(p.B, ra + each);
+__device__ __forceinline__ int64_t tree_units(const TreeArgs& p, int32_t* err) {
+  const int each = (p.B + NT - 1) / NT, ra = min(p.B, int(threadIdx.x) * each), rb = min(p.B, ra + each);
   TreeReq q;
   int64_t sum = 0;
   for (int r = ra; r < rb; ++r) {
     if (tree_request(p, r, q) < 0 && err) atomicOr(err, SMLA_DEVERR_INDEX);
     sum += q.units;
   }
+  return sum;
+}
+template <int NT>
+__device__ void tree_schedule(const TreeArgs& p, int64_t sum, int g, int G, TreeRun* run, int64_t* s_warp) {
+  constexpr int kWarps = NT / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int each = (p.B + NT - 1) / NT;
+  const int ra = min(p.B, tid * each), rb = min(p.B, ra + each);
+  TreeReq q;
   int64_t v = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -295,7 +301,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
 
 template <int FMT>
 __global__ void __launch_bounds__(kTrThreads, 1)
-    tree_decode_kernel(const TreeArgs p, const __grid_constant__ CUtensorMap kv_map) {
+    tree_decode_kernel(const TreeArgs p, const __grid_constant__ CUtensorMap kv_map,
+                       const __grid_constant__ CUtensorMap q_map) {
   using Y = Lay<FMT>;
   constexpr bool BF = Y::bf16, tens = Y::tens;
   extern __shared__ __align__(1024) uint8_t sm[];  // all of it: the swizzle atoms need its start
@@ -308,6 +315,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 
   // ------------------------------------------------------------------ set-up
   if (BF && tid == 0) prefetch_tensormap(&kv_map);
+  if (tid == 32) prefetch_tensormap(&q_map);
+  const int64_t units = tree_units<kTrThreads>(p, blockIdx.x == 0 ? err : nullptr);
   {
     uint4* zp = reinterpret_cast<uint4*>(sm + Y::P);  // the zero blocks beside P stay zero
     for (int k = tid; k < 3 * kTrPBlk / 16; k += kTrThreads) zp[k] = make_uint4(0, 0, 0, 0);
@@ -325,13 +334,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       mbar_init(bar(R_P_READY), kTrSoftWarps);
       mbar_init(bar(R_PV_DONE), 1);
       mbar_init(bar(R_Q), kTrConvWarps);
+      mbar_init(bar(R_QRAW), 1);
+      mbar_init(bar(R_QX), kTrConvWarps);
       mbar_init(bar(R_DRAIN), 1);
       tc::fence_mbarrier_init_cluster();
     }
     if (warp == kTrMmaWarp) tc::alloc(sb + uint32_t(Y::tmem), 512);
     tc::fence_before();
-    tree_schedule<kTrThreads>(p, blockIdx.x, gridDim.x, reinterpret_cast<TreeRun*>(sm + Y::run),
-                              reinterpret_cast<int64_t*>(sm + Y::xs), blockIdx.x == 0 ? err : nullptr);
+    tree_schedule<kTrThreads>(p, units, blockIdx.x, gridDim.x, reinterpret_cast<TreeRun*>(sm + Y::run),
+                              reinterpret_cast<int64_t*>(sm + Y::xs));
     tc::fence_after();
   }
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + Y::tmem);
@@ -369,14 +380,16 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     bool more = walk.next(p, seg);
     int k = seg.k0;
     int32_t e0 = -2, e1 = -2;
+    int nseg = 0, qseg = -1;  // this row tile's number; that of the tile before if it began one
     if (more) entries(seg, k, e0, e1);
     while (more && ok) {
       TreeSeg ns = seg;
-      int nk = k + 1;
+      int nk = k + 1, nnext = nseg;
       bool nm = true;
       if (nk == seg.k1) {
         nm = walk.next(p, ns);
         nk = ns.k0;
+        ++nnext;
       }
       int32_t n0 = -2, n1 = -2;
       if (nm) entries(ns, nk, n0, n1);  // a tile ahead: their latency is hidden
@@ -390,6 +403,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       if constexpr (BF) {
         const int b = gi & 1;
         if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * b + 3), ((gi >> 1) - 1) & 1)) { ok = false; break; }
+        // the tile before began a row tile: its q passes through this buffer
+        if (qseg >= 0 && !warp_wait(bar(R_Q), qseg & 1)) { ok = false; break; }
+        qseg = k == seg.k0 ? nseg : -1;
         const int rb = min(P, kTrN), runs = kTrN / rb;
         // a run of slots of one page is loaded whole when its first slot counts; what lies past the
         // last slot is cleared later
@@ -445,6 +461,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       e0 = n0;
       e1 = n1;
       more = nm;
+      nseg = nnext;
       ++gi;
     }
     // no copy may land after the CTA has left
@@ -567,26 +584,44 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     const int quarter = warp & 3, part = dw >> 2, half = quarter >> 1;
     const int hl = 32 * (quarter & 1) + lane, row = 32 * quarter + lane;
     const uint32_t lrow = tm + (uint32_t(32 * quarter) << 16);
+    int nseg = 0;
     while (ok && walk.next(p, seg)) {
       // q of this row tile, once the softmax has taken the last scores of the previous one (and with them
       // its factors of q): dims [256 half + 128 part, + 128) of
       // a row by this thread, and its 32 RoPE dims by part 1. FP8 formats: f16, scaled by a power of two
       // that brings the row's largest value into [1, 2); the factor goes back into the scores.
-      // PV two tiles back comes first: a barrier's parity tells its last phase from the one before only
-      if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * (gi & 1) + 3), ((gi >> 1) - 1) & 1)) { ok = false; break; }
+      // q arrives as nine boxes of 64 rows x 64 dims in a key-tile buffer that is free: this warp group's own
+      // next one, or (BF16, where the copies write the key tiles) the one after, whose copies wait for R_Q.
+      // A lane per row from global memory instead took 5-7 us.
+      // PV of the tile that last used the buffer comes first; its wait also tells S_FREE's last phase from the
+      // one before (a barrier's parity tells no more).
+      const int qb = BF ? (gi + 1) & 1 : gi & 1;
+      if (BF ? gi >= 1 : gi >= 2) {
+        const int last = BF ? gi - 1 : gi - 2;
+        if (!warp_wait(bar(R_K_FREE + 4 * qb + 3), (last >> 1) & 1)) { ok = false; break; }
+      }
       if (gi > 0 && !warp_wait(bar(R_S_FREE), (gi - 1) & 1)) { ok = false; break; }
+      const uint32_t qlat = sb + uint32_t(Y::K) + uint32_t(qb * kTrKLat);
+      const uint32_t qrop = sb + uint32_t(Y::rope) + uint32_t(BF ? qb * Y::rope_blk : 0);
+      if (dw == 0) {
+        if (lane == 0) mbar_arrive_expect_tx(bar(R_QRAW), 9u * kTrM * 128u);
+        __syncwarp();
+        if (lane < 9)
+          tma_load_2d(lane < 8 ? qlat + lane * (kTrM * 128) : qrop, &q_map, 64 * lane, seg.q.cu0 * p.H + seg.m * kTrM, bar(R_QRAW));
+      }
       {
+        const bool have = int64_t(seg.m) * kTrM + hl < int64_t(seg.q.n) * p.H;
+        if (!warp_wait(bar(R_QRAW), nseg & 1)) { ok = false; break; }
         tc::fence_after();
-        const int64_t R = int64_t(seg.m) * kTrM + hl;
-        const bool have = R < int64_t(seg.q.n) * p.H;
-        const uint16_t* qrow = static_cast<const uint16_t*>(p.q) + (int64_t(seg.q.cu0) * p.H + (have ? R : 0)) * kDim;
-        const uint4* lat = reinterpret_cast<const uint4*>(qrow + 256 * half + 128 * part);
-        const uint4* rop = reinterpret_cast<const uint4*>(qrow + kLatent + 32 * half);
-        uint4 w[16], wr[4];  // all loads in flight together
+        uint4 w[16], wr[4];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) w[c] = have ? __ldg(lat + c) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 16; ++c) {
+          const uint32_t at = qlat + uint32_t(4 * half + 2 * part + (c >> 3)) * (kTrM * 128) + uint32_t(hl) * 128;
+          w[c] = have ? lds128(at + (((c & 7) ^ (hl & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) wr[c] = have && part == 1 ? __ldg(rop + c) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 4; ++c)
+          wr[c] = have && part == 1 ? lds128(qrop + uint32_t(hl) * 128 + (((4 * half + c) ^ (hl & 7)) << 4)) : make_uint4(0, 0, 0, 0);
         float qdown = 1.f;
         if constexpr (!BF) {
           uint32_t m4[4] = {0, 0, 0, 0};
@@ -601,12 +636,17 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) look(wr[c]);
           const uint32_t mx = bf16x2_hmax_bits(bf16x2_max(bf16x2_max(m4[0], m4[1]), bf16x2_max(m4[2], m4[3])));
-          // the two warps of a row meet in the halves of its factor's word
+          // the two warps of a row meet in the halves of its factor's word (and all of them have read q before
+          // one writes a key tile there)
           const uint32_t at = sb + uint32_t(Y::qf) + uint32_t(row) * 4;
           asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 2 * part), "h"(uint16_t(mx)) : "memory");
-          named_bar(kTrBarConv, 32 * kTrConvWarps);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(R_QX));
+          if (!warp_wait(bar(R_QX), 0)) { ok = false; break; }
           const uint32_t both = lds_u32(at);
-          named_bar(kTrBarConv, 32 * kTrConvWarps);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(R_QX));
+          if (!warp_wait(bar(R_QX), 1)) { ok = false; break; }
           const int qe = pow2_exponent_of_bf16(max(both & 0xffffu, both >> 16));
           qdown = exp2_int(-qe);
           if (part == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(exp2_int(qe)) : "memory");
@@ -633,9 +673,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           }
           fence_proxy_async_smem();
         }
+        // (the copies wait for R_Q in turn: the first tile's arrival says that they have seen the last one)
+        if (BF && !warp_wait(bar(R_RAW_FULL + (gi & 1)), (gi >> 1) & 1)) { ok = false; break; }
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(R_Q));
+        ++nseg;
       }
       for (int k = seg.k0; k < seg.k1 && ok; ++k, ++gi) {
         const int b = gi & 1;
@@ -1067,23 +1110,23 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeArg
   }
 }
 
-// The cache as [slots, 576] bf16 with boxes of one page's slots (at most 64) x 64 dims.
-cudaError_t tree_bf16_map(const TreeArgs& a, CUtensorMap* out) {
+// [rows, 576] bf16 with boxes of `box_rows` rows x 64 dims, 128-byte swizzle: q, and the BF16 cache with
+// boxes of one page's slots (at most 64).
+cudaError_t tree_map(const void* base, int64_t rows, unsigned box_rows, CUtensorMap* out) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (tensor_map_encoder(&encode) != cudaSuccess) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {cuuint64_t(kDim), cuuint64_t(a.num_pages << a.log2_page)};
-  const cuuint64_t strides[1] = {cuuint64_t(kBf16RowBytes)};
-  const cuuint32_t rows = a.log2_page >= 6 ? 64u : 1u << a.log2_page;
-  const cuuint32_t box[2] = {64, rows};
+  const cuuint64_t dims[2] = {cuuint64_t(kDim), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(2 * kDim)};
+  const cuuint32_t box[2] = {64, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(a.kv), dims, strides, box, estr,
+  const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <int FMT>
-cudaError_t launch_fmt(const TreeArgs& a, int sms, const CUtensorMap& map, cudaStream_t s) {
+cudaError_t launch_fmt(const TreeArgs& a, int sms, const CUtensorMap& map, const CUtensorMap& qmap, cudaStream_t s) {
   // devices (below 64) whose kernel attribute is set; concurrent first calls set it twice
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
@@ -1094,7 +1137,7 @@ cudaError_t launch_fmt(const TreeArgs& a, int sms, const CUtensorMap& map, cudaS
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_release);
   }
-  tree_decode_kernel<FMT><<<sms, kTrThreads, Lay<FMT>::bytes, s>>>(a, map);
+  tree_decode_kernel<FMT><<<sms, kTrThreads, Lay<FMT>::bytes, s>>>(a, map, qmap);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1115,14 +1158,14 @@ size_t tree_workspace_bytes(int num_sms) { return 256 + num_sms * (sizeof(TreeJo
 
 cudaError_t launch_tree_decode(const TreeArgs& a, int num_sms, cudaStream_t s) {
   if (num_sms > kTrMaxRuns) return cudaErrorInvalidConfiguration;
-  alignas(64) CUtensorMap map = {};
-  if (a.kv_format == SMLA_KV_BF16) {
-    const cudaError_t e = tree_bf16_map(a, &map);
-    if (e != cudaSuccess) return e;
-    return launch_fmt<SMLA_KV_BF16>(a, num_sms, map, s);
-  }
-  if (a.kv_format == SMLA_KV_FP8_TENSOR) return launch_fmt<SMLA_KV_FP8_TENSOR>(a, num_sms, map, s);
-  return launch_fmt<SMLA_KV_FP8_DS>(a, num_sms, map, s);
+  alignas(64) CUtensorMap map = {}, qmap = {};
+  cudaError_t e = tree_map(a.q, int64_t(a.T) * a.H, kTrM, &qmap);
+  if (e != cudaSuccess) return e;
+  if (a.kv_format == SMLA_KV_FP8_TENSOR) return launch_fmt<SMLA_KV_FP8_TENSOR>(a, num_sms, map, qmap, s);
+  if (a.kv_format == SMLA_KV_FP8_DS) return launch_fmt<SMLA_KV_FP8_DS>(a, num_sms, map, qmap, s);
+  e = tree_map(a.kv, a.num_pages << a.log2_page, a.log2_page >= 6 ? 64u : 1u << a.log2_page, &map);
+  if (e != cudaSuccess) return e;
+  return launch_fmt<SMLA_KV_BF16>(a, num_sms, map, qmap, s);
 }
 
 }  // namespace smla
