@@ -3,6 +3,7 @@
 // All of them move bytes or whole numbers: nothing is computed, every result is exact, and
 // none depends on the order in which threads run.
 #include "cache_pages.h"
+#include "common.cuh"
 #include "tcgen05.cuh"
 
 namespace smla {
@@ -44,27 +45,32 @@ __global__ void __launch_bounds__(256) cache_copy_kernel(const CachePages c, con
 // ---------------------------------------------------------------- compacting rows
 
 constexpr int kCpThreads = 256;
-constexpr int kCpItems = 8;                          // 16-byte pieces a thread holds
-constexpr int kCpRows = 512;                         // rows of a chunk at most
-constexpr int kCpPieces = kCpThreads * kCpItems;     // pieces of a chunk at most
+constexpr int kCpItems = 8;   // 16-byte pieces a thread holds
+constexpr int kCpRows = 512;  // rows of a chunk at most
 
 // Row starts[r] + keep[k] -> row starts[r] + k for each kept row k of request r, in place, in
 // every layer. One CTA takes one (layer, request, range of 16-byte columns) and walks the kept
-// rows in ascending chunks: it loads a chunk's pieces into registers, waits for the whole CTA,
-// then stores them. With keep strictly ascending, keep[k] >= k, so row k of the result is a
-// source of rows <= k only: those of earlier chunks, already loaded, and of this one, loaded
-// before the barrier. No row that a later chunk reads is written early, and no other CTA
-// touches these columns of this request.
+// rows in ascending chunks: it loads a chunk's pieces into registers, the whole CTA meets, and they are
+// stored. With keep strictly ascending, keep[k] >= k, so row k of the result is a source of
+// rows <= k only: those of earlier chunks, already loaded, and of this one, loaded before the
+// barrier. No row that a later chunk reads is written early, and no other CTA touches these
+// columns of this request. Bound: HBM, every moved row read and written once. Loads through registers:
+// pieces staged in shared memory by cp.async, four chunks ahead, took 182 us where this takes 125 (half of
+// 16 contexts of 4k-16k slots kept, 656-byte rows, 4 layers: 437 MB, 3.5 TB/s; the longest context's chunks,
+// one after the other, set the time).
 __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
     const CachePages c, const int32_t* __restrict__ page_table, const int32_t* __restrict__ starts,
     const int32_t* __restrict__ cu_keep, const int32_t* __restrict__ keep, int64_t n_keep, int32_t* new_lens, int columns,
-    int slices) {
-  __shared__ int64_t s_src[kCpRows], s_dst[kCpRows];  // byte offsets of the rows; -1: not moved
+    int slices, int group) {
+  // byte offsets of the rows' old and new places, -1: not moved. Three chunks' worth: a chunk's are found
+  // while others still store the one before the last.
+  __shared__ longlong2 s_row[3][kCpRows];
   const int tid = threadIdx.x;
   const int slice = blockIdx.x % slices;
   const int64_t rest = blockIdx.x / slices;
-  const int r = static_cast<int>(rest % c.B), layer = static_cast<int>(rest / c.B);
-  const bool first = slice == 0 && layer == 0;
+  const int r = static_cast<int>(rest % c.B), layer0 = static_cast<int>(rest / c.B) * group;
+  const int layer1 = min(c.L, layer0 + group);
+  bool first = slice == 0 && layer0 == 0;  // this CTA reports errors (once: for its first layer)
   const int32_t start = __ldg(starts + r), a = __ldg(cu_keep + r), b = __ldg(cu_keep + r + 1);
   if (start < 0 || a < 0 || b < a || b > n_keep) {
     if (first && tid == 0) flag(c.err, SMLA_DEVERR_INDEX);
@@ -74,8 +80,9 @@ __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
   if (first && tid == 0 && new_lens) new_lens[r] = start + count;
   const int c0 = int(int64_t(columns) * slice / slices), c1 = int(int64_t(columns) * (slice + 1) / slices);
   const int cols = c1 - c0;
-  const int rows = min(kCpRows, kCpPieces / cols);
-  uint8_t* base = c.kv + int64_t(layer) * c.layer_stride;
+  // thread tid: column tid % cols of rows tid / cols + j (256 / cols) of a chunk
+  const int step = kCpThreads / cols, my = tid / cols, col = c0 + tid - my * cols;
+  const int rows = step * kCpItems;
   const int32_t* pt = page_table + int64_t(r) * c.stride;
   const int P = 1 << c.log2_page;
   // byte offset of a slot's row (index keys: of its codes), -1 where the slot has no page
@@ -97,52 +104,84 @@ __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
     const int64_t page = off / c.page_bytes, in = off - page * c.page_bytes;
     return page * c.page_bytes + int64_t(P) * 128 + (in >> 7) * 4;
   };
-  for (int k0 = 0; k0 < count; k0 += rows) {
-    const int m = min(rows, count - k0);
-    for (int i = tid; i < m; i += kCpThreads) {
-      const int k = k0 + i;
-      const int32_t from = __ldg(keep + a + k);
-      const int32_t before = k ? __ldg(keep + a + k - 1) : -1;
-      int64_t so = -1, dp = -1;
-      if (from < k || from <= before) {
-        if (first) flag(c.err, SMLA_DEVERR_INDEX);
-      } else if (from != k) {
-        so = row_at(int64_t(start) + from);
-        dp = row_at(int64_t(start) + k);
-        if (dp < 0) so = -1;
+  const int chunks = (count + rows - 1) / rows;
+  // the places of row i of chunk ch
+  auto place = [&](int ch, int i) -> longlong2 {
+    const int k = ch * rows + i;
+    const int32_t from = __ldg(keep + a + k);
+    const int32_t before = k ? __ldg(keep + a + k - 1) : -1;
+    longlong2 x = make_longlong2(-1, -1);
+    if (from < k || from <= before) {
+      if (first) flag(c.err, SMLA_DEVERR_INDEX);
+    } else if (from != k) {
+      x.x = row_at(int64_t(start) + from);
+      x.y = row_at(int64_t(start) + k);
+      if (x.y < 0) x.x = -1;
+    }
+    return x;
+  };
+  auto find = [&](int ch) {  // the places of chunk ch's rows
+    const int m = min(rows, count - ch * rows);
+    for (int i = tid; i < m; i += kCpThreads) s_row[ch % 3][i] = place(ch, i);
+  };
+  auto get = [&](uint4& v, const uint8_t* base, int64_t so) {
+    if (c.index_keys && col == 8)
+      v.x = *reinterpret_cast<const uint32_t*>(base + scale_at(so));
+    else
+      v = *reinterpret_cast<const uint4*>(base + so + 16 * col);
+  };
+  auto put = [&](const uint4& v, uint8_t* base, int64_t dp) {
+    if (c.index_keys && col == 8)
+      *reinterpret_cast<uint32_t*>(base + scale_at(dp)) = v.x;
+    else
+      *reinterpret_cast<uint4*>(base + dp + 16 * col) = v;
+  };
+  uint4 v[kCpItems];
+  if (chunks <= 1) {
+    // Few rows (an accepted path): their places are found once, and as many layers as fit are loaded
+    // together.
+    if (count == 0) return;
+    find(0);
+    __syncthreads();
+    const int each = (count + step - 1) / step, together = kCpItems / each;  // items of a layer; layers at once
+    for (int l0 = layer0; l0 < layer1; l0 += together) {
+#pragma unroll
+      for (int j = 0; j < kCpItems; ++j) {
+        const int l = j / each, i = my + (j - l * each) * step;
+        if (my >= step || i >= count || l >= together || l0 + l >= layer1 || s_row[0][i].x < 0) continue;
+        get(v[j], c.kv + int64_t(l0 + l) * c.layer_stride, s_row[0][i].x);
       }
-      s_src[i] = so;
-      s_dst[i] = dp;
-    }
-    __syncthreads();
-    uint4 v[kCpItems];
-    const int items = m * cols;
+      __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kCpItems; ++j) {
-      const int it = tid + j * kCpThreads;
-      if (it >= items) continue;
-      const int i = it / cols, col = c0 + it - i * cols;
-      const int64_t so = s_src[i];
-      if (so < 0) continue;
-      if (c.index_keys && col == 8)
-        v[j].x = *reinterpret_cast<const uint32_t*>(base + scale_at(so));
-      else
-        v[j] = *reinterpret_cast<const uint4*>(base + so + 16 * col);
+      for (int j = 0; j < kCpItems; ++j) {
+        const int l = j / each, i = my + (j - l * each) * step;
+        if (my >= step || i >= count || l >= together || l0 + l >= layer1 || s_row[0][i].x < 0) continue;
+        put(v[j], c.kv + int64_t(l0 + l) * c.layer_stride, s_row[0][i].y);
+      }
     }
+    return;
+  }
+  for (int layer = layer0; layer < layer1; ++layer) {
+    uint8_t* base = c.kv + int64_t(layer) * c.layer_stride;
+    find(0);
     __syncthreads();
+    for (int ch = 0; ch < chunks; ++ch) {
+      const int m = min(rows, count - ch * rows);
 #pragma unroll
-    for (int j = 0; j < kCpItems; ++j) {
-      const int it = tid + j * kCpThreads;
-      if (it >= items) continue;
-      const int i = it / cols, col = c0 + it - i * cols;
-      if (s_src[i] < 0) continue;
-      const int64_t dp = s_dst[i];
-      if (c.index_keys && col == 8)
-        *reinterpret_cast<uint32_t*>(base + scale_at(dp)) = v[j].x;
-      else
-        *reinterpret_cast<uint4*>(base + dp + 16 * col) = v[j];
+      for (int j = 0; j < kCpItems; ++j) {
+        const int i = my + j * step;
+        if (my < step && i < m && s_row[ch % 3][i].x >= 0) get(v[j], base, s_row[ch % 3][i].x);
+      }
+      if (ch + 1 < chunks) find(ch + 1);  // behind this chunk's loads
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kCpItems; ++j) {
+        const int i = my + j * step;
+        if (my < step && i < m && s_row[ch % 3][i].x >= 0) put(v[j], base, s_row[ch % 3][i].y);
+      }
     }
-    __syncthreads();  // s_src and s_dst are rewritten
+    first = false;
+    __syncthreads();
   }
 }
 
@@ -260,9 +299,10 @@ __global__ void __launch_bounds__(kListThreads) cache_fork_plan_kernel(const Cac
 __global__ void __launch_bounds__(256) cache_fork_kernel(const CachePages c, const CacheTables t,
                                                          const int32_t* __restrict__ src_req,
                                                          const int32_t* __restrict__ dst_req,
-                                                         const int32_t* __restrict__ fork_pages) {
+                                                         const int32_t* fork_pages) {
   const int i = blockIdx.x, y = blockIdx.y, ny = gridDim.y, tid = threadIdx.x;
-  const int32_t got = fork_pages[i];
+  pdl_wait();
+  const int32_t got = __ldcg(fork_pages + i);
   if (got == -2) return;
   const int32_t s = src_req[i], d = dst_req[i];
   const int64_t len = t.lens[s];
@@ -330,22 +370,14 @@ __device__ __forceinline__ Resize resize_entry(const CachePages& c, const CacheT
   return e;
 }
 
-// First step of a resize: the pages beyond the new length leave the table and lose a holder.
-// CTA (i, y) takes every y-th group of request i's entries.
-__global__ void __launch_bounds__(256) cache_release_kernel(const CachePages c, const CacheTables t,
-                                                            const int32_t* __restrict__ req,
-                                                            const int32_t* __restrict__ new_lens, int32_t n) {
-  const int i = blockIdx.x;
-  const Resize e = resize_entry(c, t, req, new_lens, i);
-  int twice = 0;
-  for (int j = threadIdx.x; j < n; j += 256) twice |= j != i && req[j] == e.r;
-  twice = __syncthreads_or(twice);
-  if (!e.ok || twice) {
-    if (threadIdx.x == 0) flag(c.err, SMLA_DEVERR_INDEX);
-    return;
-  }
+constexpr int kPushCtas = 8;
+constexpr int kMarkWords = 2048;  // words of marks a CTA and round
+constexpr int64_t kResizeOneLaunch = 1 << 16;  // table entries
+
+// The pages of entry e beyond its new length leave the table and lose a holder; threads `at`, at + step, ...
+__device__ __forceinline__ void release_pages(const CachePages& c, const CacheTables& t, const Resize& e, int64_t at, int64_t step) {
   int32_t* row = t.page_table + int64_t(e.r) * c.stride;
-  for (int64_t k = e.new_pages + blockIdx.y * 256 + threadIdx.x; k < e.old_pages; k += int64_t(gridDim.y) * 256) {
+  for (int64_t k = e.new_pages + at; k < e.old_pages; k += step) {
     const int32_t page = row[k];
     row[k] = -1;
     if (page < 0 || page >= c.num_pages) {
@@ -362,14 +394,46 @@ __global__ void __launch_bounds__(256) cache_release_kernel(const CachePages c, 
   }
 }
 
-constexpr int kPushCtas = 8;
+// A growing request takes its pages off the list, the last one first.
+__device__ __forceinline__ void pop_pages(const CachePages& c, const CacheTables& t, int32_t r, int64_t pos, int64_t old_pages,
+                                          int64_t new_pages, int64_t at, int64_t step) {
+  int32_t* row = t.page_table + int64_t(r) * c.stride;
+  for (int64_t k = old_pages + at; k < new_pages; k += step) {
+    const int64_t from = pos - (k - old_pages);
+    const int32_t page = __ldcg(t.free_list + from);
+    t.free_list[from] = -1;
+    row[k] = page;
+    if (page >= 0 && page < c.num_pages)
+      t.refs[page] = 1;
+    else
+      flag(c.err, SMLA_DEVERR_PAGE);
+  }
+}
+
+// First step of a resize: the releases. CTA (i, y) takes every y-th group of request i's entries.
+__global__ void __launch_bounds__(256) cache_release_kernel(const CachePages c, const CacheTables t,
+                                                            const int32_t* __restrict__ req,
+                                                            const int32_t* __restrict__ new_lens, int32_t n) {
+  const int i = blockIdx.x;
+  const Resize e = resize_entry(c, t, req, new_lens, i);
+  int twice = 0;
+  for (int j = threadIdx.x; j < n; j += 256) twice |= j != i && req[j] == e.r;
+  twice = __syncthreads_or(twice);
+  if (!e.ok || twice) {
+    if (threadIdx.x == 0) flag(c.err, SMLA_DEVERR_INDEX);
+    return;
+  }
+  release_pages(c, t, e, blockIdx.y * 256 + threadIdx.x, int64_t(gridDim.y) * 256);
+}
 
 // Second step, one cluster of eight CTAs: the freed pages go to the end of the free list in
 // ascending order (each CTA counts its range of pages, the counts meet over distributed shared
 // memory), then the first CTA gives each growing request its place in the list, in the order of
 // the call. A request is refused (SMLA_DEVERR_PAGE) when fewer pages are free than it and those
 // before it ask for. work[2i]: the list position of the request's first page, -1 where it takes
-// none; work[2i+1]: its old page count.
+// none; work[2i+1]: its old page count. With ALL the cluster does the first and the third step as well: one
+// launch in place of three, where few entries are listed.
+template <bool ALL>
 __global__ void __cluster_dims__(kPushCtas, 1, 1) __launch_bounds__(kListThreads)
     cache_push_kernel(const CachePages c, const CacheTables t, const int32_t* __restrict__ req,
                       const int32_t* __restrict__ new_lens, int32_t n, int32_t* work) {
@@ -377,6 +441,12 @@ __global__ void __cluster_dims__(kPushCtas, 1, 1) __launch_bounds__(kListThreads
   __shared__ int64_t s_warp[32];
   __shared__ int64_t s_mine;
   const int tid = threadIdx.x, rank = blockIdx.x, words = (c.B + 31) >> 5;
+  const int lane = tid & 31;
+  // ALL: the cluster's threads form teams of 32 to 1024, about one a request
+  int team = kListThreads;
+  while (team > 32 && int64_t(team) * n > kPushCtas * kListThreads) team >>= 1;
+  const int teams = kPushCtas * kListThreads / team, mine_at = tid & (team - 1);
+  const int first_i = rank * (kListThreads / team) + tid / team;
   for (int i = tid; i < 2 * words; i += kListThreads) bits[i] = 0;
   __syncthreads();
   for (int i = tid; i < n; i += kListThreads) {
@@ -387,106 +457,179 @@ __global__ void __cluster_dims__(kPushCtas, 1, 1) __launch_bounds__(kListThreads
     }
   }
   __syncthreads();
-  auto entry = [&](int i) {
+  __shared__ int3 s_entry[kListThreads];  // (request or -1, old pages, new pages) of a list that fits
+  auto look = [&](int i) {
     Resize e = resize_entry(c, t, req, new_lens, i);
     if (e.ok && (bits[words + (e.r >> 5)] >> (e.r & 31)) & 1) e.ok = false;
     return e;
   };
-  // nothing was released when no listed request shrinks
+  auto entry = [&](int i) {
+    if (n > kListThreads) return look(i);
+    const int3 x = s_entry[i];
+    Resize e;
+    e.ok = x.x >= 0;
+    e.r = x.x;
+    e.old_pages = x.y;
+    e.new_pages = x.z;
+    return e;
+  };
+  // nothing is released when no listed request shrinks
   int any = 0;
   for (int i = tid; i < n; i += kListThreads) {
-    const Resize e = entry(i);
+    const Resize e = look(i);
     any |= e.ok && e.new_pages < e.old_pages;
+    if (n <= kListThreads) s_entry[i] = make_int3(e.ok ? e.r : -1, static_cast<int>(e.old_pages), static_cast<int>(e.new_pages));
   }
   any = __syncthreads_or(any);
-  const int64_t count = clamp_count(*t.free_count, c.num_pages, c.err, rank == 0 && tid == 0);
+  if constexpr (!ALL) pdl_wait();  // the releases have been made
+  const int64_t count = clamp_count(__ldcg(t.free_count), c.num_pages, c.err, rank == 0 && tid == 0);
+  if constexpr (ALL) {
+    for (int i = first_i; i < n; i += teams) {
+      const Resize e = entry(i);
+      if (e.ok)
+        release_pages(c, t, e, mine_at, team);
+      else if (mine_at == 0)
+        flag(c.err, SMLA_DEVERR_INDEX);
+    }
+    if (any) {
+      tc::cluster_arrive();
+      tc::cluster_wait();
+    }
+  }
   int64_t freed = 0;
   if (any) {
-    const int64_t per = ((c.num_pages + kPushCtas - 1) / kPushCtas + 3) & ~int64_t(3);
-    const int64_t lo = min(c.num_pages, per * rank), hi = min(c.num_pages, lo + per);
-    int64_t mine = 0;
-    for (int64_t p = lo + tid; p < hi; p += kListThreads) mine += (__ldcg(t.refs + p) & kRefFreed) != 0;
-    int64_t total;
-    block_sum_scan(mine, s_warp, total);
-    if (tid == 0) s_mine = total;
-    __syncthreads();
-    tc::cluster_arrive();
-    tc::cluster_wait();
+    // The marks of a range of pages, an eighth a CTA, a bit a page, go to shared memory in one pass; then each
+    // warp lists the pages of a word, so that its stores are next to one another.
+    uint32_t* marks = bits + 2 * words;
+    int32_t* before = reinterpret_cast<int32_t*>(marks + kMarkWords);  // marks of the CTA's words before
+    constexpr int64_t kRound = 32 * int64_t(kMarkWords) * kPushCtas;  // pages a round: half a million
     int64_t at = count;
-    for (int k = 0; k < kPushCtas; ++k) {
-      int64_t v;
-      asm volatile("ld.shared::cluster.b64 %0, [%1];"
-                   : "=l"(v)
-                   : "r"(tc::mapa(static_cast<uint32_t>(__cvta_generic_to_shared(&s_mine)), k)));
-      freed += v;
-      if (k < rank) at += v;
-    }
-    for (int64_t p0 = lo; p0 < hi; p0 += kListThreads) {
-      const int64_t p = p0 + tid;
-      const int32_t v = p < hi ? __ldcg(t.refs + p) : 0;
-      const bool f = (v & kRefFreed) != 0;
-      const int64_t before = at + block_sum_scan(f ? 1 : 0, s_warp, total) - 1;
-      at += total;
-      if (f) {
-        t.refs[p] = v & ~kRefFreed;
-        if (before < c.num_pages)
-          t.free_list[before] = static_cast<int32_t>(p);
+    for (int64_t r0 = 0; r0 < c.num_pages; r0 += kRound) {
+      const int64_t r1 = min(c.num_pages, r0 + kRound), per = ((r1 - r0 + kPushCtas - 1) / kPushCtas + 31) & ~int64_t(31);
+      const int64_t a = min(r1, r0 + per * rank), b = min(r1, a + per);
+      const int nw = static_cast<int>((b - a + 31) >> 5);
+      constexpr int kAhead = 16, kW = kListThreads / 32;  // words a warp loads at once
+      for (int w = tid >> 5; w < nw; w += kAhead * kW) {
+        int32_t v[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {  // (past the end: the last page again, so that no load hangs on a branch)
+          const int64_t p = a + 32 * int64_t(w + x * kW) + lane;
+          v[x] = __ldcg(t.refs + min(p, b - 1));
+          if (p >= b) v[x] = 0;
+        }
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+          const uint32_t m = __ballot_sync(0xffffffffu, (v[x] & kRefFreed) != 0);
+          if (lane == 0 && w + x * kW < nw) marks[w + x * kW] = m;
+        }
+      }
+      __syncthreads();
+      const int each = (nw + kListThreads - 1) / kListThreads, w0 = min(nw, tid * each), w1 = min(nw, w0 + each);
+      int64_t mine = 0;
+      for (int w = w0; w < w1; ++w) mine += __popc(marks[w]);
+      int64_t total;
+      int64_t upto = block_sum_scan(mine, s_warp, total) - mine;
+      for (int w = w0; w < w1; ++w) {
+        before[w] = static_cast<int32_t>(upto);
+        upto += __popc(marks[w]);
+      }
+      if (tid == 0) s_mine = total;
+      __syncthreads();
+      tc::cluster_arrive();
+      tc::cluster_wait();
+      int64_t from = at, sum = 0;
+      for (int k = 0; k < kPushCtas; ++k) {
+        int64_t v;
+        asm volatile("ld.shared::cluster.b64 %0, [%1];"
+                     : "=l"(v)
+                     : "r"(tc::mapa(static_cast<uint32_t>(__cvta_generic_to_shared(&s_mine)), k)));
+        if (k < rank) from += v;
+        sum += v;
+      }
+      at += sum;
+      freed += sum;
+      for (int w = tid >> 5; w < nw; w += kListThreads / 32) {
+        const uint32_t m = marks[w];
+        if (!((m >> lane) & 1)) continue;
+        const int64_t p = a + 32 * int64_t(w) + lane, pos = from + before[w] + __popc(m & ((1u << lane) - 1));
+        t.refs[p] = 0;
+        if (pos < c.num_pages)
+          t.free_list[pos] = static_cast<int32_t>(p);
         else
           flag(c.err, SMLA_DEVERR_PAGE);
+      }
+      if (r0 + kRound < c.num_pages) {  // the counts and the marks are rewritten
+        tc::cluster_arrive();
+        tc::cluster_wait();
       }
     }
   }
   // every CTA has read the others' counts and the old lengths, and its pushes are visible
   tc::cluster_arrive();
   tc::cluster_wait();
-  if (rank != 0) return;
-  const int64_t avail = min(c.num_pages, count + freed);
-  int64_t asked = 0, given = 0;
-  for (int i0 = 0; i0 < n; i0 += kListThreads) {
-    const int i = i0 + tid;
-    Resize e;
-    e.ok = false;
-    e.r = 0;
-    e.old_pages = e.new_pages = 0;
-    if (i < n) e = entry(i);
-    const int64_t need = e.ok && e.new_pages > e.old_pages ? e.new_pages - e.old_pages : 0;
-    int64_t total;
-    const int64_t upto = asked + block_sum_scan(need, s_warp, total);
-    asked += total;
-    const bool fits = need == 0 || upto <= avail;
-    int64_t took;
-    block_sum_scan(fits ? need : 0, s_warp, took);
-    given += took;
-    if (i < n) {
-      work[2 * i] = need != 0 && fits ? static_cast<int32_t>(avail - 1 - (upto - need)) : -1;
-      work[2 * i + 1] = static_cast<int32_t>(e.old_pages);
-      if (!fits) flag(c.err, SMLA_DEVERR_PAGE);
-      if (e.ok && fits) t.lens[e.r] = new_lens[i];
+  if (rank == 0) {
+    const int64_t avail = min(c.num_pages, count + freed);
+    int64_t asked = 0, given = 0;
+    for (int i0 = 0; i0 < n; i0 += kListThreads) {
+      const int i = i0 + tid;
+      Resize e;
+      e.ok = false;
+      e.r = 0;
+      e.old_pages = e.new_pages = 0;
+      if (i < n) e = entry(i);
+      const int64_t need = e.ok && e.new_pages > e.old_pages ? e.new_pages - e.old_pages : 0;
+      int64_t total;
+      const int64_t upto = asked + block_sum_scan(need, s_warp, total);
+      asked += total;
+      const bool fits = need == 0 || upto <= avail;
+      int64_t took;
+      block_sum_scan(fits ? need : 0, s_warp, took);
+      given += took;
+      if (i < n) {
+        work[2 * i] = need != 0 && fits ? static_cast<int32_t>(avail - 1 - (upto - need)) : -1;
+        work[2 * i + 1] = static_cast<int32_t>(e.old_pages);
+        if (!fits) flag(c.err, SMLA_DEVERR_PAGE);
+        if (e.ok && fits) t.lens[e.r] = new_lens[i];
+      }
+    }
+    if (tid == 0) *t.free_count = static_cast<int32_t>(avail - given);
+  }
+  if constexpr (ALL) {
+    tc::cluster_arrive();
+    tc::cluster_wait();
+    for (int i = first_i; i < n; i += teams) {
+      const int64_t pos = __ldcg(work + 2 * i);
+      if (pos >= 0) pop_pages(c, t, req[i], pos, __ldcg(work + 2 * i + 1), pages_of(new_lens[i], c.log2_page), mine_at, team);
     }
   }
-  if (tid == 0) *t.free_count = static_cast<int32_t>(avail - given);
 }
 
-// Third step: each growing request takes its pages off the list, the last one first.
+// Third step: the growing requests' pages.
 __global__ void __launch_bounds__(256) cache_pop_kernel(const CachePages c, const CacheTables t,
                                                         const int32_t* __restrict__ req,
-                                                        const int32_t* __restrict__ new_lens,
-                                                        const int32_t* __restrict__ work) {
+                                                        const int32_t* __restrict__ new_lens, const int32_t* work) {
   const int i = blockIdx.x;
-  const int64_t pos = work[2 * i];
+  pdl_wait();
+  const int64_t pos = __ldcg(work + 2 * i);
   if (pos < 0) return;
-  const int64_t old_pages = work[2 * i + 1], new_pages = pages_of(new_lens[i], c.log2_page);
-  int32_t* row = t.page_table + int64_t(req[i]) * c.stride;
-  for (int64_t k = old_pages + blockIdx.y * 256 + threadIdx.x; k < new_pages; k += int64_t(gridDim.y) * 256) {
-    const int64_t at = pos - (k - old_pages);
-    const int32_t page = t.free_list[at];
-    t.free_list[at] = -1;
-    row[k] = page;
-    if (page >= 0 && page < c.num_pages)
-      t.refs[page] = 1;
-    else
-      flag(c.err, SMLA_DEVERR_PAGE);
-  }
+  pop_pages(c, t, req[i], pos, __ldcg(work + 2 * i + 1), pages_of(new_lens[i], c.log2_page), blockIdx.y * 256 + threadIdx.x,
+            int64_t(gridDim.y) * 256);
+}
+
+// A kernel that starts up while the one before it on the stream ends, and waits for it itself (pdl_wait).
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
@@ -515,10 +658,14 @@ cudaError_t launch_cache_compact(const CachePages& c, const int32_t* page_table,
   int64_t slices = (int64_t(sms) * 8 + pairs - 1) / pairs;
   if (slices > columns / 4) slices = columns / 4;
   if (slices < 1) slices = 1;
-  const int64_t blocks = pairs * slices;
+  // a few layers a CTA where there are more than four CTAs an SM
+  int64_t group = pairs * slices / (int64_t(sms) * 4);
+  if (group > 8) group = 8;
+  if (group < 1) group = 1;
+  const int64_t blocks = c.B * ((c.L + group - 1) / group) * slices;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cache_compact_kernel<<<static_cast<unsigned>(blocks), kCpThreads, 0, s>>>(
-      c, page_table, starts, cu_keep, keep, n_keep, new_lens, columns, static_cast<int>(slices));
+      c, page_table, starts, cu_keep, keep, n_keep, new_lens, columns, static_cast<int>(slices), static_cast<int>(group));
   return cudaGetLastError();
 }
 
@@ -532,25 +679,28 @@ cudaError_t launch_cache_fork(const CachePages& c, const CacheTables& t, const i
   int64_t y = (int64_t(sms) * 8 + n - 1) / n;
   if (y > pieces) y = pieces;
   if (y > 65535) y = 65535;
-  cache_fork_kernel<<<dim3(static_cast<unsigned>(n), static_cast<unsigned>(y)), 256, 0, s>>>(c, t, src_req, dst_req,
-                                                                                           fork_pages);
-  return cudaGetLastError();
+  return launch_behind(cache_fork_kernel, dim3(static_cast<unsigned>(n), static_cast<unsigned>(y)), 256, 0, s, c, t, src_req,
+                       dst_req, (const int32_t*)fork_pages);
 }
 
 cudaError_t launch_cache_resize(const CachePages& c, const CacheTables& t, const int32_t* req, const int32_t* new_lens,
                                 int32_t n, int32_t* work, int sms, cudaStream_t s) {
+  const size_t smem = size_t(2) * ((c.B + 31) / 32) * 4 + 2 * kMarkWords * 4;
+  // One launch while the cluster has few table entries to walk (the lengths are known on the device only: all
+  // of the listed rows count). Two calls, one launch each against three: at 32,000 entries growing 20.6 us
+  // against 24.2, freeing everything 26.7 against 26.7; at 128,000 20.6 against 28 and 57 against 45.
+  if (int64_t(n) * c.stride <= kResizeOneLaunch) {
+    cache_push_kernel<true><<<kPushCtas, kListThreads, smem, s>>>(c, t, req, new_lens, n, work);
+    return cudaGetLastError();
+  }
   int64_t y = (int64_t(sms) * 4 + n - 1) / n;
   if (y > (c.stride + 255) / 256) y = (c.stride + 255) / 256;
   const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(y));
   cache_release_kernel<<<grid, 256, 0, s>>>(c, t, req, new_lens, n);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const size_t smem = size_t(2) * ((c.B + 31) / 32) * 4;
-  cache_push_kernel<<<kPushCtas, kListThreads, smem, s>>>(c, t, req, new_lens, n, work);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cache_pop_kernel<<<grid, 256, 0, s>>>(c, t, req, new_lens, work);
-  return cudaGetLastError();
+  if (e == cudaSuccess) e = launch_behind(cache_push_kernel<false>, dim3(kPushCtas), kListThreads, smem, s, c, t, req, new_lens, n, work);
+  if (e == cudaSuccess) e = launch_behind(cache_pop_kernel, grid, 256, 0, s, c, t, req, new_lens, (const int32_t*)work);
+  return e;
 }
 
 }  // namespace smla

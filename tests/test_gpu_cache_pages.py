@@ -279,3 +279,47 @@ def test_streams_and_graphs():
             e, p.count = C.resize(p.P, p.table, p.lens, p.refs, p.free, p.count, [0, 1], new)
             assert e == 0
         p.check()
+
+
+def test_resize_of_more_pages_than_a_round_of_marks():
+    # over a million pages: the freed ones still come back in ascending order over all of them
+    pages, B, stride = 2_300_001, 3, 1_200_000
+    g = np.random.default_rng(5)
+    perm = g.permutation(pages).astype(np.int32)
+    lens = np.array([1_150_000, 700_000, 400_000], dtype=np.int32)
+    table = np.full((B, stride), -1, dtype=np.int32)
+    at = 0
+    for r, n in enumerate(lens):
+        table[r, :n] = perm[at:at + n]
+        at += n
+    refs = np.zeros(pages, dtype=np.int32)
+    refs[perm[:at]] = 1
+    free = np.full(pages, -1, dtype=np.int32)
+    free[:pages - at] = perm[at:]
+    d = smla.make_cache_desc(0, 1, 1, pages, B, stride)
+    dv = [_dev(x) for x in (table, lens, refs, free, [pages - at])]
+    work, err = torch.empty(4, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    smla.cache_resize(d, *dv, _dev([2, 0]), _dev([5, 100]), work, err)
+    assert err.item() == 0
+    gone = np.sort(np.concatenate([table[2, 5:400_000], table[0, 100:1_150_000]]))
+    got = dv[3].cpu().numpy()
+    assert dv[4].item() == pages - at + len(gone)
+    assert np.array_equal(got[:pages - at], free[:pages - at])
+    assert np.array_equal(got[pages - at:pages - at + len(gone)], gone) and (got[pages - at + len(gone):] == -1).all()
+    left = dv[2].cpu().numpy()
+    refs[gone] = 0
+    assert np.array_equal(left, refs)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "index_keys"])
+def test_compact_many_layers_and_chunks(fmt):
+    # more layers than a CTA takes together, rows of one chunk and of several in one call
+    g = np.random.default_rng(3)
+    lens = [40, 900, 17, 0, 260] * 12
+    p = Pool(fmt, 40, 16, lens, 60, sum(-(-n // 16) for n in lens) + 1, seed=7)
+    keep = [sorted(g.choice(n, n * 2 // 3, replace=False).tolist()) if n else [] for n in lens]
+    cu = np.concatenate([[0], np.cumsum([len(k) for k in keep])])
+    flat = [x for k in keep for x in k]
+    smla.cache_compact(p.desc, p.d_table, _dev([0] * 60), _dev(cu), _dev(flat), p.raw, None, p.err)
+    C.compact(p.cache, fmt, 16, p.table, [0] * 60, cu, flat)
+    p.check()
