@@ -377,3 +377,70 @@ def test_draft_verify_accept_fork():
     q[2] = q[1]
     out = attend(ctx, [0, 1, 2, 3], None, 3, q)
     assert torch.equal(out[1], out[2])  # a fork answers as its source does
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_long_chain_over_several_row_tiles(fmt):
+    # a chunk of a prompt: many more nodes than a mask would hold, every key tile cut by the diagonal
+    Batch(fmt, 3, ctx=(10, 0), nodes=(333, 130), page=32, tree=False, sink=True, seed=20).check()
+
+
+def test_rows_before_the_first_node_and_odd_bounds():
+    b = Batch("fp8_ds", 16, ctx=(70, 20), nodes=(3, 2), seed=21, spare_rows=7)
+    # the nodes stand at rows 4..8 of q; the mask rows with them
+    b.q[4:9], b.mask[4:9] = b.q[0:5].copy(), b.mask[0:5].copy()
+    b.cu = (b.cu + 4).astype(np.int32)
+    ref = b.oracle()
+    out, lse = b.run()
+    assert (out[:4] == -77).all() and (out[9:] == -77).all() and (lse[:4] == -77).all() and (lse[9:] == -77).all()
+    b.check(ref, (out, lse))
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_a_cache_past_four_gigabytes(fmt):
+    # rows behind 4 GiB of others: 32-bit byte offsets would read elsewhere
+    b = Batch(fmt, 16, ctx=(200, 90), nodes=(3, 2), page=64, seed=22)
+    ref = b.oracle()
+    R = b.rows.shape[1]
+    far = (1 << 32) // (R * 64) + 5
+    small = b.rows
+    b.rows = np.zeros((1, R), dtype=np.uint8)
+    table = b.table.copy()
+    b.table = np.where(table >= 0, table + far, -1).astype(np.int32)
+    pages = b.pages
+    b.pages = pages + far
+    b.to_gpu()
+    kv = torch.zeros((b.pages * 64, R), dtype=torch.uint8, device="cuda")
+    kv[far * 64:] = torch.from_numpy(small).cuda()
+    b.d_kv = kv
+    b.call()
+    assert smla.read_error(b.desc, b.ws) == 0
+    b.check(ref, (b.out.double().cpu().numpy(), b.lse.double().cpu().numpy()))
+
+
+def test_one_row_tile_shared_by_every_sm():
+    # one node over a long context: its 16 rows are split over the whole GPU
+    b = Batch("fp8_tensor", 16, ctx=(20011,), nodes=(1,), seed=23, tree=False)
+    b.check()
+
+
+def test_queries_that_are_not_finite_stay_in_their_rows():
+    for fmt in FMT:
+        b = Batch(fmt, 16, ctx=(100,), nodes=(4,), seed=24)
+        clean = b.run()
+        b.q[1, 5, 7] = 0x7FC0        # NaN
+        b.q[2, 3, 550] = 0x7F80      # infinity
+        out, lse = b.run()
+        assert np.isnan(out[1, 5]).all() and not np.isfinite(lse[2, 3])
+        keep = np.ones((4, 16), dtype=bool)
+        keep[1, 5] = keep[2, 3] = False
+        assert np.array_equal(out[keep], clean[0][keep]) and np.array_equal(lse[keep], clean[1][keep])
+
+
+def test_random_batches():
+    g = np.random.default_rng(25)
+    for n in range(24):
+        B = int(g.integers(1, 9))
+        Batch(["bf16", "fp8_ds", "fp8_tensor"][n % 3], int(g.integers(1, 129)), ctx=[int(x) for x in g.integers(0, 400, B)],
+              nodes=[int(x) for x in g.integers(0, 12, B - 1)] + [1], page=1 << int(g.integers(0, 9)), tree=bool(g.integers(0, 2)),
+              sink=bool(g.integers(0, 2)), seed=100 + n, spare_rows=int(g.integers(0, 3))).check()
