@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kListThreads) cache_fork_plan_kernel(const Cac
                                                                        int32_t* fork_pages) {
   extern __shared__ uint32_t bits[];  // targets seen, targets seen twice, sources: a bit a request
   __shared__ int64_t s_warp[32];
+  pdl_trigger();
   const int tid = threadIdx.x, words = (c.B + 31) >> 5;
   for (int i = tid; i < 3 * words; i += kListThreads) bits[i] = 0;
   const int64_t count = clamp_count(*t.free_count, c.num_pages, c.err, tid == 0);
@@ -301,14 +302,17 @@ __global__ void __launch_bounds__(256) cache_fork_kernel(const CachePages c, con
                                                          const int32_t* __restrict__ dst_req,
                                                          const int32_t* fork_pages) {
   const int i = blockIdx.x, y = blockIdx.y, ny = gridDim.y, tid = threadIdx.x;
+  // the sources' lengths and table rows are not touched by the first step: they are read while it runs
+  const int32_t s = src_req[i], d = dst_req[i];
+  const bool in = s >= 0 && s < c.B;
+  const int64_t cap = int64_t(c.stride) << c.log2_page, len = in ? min(max(int64_t(t.lens[s]), int64_t(0)), cap) : 0;
+  const int full = static_cast<int>(len >> c.log2_page);
+  const int part = static_cast<int>(len & ((1 << c.log2_page) - 1));
+  const int32_t* from = t.page_table + int64_t(in ? s : 0) * c.stride;
+  const int32_t last = part ? from[full] : -1;
   pdl_wait();
   const int32_t got = __ldcg(fork_pages + i);
   if (got == -2) return;
-  const int32_t s = src_req[i], d = dst_req[i];
-  const int64_t len = t.lens[s];
-  const int full = static_cast<int>(len >> c.log2_page);
-  const int part = static_cast<int>(len & ((1 << c.log2_page) - 1));
-  const int32_t* from = t.page_table + int64_t(s) * c.stride;
   int32_t* to = t.page_table + int64_t(d) * c.stride;
   for (int k = y * 256 + tid; k < full; k += ny * 256) {
     const int32_t page = from[k];
@@ -319,7 +323,6 @@ __global__ void __launch_bounds__(256) cache_fork_kernel(const CachePages c, con
       flag(c.err, SMLA_DEVERR_PAGE);
   }
   if (part == 0) return;
-  const int32_t last = from[full];
   if (last < 0 || last >= c.num_pages) {
     if (y == 0 && tid == 0) flag(c.err, SMLA_DEVERR_PAGE);
     return;
@@ -371,7 +374,7 @@ __device__ __forceinline__ Resize resize_entry(const CachePages& c, const CacheT
 }
 
 constexpr int kPushCtas = 8;
-constexpr int kMarkWords = 2048;  // words of marks a CTA and round
+constexpr int kMarkWords = 1536;  // words of marks a CTA and round
 constexpr int64_t kResizeOneLaunch = 1 << 16;  // table entries
 
 // The pages of entry e beyond its new length leave the table and lose a holder; threads `at`, at + step, ...
@@ -415,6 +418,7 @@ __global__ void __launch_bounds__(256) cache_release_kernel(const CachePages c, 
                                                             const int32_t* __restrict__ req,
                                                             const int32_t* __restrict__ new_lens, int32_t n) {
   const int i = blockIdx.x;
+  pdl_trigger();
   const Resize e = resize_entry(c, t, req, new_lens, i);
   int twice = 0;
   for (int j = threadIdx.x; j < n; j += 256) twice |= j != i && req[j] == e.r;
@@ -426,27 +430,166 @@ __global__ void __launch_bounds__(256) cache_release_kernel(const CachePages c, 
   release_pages(c, t, e, blockIdx.y * 256 + threadIdx.x, int64_t(gridDim.y) * 256);
 }
 
-// Second step, one cluster of eight CTAs: the freed pages go to the end of the free list in
-// ascending order (each CTA counts its range of pages, the counts meet over distributed shared
-// memory), then the first CTA gives each growing request its place in the list, in the order of
-// the call. A request is refused (SMLA_DEVERR_PAGE) when fewer pages are free than it and those
-// before it ask for. work[2i]: the list position of the request's first page, -1 where it takes
-// none; work[2i+1]: its old page count. With ALL the cluster does the first and the third step as well: one
-// launch in place of three, where few entries are listed.
-template <bool ALL>
+// Lists the freed pages behind the `count` pages of the free list, in ascending order, and clears their marks;
+// returns how many. All CTAs of a cluster of kPushCtas call it, 1024 threads each; marks: 2 kMarkWords
+// words of shared memory. Their pushes are visible to one another after the next cluster barrier.
+__device__ __forceinline__ int64_t push_freed(const CachePages& c, const CacheTables& t, uint32_t* marks, int64_t* s_warp,
+                                              int64_t* s_sum, int rank, int64_t count) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  int64_t freed = 0;
+  // The marks of a range of pages, an eighth a CTA, a bit a page, go to shared memory in one pass; then each
+  // warp lists the pages of a word, so that its stores are next to one another.
+  int32_t* before = reinterpret_cast<int32_t*>(marks + kMarkWords);  // marks of the CTA's words before
+  constexpr int64_t kRound = 32 * int64_t(kMarkWords) * kPushCtas;  // pages a round: 393,216
+  int64_t at = count;
+  for (int64_t r0 = 0; r0 < c.num_pages; r0 += kRound) {
+    const int64_t r1 = min(c.num_pages, r0 + kRound), per = ((r1 - r0 + kPushCtas - 1) / kPushCtas + 31) & ~int64_t(31);
+    const int64_t a = min(r1, r0 + per * rank), b = min(r1, a + per);
+    const int nw = static_cast<int>((b - a + 31) >> 5);
+    constexpr int kAhead = 16, kW = kListThreads / 32;  // words a warp loads at once
+    for (int w = tid >> 5; w < nw; w += kAhead * kW) {
+      int32_t v[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {  // (past the end: the last page again, so that no load hangs on a branch)
+        const int64_t p = a + 32 * int64_t(w + x * kW) + lane;
+        v[x] = __ldcg(t.refs + min(p, b - 1));
+        if (p >= b) v[x] = 0;
+      }
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        const uint32_t m = __ballot_sync(0xffffffffu, (v[x] & kRefFreed) != 0);
+        if (lane == 0 && w + x * kW < nw) marks[w + x * kW] = m;
+      }
+    }
+    __syncthreads();
+    const int each = (nw + kListThreads - 1) / kListThreads, w0 = min(nw, tid * each), w1 = min(nw, w0 + each);
+    int64_t mine = 0;
+    for (int w = w0; w < w1; ++w) mine += __popc(marks[w]);
+    int64_t total;
+    int64_t upto = block_sum_scan(mine, s_warp, total) - mine;
+    for (int w = w0; w < w1; ++w) {
+      before[w] = static_cast<int32_t>(upto);
+      upto += __popc(marks[w]);
+    }
+    if (tid == 0) *s_sum = total;
+    __syncthreads();
+    tc::cluster_arrive();
+    tc::cluster_wait();
+    int64_t from = at, sum = 0;
+    for (int k = 0; k < kPushCtas; ++k) {
+      int64_t v;
+      asm volatile("ld.shared::cluster.b64 %0, [%1];"
+                   : "=l"(v)
+                   : "r"(tc::mapa(static_cast<uint32_t>(__cvta_generic_to_shared(s_sum)), k)));
+      if (k < rank) from += v;
+      sum += v;
+    }
+    at += sum;
+    freed += sum;
+    for (int w = tid >> 5; w < nw; w += kListThreads / 32) {
+      const uint32_t m = marks[w];
+      if (!((m >> lane) & 1)) continue;
+      const int64_t p = a + 32 * int64_t(w) + lane, pos = from + before[w] + __popc(m & ((1u << lane) - 1));
+      t.refs[p] = 0;
+      if (pos < c.num_pages)
+        t.free_list[pos] = static_cast<int32_t>(p);
+      else
+        flag(c.err, SMLA_DEVERR_PAGE);
+    }
+    if (r0 + kRound < c.num_pages) {  // the counts and the marks are rewritten
+      tc::cluster_arrive();
+      tc::cluster_wait();
+    }
+  }
+  return freed;
+}
+
+// A list of up to 1024 requests in one launch, one cluster of eight CTAs. Every CTA looks at the whole list, a
+// thread a request. The cluster's threads then form teams of 32 to 1024, about one a request, that take the
+// released pages out of the tables; the freed ones are listed; every CTA gives the growing requests their
+// places in the list, in the order of the call (a request is refused, SMLA_DEVERR_PAGE, when fewer pages
+// are free than it and those before it ask for); the teams take the pages.
+__global__ void __cluster_dims__(kPushCtas, 1, 1) __launch_bounds__(kListThreads)
+    cache_resize_kernel(const CachePages c, const CacheTables t, const int32_t* __restrict__ req,
+                        const int32_t* __restrict__ new_lens, int32_t n) {
+  extern __shared__ uint32_t bits[];  // requests listed, requests listed twice; marks
+  __shared__ int64_t s_warp[32], s_sum;
+  __shared__ int3 s_entry[kListThreads];  // (request or -1, old pages, new pages)
+  __shared__ int32_t s_pos[kListThreads];
+  const int tid = threadIdx.x, rank = blockIdx.x, words = (c.B + 31) >> 5;
+  Resize e;
+  e.ok = false;
+  e.r = -1;
+  e.old_pages = e.new_pages = 0;
+  if (tid < n) e = resize_entry(c, t, req, new_lens, tid);
+  const int64_t count = clamp_count(__ldcg(t.free_count), c.num_pages, c.err, rank == 0 && tid == 0);
+  for (int i = tid; i < 2 * words; i += kListThreads) bits[i] = 0;
+  __syncthreads();
+  const bool in = tid < n && e.r >= 0 && e.r < c.B;
+  if (in) {
+    const uint32_t m = 1u << (e.r & 31);
+    if (atomicOr(&bits[e.r >> 5], m) & m) atomicOr(&bits[words + (e.r >> 5)], m);
+  }
+  __syncthreads();
+  if (in && ((bits[words + (e.r >> 5)] >> (e.r & 31)) & 1)) e.ok = false;
+  if (tid < n && !e.ok && rank == 0) flag(c.err, SMLA_DEVERR_INDEX);
+  if (tid < n) s_entry[tid] = make_int3(e.ok ? e.r : -1, static_cast<int>(e.old_pages), static_cast<int>(e.new_pages));
+  const int64_t need = e.ok && e.new_pages > e.old_pages ? e.new_pages - e.old_pages : 0;
+  const int any = __syncthreads_or(e.ok && e.new_pages < e.old_pages);
+  int64_t total;
+  const int64_t upto = block_sum_scan(need, s_warp, total);
+  int team = kListThreads;
+  while (team > 32 && int64_t(team) * n > kPushCtas * kListThreads) team >>= 1;
+  const int teams = kPushCtas * kListThreads / team, at = tid & (team - 1);
+  const int first = rank * (kListThreads / team) + tid / team;
+  tc::cluster_arrive();  // the old lengths and the count have been read
+  int64_t freed = 0;
+  if (any) {
+    for (int i = first; i < n; i += teams) {
+      const int3 x = s_entry[i];
+      if (x.x < 0) continue;
+      Resize y;
+      y.ok = true;
+      y.r = x.x;
+      y.old_pages = x.y;
+      y.new_pages = x.z;
+      release_pages(c, t, y, at, team);
+    }
+    tc::cluster_wait();
+    tc::cluster_arrive();
+    tc::cluster_wait();  // all releases are visible
+    freed = push_freed(c, t, bits + 2 * words, s_warp, &s_sum, rank, count);
+    tc::cluster_arrive();
+    tc::cluster_wait();
+  }
+  const int64_t avail = min(c.num_pages, count + freed);
+  const bool fits = need == 0 || upto <= avail;
+  int64_t given;
+  block_sum_scan(fits ? need : 0, s_warp, given);
+  if (tid < n) s_pos[tid] = need != 0 && fits ? static_cast<int32_t>(avail - 1 - (upto - need)) : -1;
+  if (rank == 0 && !fits) flag(c.err, SMLA_DEVERR_PAGE);
+  __syncthreads();
+  for (int i = first; i < n; i += teams) {
+    const int64_t pos = s_pos[i];
+    if (pos >= 0) pop_pages(c, t, s_entry[i].x, pos, s_entry[i].y, s_entry[i].z, at, team);
+  }
+  if (!any) tc::cluster_wait();
+  if (rank == 0) {
+    if (e.ok && fits) t.lens[e.r] = new_lens[tid];
+    if (tid == 0) *t.free_count = static_cast<int32_t>(avail - given);
+  }
+}
+
+// Longer lists and tables, in three launches. The second step, one cluster of eight CTAs: the freed pages are
+// listed, then the first CTA gives the growing requests their places as above. work[2i]: the list position
+// of the request's first page, -1 where it takes none; work[2i+1]: its old page count.
 __global__ void __cluster_dims__(kPushCtas, 1, 1) __launch_bounds__(kListThreads)
     cache_push_kernel(const CachePages c, const CacheTables t, const int32_t* __restrict__ req,
                       const int32_t* __restrict__ new_lens, int32_t n, int32_t* work) {
-  extern __shared__ uint32_t bits[];  // requests listed, requests listed twice
-  __shared__ int64_t s_warp[32];
-  __shared__ int64_t s_mine;
+  extern __shared__ uint32_t bits[];  // requests listed, requests listed twice; marks
+  __shared__ int64_t s_warp[32], s_sum;
+  pdl_trigger();
   const int tid = threadIdx.x, rank = blockIdx.x, words = (c.B + 31) >> 5;
-  const int lane = tid & 31;
-  // ALL: the cluster's threads form teams of 32 to 1024, about one a request
-  int team = kListThreads;
-  while (team > 32 && int64_t(team) * n > kPushCtas * kListThreads) team >>= 1;
-  const int teams = kPushCtas * kListThreads / team, mine_at = tid & (team - 1);
-  const int first_i = rank * (kListThreads / team) + tid / team;
   for (int i = tid; i < 2 * words; i += kListThreads) bits[i] = 0;
   __syncthreads();
   for (int i = tid; i < n; i += kListThreads) {
@@ -457,151 +600,50 @@ __global__ void __cluster_dims__(kPushCtas, 1, 1) __launch_bounds__(kListThreads
     }
   }
   __syncthreads();
-  __shared__ int3 s_entry[kListThreads];  // (request or -1, old pages, new pages) of a list that fits
-  auto look = [&](int i) {
+  auto entry = [&](int i) {
     Resize e = resize_entry(c, t, req, new_lens, i);
     if (e.ok && (bits[words + (e.r >> 5)] >> (e.r & 31)) & 1) e.ok = false;
-    return e;
-  };
-  auto entry = [&](int i) {
-    if (n > kListThreads) return look(i);
-    const int3 x = s_entry[i];
-    Resize e;
-    e.ok = x.x >= 0;
-    e.r = x.x;
-    e.old_pages = x.y;
-    e.new_pages = x.z;
     return e;
   };
   // nothing is released when no listed request shrinks
   int any = 0;
   for (int i = tid; i < n; i += kListThreads) {
-    const Resize e = look(i);
+    const Resize e = entry(i);
     any |= e.ok && e.new_pages < e.old_pages;
-    if (n <= kListThreads) s_entry[i] = make_int3(e.ok ? e.r : -1, static_cast<int>(e.old_pages), static_cast<int>(e.new_pages));
   }
   any = __syncthreads_or(any);
-  if constexpr (!ALL) pdl_wait();  // the releases have been made
+  pdl_wait();  // the releases have been made
   const int64_t count = clamp_count(__ldcg(t.free_count), c.num_pages, c.err, rank == 0 && tid == 0);
-  if constexpr (ALL) {
-    for (int i = first_i; i < n; i += teams) {
-      const Resize e = entry(i);
-      if (e.ok)
-        release_pages(c, t, e, mine_at, team);
-      else if (mine_at == 0)
-        flag(c.err, SMLA_DEVERR_INDEX);
-    }
-    if (any) {
-      tc::cluster_arrive();
-      tc::cluster_wait();
-    }
-  }
-  int64_t freed = 0;
-  if (any) {
-    // The marks of a range of pages, an eighth a CTA, a bit a page, go to shared memory in one pass; then each
-    // warp lists the pages of a word, so that its stores are next to one another.
-    uint32_t* marks = bits + 2 * words;
-    int32_t* before = reinterpret_cast<int32_t*>(marks + kMarkWords);  // marks of the CTA's words before
-    constexpr int64_t kRound = 32 * int64_t(kMarkWords) * kPushCtas;  // pages a round: half a million
-    int64_t at = count;
-    for (int64_t r0 = 0; r0 < c.num_pages; r0 += kRound) {
-      const int64_t r1 = min(c.num_pages, r0 + kRound), per = ((r1 - r0 + kPushCtas - 1) / kPushCtas + 31) & ~int64_t(31);
-      const int64_t a = min(r1, r0 + per * rank), b = min(r1, a + per);
-      const int nw = static_cast<int>((b - a + 31) >> 5);
-      constexpr int kAhead = 16, kW = kListThreads / 32;  // words a warp loads at once
-      for (int w = tid >> 5; w < nw; w += kAhead * kW) {
-        int32_t v[kAhead];
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) {  // (past the end: the last page again, so that no load hangs on a branch)
-          const int64_t p = a + 32 * int64_t(w + x * kW) + lane;
-          v[x] = __ldcg(t.refs + min(p, b - 1));
-          if (p >= b) v[x] = 0;
-        }
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) {
-          const uint32_t m = __ballot_sync(0xffffffffu, (v[x] & kRefFreed) != 0);
-          if (lane == 0 && w + x * kW < nw) marks[w + x * kW] = m;
-        }
-      }
-      __syncthreads();
-      const int each = (nw + kListThreads - 1) / kListThreads, w0 = min(nw, tid * each), w1 = min(nw, w0 + each);
-      int64_t mine = 0;
-      for (int w = w0; w < w1; ++w) mine += __popc(marks[w]);
-      int64_t total;
-      int64_t upto = block_sum_scan(mine, s_warp, total) - mine;
-      for (int w = w0; w < w1; ++w) {
-        before[w] = static_cast<int32_t>(upto);
-        upto += __popc(marks[w]);
-      }
-      if (tid == 0) s_mine = total;
-      __syncthreads();
-      tc::cluster_arrive();
-      tc::cluster_wait();
-      int64_t from = at, sum = 0;
-      for (int k = 0; k < kPushCtas; ++k) {
-        int64_t v;
-        asm volatile("ld.shared::cluster.b64 %0, [%1];"
-                     : "=l"(v)
-                     : "r"(tc::mapa(static_cast<uint32_t>(__cvta_generic_to_shared(&s_mine)), k)));
-        if (k < rank) from += v;
-        sum += v;
-      }
-      at += sum;
-      freed += sum;
-      for (int w = tid >> 5; w < nw; w += kListThreads / 32) {
-        const uint32_t m = marks[w];
-        if (!((m >> lane) & 1)) continue;
-        const int64_t p = a + 32 * int64_t(w) + lane, pos = from + before[w] + __popc(m & ((1u << lane) - 1));
-        t.refs[p] = 0;
-        if (pos < c.num_pages)
-          t.free_list[pos] = static_cast<int32_t>(p);
-        else
-          flag(c.err, SMLA_DEVERR_PAGE);
-      }
-      if (r0 + kRound < c.num_pages) {  // the counts and the marks are rewritten
-        tc::cluster_arrive();
-        tc::cluster_wait();
-      }
-    }
-  }
-  // every CTA has read the others' counts and the old lengths, and its pushes are visible
+  const int64_t freed = any ? push_freed(c, t, bits + 2 * words, s_warp, &s_sum, rank, count) : 0;
+  // every CTA has read the count, and no other CTA's counts are read any more
   tc::cluster_arrive();
   tc::cluster_wait();
-  if (rank == 0) {
-    const int64_t avail = min(c.num_pages, count + freed);
-    int64_t asked = 0, given = 0;
-    for (int i0 = 0; i0 < n; i0 += kListThreads) {
-      const int i = i0 + tid;
-      Resize e;
-      e.ok = false;
-      e.r = 0;
-      e.old_pages = e.new_pages = 0;
-      if (i < n) e = entry(i);
-      const int64_t need = e.ok && e.new_pages > e.old_pages ? e.new_pages - e.old_pages : 0;
-      int64_t total;
-      const int64_t upto = asked + block_sum_scan(need, s_warp, total);
-      asked += total;
-      const bool fits = need == 0 || upto <= avail;
-      int64_t took;
-      block_sum_scan(fits ? need : 0, s_warp, took);
-      given += took;
-      if (i < n) {
-        work[2 * i] = need != 0 && fits ? static_cast<int32_t>(avail - 1 - (upto - need)) : -1;
-        work[2 * i + 1] = static_cast<int32_t>(e.old_pages);
-        if (!fits) flag(c.err, SMLA_DEVERR_PAGE);
-        if (e.ok && fits) t.lens[e.r] = new_lens[i];
-      }
-    }
-    if (tid == 0) *t.free_count = static_cast<int32_t>(avail - given);
-  }
-  if constexpr (ALL) {
-    tc::cluster_arrive();
-    tc::cluster_wait();
-    for (int i = first_i; i < n; i += teams) {
-      const int64_t pos = __ldcg(work + 2 * i);
-      if (pos >= 0) pop_pages(c, t, req[i], pos, __ldcg(work + 2 * i + 1), pages_of(new_lens[i], c.log2_page), mine_at, team);
+  if (rank != 0) return;
+  const int64_t avail = min(c.num_pages, count + freed);
+  int64_t asked = 0, given = 0;
+  for (int i0 = 0; i0 < n; i0 += kListThreads) {
+    const int i = i0 + tid;
+    Resize e;
+    e.ok = false;
+    e.r = 0;
+    e.old_pages = e.new_pages = 0;
+    if (i < n) e = entry(i);
+    const int64_t need = e.ok && e.new_pages > e.old_pages ? e.new_pages - e.old_pages : 0;
+    int64_t total;
+    const int64_t upto = asked + block_sum_scan(need, s_warp, total);
+    asked += total;
+    const bool fits = need == 0 || upto <= avail;
+    int64_t took;
+    block_sum_scan(fits ? need : 0, s_warp, took);
+    given += took;
+    if (i < n) {
+      work[2 * i] = need != 0 && fits ? static_cast<int32_t>(avail - 1 - (upto - need)) : -1;
+      work[2 * i + 1] = static_cast<int32_t>(e.old_pages);
+      if (!fits) flag(c.err, SMLA_DEVERR_PAGE);
+      if (e.ok && fits) t.lens[e.r] = new_lens[i];
     }
   }
+  if (tid == 0) *t.free_count = static_cast<int32_t>(avail - given);
 }
 
 // Third step: the growing requests' pages.
@@ -689,8 +731,8 @@ cudaError_t launch_cache_resize(const CachePages& c, const CacheTables& t, const
   // One launch while the cluster has few table entries to walk (the lengths are known on the device only: all
   // of the listed rows count). Two calls, one launch each against three: at 32,000 entries growing 20.6 us
   // against 24.2, freeing everything 26.7 against 26.7; at 128,000 20.6 against 28 and 57 against 45.
-  if (int64_t(n) * c.stride <= kResizeOneLaunch) {
-    cache_push_kernel<true><<<kPushCtas, kListThreads, smem, s>>>(c, t, req, new_lens, n, work);
+  if (n <= kListThreads && int64_t(n) * c.stride <= kResizeOneLaunch) {
+    cache_resize_kernel<<<kPushCtas, kListThreads, smem, s>>>(c, t, req, new_lens, n);
     return cudaGetLastError();
   }
   int64_t y = (int64_t(sms) * 4 + n - 1) / n;
@@ -698,7 +740,7 @@ cudaError_t launch_cache_resize(const CachePages& c, const CacheTables& t, const
   const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(y));
   cache_release_kernel<<<grid, 256, 0, s>>>(c, t, req, new_lens, n);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_behind(cache_push_kernel<false>, dim3(kPushCtas), kListThreads, smem, s, c, t, req, new_lens, n, work);
+  if (e == cudaSuccess) e = launch_behind(cache_push_kernel, dim3(kPushCtas), kListThreads, smem, s, c, t, req, new_lens, n, work);
   if (e == cudaSuccess) e = launch_behind(cache_pop_kernel, grid, 256, 0, s, c, t, req, new_lens, (const int32_t*)work);
   return e;
 }

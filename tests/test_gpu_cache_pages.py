@@ -323,3 +323,41 @@ def test_compact_many_layers_and_chunks(fmt):
     smla.cache_compact(p.desc, p.d_table, _dev([0] * 60), _dev(cu), _dev(flat), p.raw, None, p.err)
     C.compact(p.cache, fmt, 16, p.table, [0] * 60, cu, flat)
     p.check()
+
+
+def test_resize_in_one_launch_over_a_large_pool():
+    # few requests (one launch) over a pool of several rounds of marks, the widest page table rows count
+    pages, B, stride = 1_000_003, 65536, 12
+    g = np.random.default_rng(6)
+    ids = g.choice(B, 300, replace=False)
+    table, lens = np.full((B, stride), -1, dtype=np.int32), np.zeros(B, dtype=np.int32)
+    refs, free = np.zeros(pages, dtype=np.int32), g.permutation(pages).astype(np.int32)
+    count = pages
+    d = smla.make_cache_desc(0, 1, 4, pages, B, stride)
+    dv = [_dev(x) for x in (table, lens, refs, free, [count])]
+    err, work = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.empty(600, dtype=torch.int32, device="cuda")
+    for new in (g.integers(0, 49, 300), g.integers(0, 49, 300) * (g.random(300) < 0.5), np.full(300, 48), np.zeros(300, dtype=int)):
+        smla.cache_resize(d, *dv, _dev(ids), _dev(new), work, err)
+        e, count = C.resize(4, table, lens, refs, free, count, ids.tolist(), new.tolist())
+        assert e == 0 and err.item() == 0 and dv[4].item() == count
+        for a, b in zip(dv, (table, lens, refs, free)):
+            assert np.array_equal(a.cpu().numpy(), b)
+
+
+def test_forks_follow_resizes_without_a_pause():
+    # calls queued one behind another, none waited for: each sees what the one before did
+    for lens in ([100, 37, 0, 0, 0, 0], [2000, 1999, 0, 0, 0, 0]):
+        p = Pool("fp8_tensor", 2, 1 if lens[0] == 100 else 2, lens, 1100, 4096, seed=11)
+        work, got = torch.empty(12, dtype=torch.int32, device="cuda"), torch.empty(4, dtype=torch.int32, device="cuda")
+        a, b, z, grow = _dev([0, 1, 1, 0]), _dev([2, 3, 4, 5]), _dev([0, 0, 0, 0]), _dev([lens[0] + 3, lens[1] + 70])
+        two = _dev([0, 1])
+        for _ in range(30):
+            smla.cache_fork(p.desc, *p.tables(), a, b, got, p.raw, p.err)
+            smla.cache_resize(p.desc, *p.tables(), b, z, work, p.err)
+            smla.cache_resize(p.desc, *p.tables(), two, grow, work, p.err)
+            smla.cache_resize(p.desc, *p.tables(), two, _dev(lens[:2]), work, p.err)
+        for _ in range(30):
+            _, p.count, _ = C.fork(p.cache, p.fmt, p.P, p.table, p.lens, p.refs, p.free, p.count, [0, 1, 1, 0], [2, 3, 4, 5])
+            for ids, new in (([2, 3, 4, 5], [0] * 4), ([0, 1], grow.tolist()), ([0, 1], lens[:2])):
+                _, p.count = C.resize(p.P, p.table, p.lens, p.refs, p.free, p.count, ids, new)
+        p.check()
