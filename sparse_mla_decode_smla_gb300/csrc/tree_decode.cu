@@ -434,7 +434,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const int run = min(P, kTrSub);
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
-          if (gi >= 1 && !warp_wait(bar(R_RAW_EMPTY + q), (gi - 1) & 1)) { ok = false; break; }
+          if (gi >= 1 && !warp_wait(bar(R_RAW_EMPTY + q), (gi - 1) & 1)) {
+            for (int x = 0; x < q; ++x) warp_wait(bar(R_RAW_FULL + x), gi & 1);  // copies in flight
+            ok = false;
+            break;
+          }
           const uint32_t vq = uint32_t(v >> (kTrSub * q)) & 0xffffu;
           if (lane == 0) {
             if (vq)
@@ -750,14 +754,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(R_RAW_EMPTY + q));
-          // rows [16q, 16q + 16) of the buffer are free once that chunk of PV, two tiles ago, is done
-          if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * b + q), ((gi >> 1) - 1) & 1)) { ok = false; break; }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int slot = slot_of(j), ch = piece_of(j);
+          // 16 codes of job j -> f16
+          auto convert = [&](int j, uint32_t (&o)[8]) {
+            const int slot = slot_of(j);
             const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
             const __half2 s2 = __float2half2_rn(j < 4 ? sc.x : sc.y);
-            uint32_t o[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               e4m3x4_to_f16x4(wv[e], o[2 * e], o[2 * e + 1]);  // exact
@@ -783,7 +784,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 atomicOr(badw + (sl >> 5), 1u << (sl & 31));
               }
             }
-            const int rr = kTrN * hw + kTrSub * q + slot;
+          };
+          auto put = [&](int j, const uint32_t (&o)[8]) {
+            const int rr = kTrN * hw + kTrSub * q + slot_of(j), ch = piece_of(j);
             const uint32_t at = kt + ((ch >> 2) & 3) * kTrPairBlk + rr * 128;
             const int c0 = 2 * (ch & 3);
             const uint32_t sw = rr & 7;
@@ -791,6 +794,23 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                          "r"(o[3]) : "memory");
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((c0 + 1) ^ sw) << 4)), "r"(o[4]), "r"(o[5]),
                          "r"(o[6]), "r"(o[7]) : "memory");
+          };
+          // Some jobs are converted before the wait for the buffer, as many as measured best: fp8_ds, 16 requests x 64
+          // nodes x 128 heads, 3,880 us with 4 of 8, 3,990 with 1 and 4,023 with all (registers spill);
+          // per-tensor rows, without scales to apply, 693.8 us with 1 and 712.7 with 4.
+          constexpr int kTrEarly = tens ? 1 : 4;
+          uint32_t early[kTrEarly][8];
+#pragma unroll
+          for (int j = 0; j < kTrEarly; ++j) convert(j, early[j]);
+          // rows [16q, 16q + 16) of the buffer are free once that chunk of PV, two tiles ago, is done
+          if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * b + q), ((gi >> 1) - 1) & 1)) { ok = false; break; }
+#pragma unroll
+          for (int j = 0; j < kTrEarly; ++j) put(j, early[j]);
+#pragma unroll
+          for (int j = kTrEarly; j < 8; ++j) {
+            uint32_t o[8];
+            convert(j, o);
+            put(j, o);
           }
           fence_proxy_async_smem();
           __syncwarp();
