@@ -256,6 +256,38 @@ __device__ __forceinline__ float* tree_part(const TreeArgs& p, int64_t g, int sl
   return reinterpret_cast<float*>(p.ws + 256 + size_t(G) * sizeof(TreeJoin) + size_t(2 * g + slot) * kTrPart);
 }
 
+// Two fp32 values in one register pair: one instruction for both.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 f2_split(uint64_t d) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -754,9 +786,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(R_RAW_EMPTY + q));
-          // 16 codes of job j -> f16
-          auto convert = [&](int j, uint32_t (&o)[8]) {
-            const int slot = slot_of(j);
+          // 16 codes of job j -> f16; `whole`: every slot has a row and none is a node
+          auto convert = [&](int j, uint32_t (&o)[8], bool whole) {
             const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
             const __half2 s2 = __float2half2_rn(j < 4 ? sc.x : sc.y);
 #pragma unroll
@@ -769,49 +800,46 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 o[2 * e + 1] = *reinterpret_cast<uint32_t*>(&y);
               }
             }
-            if (vq != 0xffffu && !((vq >> slot) & 1)) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = 0u;
-            }
+            if (whole) return;
+            const int slot = slot_of(j);
+            bool clear = !((vq >> slot) & 1);
             if (nodes) {
               bool odd = false;
 #pragma unroll
               for (int e = 0; e < 8; ++e) odd |= (o[e] & 0x7c00u) == 0x7c00u || (o[e] & 0x7c000000u) == 0x7c000000u;
-              if (odd) {
+              if (odd) atomicOr(badw + ((kTrSub * q + slot) >> 5), 1u << ((kTrSub * q + slot) & 31));
+              clear |= odd;
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = 0u;
-                const int sl = kTrSub * q + slot;
-                atomicOr(badw + (sl >> 5), 1u << (sl & 31));
-              }
+            for (int e = 0; e < 8; ++e) o[e] = clear ? 0u : o[e];
+          };
+          // Job j's two 16-byte pieces c0, c0 + 1 (even c0) of row rr go to row rr's pieces c ^ (rr & 7): the
+          // address of job 0 with a bit flipped, and a constant added
+          const int rr0 = kTrN * hw + kTrSub * q + slot_of(0);
+          const uint32_t at0 = kt + uint32_t(rr0) * 128 + (((2 * (piece_of(0) & 3)) ^ (rr0 & 7)) << 4);
+          auto put = [&](int j, const uint32_t (&o)[8]) {
+            const uint32_t at = (tens ? at0 + 1024u * (j & 1) : at0 ^ (64u * (j & 1))) + uint32_t(j >> 1) * kTrPairBlk;
+            const uint32_t at1 = (tens ? (at0 ^ 16u) + 1024u * (j & 1) : at0 ^ (16u + 64u * (j & 1))) + uint32_t(j >> 1) * kTrPairBlk;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at1), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+          };
+          auto tile = [&](bool whole) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t o[8];
+              convert(j, o, whole);
+              put(j, o);
             }
           };
-          auto put = [&](int j, const uint32_t (&o)[8]) {
-            const int rr = kTrN * hw + kTrSub * q + slot_of(j), ch = piece_of(j);
-            const uint32_t at = kt + ((ch >> 2) & 3) * kTrPairBlk + rr * 128;
-            const int c0 = 2 * (ch & 3);
-            const uint32_t sw = rr & 7;
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((c0 ^ sw) << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]),
-                         "r"(o[3]) : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((c0 + 1) ^ sw) << 4)), "r"(o[4]), "r"(o[5]),
-                         "r"(o[6]), "r"(o[7]) : "memory");
-          };
-          // Some jobs are converted before the wait for the buffer, as many as measured best: fp8_ds, 16 requests x 64
-          // nodes x 128 heads, 3,880 us with 4 of 8, 3,990 with 1 and 4,023 with all (registers spill);
-          // per-tensor rows, without scales to apply, 693.8 us with 1 and 712.7 with 4.
-          constexpr int kTrEarly = tens ? 1 : 4;
-          uint32_t early[kTrEarly][8];
-#pragma unroll
-          for (int j = 0; j < kTrEarly; ++j) convert(j, early[j]);
-          // rows [16q, 16q + 16) of the buffer are free once that chunk of PV, two tiles ago, is done
+          // Rows [16q, 16q + 16) of the buffer are free once that chunk of PV, two tiles ago, is done. (Converting
+          // some jobs before this wait measured the same or slower: none of 8 695 us, one 695, four 712; 4
+          // requests x 64 nodes x 128 heads, 8k contexts, fp8_ds.)
           if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * b + q), ((gi >> 1) - 1) & 1)) { ok = false; break; }
-#pragma unroll
-          for (int j = 0; j < kTrEarly; ++j) put(j, early[j]);
-#pragma unroll
-          for (int j = kTrEarly; j < 8; ++j) {
-            uint32_t o[8];
-            convert(j, o);
-            put(j, o);
-          }
+          // a tile without the checks of its slots takes 8 % less time than with them
+          if (vq == 0xffffu && !nodes)
+            tile(true);
+          else
+            tile(false);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(R_K_FULL + b));
@@ -913,31 +941,40 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           break;
         }
         float s[16];
+        const uint64_t c2m2 = f2(c2m, c2m), c2p2 = f2(c2p, c2p);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint4 xv = lds128(xpart + ((k ^ xsw) << 4));
           const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[4 * k + e] = fmaf(__uint_as_float(own[4 * k + e]), c2m, __uint_as_float(xw[e]) * c2p);
+          for (int e = 0; e < 4; e += 2) {
+            const float2 r = f2_split(f2_fma(f2(__uint_as_float(own[4 * k + e]), __uint_as_float(own[4 * k + e + 1])), c2m2,
+                                             f2_mul(f2(__uint_as_float(xw[e]), __uint_as_float(xw[e + 1])), c2p2)));
+            s[4 * k + e] = r.x;
+            s[4 * k + e + 1] = r.y;
+          }
         }
         uint64_t vis = meta[gi % kTrMeta];
         uint32_t oddm = 0;
-        if (int64_t(seg.k0 + i + 1) * kTrN > seg.q.ctx) {  // a tile with nodes
-          vis &= tree_bits(p, seg.q, node, seg.k0 + i);
-          oddm = reinterpret_cast<volatile uint32_t*>(bad)[2 * (gi % kTrMeta) + half] >> (16 * sub);
-        }
-        const uint32_t msk = real ? uint32_t(vis >> (32 * half + 16 * sub)) & 0xffffu : 0u;
-        if (!__all_sync(0xffffffffu, msk == 0xffffu)) {
+        const bool nodes = int64_t(seg.k0 + i + 1) * kTrN > seg.q.ctx;  // a tile with nodes
+        if (nodes || vis != ~0ull) {
+          if (nodes) {
+            vis &= tree_bits(p, seg.q, node, seg.k0 + i);
+            oddm = reinterpret_cast<volatile uint32_t*>(bad)[2 * (gi % kTrMeta) + half] >> (16 * sub);
+          }
+          const uint32_t msk = uint32_t(vis >> (32 * half + 16 * sub)) & 0xffffu;
+          oddm &= msk;
 #pragma unroll
           for (int j = 0; j < 16; ++j) s[j] = ((msk >> j) & 1u) ? s[j] : -CUDART_INF_F;
         }
-        float mx4[4] = {s[0], s[1], s[2], s[3]};
+        float mx = max3(s[0], s[1], s[2]), my = max3(s[3], s[4], s[5]);
 #pragma unroll
-        for (int j = 4; j < 16; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], s[j]);
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        for (int j = 6; j < 14; j += 4) {
+          mx = max3(mx, s[j], s[j + 1]);
+          my = max3(my, s[j + 2], s[j + 3]);
+        }
+        mx = fmaxf(max3(mx, s[14], s[15]), my);
         asm volatile("st.shared.f32 [%0], %1;" ::"r"(mmine), "f"(mx) : "memory");
-        oddm &= msk;
         if (oddm) {  // a visible row with a non-finite value: NaN
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -951,15 +988,18 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           m = mn;
         }
         const float base = m == -CUDART_INF_F ? 0.f : m - kTrShift;
-        float sum2[2] = {0.f, 0.f};
+        const uint64_t nb2 = f2(-base, -base);
+        uint64_t sum[2] = {0, 0};
         uint32_t pw2[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float p0 = exp2_fast(s[2 * j] - base), p1 = exp2_fast(s[2 * j + 1] - base);
-          sum2[j & 1] += p0 + p1;
+          const float2 x = f2_split(f2_add(f2(s[2 * j], s[2 * j + 1]), nb2));
+          const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
+          sum[j & 1] = f2_add(sum[j & 1], f2(p0, p1));
           pw2[j] = BF ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
         }
-        l = l * a + (sum2[0] + sum2[1]);
+        const float2 sums = f2_split(f2_add(sum[0], sum[1]));
+        l = l * a + (sums.x + sums.y);
         // the P block and O are free once PV of the previous tile is complete
         if (i >= 1 && !warp_wait(bar(R_PV_DONE), (gi - 1) & 1)) good = false;
         tc::fence_after();
