@@ -448,7 +448,8 @@ smla_status smla_tree_workspace_size(const smla_tree_desc* d, size_t* bytes);
  *   lse          [T, H] fp32 or NULL: natural log of the denominator (-inf where it is empty).
  *   workspace    smla_tree_workspace_size(d) bytes, 256-byte aligned; calls that may overlap
  *                (two streams, two graphs) need one each.
- * The lengths are read on the device: a captured call serves any batch that fits `d`.
+ * The call runs on the current device, which must be the tensors'. The lengths are read on the
+ * device: a captured call serves any batch that fits `d`.
  *
  * Slots whose page entry lies outside [0, num_pages) are skipped like hidden ones
  * (SMLA_DEVERR_PAGE). A request whose context is negative, whose nodes are not within
@@ -475,7 +476,9 @@ smla_status smla_tree_decode(const smla_tree_desc* d, const void* q, const void*
  * Pages of the cache: copied, compacted, forked, and handed out and taken back. All calls work
  * on every layer of a model at once: the cache of layer l starts at kv_cache + l * layer_stride
  * and all layers share the page table. They move bytes and whole numbers only, and their
- * results do not depend on how the GPU schedules them.
+ * results do not depend on how the GPU schedules them. They run on the current device, which must
+ * be the tensors'; calls that touch the same tables or pages must be ordered by the caller (one
+ * stream, or events).
  * ---------------------------------------------------------------------------------------
  */
 enum {
@@ -501,6 +504,7 @@ typedef struct smla_cache_desc {
  * (int32 each). A pair with -1 on either side, or with both sides equal, is skipped; one outside
  * [0, num_pages) is skipped and sets SMLA_DEVERR_PAGE. The pages of dst_pages must be distinct
  * and must not stand in src_pages: their bytes are unspecified otherwise.
+ * n is at most num_pages.
  * Status of this and the calls below (before any launch): SMLA_ERR_UNSUPPORTED for another
  * kv_format, SMLA_ERR_SHAPE for a size or a reserved word, SMLA_ERR_NULL or SMLA_ERR_ALIGN for a
  * pointer (kv_cache 16-byte, the rest 4-byte aligned); n == 0 launches nothing. error_word:
