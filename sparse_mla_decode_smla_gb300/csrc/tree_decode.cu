@@ -26,10 +26,11 @@
 //  of weights through distributed shared memory makes a tile's way too long for the three key buffers that fit:
 //  5,613 us where this took 4,020 (16 requests x 64 nodes x 128 heads, contexts of 4k-16k, fp8_ds).
 //
-// Bound: the MMAs of a unit take 2,220 clocks (18 of N 128 at 66, 8 of N 256 at 128), and shared memory, at 128
-// bytes a clock, carries about 370 KB of it with the FP8 formats (2,900 clocks): raw rows in and out, f16 keys
-// in, operands, partial scores. It measures 3,050 clocks with fp8_ds (3,550 us for the batch above: 671
-// TFLOP/s of useful work), and 2,900 with BF16, whose two key buffers are refilled between PV and the next QK.
+// Bound: no unit is full. The MMAs of a unit take 2,220 clocks (18 of N 128 at 66, 8 of N 256 at 128), and shared
+// memory, at 128 bytes a clock, carries about 370 KB of it with the FP8 formats (2,900 clocks): raw rows in and
+// out, f16 keys in, operands, partial scores. It measures 4,060-4,400 clocks with fp8_ds (3,550 us for the batch
+// above: 671 TFLOP/s of useful work) and 4,240-4,630 with BF16: two key buffers and one score buffer tie the
+// tiles' ways (scores 1,250, read 800, softmax 2,000, values 1,050, the buffer's next keys 900-2,200) together.
 //
 // FP8 formats: rows come by bulk copies of up to 16 consecutive slots into a ring, eight warps turn them
 // into f16 key tiles (block scales applied, exact for powers of two). BF16: TMA boxes land in the key
