@@ -537,7 +537,7 @@ smla_status smla_cache_compact(const smla_cache_desc* d, const int32_t* page_tab
  * The tables of the two calls below:
  *   page_table [B, page_table_stride] int32: request r holds entries [0, ceil(lens[r] / P)).
  *   lens       [B] int32: slots of each request.
- *   refcounts  [num_pages] int32: requests that hold a page (below 2^30); 0 for a free page.
+ *   refcounts  [num_pages] int32: requests that hold a page (below 2^29); 0 for a free page.
  *   free_list  [num_pages] int32: its first free_count[0] entries are the free pages; pages are
  *              taken off its end and the entries they leave become -1.
  *   free_count [1] int32.
@@ -568,8 +568,8 @@ smla_status smla_cache_fork(const smla_cache_desc* d, int32_t* page_table, int32
  * A request outside [0, B), listed twice, or with a length outside [0, page_table_stride * P] is
  * left as it was (SMLA_DEVERR_INDEX). A request grows only if the pages that it and those before
  * it ask for are free; otherwise it stays as it was (SMLA_DEVERR_PAGE). A released entry that is
- * no page, or a page released more often than it was held, sets SMLA_DEVERR_PAGE and is not
- * listed. n is at most num_requests (SMLA_ERR_SHAPE). kv_format, num_layers and layer_stride
+ * no page, and a release of a page beyond its holders, leave the table, set SMLA_DEVERR_PAGE and
+ * do nothing else. n is at most num_requests (SMLA_ERR_SHAPE). kv_format, num_layers and layer_stride
  * are checked and not used.
  */
 smla_status smla_cache_resize(const smla_cache_desc* d, int32_t* page_table, int32_t* lens,

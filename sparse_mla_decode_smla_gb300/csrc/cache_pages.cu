@@ -387,10 +387,12 @@ __device__ __forceinline__ void release_pages(const CachePages& c, const CacheTa
       flag(c.err, SMLA_DEVERR_PAGE);
       continue;
     }
+    // Sums only, so that every order of several releases ends the same: a count of holders before is 1 .. 2^29 - 1,
+    // and what one release too many finds is 0, negative or near the mark.
     const int32_t had = atomicSub(t.refs + page, 1);
     if (had == 1) {
-      atomicOr(t.refs + page, kRefFreed);
-    } else if ((had & ~kRefFreed) <= 0) {  // more holders let go than there were
+      atomicAdd(t.refs + page, kRefFreed);
+    } else if (had <= 0 || had >= kRefFreed / 2) {  // more holders let go than there were
       atomicAdd(t.refs + page, 1);
       flag(c.err, SMLA_DEVERR_PAGE);
     }

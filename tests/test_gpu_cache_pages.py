@@ -361,3 +361,28 @@ def test_forks_follow_resizes_without_a_pause():
             for ids, new in (([2, 3, 4, 5], [0] * 4), ([0, 1], grow.tolist()), ([0, 1], lens[:2])):
                 _, p.count = C.resize(p.P, p.table, p.lens, p.refs, p.free, p.count, ids, new)
         p.check()
+
+
+@pytest.mark.parametrize("stride", [8, 2048])  # one launch; three
+def test_resize_releases_a_page_more_often_than_it_is_held(stride):
+    # 64 requests hold page 7 by their tables, three by its count, and two of them page 5, which is free by its count: three
+    # releases count, page 7 is listed once, and every order of the others ends the same
+    B, pages, P = 64, 16, 16
+    d = smla.make_cache_desc(1, 1, P, pages, B, stride)
+    for seed in range(20):
+        g = np.random.default_rng(seed)
+        table, lens = np.full((B, stride), -1, dtype=np.int32), np.full(B, P, dtype=np.int32)
+        table[:, 0] = 7
+        two = g.choice(B, 2, replace=False)
+        table[two, 1], lens[two] = 5, 2 * P
+        refs, free = np.zeros(pages, dtype=np.int32), np.full(pages, -1, dtype=np.int32)
+        refs[7] = 3
+        free[:14] = [p for p in range(16) if p not in (5, 7)]
+        dv = [_dev(x) for x in (table, lens, refs, free, [14])]
+        err, work = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.empty(2 * B, dtype=torch.int32, device="cuda")
+        ids = g.permutation(B)
+        smla.cache_resize(d, *dv, _dev(ids), _dev(np.zeros(B, dtype=int)), work, err)
+        e, count = C.resize(P, table, lens, refs, free, 14, ids.tolist(), [0] * B)
+        assert e == C.ERR_PAGE == err.item() and dv[4].item() == count == 15 and free[14] == 7
+        for a, b in zip(dv, (table, lens, refs, free)):
+            assert np.array_equal(a.cpu().numpy(), b)
