@@ -523,7 +523,8 @@ smla_status smla_cache_copy_pages(const smla_cache_desc* d, const int32_t* src_p
  *   offsets of a request are strictly ascending and not negative. new_lens [B] int32 or NULL
  *   receives starts[r] + count_r; it must not overlap the other arguments.
  * Rows of other slots stay as they were. A request whose start or count is negative or reaches
- * past n_keep is left out (SMLA_DEVERR_INDEX, its new_lens not written). A kept row that breaks
+ * past n_keep, or whose length would pass 2^31 - 1, is left out (SMLA_DEVERR_INDEX, its new_lens
+ * not written). A kept row that breaks
  * the ascending order, or has a slot outside the page table (SMLA_DEVERR_INDEX) or a page
  * outside the cache (SMLA_DEVERR_PAGE), is not moved. Pages that several requests hold must be
  * made private first (smla_cache_copy_pages): the rows of both would move.

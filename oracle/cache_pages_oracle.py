@@ -46,7 +46,7 @@ def compact(cache, fmt, P, table, starts, cu, keep, lens=None):
     err, num_pages, stride = 0, cache.shape[1], table.shape[1]
     for r in range(len(starts)):
         a, b, st = int(cu[r]), int(cu[r + 1]), int(starts[r])
-        if st < 0 or a < 0 or b < a or b > len(keep):
+        if st < 0 or a < 0 or b < a or b > len(keep) or st + b - a > 2**31 - 1:
             err |= ERR_INDEX
             continue
         for k in range(b - a):

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
   const int layer1 = min(c.L, layer0 + group);
   bool first = slice == 0 && layer0 == 0;  // this CTA reports errors (once: for its first layer)
   const int32_t start = __ldg(starts + r), a = __ldg(cu_keep + r), b = __ldg(cu_keep + r + 1);
-  if (start < 0 || a < 0 || b < a || b > n_keep) {
+  if (start < 0 || a < 0 || b < a || b > n_keep || int64_t(start) + (b - a) > 0x7fffffff) {
     if (first && tid == 0) flag(c.err, SMLA_DEVERR_INDEX);
     return;
   }

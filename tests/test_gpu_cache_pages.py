@@ -386,3 +386,16 @@ def test_resize_releases_a_page_more_often_than_it_is_held(stride):
         assert e == C.ERR_PAGE == err.item() and dv[4].item() == count == 15 and free[14] == 7
         for a, b in zip(dv, (table, lens, refs, free)):
             assert np.array_equal(a.cpu().numpy(), b)
+
+
+def test_compact_leaves_out_a_length_past_int32():
+    p = Pool("fp8_ds", 1, 4, [8, 8], 2, 6, seed=4)
+    new = torch.full((2,), -5, dtype=torch.int32, device="cuda")
+    for start, n in ((2**31 - 3, 3), (2**31 - 1, 1), (2**31 - 1, 0)):
+        starts, cu, keep = [start, 0], [0, n, n + 1], list(range(1, n + 1)) + [2]
+        want = np.full(2, -5)
+        smla.cache_compact(p.desc, p.d_table, _dev(starts), _dev(cu), _dev(keep), p.raw, new.fill_(-5), p.err)
+        e = C.compact(p.cache, "fp8_ds", 4, p.table, starts, cu, keep, want)
+        assert e == (C.ERR_INDEX if n else 0)
+        p.check(e)
+        assert new.tolist() == want.tolist() == ([-5, 1] if n else [2**31 - 1, 1])
