@@ -444,3 +444,25 @@ def test_random_batches():
         Batch(["bf16", "fp8_ds", "fp8_tensor"][n % 3], int(g.integers(1, 129)), ctx=[int(x) for x in g.integers(0, 400, B)],
               nodes=[int(x) for x in g.integers(0, 12, B - 1)] + [1], page=1 << int(g.integers(0, 9)), tree=bool(g.integers(0, 2)),
               sink=bool(g.integers(0, 2)), seed=100 + n, spare_rows=int(g.integers(0, 3))).check()
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_more_requests_than_threads(fmt):
+    # every thread of the schedule counts several requests; and the largest number of them, hardly any with nodes
+    g = np.random.default_rng(26)
+    nodes = [int(x) for x in g.integers(0, 3, 2500)]
+    Batch(fmt, 8, ctx=[int(x) for x in g.integers(0, 70, 2500)], nodes=nodes, page=16, seed=26, tree=fmt != "bf16").check()
+    nodes = np.zeros(65536, dtype=int)
+    nodes[g.choice(65536, 40, replace=False)] = 2
+    nodes[-1] = 1
+    Batch(fmt, 4, ctx=[int(x) for x in np.where(nodes > 0, 40, 0)], nodes=nodes.tolist(), page=32, seed=27).check()
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_key_tiles_of_context_beside_tiles_with_nodes(fmt):
+    # contexts that are whole key tiles, one slot less and one more: tiles without checks next to tiles with them, a missing
+    # page inside one of the former, and rows of a tile that belong to no node
+    b = Batch(fmt, 7, ctx=(128, 127, 129, 64, 192), nodes=(9, 3, 1, 64, 2), page=16, seed=28, sink=True)
+    b.check()
+    b.table[0, 3] = b.table[4, 11] = -1
+    b.check(err=smla.SMLA_DEVERR_PAGE)
