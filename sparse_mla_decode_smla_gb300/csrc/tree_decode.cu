@@ -658,16 +658,24 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const bool have = int64_t(seg.m) * kTrM + hl < int64_t(seg.q.n) * p.H;
         if (!warp_wait(bar(R_QRAW), nseg & 1)) { ok = false; break; }
         tc::fence_after();
-        uint4 w[16], wr[4];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        // 16-byte piece c of this thread's 16 latent and 4 RoPE ones. BF16: all loads in flight together. FP8 formats:
+        // read twice, for the largest value and for the conversion (held, they spill: 1-2 % of every case).
+        auto lat = [&](int c) {
           const uint32_t at = qlat + uint32_t(4 * half + 2 * part + (c >> 3)) * (kTrM * 128) + uint32_t(hl) * 128;
-          w[c] = have ? lds128(at + (((c & 7) ^ (hl & 7)) << 4)) : make_uint4(0, 0, 0, 0);
-        }
+          return have ? lds128(at + (((c & 7) ^ (hl & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+        };
+        auto rop = [&](int c) {
+          return have ? lds128(qrop + uint32_t(hl) * 128 + (((4 * half + c) ^ (hl & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+        };
+        uint4 w[16], wr[4];
+        if constexpr (BF) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          wr[c] = have && part == 1 ? lds128(qrop + uint32_t(hl) * 128 + (((4 * half + c) ^ (hl & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < 16; ++c) w[c] = lat(c);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) wr[c] = part == 1 ? rop(c) : make_uint4(0, 0, 0, 0);
+        }
         float qdown = 1.f;
+        int qe = 0;
         if constexpr (!BF) {
           uint32_t m4[4] = {0, 0, 0, 0};
           auto look = [&](const uint4 v) {
@@ -676,33 +684,31 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             m4[2] = bf16x2_max(m4[2], v.z & 0x7fff7fffu);
             m4[3] = bf16x2_max(m4[3], v.w & 0x7fff7fffu);
           };
+#pragma unroll 4
+          for (int c = 0; c < 16; ++c) look(lat(c));
+          if (part == 1) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) look(w[c]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) look(wr[c]);
+            for (int c = 0; c < 4; ++c) look(rop(c));
+          }
           const uint32_t mx = bf16x2_hmax_bits(bf16x2_max(bf16x2_max(m4[0], m4[1]), bf16x2_max(m4[2], m4[3])));
-          // the two warps of a row meet in the halves of its factor's word (and all of them have read q before
-          // one writes a key tile there)
+          // the two warps of a row meet in the halves of its factor's word
           const uint32_t at = sb + uint32_t(Y::qf) + uint32_t(row) * 4;
           asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 2 * part), "h"(uint16_t(mx)) : "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(R_QX));
           if (!warp_wait(bar(R_QX), 0)) { ok = false; break; }
           const uint32_t both = lds_u32(at);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(R_QX));
-          if (!warp_wait(bar(R_QX), 1)) { ok = false; break; }
-          const int qe = pow2_exponent_of_bf16(max(both & 0xffffu, both >> 16));
+          qe = pow2_exponent_of_bf16(max(both & 0xffffu, both >> 16));
           qdown = exp2_int(-qe);
-          if (part == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(exp2_int(qe)) : "memory");
         }
         auto cvt = [&](uint32_t x) -> uint32_t { return BF ? x : pack_f16x2(bf16_lo(x) * qdown, bf16_hi(x) * qdown); };
-#pragma unroll
+        constexpr int kUnroll = BF ? 4 : 1;
+#pragma unroll kUnroll
         for (int ch = 0; ch < 4; ++ch) {
           uint32_t wv[16];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 v = w[4 * ch + k];
+            const uint4 v = BF ? w[4 * ch + k] : lat(4 * ch + k);
             wv[4 * k] = cvt(v.x); wv[4 * k + 1] = cvt(v.y);
             wv[4 * k + 2] = cvt(v.z); wv[4 * k + 3] = cvt(v.w);
           }
@@ -710,13 +716,21 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         }
         tc::wait_st();
         if (part == 1) {
-#pragma unroll
+#pragma unroll kUnroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t dst = sb + uint32_t(Y::qr) + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(cvt(wr[c].x)), "r"(cvt(wr[c].y)),
-                         "r"(cvt(wr[c].z)), "r"(cvt(wr[c].w)) : "memory");
+            const uint4 v = BF ? wr[c] : rop(c);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(cvt(v.x)), "r"(cvt(v.y)), "r"(cvt(v.z)),
+                         "r"(cvt(v.w)) : "memory");
           }
           fence_proxy_async_smem();
+        }
+        if constexpr (!BF) {  // q and the halves of the factors have been read before either is written over
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(R_QX));
+          if (!warp_wait(bar(R_QX), 1)) { ok = false; break; }
+          if (part == 0)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + uint32_t(Y::qf) + uint32_t(row) * 4), "f"(exp2_int(qe)) : "memory");
         }
         // (the copies wait for R_Q in turn: the first tile's arrival says that they have seen the last one)
         if (BF && !warp_wait(bar(R_RAW_FULL + (gi & 1)), (gi >> 1) & 1)) { ok = false; break; }
