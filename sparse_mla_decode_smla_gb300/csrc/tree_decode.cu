@@ -28,8 +28,8 @@
 //
 // Bound: no unit is full. The MMAs of a unit take 2,220 clocks (18 of N 128 at 66, 8 of N 256 at 128), and shared
 // memory, at 128 bytes a clock, carries about 370 KB of it with the FP8 formats (2,900 clocks): raw rows in and
-// out, f16 keys in, operands, partial scores. It measures 4,060-4,400 clocks with fp8_ds (3,550 us for the batch
-// above: 671 TFLOP/s of useful work) and 4,240-4,630 with BF16: two key buffers and one score buffer tie the
+// out, f16 keys in, operands, partial scores. It measures 4,000-4,350 clocks with fp8_ds (3,495 us for the batch
+// above: 682 TFLOP/s of useful work) and 4,240-4,630 with BF16: two key buffers and one score buffer tie the
 // tiles' ways (scores 1,250, read 800, softmax 2,000, values 1,050, the buffer's next keys 900-2,200) together.
 //
 // FP8 formats: rows come by bulk copies of up to 16 consecutive slots into a ring, eight warps turn them
