@@ -19,12 +19,13 @@ __device__ __forceinline__ void flag(int32_t* err, int32_t bit) {
 // layer: U 16-byte loads a thread in flight, then U stores. Bound: HBM, 2 bytes moved for each
 // byte of a page.
 template <int U>
-__global__ void __launch_bounds__(256) cache_copy_kernel(const CachePages c, const int32_t* __restrict__ src,
-                                                         const int32_t* __restrict__ dst, int64_t n, int pieces) {
+__global__ void __launch_bounds__(256) cache_copy_kernel(const CachePages c, const int32_t* src,
+                                                         const int32_t* dst, int64_t n, int pieces) {
   const int64_t b = blockIdx.x;
   const int piece = static_cast<int>(b % pieces);
   const int64_t li = b / pieces, i = li % n, layer = li / n;
-  const int32_t s = __ldg(src + i), d = __ldg(dst + i);
+  pdl_wait();
+  const int32_t s = src[i], d = dst[i];
   if (s == -1 || d == -1 || s == d) return;
   if (s < 0 || d < 0 || s >= c.num_pages || d >= c.num_pages) {
     if (piece == 0 && layer == 0 && threadIdx.x == 0) flag(c.err, SMLA_DEVERR_PAGE);
@@ -59,8 +60,8 @@ constexpr int kCpRows = 512;  // rows of a chunk at most
 // 16 contexts of 4k-16k slots kept, 656-byte rows, 4 layers: 437 MB, 3.5 TB/s; the longest context's chunks,
 // one after the other, set the time).
 __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
-    const CachePages c, const int32_t* __restrict__ page_table, const int32_t* __restrict__ starts,
-    const int32_t* __restrict__ cu_keep, const int32_t* __restrict__ keep, int64_t n_keep, int32_t* new_lens, int columns,
+    const CachePages c, const int32_t* page_table, const int32_t* starts,
+    const int32_t* cu_keep, const int32_t* keep, int64_t n_keep, int32_t* new_lens, int columns,
     int slices, int group) {
   // byte offsets of the rows' old and new places, -1: not moved. Three chunks' worth: a chunk's are found
   // while others still store the one before the last.
@@ -71,7 +72,8 @@ __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
   const int r = static_cast<int>(rest % c.B), layer0 = static_cast<int>(rest / c.B) * group;
   const int layer1 = min(c.L, layer0 + group);
   bool first = slice == 0 && layer0 == 0;  // this CTA reports errors (once: for its first layer)
-  const int32_t start = __ldg(starts + r), a = __ldg(cu_keep + r), b = __ldg(cu_keep + r + 1);
+  pdl_wait();
+  const int32_t start = starts[r], a = cu_keep[r], b = cu_keep[r + 1];
   if (start < 0 || a < 0 || b < a || b > n_keep || int64_t(start) + (b - a) > 0x7fffffff) {
     if (first && tid == 0) flag(c.err, SMLA_DEVERR_INDEX);
     return;
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
       if (first) flag(c.err, SMLA_DEVERR_INDEX);
       return -1;
     }
-    const int32_t page = __ldg(pt + k);
+    const int32_t page = pt[k];
     if (page < 0 || page >= c.num_pages) {
       if (first) flag(c.err, SMLA_DEVERR_PAGE);
       return -1;
@@ -108,8 +110,8 @@ __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
   // the places of row i of chunk ch
   auto place = [&](int ch, int i) -> longlong2 {
     const int k = ch * rows + i;
-    const int32_t from = __ldg(keep + a + k);
-    const int32_t before = k ? __ldg(keep + a + k - 1) : -1;
+    const int32_t from = keep[a + k];
+    const int32_t before = k ? keep[a + k - 1] : -1;
     longlong2 x = make_longlong2(-1, -1);
     if (from < k || from <= before) {
       if (first) flag(c.err, SMLA_DEVERR_INDEX);
@@ -231,14 +233,15 @@ __device__ __forceinline__ int64_t clamp_count(int64_t v, int64_t num_pages, int
 // (SMLA_DEVERR_PAGE) when fewer free pages are left than it and those before it need.
 // fork_pages[i]: the page taken, -1 where none was needed, -2 for a refused fork.
 __global__ void __launch_bounds__(kListThreads) cache_fork_plan_kernel(const CachePages c, const CacheTables t,
-                                                                       const int32_t* __restrict__ src_req,
-                                                                       const int32_t* __restrict__ dst_req, int32_t n,
+                                                                       const int32_t* src_req,
+                                                                       const int32_t* dst_req, int32_t n,
                                                                        int32_t* fork_pages) {
   extern __shared__ uint32_t bits[];  // targets seen, targets seen twice, sources: a bit a request
   __shared__ int64_t s_warp[32];
-  pdl_trigger();
   const int tid = threadIdx.x, words = (c.B + 31) >> 5;
   for (int i = tid; i < 3 * words; i += kListThreads) bits[i] = 0;
+  pdl_wait();
+  pdl_trigger();  // (the copies read lengths and tables before they wait for this kernel)
   const int64_t count = clamp_count(*t.free_count, c.num_pages, c.err, tid == 0);
   __syncthreads();
   for (int i = tid; i < n; i += kListThreads) {
@@ -298,8 +301,8 @@ __global__ void __launch_bounds__(kListThreads) cache_fork_plan_kernel(const Cac
 // Second step: the full pages are shared, and the used rows of the last page are copied in every
 // layer. CTA (i, y) of a fork takes every y-th group of table entries and piece of rows.
 __global__ void __launch_bounds__(256) cache_fork_kernel(const CachePages c, const CacheTables t,
-                                                         const int32_t* __restrict__ src_req,
-                                                         const int32_t* __restrict__ dst_req,
+                                                         const int32_t* src_req,
+                                                         const int32_t* dst_req,
                                                          const int32_t* fork_pages) {
   const int i = blockIdx.x, y = blockIdx.y, ny = gridDim.y, tid = threadIdx.x;
   // the sources' lengths and table rows are not touched by the first step: they are read while it runs
@@ -417,10 +420,11 @@ __device__ __forceinline__ void pop_pages(const CachePages& c, const CacheTables
 
 // First step of a resize: the releases. CTA (i, y) takes every y-th group of request i's entries.
 __global__ void __launch_bounds__(256) cache_release_kernel(const CachePages c, const CacheTables t,
-                                                            const int32_t* __restrict__ req,
-                                                            const int32_t* __restrict__ new_lens, int32_t n) {
+                                                            const int32_t* req,
+                                                            const int32_t* new_lens, int32_t n) {
   const int i = blockIdx.x;
-  pdl_trigger();
+  pdl_wait();
+  pdl_trigger();  // (the next step reads the lists and lengths before it waits for this kernel)
   const Resize e = resize_entry(c, t, req, new_lens, i);
   int twice = 0;
   for (int j = threadIdx.x; j < n; j += 256) twice |= j != i && req[j] == e.r;
@@ -512,8 +516,8 @@ __device__ __forceinline__ int64_t push_freed(const CachePages& c, const CacheTa
 // places in the list, in the order of the call (a request is refused, SMLA_DEVERR_PAGE, when fewer pages
 // are free than it and those before it ask for); the teams take the pages.
 __global__ void __cluster_dims__(kPushCtas, 1, 1) __launch_bounds__(kListThreads)
-    cache_resize_kernel(const CachePages c, const CacheTables t, const int32_t* __restrict__ req,
-                        const int32_t* __restrict__ new_lens, int32_t n) {
+    cache_resize_kernel(const CachePages c, const CacheTables t, const int32_t* req,
+                        const int32_t* new_lens, int32_t n) {
   extern __shared__ uint32_t bits[];  // requests listed, requests listed twice; marks
   __shared__ int64_t s_warp[32], s_sum;
   __shared__ int3 s_entry[kListThreads];  // (request or -1, old pages, new pages)
@@ -523,6 +527,7 @@ __global__ void __cluster_dims__(kPushCtas, 1, 1) __launch_bounds__(kListThreads
   e.ok = false;
   e.r = -1;
   e.old_pages = e.new_pages = 0;
+  pdl_wait();
   if (tid < n) e = resize_entry(c, t, req, new_lens, tid);
   const int64_t count = clamp_count(__ldcg(t.free_count), c.num_pages, c.err, rank == 0 && tid == 0);
   for (int i = tid; i < 2 * words; i += kListThreads) bits[i] = 0;
@@ -586,8 +591,8 @@ __global__ void __cluster_dims__(kPushCtas, 1, 1) __launch_bounds__(kListThreads
 // listed, then the first CTA gives the growing requests their places as above. work[2i]: the list position
 // of the request's first page, -1 where it takes none; work[2i+1]: its old page count.
 __global__ void __cluster_dims__(kPushCtas, 1, 1) __launch_bounds__(kListThreads)
-    cache_push_kernel(const CachePages c, const CacheTables t, const int32_t* __restrict__ req,
-                      const int32_t* __restrict__ new_lens, int32_t n, int32_t* work) {
+    cache_push_kernel(const CachePages c, const CacheTables t, const int32_t* req,
+                      const int32_t* new_lens, int32_t n, int32_t* work) {
   extern __shared__ uint32_t bits[];  // requests listed, requests listed twice; marks
   __shared__ int64_t s_warp[32], s_sum;
   pdl_trigger();
@@ -650,8 +655,8 @@ __global__ void __cluster_dims__(kPushCtas, 1, 1) __launch_bounds__(kListThreads
 
 // Third step: the growing requests' pages.
 __global__ void __launch_bounds__(256) cache_pop_kernel(const CachePages c, const CacheTables t,
-                                                        const int32_t* __restrict__ req,
-                                                        const int32_t* __restrict__ new_lens, const int32_t* work) {
+                                                        const int32_t* req,
+                                                        const int32_t* new_lens, const int32_t* work) {
   const int i = blockIdx.x;
   pdl_wait();
   const int64_t pos = __ldcg(work + 2 * i);
@@ -660,7 +665,8 @@ __global__ void __launch_bounds__(256) cache_pop_kernel(const CachePages c, cons
             int64_t(gridDim.y) * 256);
 }
 
-// A kernel that starts up while the one before it on the stream ends, and waits for it itself (pdl_wait).
+// A kernel that starts up while the one before it on the stream ends, and waits for it itself (pdl_wait). What
+// another kernel may have written is read after that, by plain or L2 loads.
 template <typename... Params, typename... Args>
 cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
@@ -687,10 +693,8 @@ cudaError_t launch_cache_copy_pages(const CachePages& c, const int32_t* src, con
   const int64_t blocks = pieces * n * c.L;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (wide)
-    cache_copy_kernel<4><<<static_cast<unsigned>(blocks), 256, 0, s>>>(c, src, dst, n, static_cast<int>(pieces));
-  else
-    cache_copy_kernel<1><<<static_cast<unsigned>(blocks), 256, 0, s>>>(c, src, dst, n, static_cast<int>(pieces));
-  return cudaGetLastError();
+    return launch_behind(cache_copy_kernel<4>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, c, src, dst, n, static_cast<int>(pieces));
+  return launch_behind(cache_copy_kernel<1>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, c, src, dst, n, static_cast<int>(pieces));
 }
 
 cudaError_t launch_cache_compact(const CachePages& c, const int32_t* page_table, const int32_t* starts,
@@ -708,16 +712,14 @@ cudaError_t launch_cache_compact(const CachePages& c, const int32_t* page_table,
   if (group < 1) group = 1;
   const int64_t blocks = c.B * ((c.L + group - 1) / group) * slices;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  cache_compact_kernel<<<static_cast<unsigned>(blocks), kCpThreads, 0, s>>>(
-      c, page_table, starts, cu_keep, keep, n_keep, new_lens, columns, static_cast<int>(slices), static_cast<int>(group));
-  return cudaGetLastError();
+  return launch_behind(cache_compact_kernel, dim3(static_cast<unsigned>(blocks)), kCpThreads, 0, s, c, page_table, starts, cu_keep,
+                       keep, n_keep, new_lens, columns, static_cast<int>(slices), static_cast<int>(group));
 }
 
 cudaError_t launch_cache_fork(const CachePages& c, const CacheTables& t, const int32_t* src_req, const int32_t* dst_req,
                               int32_t n, int32_t* fork_pages, int sms, cudaStream_t s) {
   const size_t smem = size_t(3) * ((c.B + 31) / 32) * 4;
-  cache_fork_plan_kernel<<<1, kListThreads, smem, s>>>(c, t, src_req, dst_req, n, fork_pages);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(cache_fork_plan_kernel, dim3(1), kListThreads, smem, s, c, t, src_req, dst_req, n, fork_pages);
   if (e != cudaSuccess) return e;
   const int64_t pieces = ((c.page_bytes + 8191) / 8192) * c.L;
   int64_t y = (int64_t(sms) * 8 + n - 1) / n;
@@ -734,14 +736,12 @@ cudaError_t launch_cache_resize(const CachePages& c, const CacheTables& t, const
   // of the listed rows count). Two calls, one launch each against three: at 32,000 entries growing 20.6 us
   // against 24.2, freeing everything 26.7 against 26.7; at 128,000 20.6 against 28 and 57 against 45.
   if (n <= kListThreads && int64_t(n) * c.stride <= kResizeOneLaunch) {
-    cache_resize_kernel<<<kPushCtas, kListThreads, smem, s>>>(c, t, req, new_lens, n);
-    return cudaGetLastError();
+    return launch_behind(cache_resize_kernel, dim3(kPushCtas), kListThreads, smem, s, c, t, req, new_lens, n);
   }
   int64_t y = (int64_t(sms) * 4 + n - 1) / n;
   if (y > (c.stride + 255) / 256) y = (c.stride + 255) / 256;
   const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(y));
-  cache_release_kernel<<<grid, 256, 0, s>>>(c, t, req, new_lens, n);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_behind(cache_release_kernel, grid, 256, 0, s, c, t, req, new_lens, n);
   if (e == cudaSuccess) e = launch_behind(cache_push_kernel, dim3(kPushCtas), kListThreads, smem, s, c, t, req, new_lens, n, work);
   if (e == cudaSuccess) e = launch_behind(cache_pop_kernel, grid, 256, 0, s, c, t, req, new_lens, (const int32_t*)work);
   return e;

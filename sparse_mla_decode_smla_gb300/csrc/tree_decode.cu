@@ -128,7 +128,7 @@ struct TreeReq {
 
 // 1: a request with nodes, 0: without, -1: one that does not fit the description.
 __device__ __forceinline__ int tree_request(const TreeArgs& p, int r, TreeReq& q) {
-  const int a = __ldg(p.cu + r), b = __ldg(p.cu + r + 1), c = __ldg(p.ctx + r);
+  const int a = *(p.cu + r), b = *(p.cu + r + 1), c = *(p.ctx + r);
   q.ctx = c;
   q.cu0 = a;
   q.n = 0;
@@ -308,7 +308,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // Final factor of a row whose output is divided by its sum already, and its log-sum-exp, with the sink.
 __device__ __forceinline__ void apply_sink(const float* sink, int h, float& lse, float& f) {
   if (!sink) return;
-  const float sg = __ldg(sink + h);
+  const float sg = *(sink + h);
   if (sg == -CUDART_INF_F) return;
   const float both = fmaxf(lse, sg) + log1pf(expf(-fabsf(lse - sg)));
   f *= expf(lse - both);
@@ -327,8 +327,8 @@ __device__ __forceinline__ uint64_t tree_bits(const TreeArgs& p, const TreeReq& 
   const uint32_t* row = p.mask + int64_t(q.cu0 + i) * p.W;
   const int64_t from = base < 0 ? 0 : base;
   const int w = static_cast<int>(from >> 5), sh = static_cast<int>(from & 31);
-  const uint64_t w0 = w < p.W ? __ldg(row + w) : 0u, w1 = w + 1 < p.W ? __ldg(row + w + 1) : 0u,
-                 w2 = w + 2 < p.W ? __ldg(row + w + 2) : 0u;
+  const uint64_t w0 = w < p.W ? *(row + w) : 0u, w1 = w + 1 < p.W ? *(row + w + 1) : 0u,
+                 w2 = w + 2 < p.W ? *(row + w + 2) : 0u;
   uint64_t b = (w0 | (w1 << 32)) >> sh;
   if (sh) b |= w2 << (64 - sh);
   if (base < 0) b = (b << -base) | ((1ull << -base) - 1);  // -base in 1..63
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   // ------------------------------------------------------------------ set-up
   if (BF && tid == 0) prefetch_tensormap(&kv_map);
   if (tid == 32) prefetch_tensormap(&q_map);
-  const int64_t units = tree_units<kTrThreads>(p, blockIdx.x == 0 ? err : nullptr);
+  int64_t units;
   {
     uint4* zp = reinterpret_cast<uint4*>(sm + Y::P);  // the zero blocks beside P stay zero
     for (int k = tid; k < 3 * kTrPBlk / 16; k += kTrThreads) zp[k] = make_uint4(0, 0, 0, 0);
@@ -384,6 +384,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     }
     if (warp == kTrMmaWarp) tc::alloc(sb + uint32_t(Y::tmem), 512);
     tc::fence_before();
+    pdl_wait();  // what came before on the stream is complete; nothing of it is read before this line
+    units = tree_units<kTrThreads>(p, blockIdx.x == 0 ? err : nullptr);
     tree_schedule<kTrThreads>(p, units, blockIdx.x, gridDim.x, reinterpret_cast<TreeRun*>(sm + Y::run),
                               reinterpret_cast<int64_t*>(sm + Y::xs));
     tc::fence_after();
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     auto entries = [&](const TreeSeg& s, int k, int32_t& e0, int32_t& e1) {
       const int32_t* row = p.page_table + int64_t(s.r) * p.stride;
       const int64_t a = int64_t(k) * kTrN + lane, end = int64_t(s.q.ctx) + s.q.n;
-      e0 = a < end ? __ldg(row + (a >> p.log2_page)) : -2;  // -2: no such slot
+      e0 = a < end ? *(row + (a >> p.log2_page)) : -2;  // -2: no such slot
       e1 = a + 32 < end ? __ldg(row + ((a + 32) >> p.log2_page)) : -2;
     };
     const int P = 1 << p.log2_page;
@@ -1222,18 +1224,22 @@ cudaError_t launch_fmt(const TreeArgs& a, int sms, const CUtensorMap& map, const
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_release);
   }
-  tree_decode_kernel<FMT><<<sms, kTrThreads, Lay<FMT>::bytes, s>>>(a, map, qmap);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // both kernels start up while what is before them on the stream ends, and wait for it themselves (pdl_wait)
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(sms * kTrJoinCtas));
-  cfg.blockDim = dim3(kTrJoinThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(sms));
+  cfg.blockDim = dim3(kTrThreads);
+  cfg.dynamicSmemBytes = Lay<FMT>::bytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_decode_kernel<FMT>, a, map, qmap);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(sms * kTrJoinCtas));
+  cfg.blockDim = dim3(kTrJoinThreads);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, tree_join_kernel, a, sms);
 }
 

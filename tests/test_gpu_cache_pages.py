@@ -399,3 +399,65 @@ def test_compact_leaves_out_a_length_past_int32():
         assert e == (C.ERR_INDEX if n else 0)
         p.check(e)
         assert new.tolist() == want.tolist() == ([-5, 1] if n else [2**31 - 1, 1])
+
+
+@pytest.mark.parametrize("big", [False, True])  # one launch a resize; three
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_behind_writes_of_what_they_read(captured, big):
+    # tables, lists and rows change just before each call, by kernels and by copies, and nothing waits in between; the same
+    # captured into a graph
+    lens = [2000, 1999, 0, 0, 0, 0] if big else [100, 37, 0, 0, 0, 0]
+    p = Pool("fp8_ds", 2, 1 if big else 4, lens, 17000 if big else 70, 11000 if big else 100, seed=12)
+    h_src, h_dst, h_req, h_new, h_start, h_cu, h_keep = ([0, 1], [2, 3], [0, 1, 2, 3], [lens[0] + 9, 20, 0, 41], [30] + [0] * 5,
+                                                         [0] + [2] * 6, [1, 3])
+    a, b = [int(p.table[0, 0])], [int(p.free[0])]
+    first = [x.clone() for x in (p.raw, *p.tables())] + [_dev(x) for x in (h_src, h_dst, h_req, h_new, h_start, h_cu, h_keep, a, b)]
+    src, dst, req, new, start, cu, keep, d_a, d_b = (torch.empty_like(x) for x in first[6:])
+    state = [p.raw, *p.tables(), src, dst, req, new, start, cu, keep, d_a, d_b]
+    new_lens, got, work = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (6, 2, 8))
+
+    def write(i, names):
+        for k in names:
+            if i % 2:
+                state[k].copy_(first[k])
+            else:
+                torch.bitwise_or(first[k], 0, out=state[k])
+
+    def once(i):
+        write(i, [(k + i) % 15 for k in range(15)])
+        smla.cache_copy_pages(p.desc, d_a, d_b, p.raw, p.err)
+        write(i, [6, 7])
+        smla.cache_fork(p.desc, *p.tables(), src, dst, got, p.raw, p.err)
+        write(i, [8, 9])
+        smla.cache_resize(p.desc, *p.tables(), req, new, work, p.err)
+        write(i, [10, 11, 12])
+        smla.cache_compact(p.desc, p.d_table, start, cu, keep, p.raw, new_lens, p.err)
+
+    once(0)
+    C.copy_pages(p.cache, a, b)
+    e, p.count, pages = C.fork(p.cache, "fp8_ds", p.P, p.table, p.lens, p.refs, p.free, p.count, h_src, h_dst)
+    assert e == 0 and got.tolist() == pages
+    e, p.count = C.resize(p.P, p.table, p.lens, p.refs, p.free, p.count, h_req, h_new)
+    lens_after = np.zeros(6, dtype=int)
+    assert e == 0 and C.compact(p.cache, "fp8_ds", p.P, p.table, h_start, h_cu, h_keep, lens_after) == 0
+    p.check()
+    assert new_lens.tolist() == lens_after.tolist()
+    want = [x.clone() for x in (*state, got, new_lens)]
+    marks = []
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            once(0)
+            once(1)
+        for _ in range(4):
+            g.replay()
+            marks.append([x.clone() for x in (*state, got, new_lens)])
+    else:
+        for i in range(30):
+            once(i)
+            marks.append([x.clone() for x in (*state, got, new_lens)])
+    torch.cuda.synchronize()
+    assert p.err.item() == 0
+    for m in marks:
+        for x, y in zip(m, want):
+            assert torch.equal(x, y)

@@ -466,3 +466,84 @@ def test_key_tiles_of_context_beside_tiles_with_nodes(fmt):
     b.check()
     b.table[0, 3] = b.table[4, 11] = -1
     b.check(err=smla.SMLA_DEVERR_PAGE)
+
+
+def _pair(fmt):
+    """Two batches of one shape, and their results."""
+    a = Batch(fmt, 16, ctx=(700, 40, 3), nodes=(6, 2, 4), page=16, seed=30, sink=True)
+    b = Batch(fmt, 16, ctx=(40, 3, 700), nodes=(2, 4, 6), page=16, seed=31, sink=True)
+    refs = []
+    for x in (a, b):
+        out, lse = x.run()
+        x.check(None, (out, lse))
+        refs.append((x.out.clone(), x.lse.clone()))
+    assert a.desc.num_pages == b.desc.num_pages and a.desc.page_table_stride == b.desc.page_table_stride
+    return a, b, refs
+
+
+NAMES = ("d_q", "d_kv", "d_table", "d_ctx", "d_cu", "d_mask", "d_sink")
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_inputs_written_just_before_the_call(fmt):
+    # every input changes from call to call, by kernels and by copies, each of them last in turn; nothing waits in between
+    a, b, refs = _pair(fmt)
+    x = Batch(fmt, 16, ctx=(700, 40, 3), nodes=(6, 2, 4), page=16, seed=30, sink=True)
+    x.to_gpu()
+    got = []
+    for i in range(42):
+        src, order = (a, b)[i % 2], NAMES[i % 7:] + NAMES[:i % 7]
+        for name in order:
+            s, d = getattr(src, name), getattr(x, name)
+            if i % 3 == 0:
+                d.copy_(s)
+            elif d.is_floating_point():
+                torch.mul(s, 1, out=d)
+            else:
+                torch.bitwise_or(s, 0, out=d)
+        x.call()
+        got.append((x.out.clone(), x.lse.clone()))
+    assert smla.read_error(x.desc, x.ws) == 0
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, refs[i % 2][0]) and torch.equal(l, refs[i % 2][1]), i
+
+
+def test_graph_nodes_of_every_kind_before_the_call():
+    # a captured call as the first node, behind a copy, behind a memset, behind a kernel, and behind two streams
+    a, b, refs = _pair("fp8_ds")
+    x = Batch("fp8_ds", 16, ctx=(700, 40, 3), nodes=(6, 2, 4), page=16, seed=30, sink=True)
+    x.to_gpu()
+    x.call()
+    outs = [torch.zeros_like(x.out) for _ in range(5)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x.call()
+        outs[0].copy_(x.out)
+        for name in NAMES:
+            getattr(x, name).copy_(getattr(b, name))
+        x.call()
+        outs[1].copy_(x.out)
+        x.out.zero_()
+        x.call()
+        torch.mul(x.out, 1, out=outs[2])
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for name in NAMES[:3]:
+                getattr(x, name).copy_(getattr(a, name))
+        for name in NAMES[3:]:
+            getattr(x, name).copy_(getattr(a, name))
+        torch.cuda.current_stream().wait_stream(side)
+        x.call()
+        outs[3].copy_(x.out)
+        x.call()
+        outs[4].copy_(x.out)
+    for _ in range(3):
+        for o in outs:
+            o.fill_(-1)
+        g.replay()
+        torch.cuda.synchronize()
+        for o, r in zip(outs, (0, 1, 1, 0, 0)):
+            assert torch.equal(o, refs[r][0])
+    assert smla.read_error(x.desc, x.ws) == 0
