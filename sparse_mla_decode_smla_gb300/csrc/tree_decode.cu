@@ -61,9 +61,6 @@ constexpr int kTrSub = 16; // slots of a raw stage
 constexpr int kTrSoftWarps = 8, kTrFirstConv = kTrSoftWarps, kTrConvWarps = 8;
 constexpr int kTrProducer = kTrFirstConv + kTrConvWarps, kTrMmaWarp = kTrProducer + 1, kTrCheckWarp = kTrMmaWarp + 1;
 constexpr int kTrThreads = 32 * (kTrCheckWarp + 1);
-// key tiles a CTA takes at least: shorter runs would spend more on their start and on joining
-// parts than they save
-constexpr int kTrMinUnits = 2;
 constexpr float kTrRescale = 8.f;  // the running maximum moves when it grows by more (log2 units)
 // weights are 2^(s - m + 7): at most 2^15 between moves of the maximum, within f16, and exact to
 // 2^-11 down to 2^-21 of the largest one
@@ -182,8 +179,7 @@ __device__ void tree_schedule(const TreeArgs& p, int64_t sum, int g, int G, Tree
   const int64_t total = __shfl_sync(0xffffffffu, all, 31), upto = __shfl_sync(0xffffffffu, all, warp ? warp - 1 : 0);
   const int64_t before = warp ? upto : 0;
   v += before - sum;  // units before this thread's requests
-  int64_t per = (total + G - 1) / G;
-  if (per < kTrMinUnits) per = kTrMinUnits;
+  const int64_t per = (total + G - 1) / G;
   const int64_t u0 = min(total, g * per), u1 = min(total, u0 + per);
   if (tid == 0) {
     run->u0 = u0;
@@ -213,6 +209,33 @@ struct alignas(32) TreeJoin {
 };
 __device__ __forceinline__ TreeJoin* tree_join_of(const TreeArgs& p, int g) {
   return reinterpret_cast<TreeJoin*>(p.ws + 256) + g;
+}
+
+// The same for up to 32 requests by one warp, a lane a request, without barriers: 0.4 us less on the way to the first copy
+// than with the whole CTA (one request of 16 rows and 1000 slots: 15.9 us a call against 16.5).
+__device__ void tree_schedule_warp(const TreeArgs& p, int g, int G, int32_t* err, TreeRun* out) {
+  const int lane = threadIdx.x & 31;
+  TreeReq q;
+  q.units = 0;
+  if (lane < p.B && tree_request(p, lane, q) < 0 && err) atomicOr(err, SMLA_DEVERR_INDEX);
+  int64_t v = q.units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  const int64_t total = __shfl_sync(0xffffffffu, v, 31), before = v - q.units;
+  TreeRun run;
+  run.per = (total + G - 1) / G;
+  run.u0 = min(total, g * run.per);
+  run.u1 = min(total, run.u0 + run.per);
+  const uint32_t m0 = __ballot_sync(0xffffffffu, before <= run.u0 && run.u0 < v);
+  const uint32_t m1 = __ballot_sync(0xffffffffu, before < run.u1 && run.u1 <= v);
+  run.r0 = m0 ? __ffs(m0) - 1 : p.B;
+  run.r1 = m1 ? __ffs(m1) - 1 : p.B;
+  run.base0 = __shfl_sync(0xffffffffu, before, run.r0 & 31);
+  run.base1 = __shfl_sync(0xffffffffu, before, run.r1 & 31);
+  if (lane == 0) *out = run;
 }
 
 struct TreeSeg {  // key tiles [k0, k1) of row tile m of a request
@@ -359,7 +382,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   // ------------------------------------------------------------------ set-up
   if (BF && tid == 0) prefetch_tensormap(&kv_map);
   if (tid == 32) prefetch_tensormap(&q_map);
-  int64_t units;
   {
     uint4* zp = reinterpret_cast<uint4*>(sm + Y::P);  // the zero blocks beside P stay zero
     for (int k = tid; k < 3 * kTrPBlk / 16; k += kTrThreads) zp[k] = make_uint4(0, 0, 0, 0);
@@ -385,9 +407,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     if (warp == kTrMmaWarp) tc::alloc(sb + uint32_t(Y::tmem), 512);
     tc::fence_before();
     pdl_wait();  // what came before on the stream is complete; nothing of it is read before this line
-    units = tree_units<kTrThreads>(p, blockIdx.x == 0 ? err : nullptr);
-    tree_schedule<kTrThreads>(p, units, blockIdx.x, gridDim.x, reinterpret_cast<TreeRun*>(sm + Y::run),
-                              reinterpret_cast<int64_t*>(sm + Y::xs));
+    TreeRun* shared = reinterpret_cast<TreeRun*>(sm + Y::run);
+    if (p.B <= 32) {
+      if (warp == 0) tree_schedule_warp(p, blockIdx.x, gridDim.x, blockIdx.x == 0 ? err : nullptr, shared);
+      __syncthreads();
+    } else {
+      const int64_t units = tree_units<kTrThreads>(p, blockIdx.x == 0 ? err : nullptr);
+      tree_schedule<kTrThreads>(p, units, blockIdx.x, gridDim.x, shared, reinterpret_cast<int64_t*>(sm + Y::xs));
+    }
     tc::fence_after();
   }
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + Y::tmem);
