@@ -1150,28 +1150,38 @@ constexpr int kTrMaxRuns = 512;
 // a few dependent loads: spread over the whole GPU it takes a few microseconds, where one CTA a run,
 // two rows at a time, took 30-55 us.
 __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeArgs p, int G) {
-  __shared__ int s_list[kTrMaxRuns], s_count;
+  __shared__ int s_list[kTrMaxRuns], s_found[kTrJoinThreads / 32];
   __shared__ float s_w[4][kTrMaxRuns], s_lse[4], s_f[4];
   __shared__ float4 s_acc[128];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
-  if (warp == 0) {  // the runs that leave a row tile to join
-    int n = 0;
-    for (int x = 0; x < G; x += 32) {
-      const bool has = x + lane < G && tree_join_of(p, x + lane)->rows > 0;
-      const uint32_t b = __ballot_sync(0xffffffffu, has);
-      if (has) s_list[n + __popc(b & ((1u << lane) - 1))] = x + lane;
-      n += __popc(b);
+  // the runs that leave a row tile to join, in order; every thread looks at one (a warp at all of them took a
+  // microsecond more)
+  int count = 0;
+  for (int x0 = 0; x0 < G; x0 += kTrJoinThreads) {
+    const bool has = x0 + tid < G && tree_join_of(p, x0 + tid)->rows > 0;
+    const uint32_t b = __ballot_sync(0xffffffffu, has);
+    if (lane == 0) s_found[warp] = __popc(b);
+    __syncthreads();
+    for (int w = 0; w < kTrJoinThreads / 32; ++w) {
+      if (w == warp && has) s_list[count + __popc(b & ((1u << lane) - 1))] = x0 + tid;
+      count += s_found[w];
     }
-    if (lane == 0) s_count = n;
+    __syncthreads();
   }
-  __syncthreads();
-  const int items = 64 * s_count;
+  const int items = 64 * count;
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const int g = s_list[item >> 6];
     const TreeJoin jn = *tree_join_of(p, g);
     const int row0 = 4 * ((item >> 2) & 15);
     if (row0 >= jn.rows) continue;
+    const int r = tid & 3, quad = 32 * (item & 3) + ((tid >> 2) & 31), odd = tid >> 7;
+    auto piece = [&](int i) { return reinterpret_cast<const float4*>(tree_part(p, g + i, i ? 0 : jn.slot, G))[quad * kTrM + row0 + r]; };
+    constexpr int kAhead = 4;  // loads that pass behind the weights
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (odd + 2 * k < jn.parts) ahead[k] = piece(odd + 2 * k);
     if (warp < 4) {  // the weights of row row0 + warp
       const int row = row0 + warp;
       float M = -CUDART_INF_F, W = 0.f;
@@ -1199,17 +1209,19 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeArg
       }
     }
     __syncthreads();
-    const int r = tid & 3, quad = 32 * (item & 3) + ((tid >> 2) & 31), odd = tid >> 7;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = odd; i < jn.parts; i += 2) {
-      const float4 o = reinterpret_cast<const float4*>(tree_part(p, g + i, i ? 0 : jn.slot, G))[quad * kTrM + row0 + r];
+    auto add = [&](int i, const float4& o) {
       const float w = s_w[r][i];
       a.x = fmaf(w, o.x, a.x);
       a.y = fmaf(w, o.y, a.y);
       a.z = fmaf(w, o.z, a.z);
       a.w = fmaf(w, o.w, a.w);
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (odd + 2 * k < jn.parts) add(odd + 2 * k, ahead[k]);
+#pragma unroll 8
+    for (int i = odd + 2 * kAhead; i < jn.parts; i += 2) add(i, piece(i));
     if (odd) s_acc[tid & 127] = a;
     __syncthreads();
     if (!odd && row0 + r < jn.rows) {
