@@ -33,8 +33,8 @@
 // tiles' ways (scores 1,250, read 800, softmax 2,000, values 1,050, the buffer's next keys 900-2,200) together.
 //
 // FP8 formats: rows come by bulk copies of up to 16 consecutive slots into a ring, eight warps turn them
-// into f16 key tiles (block scales applied, exact for powers of two). BF16: TMA boxes land in the key
-// tile itself, and the same warps only look after tiles with hidden or unused slots.
+// into f16 key tiles (block scales applied, exact for powers of two). BF16: the same warps copy rows into the
+// key tile by asynchronous 16-byte copies.
 //
 // What is hidden never counts: slots without a page or past the last node become zero rows with weight
 // zero, and in tiles that hold nodes a row with a non-finite latent value is zeroed and marked, so that
@@ -84,8 +84,7 @@ template <int FMT>
 struct Lay {
   static constexpr bool bf16 = FMT == SMLA_KV_BF16, tens = FMT == SMLA_KV_FP8_TENSOR;
   static constexpr int row = bf16 ? kBf16RowBytes : tens ? kFp8TensorRowBytes : kFp8RowBytes;
-  // BF16: the 64 RoPE dims as loaded, and the same slots from dim 32 on (the high half), a buffer
-  static constexpr int rope_blk = bf16 ? 2 * kTrN * 128 : 2 * kTrN * 64;
+  static constexpr int rope_blk = 2 * kTrN * 64;
   static constexpr int rope_bufs = bf16 ? 2 : 1;
   static constexpr int raw_stage = kTrSub * row;
   static constexpr size_t K = 0;
@@ -96,7 +95,7 @@ struct Lay {
   static constexpr size_t xs = raw + (bf16 ? 0 : 4 * size_t(raw_stage));
   static constexpr size_t xm = xs + 256 * 64;   // xs: 16 partial scores a softmax thread
   static constexpr size_t qf = xm + 256 * 4;    // xm: a maximum a softmax thread
-  static constexpr size_t meta = qf + 128 * 4;
+  static constexpr size_t meta = qf + 128 * 4;  // qf: factors of q; BF16: rows of the key tiles [buffer][slot]
   static constexpr size_t bad = meta + kTrMeta * 8;
   static constexpr size_t run = bad + kTrMeta * 8;
   static constexpr size_t tmem = run + sizeof(TreeRun);
@@ -107,8 +106,8 @@ struct Lay {
                 "swizzle atoms and copies");
 };
 enum {
-  R_RAW_FULL = 0,                  // [stage]; BF16: [buffer]
-  R_RAW_EMPTY = R_RAW_FULL + 4,    // [stage]
+  R_RAW_FULL = 0,                  // [stage]; BF16: the rows of the tile in [buffer] are known
+  R_RAW_EMPTY = R_RAW_FULL + 4,    // [stage]; BF16: and have been taken
   R_K_FULL = R_RAW_EMPTY + 4,      // [buffer]
   R_K_FREE = R_K_FULL + 2,         // [buffer][16-slot chunk]
   R_ROPE_FULL = R_K_FREE + 8,
@@ -367,8 +366,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
 
 template <int FMT>
 __global__ void __launch_bounds__(kTrThreads, 1)
-    tree_decode_kernel(const TreeArgs p, const __grid_constant__ CUtensorMap kv_map,
-                       const __grid_constant__ CUtensorMap q_map) {
+    tree_decode_kernel(const TreeArgs p, const __grid_constant__ CUtensorMap q_map) {
   using Y = Lay<FMT>;
   constexpr bool BF = Y::bf16, tens = Y::tens;
   extern __shared__ __align__(1024) uint8_t sm[];  // all of it: the swizzle atoms need its start
@@ -380,7 +378,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   uint32_t* bad = reinterpret_cast<uint32_t*>(sm + Y::bad);                     // non-finite rows, per tile
 
   // ------------------------------------------------------------------ set-up
-  if (BF && tid == 0) prefetch_tensormap(&kv_map);
   if (tid == 32) prefetch_tensormap(&q_map);
   {
     uint4* zp = reinterpret_cast<uint4*>(sm + Y::P);  // the zero blocks beside P stay zero
@@ -389,7 +386,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     if (tid == 0) {
       for (int s = 0; s < 4; ++s) {
         mbar_init(bar(R_RAW_FULL + s), 1);
-        mbar_init(bar(R_RAW_EMPTY + s), 2 + (FMT == SMLA_KV_FP8_DS ? 1 : 0));
+        mbar_init(bar(R_RAW_EMPTY + s), BF ? kTrConvWarps : 2 + (FMT == SMLA_KV_FP8_DS ? 1 : 0));
       }
       for (int b = 0; b < 2; ++b) mbar_init(bar(R_K_FULL + b), kTrConvWarps);
       for (int c = 0; c < 8; ++c) mbar_init(bar(R_K_FREE + c), 1);
@@ -452,16 +449,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     bool more = walk.next(p, seg);
     int k = seg.k0;
     int32_t e0 = -2, e1 = -2;
-    int nseg = 0, qseg = -1;  // this row tile's number; that of the tile before if it began one
     if (more) entries(seg, k, e0, e1);
     while (more && ok) {
       TreeSeg ns = seg;
-      int nk = k + 1, nnext = nseg;
+      int nk = k + 1;
       bool nm = true;
       if (nk == seg.k1) {
         nm = walk.next(p, ns);
         nk = ns.k0;
-        ++nnext;
       }
       int32_t n0 = -2, n1 = -2;
       if (nm) entries(ns, nk, n0, n1);  // a tile ahead: their latency is hidden
@@ -474,34 +469,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       }
       if constexpr (BF) {
         const int b = gi & 1;
-        if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * b + 3), ((gi >> 1) - 1) & 1)) { ok = false; break; }
-        // the tile before began a row tile: its q passes through this buffer
-        if (qseg >= 0 && !warp_wait(bar(R_Q), qseg & 1)) { ok = false; break; }
-        qseg = k == seg.k0 ? nseg : -1;
-        const int rb = min(P, kTrN), runs = kTrN / rb;
-        // a run of slots of one page is loaded whole when its first slot counts; what lies past the
-        // last slot is cleared later
-        int nvalid = 0;
-        for (int x = 0; x < runs; ++x) nvalid += (v >> (x * rb)) & 1;
-        if (lane == 0) {
-          if (nvalid)
-            mbar_arrive_expect_tx(bar(R_RAW_FULL + b), uint32_t(nvalid) * 10u * rb * 128u);
-          else
-            mbar_arrive(bar(R_RAW_FULL + b));
-        }
+        if (gi >= 2 && !warp_wait(bar(R_RAW_EMPTY + b), ((gi >> 1) - 1) & 1)) { ok = false; break; }
+        int32_t* rows = reinterpret_cast<int32_t*>(sm + Y::qf) + 64 * b;
+        const int64_t s0 = int64_t(k) * kTrN + lane;
+        rows[lane] = ok0 ? (e0 << p.log2_page) + static_cast<int32_t>(s0 & (P - 1)) : -1;
+        rows[lane + 32] = ok1 ? (e1 << p.log2_page) + static_cast<int32_t>((s0 + 32) & (P - 1)) : -1;
         __syncwarp();
-        const uint32_t kt = sb + uint32_t(Y::K) + uint32_t(b * kTrKLat);
-        const uint32_t rp = sb + uint32_t(Y::rope) + uint32_t(b * Y::rope_blk);
-        for (int x0 = 0; x0 < runs * 10; x0 += 32) {
-          const int x = x0 + lane, run = min(x / 10, runs - 1), bx = x - 10 * (x / 10), j = run * rb;
-          const int32_t ea = __shfl_sync(0xffffffffu, e0, j & 31), eb = __shfl_sync(0xffffffffu, e1, j & 31);
-          if (x < runs * 10 && ((v >> j) & 1)) {
-            const int64_t y = (int64_t(j < 32 ? ea : eb) << p.log2_page) + ((int64_t(k) * kTrN + j) & (P - 1));
-            const uint32_t dst = bx < 8 ? kt + (bx & 3) * kTrPairBlk + (bx >> 2) * (kTrN * 128) : rp + (bx - 8) * (kTrN * 128);
-            tma_load_2d(dst + j * 128, &kv_map, bx < 8 ? 64 * bx : kLatent + 32 * (bx - 8), static_cast<int32_t>(y),
-                        bar(R_RAW_FULL + b));
-          }
-        }
+        if (lane == 0) mbar_arrive(bar(R_RAW_FULL + b));
       } else {
         const int run = min(P, kTrSub);
 #pragma unroll 1
@@ -537,14 +511,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       e0 = n0;
       e1 = n1;
       more = nm;
-      nseg = nnext;
       ++gi;
     }
     // no copy may land after the CTA has left
-    if constexpr (BF) {
-      for (int x = max(0, gi - 2); x < gi; ++x)
-        if (!mbar_wait(bar(R_RAW_FULL + (x & 1)), (x >> 1) & 1)) break;
-    } else if (gi > 0) {
+    if (!BF && gi > 0) {
       for (int q = 0; q < 4; ++q)
         if (!mbar_wait(bar(R_RAW_FULL + q), (gi - 1) & 1)) break;
     }
@@ -577,7 +547,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             tc::mma_ss(d, tc::sdesc_sw64(qr + 32 * j, 16, 512),
-                       BF ? tc::sdesc_sw128(rope + 32 * j, 16, 1024) : tc::sdesc_sw64(rope + 32 * j, 16, 512), kIdQK, 1);
+                       tc::sdesc_sw64(rope + 32 * j, 16, 512), kIdQK, 1);
           tc::commit(bar(R_S_FULL));
         };
         auto pv = [&](int g) {
@@ -666,16 +636,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       // its factors of q): dims [256 half + 128 part, + 128) of
       // a row by this thread, and its 32 RoPE dims by part 1. FP8 formats: f16, scaled by a power of two
       // that brings the row's largest value into [1, 2); the factor goes back into the scores.
-      // q arrives as nine boxes of 64 rows x 64 dims in a key-tile buffer that is free: this warp group's own
-      // next one, or (BF16, where the copies write the key tiles) the one after, whose copies wait for R_Q.
-      // A lane per row from global memory instead took 5-7 us.
+      // q arrives as nine boxes of 64 rows x 64 dims in the key-tile buffer that this warp group fills next. A lane
+      // per row from global memory instead took 5-7 us.
       // PV of the tile that last used the buffer comes first; its wait also tells S_FREE's last phase from the
       // one before (a barrier's parity tells no more).
-      const int qb = BF ? (gi + 1) & 1 : gi & 1;
-      if (BF ? gi >= 1 : gi >= 2) {
-        const int last = BF ? gi - 1 : gi - 2;
-        if (!warp_wait(bar(R_K_FREE + 4 * qb + 3), (last >> 1) & 1)) { ok = false; break; }
-      }
+      const int qb = gi & 1;
+      if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * qb + 3), ((gi - 2) >> 1) & 1)) { ok = false; break; }
       if (gi > 0 && !warp_wait(bar(R_S_FREE), (gi - 1) & 1)) { ok = false; break; }
       const uint32_t qlat = sb + uint32_t(Y::K) + uint32_t(qb * kTrKLat);
       const uint32_t qrop = sb + uint32_t(Y::rope) + uint32_t(BF ? qb * Y::rope_blk : 0);
@@ -756,15 +722,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        if constexpr (!BF) {  // q and the halves of the factors have been read before either is written over
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(R_QX));
-          if (!warp_wait(bar(R_QX), 1)) { ok = false; break; }
+        // q (and the halves of the factors) has been read before it is written over
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(R_QX));
+        if (!warp_wait(bar(R_QX), BF ? nseg & 1 : 1)) { ok = false; break; }
+        if constexpr (!BF) {
           if (part == 0)
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + uint32_t(Y::qf) + uint32_t(row) * 4), "f"(exp2_int(qe)) : "memory");
         }
-        // (the copies wait for R_Q in turn: the first tile's arrival says that they have seen the last one)
-        if (BF && !warp_wait(bar(R_RAW_FULL + (gi & 1)), (gi >> 1) & 1)) { ok = false; break; }
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(R_Q));
@@ -776,34 +741,48 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const bool nodes = int64_t(k + 1) * kTrN > seg.q.ctx;  // the tile holds drafted nodes
         uint32_t* badw = bad + 2 * (gi % kTrMeta);
         if constexpr (BF) {
+          // Warp dw loads slots [8 dw, 8 dw + 8), four of them (8 lanes of 16 bytes each) and 64 dims at a time, as soon
+          // as PV has freed them; what has no row becomes zero. Copies by the threads keep pace whatever the page size,
+          // where TMA boxes cost 65 clocks each, ten for every run of slots in one page: pages of 1, 8, 64 slots, 4
+          // requests x 64 nodes x 128 heads, 4k contexts, 295 us each against 2,737, 475 and 302.
           if (!warp_wait(bar(R_RAW_FULL + b), (gi >> 1) & 1)) { ok = false; break; }
-          const uint64_t v = meta[gi % kTrMeta];
-          if (v != ~0ull || nodes) {
-            const int sl = dtid & 63, grp = dtid >> 6;  // a slot's pieces [16 grp, 16 grp + 16) of 64
-            const bool has = (v >> sl) & 1;
-            bool odd = false;
-            for (int pc = 16 * grp; pc < 16 * grp + 16; ++pc) {
-              const int bx = pc >> 3;
-              const uint32_t at = kt + (bx & 3) * kTrPairBlk + (bx >> 2) * (kTrN * 128) + sl * 128 + (((pc & 7) ^ (sl & 7)) << 4);
-              bool clear = !has;
-              if (has && nodes) {
-                const uint4 x = lds128(at);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          int32_t r[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  clear |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-                odd |= clear;
-              }
-              if (clear) asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
-            }
-            if (!has) {
-              const uint32_t rp = sb + uint32_t(Y::rope) + uint32_t(b * Y::rope_blk) + (grp >> 1) * (kTrN * 128) + sl * 128;
-              for (int c = 4 * (grp & 1); c < 4 * (grp & 1) + 4; ++c)
-                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(rp + (c << 4)), "r"(0) : "memory");
-            }
-            if (odd) atomicOr(badw + (sl >> 5), 1u << (sl & 31));
-            fence_proxy_async_smem();
+          for (int g = 0; g < 2; ++g)
+            r[g] = static_cast<int32_t>(lds_u32(sb + uint32_t(Y::qf) + uint32_t(64 * b + 8 * dw + 4 * g + (lane >> 3)) * 4));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(R_RAW_EMPTY + b));
+          if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * b + (dw >> 1)), ((gi >> 1) - 1) & 1)) { ok = false; break; }
+          const uint32_t rp = sb + uint32_t(Y::rope) + uint32_t(b * Y::rope_blk), c = lane & 7;
+          auto at = [&](int g, int bx) -> uint32_t {  // piece c of 64 dims of a slot
+            const int sl = 8 * dw + 4 * g + (lane >> 3);
+            return kt + (bx & 3) * kTrPairBlk + (bx >> 2) * (kTrN * 128) + sl * 128 + ((c ^ (sl & 7)) << 4);
+          };
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const uint8_t* src = p.kv + int64_t(max(r[g], 0)) * kBf16RowBytes + 16 * c;
+#pragma unroll
+            for (int bx = 0; bx < 8; ++bx) cp_async16(at(g, bx), src + 128 * bx, r[g] >= 0 ? 16 : 0);
+            const int rr = kTrN * (c >> 2) + 8 * dw + 4 * g + (lane >> 3);
+            cp_async16(rp + rr * 64 + (((c & 3) ^ ((rr >> 1) & 3)) << 4), src + 1024, r[g] >= 0 ? 16 : 0);
           }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          if (nodes) {
+#pragma unroll 1
+            for (int x = 0; x < 16; ++x) {
+              const uint4 y = lds128(at(x >> 3, x & 7));
+              const uint32_t w4[4] = {y.x, y.y, y.z, y.w};
+              bool odd = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) odd |= (w4[e] & 0x7f80u) == 0x7f80u || (w4[e] & 0x7f800000u) == 0x7f800000u;
+              if (odd) {
+                const int sl = 8 * dw + 4 * (x >> 3) + (lane >> 3);
+                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at(x >> 3, x & 7)), "r"(0) : "memory");
+                atomicOr(badw + (sl >> 5), 1u << (sl & 31));
+              }
+            }
+          }
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(R_K_FULL + b));
         } else {
@@ -1236,14 +1215,13 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeArg
   }
 }
 
-// [rows, 576] bf16 with boxes of `box_rows` rows x 64 dims, 128-byte swizzle: q, and the BF16 cache with
-// boxes of one page's slots (at most 64).
-cudaError_t tree_map(const void* base, int64_t rows, unsigned box_rows, CUtensorMap* out) {
+// q, [rows, 576] bf16, in boxes of a row tile x 64 dims, 128-byte swizzle.
+cudaError_t tree_q_map(const void* base, int64_t rows, CUtensorMap* out) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (tensor_map_encoder(&encode) != cudaSuccess) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {cuuint64_t(kDim), cuuint64_t(rows)};
   const cuuint64_t strides[1] = {cuuint64_t(2 * kDim)};
-  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t box[2] = {64, kTrM};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1252,7 +1230,7 @@ cudaError_t tree_map(const void* base, int64_t rows, unsigned box_rows, CUtensor
 }
 
 template <int FMT>
-cudaError_t launch_fmt(const TreeArgs& a, int sms, const CUtensorMap& map, const CUtensorMap& qmap, cudaStream_t s) {
+cudaError_t launch_fmt(const TreeArgs& a, int sms, const CUtensorMap& qmap, cudaStream_t s) {
   // devices (below 64) whose kernel attribute is set; concurrent first calls set it twice
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
@@ -1274,7 +1252,7 @@ cudaError_t launch_fmt(const TreeArgs& a, int sms, const CUtensorMap& map, const
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_decode_kernel<FMT>, a, map, qmap);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_decode_kernel<FMT>, a, qmap);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(sms * kTrJoinCtas));
   cfg.blockDim = dim3(kTrJoinThreads);
@@ -1288,14 +1266,12 @@ size_t tree_workspace_bytes(int num_sms) { return 256 + num_sms * (sizeof(TreeJo
 
 cudaError_t launch_tree_decode(const TreeArgs& a, int num_sms, cudaStream_t s) {
   if (num_sms > kTrMaxRuns) return cudaErrorInvalidConfiguration;
-  alignas(64) CUtensorMap map = {}, qmap = {};
-  cudaError_t e = tree_map(a.q, int64_t(a.T) * a.H, kTrM, &qmap);
+  alignas(64) CUtensorMap qmap = {};
+  const cudaError_t e = tree_q_map(a.q, int64_t(a.T) * a.H, &qmap);
   if (e != cudaSuccess) return e;
-  if (a.kv_format == SMLA_KV_FP8_TENSOR) return launch_fmt<SMLA_KV_FP8_TENSOR>(a, num_sms, map, qmap, s);
-  if (a.kv_format == SMLA_KV_FP8_DS) return launch_fmt<SMLA_KV_FP8_DS>(a, num_sms, map, qmap, s);
-  e = tree_map(a.kv, a.num_pages << a.log2_page, a.log2_page >= 6 ? 64u : 1u << a.log2_page, &map);
-  if (e != cudaSuccess) return e;
-  return launch_fmt<SMLA_KV_BF16>(a, num_sms, map, qmap, s);
+  if (a.kv_format == SMLA_KV_FP8_TENSOR) return launch_fmt<SMLA_KV_FP8_TENSOR>(a, num_sms, qmap, s);
+  if (a.kv_format == SMLA_KV_FP8_DS) return launch_fmt<SMLA_KV_FP8_DS>(a, num_sms, qmap, s);
+  return launch_fmt<SMLA_KV_BF16>(a, num_sms, qmap, s);
 }
 
 }  // namespace smla
