@@ -59,8 +59,8 @@ constexpr int kTrN = 64;   // slots of a key tile
 constexpr int kTrM = 64;   // rows of a row tile
 constexpr int kTrSub = 16; // slots of a raw stage
 constexpr int kTrSoftWarps = 8, kTrFirstConv = kTrSoftWarps, kTrConvWarps = 8;
-constexpr int kTrProducer = kTrFirstConv + kTrConvWarps, kTrMmaWarp = kTrProducer + 1, kTrCheckWarp = kTrMmaWarp + 1;
-constexpr int kTrThreads = 32 * (kTrCheckWarp + 1);
+constexpr int kTrProducer = kTrFirstConv + kTrConvWarps, kTrMmaWarp = kTrProducer + 1;
+constexpr int kTrThreads = 32 * (kTrMmaWarp + 1);
 constexpr float kTrRescale = 8.f;  // the running maximum moves when it grows by more (log2 units)
 // weights are 2^(s - m + 7): at most 2^15 between moves of the maximum, within f16, and exact to
 // 2^-11 down to 2^-21 of the largest one
@@ -85,33 +85,31 @@ struct Lay {
   static constexpr bool bf16 = FMT == SMLA_KV_BF16, tens = FMT == SMLA_KV_FP8_TENSOR;
   static constexpr int row = bf16 ? kBf16RowBytes : tens ? kFp8TensorRowBytes : kFp8RowBytes;
   static constexpr int rope_blk = 2 * kTrN * 64;
-  static constexpr int rope_bufs = bf16 ? 2 : 1;
-  static constexpr int raw_stage = kTrSub * row;
   static constexpr size_t K = 0;
   static constexpr size_t rope = K + 2 * size_t(kTrKLat);
-  static constexpr size_t P = rope + size_t(rope_bufs) * rope_blk;  // [0 | P | 0]
+  static constexpr size_t P = rope + 2 * size_t(rope_blk);  // [0 | P | 0]
   static constexpr size_t qr = P + 3 * size_t(kTrPBlk);
-  static constexpr size_t raw = qr + 128 * 64;
-  static constexpr size_t xs = raw + (bf16 ? 0 : 4 * size_t(raw_stage));
+  static constexpr size_t xs = qr + 128 * 64;
   static constexpr size_t xm = xs + 256 * 64;   // xs: 16 partial scores a softmax thread
   static constexpr size_t qf = xm + 256 * 4;    // xm: a maximum a softmax thread
-  static constexpr size_t meta = qf + 128 * 4;  // qf: factors of q; BF16: rows of the key tiles [buffer][slot]
+  static constexpr size_t rows = qf + 128 * 4;  // qf: factors of q; rows of the key tiles' slots, -1: none [buffer]
+  static constexpr size_t meta = rows + 2 * kTrN * 4;
   static constexpr size_t bad = meta + kTrMeta * 8;
   static constexpr size_t run = bad + kTrMeta * 8;
   static constexpr size_t tmem = run + sizeof(TreeRun);
   static constexpr size_t bars = tmem + 16;
   static constexpr size_t bytes = bars + 32 * 8;
   static_assert(bytes <= 232448, "shared memory budget");
-  static_assert(rope % 1024 == 0 && P % 1024 == 0 && qr % 1024 == 0 && raw % 128 == 0 && bars % 8 == 0 && raw_stage % 16 == 0,
+  static_assert(rope % 1024 == 0 && P % 1024 == 0 && qr % 1024 == 0 && bars % 8 == 0,
                 "swizzle atoms and copies");
 };
 enum {
-  R_RAW_FULL = 0,                  // [stage]; BF16: the rows of the tile in [buffer] are known
-  R_RAW_EMPTY = R_RAW_FULL + 4,    // [stage]; BF16: and have been taken
-  R_K_FULL = R_RAW_EMPTY + 4,      // [buffer]
-  R_K_FREE = R_K_FULL + 2,         // [buffer][16-slot chunk]
-  R_ROPE_FULL = R_K_FREE + 8,
-  R_S_FULL, R_S_FREE, R_P_READY, R_PV_DONE, R_Q, R_QRAW, R_QX, R_DRAIN, R_COUNT
+  R_ROWS = 0,               // [buffer]: the rows of its tile are known
+  R_TAKEN = R_ROWS + 2,     // [buffer]: and have been taken
+  R_K_FULL = R_TAKEN + 2,   // [buffer]
+  R_K_FREE = R_K_FULL + 2,  // [buffer][16-slot chunk]
+  R_S_FULL = R_K_FREE + 8,
+  R_S_FREE, R_P_READY, R_PV_DONE, R_Q, R_QRAW, R_QX, R_DRAIN, R_COUNT
 };
 static_assert(R_COUNT <= 32, "barriers");
 
@@ -384,13 +382,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     for (int k = tid; k < 3 * kTrPBlk / 16; k += kTrThreads) zp[k] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     if (tid == 0) {
-      for (int s = 0; s < 4; ++s) {
-        mbar_init(bar(R_RAW_FULL + s), 1);
-        mbar_init(bar(R_RAW_EMPTY + s), BF ? kTrConvWarps : 2 + (FMT == SMLA_KV_FP8_DS ? 1 : 0));
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(bar(R_ROWS + b), 1);
+        mbar_init(bar(R_TAKEN + b), kTrConvWarps);
+        mbar_init(bar(R_K_FULL + b), kTrConvWarps);
       }
-      for (int b = 0; b < 2; ++b) mbar_init(bar(R_K_FULL + b), kTrConvWarps);
       for (int c = 0; c < 8; ++c) mbar_init(bar(R_K_FREE + c), 1);
-      mbar_init(bar(R_ROPE_FULL), kTrConvWarps);
       mbar_init(bar(R_S_FULL), 1);
       mbar_init(bar(R_S_FREE), kTrSoftWarps);
       mbar_init(bar(R_P_READY), kTrSoftWarps);
@@ -417,7 +414,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + Y::tmem);
   const TreeRun run = *reinterpret_cast<const TreeRun*>(sm + Y::run);
   TreeWalk walk(p, run);
-  if (tid == 32 * kTrCheckWarp) {  // the row tile this run ends in, for the joining kernel
+  if (tid == 32 * kTrMmaWarp) {  // the row tile this run ends in, for the joining kernel
     TreeJoin jn = {};
     if (run.u0 < run.u1) {
       TreeReq q;
@@ -443,7 +440,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       const int32_t* row = p.page_table + int64_t(s.r) * p.stride;
       const int64_t a = int64_t(k) * kTrN + lane, end = int64_t(s.q.ctx) + s.q.n;
       e0 = a < end ? *(row + (a >> p.log2_page)) : -2;  // -2: no such slot
-      e1 = a + 32 < end ? __ldg(row + ((a + 32) >> p.log2_page)) : -2;
+      e1 = a + 32 < end ? *(row + ((a + 32) >> p.log2_page)) : -2;
     };
     const int P = 1 << p.log2_page;
     bool more = walk.next(p, seg);
@@ -467,44 +464,21 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         meta[gi % kTrMeta] = v;
         bad[2 * (gi % kTrMeta)] = bad[2 * (gi % kTrMeta) + 1] = 0;
       }
-      if constexpr (BF) {
-        const int b = gi & 1;
-        if (gi >= 2 && !warp_wait(bar(R_RAW_EMPTY + b), ((gi >> 1) - 1) & 1)) { ok = false; break; }
-        int32_t* rows = reinterpret_cast<int32_t*>(sm + Y::qf) + 64 * b;
-        const int64_t s0 = int64_t(k) * kTrN + lane;
-        rows[lane] = ok0 ? (e0 << p.log2_page) + static_cast<int32_t>(s0 & (P - 1)) : -1;
-        rows[lane + 32] = ok1 ? (e1 << p.log2_page) + static_cast<int32_t>((s0 + 32) & (P - 1)) : -1;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(R_RAW_FULL + b));
-      } else {
-        const int run = min(P, kTrSub);
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          if (gi >= 1 && !warp_wait(bar(R_RAW_EMPTY + q), (gi - 1) & 1)) {
-            for (int x = 0; x < q; ++x) warp_wait(bar(R_RAW_FULL + x), gi & 1);  // copies in flight
-            ok = false;
-            break;
-          }
-          const uint32_t vq = uint32_t(v >> (kTrSub * q)) & 0xffffu;
-          if (lane == 0) {
-            if (vq)
-              mbar_arrive_expect_tx(bar(R_RAW_FULL + q), uint32_t(__popc(vq)) * Y::row);
-            else
-              mbar_arrive(bar(R_RAW_FULL + q));
-          }
-          __syncwarp();
-          const int j = kTrSub * q + lane;
-          const int32_t page = __shfl_sync(0xffffffffu, q < 2 ? e0 : e1, j & 31);
-          if (lane < kTrSub && (lane & (run - 1)) == 0) {
-            const int cnt = __popc((vq >> lane) & ((1u << run) - 1));  // the run's slots are its first cnt
-            if (cnt) {
-              const int64_t slot = (int64_t(page) << p.log2_page) + ((int64_t(k) * kTrN + j) & (P - 1));
-              bulk_g2s(sb + uint32_t(Y::raw) + uint32_t(q * Y::raw_stage + lane * Y::row), p.kv + slot * Y::row,
-                       uint32_t(cnt * Y::row), bar(R_RAW_FULL + q));
-            }
-          }
+      const int b = gi & 1;
+      if (gi >= 2 && !warp_wait(bar(R_TAKEN + b), ((gi >> 1) - 1) & 1)) { ok = false; break; }
+      int32_t* rows = reinterpret_cast<int32_t*>(sm + Y::rows) + kTrN * b;
+      const int64_t s0 = int64_t(k) * kTrN + lane;
+      rows[lane] = ok0 ? (e0 << p.log2_page) + static_cast<int32_t>(s0 & (P - 1)) : -1;
+      rows[lane + 32] = ok1 ? (e1 << p.log2_page) + static_cast<int32_t>((s0 + 32) & (P - 1)) : -1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(R_ROWS + b));
+      {  // the rows start on their way to L2: 118 -> 113 us for the 128k chain, 3,507 -> 3,463 for the trees above
+        const int32_t ra = rows[lane], rb = rows[lane + 32];
+#pragma unroll
+        for (int o = 0; o < Y::row; o += 128) {
+          if (ra >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.kv + int64_t(ra) * Y::row + o));
+          if (rb >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.kv + int64_t(rb) * Y::row + o));
         }
-        if (!ok) break;
       }
       seg = ns;
       k = nk;
@@ -512,11 +486,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       e1 = n1;
       more = nm;
       ++gi;
-    }
-    // no copy may land after the CTA has left
-    if (!BF && gi > 0) {
-      for (int q = 0; q < 4; ++q)
-        if (!mbar_wait(bar(R_RAW_FULL + q), (gi - 1) & 1)) break;
     }
   }
   // ------------------------------------------------------------------ MMA issuer
@@ -536,14 +505,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         auto qk = [&](int g) {
           tc::fence_after();
           const uint32_t kt = sb + uint32_t(Y::K) + uint32_t((g & 1) * kTrKLat);
-          const uint32_t rope = sb + uint32_t(Y::rope) + uint32_t(BF ? (g & 1) * Y::rope_blk : 0);
+          const uint32_t rope = sb + uint32_t(Y::rope) + uint32_t((g & 1) * Y::rope_blk);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             tc::mma_ts(d, tm + kTrTmQ + 8 * j, tc::sdesc_sw128(kt + (j >> 2) * kTrPairBlk + (j & 3) * 32, 16, 1024), kIdQK, j > 0);
-          // the one RoPE block is rewritten once the previous tile's scores are complete: that hides behind
-          // the 16 MMAs above
-          if (!BF && !mbar_wait(bar(R_ROPE_FULL), g & 1)) ok = false;
-          tc::fence_after();
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             tc::mma_ss(d, tc::sdesc_sw64(qr + 32 * j, 16, 512),
@@ -591,45 +556,46 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     }
     __syncwarp();
   }
-  // ------------------------------------------------------------------ f16 window check
-  else if (warp == kTrCheckWarp) {
-    if constexpr (FMT == SMLA_KV_FP8_DS) {
-      // lane l looks at row l % 16 of each raw stage, scales 2h and 2h + 1 (h = l / 16): the largest, the
-      // smallest power of two and the smallest other one over all rows, compared with the window at
-      // the end
-      const int r = lane & 15, hh = lane >> 4;
-      uint32_t smax = 0, smin_p2 = ~0u, smin_other = ~0u;
-      while (ok && walk.next(p, seg)) {
-        for (int k = seg.k0; k < seg.k1 && ok; ++k, ++gi) {
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            if (!warp_wait(bar(R_RAW_FULL + q), gi & 1)) { ok = false; break; }
-            if ((meta[gi % kTrMeta] >> (kTrSub * q + r)) & 1) {
-              const uint2 sc2 = lds64(sb + uint32_t(Y::raw) + uint32_t(q * Y::raw_stage + r * Y::row) + kScaleOff + 8 * hh);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t a = (e ? sc2.y : sc2.x) & 0x7fffffffu;
-                const bool p2 = (a & 0x7fffffu) == 0;
-                smax = max(smax, a);
-                smin_p2 = min(smin_p2, (p2 && a != 0) ? a : ~0u);
-                smin_other = min(smin_other, p2 ? ~0u : a);
-              }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(R_RAW_EMPTY + q));
-          }
-        }
-      }
-      const bool out_of_window = smax > 0x43000000u || smin_p2 < 0x38000000u || smin_other < 0x38800000u;
-      if (__any_sync(0xffffffffu, out_of_window) && lane == 0) atomicOr(err, SMLA_DEVERR_RANGE);
-    }
-  }
   // ------------------------------------------------------------------ key tiles and q
   else if (warp >= kTrFirstConv) {
     const int dtid = tid - 32 * kTrFirstConv, dw = dtid >> 5;
     const int quarter = warp & 3, part = dw >> 2, half = quarter >> 1;
     const int hl = 32 * (quarter & 1) + lane, row = 32 * quarter + lane;
     const uint32_t lrow = tm + (uint32_t(32 * quarter) << 16);
+    // FP8 formats: warp dw holds 256 dims (half dw >> 2) of the 16 slots of chunk dw & 3, and their share of the RoPE
+    // dims, in registers from the moment it is done with the tile before. Four lanes take 64 consecutive bytes of a
+    // row, a warp eight rows: the f16 stores, two 16-byte pieces a job, then spread over the 128-byte swizzle. (Bulk
+    // copies into a ring in shared memory instead, read from there, put 84 KB a unit more on it: 3,507 us
+    // where this takes 3,463, and 518 against 314 with pages of one slot.)
+    const int q = dw & 3, hw = dw >> 2, total = static_cast<int>(run.u1 - run.u0);
+    uint4 v[8], rv[2];
+    float2 sc[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};  // of slots lane / 4 and lane / 4 + 8
+    uint32_t smax = 0, smin_p2 = ~0u, smin_other = ~0u;  // of the block scales seen: one of the four is this lane's to look at
+    auto fetch = [&](int g) -> bool {
+      const int fb = g & 1;
+      if (!warp_wait(bar(R_ROWS + fb), (g >> 1) & 1)) return false;
+      int32_t r[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        r[h] = static_cast<int32_t>(lds_u32(sb + uint32_t(Y::rows) + uint32_t(kTrN * fb + kTrSub * q + (lane >> 2) + 8 * h) * 4));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(R_TAKEN + fb));
+      const uint8_t* src[2] = {p.kv + int64_t(max(r[0], 0)) * Y::row, p.kv + int64_t(max(r[1], 0)) * Y::row};
+      const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = r[j & 1] >= 0 ? *reinterpret_cast<const uint4*>(src[j & 1] + 256 * hw + 64 * (j >> 1) + 16 * (lane & 3)) : none;
+      if constexpr (tens) {
+        rv[0] = r[hw] >= 0 ? *reinterpret_cast<const uint4*>(src[hw] + kLatent + 16 * (lane & 3)) : none;
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          sc[h] = r[h] >= 0 ? *reinterpret_cast<const float2*>(src[h] + kScaleOff + 8 * hw) : make_float2(1.f, 1.f);
+          rv[h] = r[h] >= 0 ? *reinterpret_cast<const uint4*>(src[h] + kRopeOffFp8 + 64 * hw + 16 * (lane & 3)) : none;
+        }
+      }
+      return true;
+    };
     int nseg = 0;
     while (ok && walk.next(p, seg)) {
       // q of this row tile, once the softmax has taken the last scores of the previous one (and with them
@@ -644,13 +610,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * qb + 3), ((gi - 2) >> 1) & 1)) { ok = false; break; }
       if (gi > 0 && !warp_wait(bar(R_S_FREE), (gi - 1) & 1)) { ok = false; break; }
       const uint32_t qlat = sb + uint32_t(Y::K) + uint32_t(qb * kTrKLat);
-      const uint32_t qrop = sb + uint32_t(Y::rope) + uint32_t(BF ? qb * Y::rope_blk : 0);
+      const uint32_t qrop = sb + uint32_t(Y::rope) + uint32_t(qb * Y::rope_blk);
       if (dw == 0) {
         if (lane == 0) mbar_arrive_expect_tx(bar(R_QRAW), 9u * kTrM * 128u);
         __syncwarp();
         if (lane < 9)
           tma_load_2d(lane < 8 ? qlat + lane * (kTrM * 128) : qrop, &q_map, 64 * lane, seg.q.cu0 * p.H + seg.m * kTrM, bar(R_QRAW));
       }
+      if (!BF && gi == 0 && !fetch(0)) { ok = false; break; }
       {
         const bool have = int64_t(seg.m) * kTrM + hl < int64_t(seg.q.n) * p.H;
         if (!warp_wait(bar(R_QRAW), nseg & 1)) { ok = false; break; }
@@ -745,13 +712,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           // as PV has freed them; what has no row becomes zero. Copies by the threads keep pace whatever the page size,
           // where TMA boxes cost 65 clocks each, ten for every run of slots in one page: pages of 1, 8, 64 slots, 4
           // requests x 64 nodes x 128 heads, 4k contexts, 295 us each against 2,737, 475 and 302.
-          if (!warp_wait(bar(R_RAW_FULL + b), (gi >> 1) & 1)) { ok = false; break; }
+          if (!warp_wait(bar(R_ROWS + b), (gi >> 1) & 1)) { ok = false; break; }
           int32_t r[2];
 #pragma unroll
           for (int g = 0; g < 2; ++g)
-            r[g] = static_cast<int32_t>(lds_u32(sb + uint32_t(Y::qf) + uint32_t(64 * b + 8 * dw + 4 * g + (lane >> 3)) * 4));
+            r[g] = static_cast<int32_t>(lds_u32(sb + uint32_t(Y::rows) + uint32_t(kTrN * b + 8 * dw + 4 * g + (lane >> 3)) * 4));
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(R_RAW_EMPTY + b));
+          if (lane == 0) mbar_arrive(bar(R_TAKEN + b));
           if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * b + (dw >> 1)), ((gi >> 1) - 1) & 1)) { ok = false; break; }
           const uint32_t rp = sb + uint32_t(Y::rope) + uint32_t(b * Y::rope_blk), c = lane & 7;
           auto at = [&](int g, int bx) -> uint32_t {  // piece c of 64 dims of a slot
@@ -786,43 +753,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(R_K_FULL + b));
         } else {
-          // A stage of 16 slots belongs to two warps, one for each half of the 512 dims: a tile's four
-          // stages are worked on at once, and a thread's loads are all in flight together. The stage
-          // goes back to the copies as soon as they are in registers.
-          // Jobs are placed so that every access phase of a warp (8 lanes of 16 bytes) meets distinct
-          // banks. fp8_ds rows (656 bytes): 8 consecutive slots, one 16-byte piece. Per-tensor rows (576):
-          // two slots, four pieces. Either way the f16 stores, two 16-byte pieces, spread over the
-          // 128-byte swizzle.
-          const int q = dw & 3, hw = dw >> 2;
-          auto slot_of = [&](int j) { return tens ? 2 * (lane >> 3) + ((lane >> 2) & 1) + 8 * (j & 1) : lane & 15; };
-          auto piece_of = [&](int j) { return 16 * hw + (tens ? 4 * (j >> 1) + (lane & 3) : 2 * j + (lane >> 4)); };
-          auto rslot_of = [&](int j) { return tens ? 8 * hw + 4 * j + (lane >> 3) : lane & 15; };
-          auto rpiece_of = [&](int j) { return tens ? lane & 7 : 4 * hw + 2 * j + (lane >> 4); };
-          if (!warp_wait(bar(R_RAW_FULL + q), gi & 1)) { ok = false; break; }
           const uint32_t vq = uint32_t(meta[gi % kTrMeta] >> (kTrSub * q)) & 0xffffu;
-          const uint32_t raw = sb + uint32_t(Y::raw) + uint32_t(q * Y::raw_stage);
-          uint4 v[8], rv[2];
-          float2 sc = make_float2(1.f, 1.f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = lds128(raw + slot_of(j) * Y::row + 16 * piece_of(j));
-          if constexpr (tens) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint2 cw = lds64(raw + rslot_of(j) * Y::row + kLatent + 8 * rpiece_of(j));
-              rv[j] = make_uint4(cw.x, cw.y, 0, 0);
-            }
-          } else {
-            const uint2 s2 = lds64(raw + (lane & 15) * Y::row + kScaleOff + 8 * hw);
-            sc = make_float2(__uint_as_float(s2.x), __uint_as_float(s2.y));
-#pragma unroll
-            for (int j = 0; j < 2; ++j) rv[j] = lds128(raw + rslot_of(j) * Y::row + kRopeOffFp8 + 16 * rpiece_of(j));
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(R_RAW_EMPTY + q));
           // 16 codes of job j -> f16; `whole`: every slot has a row and none is a node
           auto convert = [&](int j, uint32_t (&o)[8], bool whole) {
             const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-            const __half2 s2 = __float2half2_rn(j < 4 ? sc.x : sc.y);
+            const __half2 s2 = __float2half2_rn(j < 4 ? sc[j & 1].x : sc[j & 1].y);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               e4m3x4_to_f16x4(wv[e], o[2 * e], o[2 * e + 1]);  // exact
@@ -834,7 +769,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
               }
             }
             if (whole) return;
-            const int slot = slot_of(j);
+            const int slot = (lane >> 2) + 8 * (j & 1);
             bool clear = !((vq >> slot) & 1);
             if (nodes) {
               bool odd = false;
@@ -847,15 +782,22 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             for (int e = 0; e < 8; ++e) o[e] = clear ? 0u : o[e];
           };
           // Job j's two 16-byte pieces c0, c0 + 1 (even c0) of row rr go to row rr's pieces c ^ (rr & 7): the
-          // address of job 0 with a bit flipped, and a constant added
-          const int rr0 = kTrN * hw + kTrSub * q + slot_of(0);
-          const uint32_t at0 = kt + uint32_t(rr0) * 128 + (((2 * (piece_of(0) & 3)) ^ (rr0 & 7)) << 4);
+          // addresses of job 0 and a constant
+          const int rr0 = kTrN * hw + kTrSub * q + (lane >> 2);
+          const uint32_t at0 = kt + uint32_t(rr0) * 128 + (((2 * (lane & 3)) ^ (rr0 & 7)) << 4);
           auto put = [&](int j, const uint32_t (&o)[8]) {
-            const uint32_t at = (tens ? at0 + 1024u * (j & 1) : at0 ^ (64u * (j & 1))) + uint32_t(j >> 1) * kTrPairBlk;
-            const uint32_t at1 = (tens ? (at0 ^ 16u) + 1024u * (j & 1) : at0 ^ (16u + 64u * (j & 1))) + uint32_t(j >> 1) * kTrPairBlk;
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at1), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+            const uint32_t far = 1024u * (j & 1) + uint32_t(j >> 1) * kTrPairBlk;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at0 + far), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"((at0 ^ 16u) + far), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
           };
+          if constexpr (!tens) {
+            const float2 s2 = lane & 2 ? sc[1] : sc[0];
+            const uint32_t a = __float_as_uint(lane & 1 ? s2.y : s2.x) & 0x7fffffffu;
+            const bool p2 = (a & 0x7fffffu) == 0;
+            smax = max(smax, a);
+            smin_p2 = min(smin_p2, (p2 && a != 0) ? a : ~0u);
+            smin_other = min(smin_other, p2 ? ~0u : a);
+          }
           auto tile = [&](bool whole) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -873,31 +815,36 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             tile(true);
           else
             tile(false);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(R_K_FULL + b));
-          // the one RoPE block is free once QK of the previous tile has completed
-          if (gi >= 1 && !warp_wait(bar(R_S_FULL), (gi - 1) & 1)) { ok = false; break; }
+          auto rope_put = [&](int rr, int c, uint4 x) {
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(sb + uint32_t(Y::rope) + uint32_t(b * Y::rope_blk) + rr * 64 +
+                         ((c ^ ((rr >> 1) & 3)) << 4)), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+          };
+          if constexpr (tens) {  // 16 RoPE dims of a slot
+            uint4 x, y;
+            e4m3x4_to_f16x4(rv[0].x, x.x, x.y);
+            e4m3x4_to_f16x4(rv[0].y, x.z, x.w);
+            e4m3x4_to_f16x4(rv[0].z, y.x, y.y);
+            e4m3x4_to_f16x4(rv[0].w, y.z, y.w);
+            const int rr = kTrN * ((lane >> 1) & 1) + kTrSub * q + 8 * hw + (lane >> 2), c = 2 * (lane & 1);
+            rope_put(rr, c, x);
+            rope_put(rr, c + 1, y);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int rslot = rslot_of(j), rc = rpiece_of(j);
-            const int rr = kTrN * (rc >> 2) + kTrSub * q + rslot, c = rc & 3;
-            const uint32_t dst = sb + uint32_t(Y::rope) + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4);
-            uint4 x;
-            if constexpr (tens) {
-              e4m3x4_to_f16x4(rv[j].x, x.x, x.y);
-              e4m3x4_to_f16x4(rv[j].y, x.z, x.w);
-            } else {
-              x = make_uint4(bf16x2_to_f16x2(rv[j].x), bf16x2_to_f16x2(rv[j].y), bf16x2_to_f16x2(rv[j].z), bf16x2_to_f16x2(rv[j].w));
-            }
-            if (!((vq >> rslot) & 1)) x = make_uint4(0, 0, 0, 0);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+            for (int j = 0; j < 2; ++j)
+              rope_put(kTrN * hw + kTrSub * q + (lane >> 2) + 8 * j, lane & 3,
+                       make_uint4(bf16x2_to_f16x2(rv[j].x), bf16x2_to_f16x2(rv[j].y), bf16x2_to_f16x2(rv[j].z), bf16x2_to_f16x2(rv[j].w)));
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(R_ROPE_FULL));
+          if (lane == 0) mbar_arrive(bar(R_K_FULL + b));
+          // the next tile's rows come while PV frees their place
+          if (gi + 1 < total && !fetch(gi + 1)) { ok = false; break; }
         }
       }
+    }
+    if (FMT == SMLA_KV_FP8_DS) {  // the f16 window: largest scale, smallest power of two, smallest other one
+      const bool out_of_window = smax > 0x43000000u || smin_p2 < 0x38000000u || smin_other < 0x38800000u;
+      if (__any_sync(0xffffffffu, out_of_window) && lane == 0) atomicOr(err, SMLA_DEVERR_RANGE);
     }
     if (dtid == 0) pdl_trigger();  // the joining kernel may start launching
   }
