@@ -27,22 +27,21 @@
 //  5,613 us where this took 4,020 (16 requests x 64 nodes x 128 heads, contexts of 4k-16k, fp8_ds).
 //
 // Bound: no unit is full. The MMAs of a unit take 2,220 clocks (18 of N 128 at 66, 8 of N 256 at 128), and shared
-// memory, at 128 bytes a clock, carries about 370 KB of it with the FP8 formats (2,900 clocks): raw rows in and
-// out, f16 keys in, operands, partial scores. It measures 4,000-4,350 clocks with fp8_ds (3,495 us for the batch
-// above: 682 TFLOP/s of useful work) and 4,240-4,630 with BF16: two key buffers and one score buffer tie the
-// tiles' ways (scores 1,250, read 800, softmax 2,000, values 1,050, the buffer's next keys 900-2,200) together.
+// memory, at 128 bytes a clock, carries about 290 KB of it (2,270 clocks): keys in, operands, partial scores. It
+// measures 4,070-4,220 clocks with fp8_ds (3,465 us for the batch above: 688 TFLOP/s of useful work), 4,100 with
+// per-tensor FP8 and 3,840 with BF16: two key buffers and one score buffer tie the tiles' ways (scores 1,250, read
+// 800, softmax 2,000, values 1,050, the buffer's next keys about 1,000) together.
 //
-// FP8 formats: rows come by bulk copies of up to 16 consecutive slots into a ring, eight warps turn them
-// into f16 key tiles (block scales applied, exact for powers of two). BF16: the same warps copy rows into the
-// key tile by asynchronous 16-byte copies.
+// Keys come by the loads of eight warps that know a tile's rows two tiles ahead, when they are prefetched into L2. FP8
+// formats: into registers while PV still reads their place, then as f16 into the key tile (block scales applied,
+// exact for powers of two). BF16: by asynchronous 16-byte copies into the key tile as PV frees it.
 //
 // What is hidden never counts: slots without a page or past the last node become zero rows with weight
 // zero, and in tiles that hold nodes a row with a non-finite latent value is zeroed and marked, so that
 // the scores of the nodes that see it become NaN and the others' sums never meet it.
 //
-// Per CTA (608 threads): warps 0-7 softmax and epilogue, 8-15 key tiles and q, 16 copies, 17 MMA issue,
-// 18 check of the block scales against the f16 window (fp8_ds). Every wait is bounded in time; one
-// that gives up sets SMLA_DEVERR_TIMEOUT.
+// Per CTA (576 threads): warps 0-7 softmax and epilogue, 8-15 key tiles and q, 16 the tiles' rows, 17 MMA
+// issue. Every wait is bounded in time; one that gives up sets SMLA_DEVERR_TIMEOUT.
 #include <math_constants.h>
 
 #include <atomic>
@@ -57,7 +56,7 @@ namespace {
 
 constexpr int kTrN = 64;   // slots of a key tile
 constexpr int kTrM = 64;   // rows of a row tile
-constexpr int kTrSub = 16; // slots of a raw stage
+constexpr int kTrSub = 16; // slots of a chunk: what PV frees at once
 constexpr int kTrSoftWarps = 8, kTrFirstConv = kTrSoftWarps, kTrConvWarps = 8;
 constexpr int kTrProducer = kTrFirstConv + kTrConvWarps, kTrMmaWarp = kTrProducer + 1;
 constexpr int kTrThreads = 32 * (kTrMmaWarp + 1);
@@ -69,7 +68,7 @@ constexpr float kTrShift = 7.f;
 constexpr int kTrPairBlk = 2 * kTrN * 128;  // 64 dims: [64 slots, low | the same slots, high]
 constexpr int kTrKLat = 4 * kTrPairBlk;
 constexpr int kTrPBlk = kTrM * kTrN * 2;
-constexpr int kTrMeta = 8;  // key tiles between the copies' warp and the softmax at most: 5
+constexpr int kTrMeta = 8;  // key tiles between the rows' warp and the softmax at most: 6
 
 // TMEM columns
 constexpr uint32_t kTrTmO = 0, kTrTmQ = 256, kTrTmS = 384;
@@ -434,7 +433,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   bool ok = true;
   int gi = 0;  // key tiles of this CTA so far: the barriers' phases follow it across segments
 
-  // ------------------------------------------------------------------ copies
+  // ------------------------------------------------------------------ rows of the key tiles
   if (warp == kTrProducer) {
     auto entries = [&](const TreeSeg& s, int k, int32_t& e0, int32_t& e1) {
       const int32_t* row = p.page_table + int64_t(s.r) * p.stride;
