@@ -86,8 +86,8 @@ struct Lay {
   static constexpr int rope_blk = 2 * kTrN * 64;
   static constexpr size_t K = 0;
   static constexpr size_t rope = K + 2 * size_t(kTrKLat);
-  static constexpr size_t P = rope + 2 * size_t(rope_blk);  // [0 | P | 0]
-  static constexpr size_t qr = P + 3 * size_t(kTrPBlk);
+  static constexpr size_t P = rope + 2 * size_t(rope_blk);  // [0 | P of even tiles | 0 | P of odd ones | 0]
+  static constexpr size_t qr = P + 5 * size_t(kTrPBlk);
   static constexpr size_t xs = qr + 128 * 64;
   static constexpr size_t xm = xs + 256 * 64;   // xs: 16 partial scores a softmax thread
   static constexpr size_t qf = xm + 256 * 4;    // xm: a maximum a softmax thread
@@ -108,9 +108,14 @@ enum {
   R_K_FULL = R_TAKEN + 2,   // [buffer]
   R_K_FREE = R_K_FULL + 2,  // [buffer][16-slot chunk]
   R_S_FULL = R_K_FREE + 8,
-  R_S_FREE, R_P_READY, R_PV_DONE, R_Q, R_QRAW, R_QX, R_DRAIN, R_COUNT
+  R_S_FREE,
+  R_P_READY,                // [tile parity]
+  R_Q = R_P_READY + 2, R_QRAW, R_QX, R_DRAIN, R_COUNT
 };
 static_assert(R_COUNT <= 32, "barriers");
+// A tile's PV is done when its last chunk is free. (A barrier a tile parity: a wait that may be two tiles behind
+// another tells their phases apart.)
+__device__ __forceinline__ int pv_done(int t) { return R_K_FREE + 4 * (t & 1) + 3; }
 
 // ---------------------------------------------------------------- the schedule
 
@@ -378,7 +383,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   if (tid == 32) prefetch_tensormap(&q_map);
   {
     uint4* zp = reinterpret_cast<uint4*>(sm + Y::P);  // the zero blocks beside P stay zero
-    for (int k = tid; k < 3 * kTrPBlk / 16; k += kTrThreads) zp[k] = make_uint4(0, 0, 0, 0);
+    for (int k = tid; k < 5 * kTrPBlk / 16; k += kTrThreads) zp[k] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     if (tid == 0) {
       for (int b = 0; b < 2; ++b) {
@@ -389,8 +394,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       for (int c = 0; c < 8; ++c) mbar_init(bar(R_K_FREE + c), 1);
       mbar_init(bar(R_S_FULL), 1);
       mbar_init(bar(R_S_FREE), kTrSoftWarps);
-      mbar_init(bar(R_P_READY), kTrSoftWarps);
-      mbar_init(bar(R_PV_DONE), 1);
+      for (int x = 0; x < 2; ++x) mbar_init(bar(R_P_READY + x), kTrSoftWarps);
       mbar_init(bar(R_Q), kTrConvWarps);
       mbar_init(bar(R_QRAW), 1);
       mbar_init(bar(R_QX), kTrConvWarps);
@@ -517,7 +521,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         auto pv = [&](int g) {
           tc::fence_after();
           const uint32_t kt = sb + uint32_t(Y::K) + uint32_t((g & 1) * kTrKLat);
-          const uint32_t pa = sb + uint32_t(Y::P) + uint32_t(kTrPBlk);
+          const uint32_t pa = sb + uint32_t(Y::P) + uint32_t((1 + 2 * (g & 1)) * kTrPBlk);
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             tc::mma_ss(tm + kTrTmO, tc::sdesc_sw128(pa + 32 * s, 16, 1024), tc::sdesc_sw128(kt + 2048 * s, kTrPairBlk, 1024), kIdPV,
@@ -526,12 +530,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                        tc::sdesc_sw128(kt + kTrN * 128 + 2048 * s, kTrPairBlk, 1024), kIdPV, 1);
             tc::commit(bar(R_K_FREE + 4 * (g & 1) + s));
           }
-          tc::commit(bar(R_PV_DONE));
         };
         int nqk = 0, npv = 0;
         uint64_t t0 = globaltimer_ns();
         for (uint32_t it = 0; npv < nt && ok; ++it) {
-          if (npv < nqk && mbar_test_wait(bar(R_P_READY), (gi + npv) & 1)) {
+          if (npv < nqk && mbar_test_wait(bar(R_P_READY + ((gi + npv) & 1)), ((gi + npv) >> 1) & 1)) {
             pv(gi + npv++);
           } else if (nqk < nt && nqk <= npv + 1 && qk_ready(gi + nqk)) {
             qk(gi + nqk++);
@@ -979,12 +982,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         }
         const float2 sums = f2_split(f2_add(sum[0], sum[1]));
         l = l * a + (sums.x + sums.y);
-        // the P block and O are free once PV of the previous tile is complete
-        if (i >= 1 && !warp_wait(bar(R_PV_DONE), (gi - 1) & 1)) good = false;
-        tc::fence_after();
-        if (good && i > 0 && __any_sync(0xffffffffu, a != 1.f)) correct_o(a);
+        // This P block is free: the scores that came are of keys that replaced those PV read two tiles ago. O is
+        // free once PV of the previous tile is complete.
+        if (good && i > 0 && __any_sync(0xffffffffu, a != 1.f)) {
+          good = warp_wait(bar(pv_done(gi - 1)), ((gi - 1) >> 1) & 1);
+          tc::fence_after();
+          if (good) correct_o(a);
+        }
         if (good) {
-          const uint32_t prow = sb + uint32_t(Y::P) + uint32_t(kTrPBlk) + uint32_t(hl) * 128;
+          const uint32_t prow = sb + uint32_t(Y::P) + uint32_t((1 + 2 * (gi & 1)) * kTrPBlk) + uint32_t(hl) * 128;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int c = 4 * half + 2 * sub + k;
@@ -995,11 +1001,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0 && good) mbar_arrive(bar(R_P_READY));
+        if (lane == 0 && good) mbar_arrive(bar(R_P_READY + (gi & 1)));
       }
       if (!ok) break;
       // ---- epilogue: the four threads' sums of a row, then O lane -> output or part
-      const bool fin = good && warp_wait(bar(R_PV_DONE), (gi - 1) & 1);
+      const bool fin = good && warp_wait(bar(pv_done(gi - 1)), ((gi - 1) >> 1) & 1);
       tc::fence_after();
       // the sums meet in the partials' places, which this group of four warps alone uses: those of the last
       // tile were read before its second barrier
