@@ -28,8 +28,8 @@
 //
 // Bound: no unit is full. The MMAs of a unit take 2,220 clocks (18 of N 128 at 66, 8 of N 256 at 128), and shared
 // memory, at 128 bytes a clock, carries about 290 KB of it (2,270 clocks): keys in, operands, partial scores. It
-// measures 4,070-4,220 clocks with fp8_ds (3,465 us for the batch above: 688 TFLOP/s of useful work), 4,100 with
-// per-tensor FP8 and 3,840 with BF16: two key buffers and one score buffer tie the tiles' ways (scores 1,250, read
+// measures 4,000-4,150 clocks with fp8_ds (3,400 us for the batch above: 701 TFLOP/s of useful work), 3,990 with
+// per-tensor FP8 and 3,690 with BF16: two key buffers and one score buffer tie the tiles' ways (scores 1,250, read
 // 800, softmax 2,000, values 1,050, the buffer's next keys about 1,000) together.
 //
 // Keys come by the loads of eight warps that know a tile's rows two tiles ahead, when they are prefetched into L2. FP8
@@ -94,7 +94,8 @@ struct Lay {
   static constexpr size_t rows = qf + 128 * 4;  // qf: factors of q; rows of the key tiles' slots, -1: none [buffer]
   static constexpr size_t meta = rows + 2 * kTrN * 4;
   static constexpr size_t bad = meta + kTrMeta * 8;
-  static constexpr size_t run = bad + kTrMeta * 8;
+  static constexpr size_t keys = bad + kTrMeta * 8;
+  static constexpr size_t run = keys + kTrMeta * 4;
   static constexpr size_t tmem = run + sizeof(TreeRun);
   static constexpr size_t bars = tmem + 16;
   static constexpr size_t bytes = bars + 32 * 8;
@@ -241,6 +242,7 @@ __device__ void tree_schedule_warp(const TreeArgs& p, int g, int G, int32_t* err
 
 struct TreeSeg {  // key tiles [k0, k1) of row tile m of a request
   int r, m, k0, k1;
+  int from;  // the one that is worked on first; the others follow in a circle
   TreeReq q;
   bool whole, first;  // all of the row tile's key tiles; the run starts here
 };
@@ -278,6 +280,11 @@ struct TreeWalk {
     s.k1 = static_cast<int>(min(int64_t(q.kt), s.k0 + (u1 - u)));
     s.first = u == u0;
     s.whole = s.k0 == 0 && s.k1 == q.kt;
+    // All of a row tile: its keys are taken from where the CTA would be, had it gone round the request's keys
+    // since its start, as the other CTAs of this request do: they read the same keys at about the same time, and
+    // batches whose keys are more than L2 holds meet them there (16 requests x 64 nodes x 128 heads, 16k contexts:
+    // 4,865 us against 5,600 with BF16, 5,500 against 5,945 with fp8_ds).
+    s.from = s.whole ? static_cast<int>(uint32_t(u - u0) % uint32_t(q.kt)) : s.k0;
     u += s.k1 - s.k0;
     return true;
   }
@@ -378,6 +385,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   int32_t* err = reinterpret_cast<int32_t*>(p.ws);
   volatile uint64_t* meta = reinterpret_cast<volatile uint64_t*>(sm + Y::meta);  // slots with a row, per tile
   uint32_t* bad = reinterpret_cast<uint32_t*>(sm + Y::bad);                     // non-finite rows, per tile
+  volatile int32_t* keys = reinterpret_cast<volatile int32_t*>(sm + Y::keys);  // which key tile, per tile
 
   // ------------------------------------------------------------------ set-up
   if (tid == 32) prefetch_tensormap(&q_map);
@@ -447,16 +455,16 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     };
     const int P = 1 << p.log2_page;
     bool more = walk.next(p, seg);
-    int k = seg.k0;
+    int k = seg.from;
     int32_t e0 = -2, e1 = -2;
     if (more) entries(seg, k, e0, e1);
     while (more && ok) {
       TreeSeg ns = seg;
-      int nk = k + 1;
+      int nk = k + 1 == seg.k1 ? seg.k0 : k + 1;
       bool nm = true;
-      if (nk == seg.k1) {
+      if (nk == seg.from) {
         nm = walk.next(p, ns);
-        nk = ns.k0;
+        nk = ns.from;
       }
       int32_t n0 = -2, n1 = -2;
       if (nm) entries(ns, nk, n0, n1);  // a tile ahead: their latency is hidden
@@ -465,6 +473,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       const uint64_t v = uint64_t(__ballot_sync(0xffffffffu, ok0)) | uint64_t(__ballot_sync(0xffffffffu, ok1)) << 32;
       if (lane == 0) {
         meta[gi % kTrMeta] = v;
+        keys[gi % kTrMeta] = k;
         bad[2 * (gi % kTrMeta)] = bad[2 * (gi % kTrMeta) + 1] = 0;
       }
       const int b = gi & 1;
@@ -624,8 +633,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const bool have = int64_t(seg.m) * kTrM + hl < int64_t(seg.q.n) * p.H;
         if (!warp_wait(bar(R_QRAW), nseg & 1)) { ok = false; break; }
         tc::fence_after();
-        // 16-byte piece c of this thread's 16 latent and 4 RoPE ones. BF16: all loads in flight together. FP8 formats:
-        // read twice, for the largest value and for the conversion (held, they spill: 1-2 % of every case).
+        // 16-byte piece c of this thread's 16 latent and 4 RoPE ones (FP8 formats: read twice, for the largest value and
+        // for the conversion; held in registers, they spill: 1-2 % of every case)
         auto lat = [&](int c) {
           const uint32_t at = qlat + uint32_t(4 * half + 2 * part + (c >> 3)) * (kTrM * 128) + uint32_t(hl) * 128;
           return have ? lds128(at + (((c & 7) ^ (hl & 7)) << 4)) : make_uint4(0, 0, 0, 0);
@@ -633,13 +642,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         auto rop = [&](int c) {
           return have ? lds128(qrop + uint32_t(hl) * 128 + (((4 * half + c) ^ (hl & 7)) << 4)) : make_uint4(0, 0, 0, 0);
         };
-        uint4 w[16], wr[4];
-        if constexpr (BF) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) w[c] = lat(c);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) wr[c] = part == 1 ? rop(c) : make_uint4(0, 0, 0, 0);
-        }
         float qdown = 1.f;
         int qe = 0;
         if constexpr (!BF) {
@@ -674,7 +676,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           uint32_t wv[16];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 v = BF ? w[4 * ch + k] : lat(4 * ch + k);
+            const uint4 v = lat(4 * ch + k);
             wv[4 * k] = cvt(v.x); wv[4 * k + 1] = cvt(v.y);
             wv[4 * k + 2] = cvt(v.z); wv[4 * k + 3] = cvt(v.w);
           }
@@ -685,7 +687,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 #pragma unroll kUnroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t dst = sb + uint32_t(Y::qr) + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-            const uint4 v = BF ? wr[c] : rop(c);
+            const uint4 v = rop(c);
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(cvt(v.x)), "r"(cvt(v.y)), "r"(cvt(v.z)),
                          "r"(cvt(v.w)) : "memory");
           }
@@ -704,10 +706,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         if (lane == 0) mbar_arrive(bar(R_Q));
         ++nseg;
       }
-      for (int k = seg.k0; k < seg.k1 && ok; ++k, ++gi) {
+      for (const int end = gi + seg.k1 - seg.k0; gi < end && ok; ++gi) {
         const int b = gi & 1;
         const uint32_t kt = sb + uint32_t(Y::K) + uint32_t(b * kTrKLat);
-        const bool nodes = int64_t(k + 1) * kTrN > seg.q.ctx;  // the tile holds drafted nodes
+        // the tile holds drafted nodes (asked once its rows are known)
+        auto has_nodes = [&] { return int64_t(keys[gi % kTrMeta] + 1) * kTrN > seg.q.ctx; };
         uint32_t* badw = bad + 2 * (gi % kTrMeta);
         if constexpr (BF) {
           // Warp dw loads slots [8 dw, 8 dw + 8), four of them (8 lanes of 16 bytes each) and 64 dims at a time, as soon
@@ -736,7 +739,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             cp_async16(rp + rr * 64 + (((c & 3) ^ ((rr >> 1) & 3)) << 4), src + 1024, r[g] >= 0 ? 16 : 0);
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
-          if (nodes) {
+          if (has_nodes()) {
 #pragma unroll 1
             for (int x = 0; x < 16; ++x) {
               const uint4 y = lds128(at(x >> 3, x & 7));
@@ -756,6 +759,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           if (lane == 0) mbar_arrive(bar(R_K_FULL + b));
         } else {
           const uint32_t vq = uint32_t(meta[gi % kTrMeta] >> (kTrSub * q)) & 0xffffu;
+          const bool nodes = has_nodes();
           // 16 codes of job j -> f16; `whole`: every slot has a row and none is a node
           auto convert = [&](int j, uint32_t (&o)[8], bool whole) {
             const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
@@ -938,10 +942,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         }
         uint64_t vis = meta[gi % kTrMeta];
         uint32_t oddm = 0;
-        const bool nodes = int64_t(seg.k0 + i + 1) * kTrN > seg.q.ctx;  // a tile with nodes
+        const int key = keys[gi % kTrMeta];
+        const bool nodes = int64_t(key + 1) * kTrN > seg.q.ctx;  // a tile with nodes
         if (nodes || vis != ~0ull) {
           if (nodes) {
-            vis &= tree_bits(p, seg.q, node, seg.k0 + i);
+            vis &= tree_bits(p, seg.q, node, key);
             oddm = reinterpret_cast<volatile uint32_t*>(bad)[2 * (gi % kTrMeta) + half] >> (16 * sub);
           }
           const uint32_t msk = uint32_t(vis >> (32 * half + 16 * sub)) & 0xffffu;

@@ -547,3 +547,13 @@ def test_graph_nodes_of_every_kind_before_the_call():
         for o, r in zip(outs, (0, 1, 1, 0, 0)):
             assert torch.equal(o, refs[r][0])
     assert smla.read_error(x.desc, x.ws) == 0
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_row_tiles_that_start_inside_their_keys(fmt):
+    # more row tiles than SMs and several a run: whole row tiles take their keys in a circle from inside the context, with nodes
+    # of several key tiles, partly filled pages, and masks that hide the circle's start
+    b = Batch(fmt, 128, ctx=(700, 330, 64), nodes=(96, 70, 65), page=16, seed=32, sink=True, spare_rows=1)
+    b.check()
+    b = Batch(fmt, 127, ctx=(190, 500), nodes=(130, 66), page=64, tree=False, seed=33)
+    b.check()
