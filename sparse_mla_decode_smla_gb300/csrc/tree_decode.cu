@@ -813,8 +813,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             }
           };
           // Rows [16q, 16q + 16) of the buffer are free once that chunk of PV, two tiles ago, is done. (Converting
-          // some jobs before this wait measured the same or slower: none of 8 695 us, one 695, four 712; 4
-          // requests x 64 nodes x 128 heads, 8k contexts, fp8_ds.)
+          // some jobs before this wait is slower: none of 8 652 us, one 659, two 657, three 706; 4 requests x 64
+          // nodes x 128 heads, 8k contexts, fp8_ds.)
           if (gi >= 2 && !warp_wait(bar(R_K_FREE + 4 * b + q), ((gi >> 1) - 1) & 1)) { ok = false; break; }
           // a tile without the checks of its slots takes 8 % less time than with them
           if (vq == 0xffffu && !nodes)
