@@ -46,8 +46,6 @@ __global__ void __launch_bounds__(256) cache_copy_kernel(const CachePages c, con
 // ---------------------------------------------------------------- compacting rows
 
 constexpr int kCpThreads = 256;
-constexpr int kCpItems = 8;   // 16-byte pieces a thread holds
-constexpr int kCpRows = 512;  // rows of a chunk at most
 
 // Row starts[r] + keep[k] -> row starts[r] + k for each kept row k of request r, in place, in
 // every layer. One CTA takes one (layer, request, range of 16-byte columns) and walks the kept
@@ -55,16 +53,18 @@ constexpr int kCpRows = 512;  // rows of a chunk at most
 // stored. With keep strictly ascending, keep[k] >= k, so row k of the result is a source of
 // rows <= k only: those of earlier chunks, already loaded, and of this one, loaded before the
 // barrier. No row that a later chunk reads is written early, and no other CTA touches these
-// columns of this request. Bound: HBM, every moved row read and written once. Loads through registers:
-// pieces staged in shared memory by cp.async, four chunks ahead, took 182 us where this takes 125 (half of
-// 16 contexts of 4k-16k slots kept, 656-byte rows, 4 layers: 437 MB, 3.5 TB/s; the longest context's chunks,
-// one after the other, set the time).
-__global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
+// columns of this request. Bound: HBM, every moved row read and written once; what it reaches is set by how many CTAs an
+// SM holds and by the chunks that follow one another: half of 16 contexts of 4k-16k slots kept, 656-byte rows, 4 layers,
+// 437 MB, 116 us (3.8 TB/s; 128 with the places found in the chunk before, 182 with pieces staged in
+// shared memory by cp.async, four chunks ahead); half of 4 contexts of 4k slots, 32 layers, 86 us (4.0 TB/s).
+template <int kCpItems>  // 16-byte pieces a thread holds
+__global__ void __launch_bounds__(kCpThreads, kCpItems == 4 ? 4 : 3) cache_compact_kernel(
     const CachePages c, const int32_t* page_table, const int32_t* starts,
     const int32_t* cu_keep, const int32_t* keep, int64_t n_keep, int32_t* new_lens, int columns,
     int slices, int group) {
   // byte offsets of the rows' old and new places, -1: not moved. Three chunks' worth: a chunk's are found
   // while others still store the one before the last.
+  constexpr int kCpRows = kCpThreads / 4 * kCpItems;  // rows of a chunk at most: four columns a CTA at least
   __shared__ longlong2 s_row[3][kCpRows];
   const int tid = threadIdx.x;
   const int slice = blockIdx.x % slices;
@@ -87,16 +87,11 @@ __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
   const int rows = step * kCpItems;
   const int32_t* pt = page_table + int64_t(r) * c.stride;
   const int P = 1 << c.log2_page;
-  // byte offset of a slot's row (index keys: of its codes), -1 where the slot has no page
-  auto row_at = [&](int64_t slot) -> int64_t {
-    const int64_t k = slot >> c.log2_page;
-    if (k >= c.stride) {
-      if (first) flag(c.err, SMLA_DEVERR_INDEX);
-      return -1;
-    }
-    const int32_t page = pt[k];
-    if (page < 0 || page >= c.num_pages) {
-      if (first) flag(c.err, SMLA_DEVERR_PAGE);
+  // byte offset of a slot's row (index keys: of its codes), -1 where the slot has no page; `in`: the table has an
+  // entry for it, `page`
+  auto row_at = [&](int64_t slot, bool in, int32_t page) -> int64_t {
+    if (!in || page < 0 || page >= c.num_pages) {
+      if (first) flag(c.err, in ? SMLA_DEVERR_PAGE : SMLA_DEVERR_INDEX);
       return -1;
     }
     return int64_t(page) * c.page_bytes + (slot & (P - 1)) * c.row_bytes;
@@ -107,24 +102,61 @@ __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
     return page * c.page_bytes + int64_t(P) * 128 + (in >> 7) * 4;
   };
   const int chunks = (count + rows - 1) / rows;
-  // the places of row i of chunk ch
-  auto place = [&](int ch, int i) -> longlong2 {
-    const int k = ch * rows + i;
-    const int32_t from = keep[a + k];
-    const int32_t before = k ? keep[a + k - 1] : -1;
-    longlong2 x = make_longlong2(-1, -1);
-    if (from < k || from <= before) {
-      if (first) flag(c.err, SMLA_DEVERR_INDEX);
-    } else if (from != k) {
-      x.x = row_at(int64_t(start) + from);
-      x.y = row_at(int64_t(start) + k);
-      if (x.y < 0) x.x = -1;
+  // The places of a chunk's rows, kMine a thread, in three steps a chunk apart, so that no load is waited for: the kept
+  // offsets, the pages of their slots and of where they go, the byte offsets. (All in one chunk: 183 us where this
+  // takes 151, one request of 64k slots.)
+  constexpr int kMine = (kCpRows + kCpThreads - 1) / kCpThreads;
+  int32_t kept[kMine], prior[kMine], from[kMine], page0[kMine], page1[kMine];
+  auto offsets = [&](int ch) {
+#pragma unroll
+    for (int x = 0; x < kMine; ++x) {
+      const int i = tid + x * kCpThreads;
+      const int64_t k = int64_t(ch) * rows + i;
+      const bool in = i < rows && k < count;
+      kept[x] = in ? keep[a + k] : -1;
+      prior[x] = in && k ? keep[a + k - 1] : -1;
     }
-    return x;
   };
-  auto find = [&](int ch) {  // the places of chunk ch's rows
-    const int m = min(rows, count - ch * rows);
-    for (int i = tid; i < m; i += kCpThreads) s_row[ch % 3][i] = place(ch, i);
+  auto pages = [&](int ch) {
+#pragma unroll
+    for (int x = 0; x < kMine; ++x) {
+      const int i = tid + x * kCpThreads;
+      const int64_t k = int64_t(ch) * rows + i;
+      from[x] = -1;  // not moved
+      if (i >= rows || k >= count) continue;
+      if (kept[x] < k || kept[x] <= prior[x]) {
+        if (first) flag(c.err, SMLA_DEVERR_INDEX);
+      } else if (kept[x] != k) {
+        from[x] = kept[x];
+        const int64_t s0 = (int64_t(start) + kept[x]) >> c.log2_page, s1 = (int64_t(start) + k) >> c.log2_page;
+        page0[x] = s0 < c.stride ? pt[s0] : -1;
+        page1[x] = s1 < c.stride ? pt[s1] : -1;
+      }
+    }
+  };
+  auto places = [&](int ch) {
+#pragma unroll
+    for (int x = 0; x < kMine; ++x) {
+      const int i = tid + x * kCpThreads;
+      const int64_t k = int64_t(ch) * rows + i;
+      if (i >= rows || k >= count) continue;
+      longlong2 v = make_longlong2(-1, -1);
+      if (from[x] >= 0) {
+        const int64_t s0 = int64_t(start) + from[x], s1 = int64_t(start) + k;
+        v.x = row_at(s0, (s0 >> c.log2_page) < c.stride, page0[x]);
+        v.y = row_at(s1, (s1 >> c.log2_page) < c.stride, page1[x]);
+        if (v.y < 0) v.x = -1;
+      }
+      s_row[ch % 3][i] = v;
+    }
+  };
+  auto begin = [&] {  // the first chunk's, and what the next ones need
+    offsets(0);
+    pages(0);
+    offsets(1);
+    places(0);
+    pages(1);
+    offsets(2);
   };
   auto get = [&](uint4& v, const uint8_t* base, int64_t so) {
     if (c.index_keys && col == 8)
@@ -143,7 +175,7 @@ __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
     // Few rows (an accepted path): their places are found once, and as many layers as fit are loaded
     // together.
     if (count == 0) return;
-    find(0);
+    begin();
     __syncthreads();
     const int each = (count + step - 1) / step, together = kCpItems / each;  // items of a layer; layers at once
     for (int l0 = layer0; l0 < layer1; l0 += together) {
@@ -165,7 +197,7 @@ __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
   }
   for (int layer = layer0; layer < layer1; ++layer) {
     uint8_t* base = c.kv + int64_t(layer) * c.layer_stride;
-    find(0);
+    begin();
     __syncthreads();
     for (int ch = 0; ch < chunks; ++ch) {
       const int m = min(rows, count - ch * rows);
@@ -174,7 +206,9 @@ __global__ void __launch_bounds__(kCpThreads) cache_compact_kernel(
         const int i = my + j * step;
         if (my < step && i < m && s_row[ch % 3][i].x >= 0) get(v[j], base, s_row[ch % 3][i].x);
       }
-      if (ch + 1 < chunks) find(ch + 1);  // behind this chunk's loads
+      places(ch + 1);  // behind this chunk's loads
+      pages(ch + 2);
+      offsets(ch + 3);
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < kCpItems; ++j) {
@@ -712,8 +746,13 @@ cudaError_t launch_cache_compact(const CachePages& c, const int32_t* page_table,
   if (group < 1) group = 1;
   const int64_t blocks = c.B * ((c.L + group - 1) / group) * slices;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_behind(cache_compact_kernel, dim3(static_cast<unsigned>(blocks)), kCpThreads, 0, s, c, page_table, starts, cu_keep,
-                       keep, n_keep, new_lens, columns, static_cast<int>(slices), static_cast<int>(group));
+  const dim3 grid(static_cast<unsigned>(blocks));
+  const int nc = columns, ns = static_cast<int>(slices), ng = static_cast<int>(group);
+  // Short lists: fewer registers, four CTAs an SM instead of three. 64 x 16 kept rows, 32 layers: 8.0 us against 9.0;
+  // 64 x 32: 16.8 against 13.1.
+  if (n_keep <= int64_t(c.B) * 24)
+    return launch_behind(cache_compact_kernel<4>, grid, kCpThreads, 0, s, c, page_table, starts, cu_keep, keep, n_keep, new_lens, nc, ns, ng);
+  return launch_behind(cache_compact_kernel<7>, grid, kCpThreads, 0, s, c, page_table, starts, cu_keep, keep, n_keep, new_lens, nc, ns, ng);
 }
 
 cudaError_t launch_cache_fork(const CachePages& c, const CacheTables& t, const int32_t* src_req, const int32_t* dst_req,
