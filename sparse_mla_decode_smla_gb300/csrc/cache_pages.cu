@@ -772,8 +772,9 @@ cudaError_t launch_cache_resize(const CachePages& c, const CacheTables& t, const
                                 int32_t n, int32_t* work, int sms, cudaStream_t s) {
   const size_t smem = size_t(2) * ((c.B + 31) / 32) * 4 + 2 * kMarkWords * 4;
   // One launch while the cluster has few table entries to walk (the lengths are known on the device only: all
-  // of the listed rows count). Two calls, one launch each against three: at 32,000 entries growing 20.6 us
-  // against 24.2, freeing everything 26.7 against 26.7; at 128,000 20.6 against 28 and 57 against 45.
+  // of the listed rows count). Two calls, one launch each against three: at 32,000 entries growing 14.4 us
+  // against 20.8, freeing everything and taking it again 20.4 against 20.5; at 128,000 15.4 against 24.3 and 29.3
+  // against 26.3.
   if (n <= kListThreads && int64_t(n) * c.stride <= kResizeOneLaunch) {
     return launch_behind(cache_resize_kernel, dim3(kPushCtas), kListThreads, smem, s, c, t, req, new_lens, n);
   }
