@@ -819,6 +819,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
     tc::fence_after();
     tc::dealloc(tm, 512);
   }
+  // A launch that started while the one before it drained ends after it: what follows on the stream, or in a graph, waits
+  // for this grid alone. (Every CTA of that launch is resident by now; its end needs nothing of this one.)
+  if (p.overlap_prev && tid == 0) pdl_wait();
 }
 
 }  // namespace

@@ -41,7 +41,7 @@ struct DecodeArgs {
   // nitems), nitems = 0 meaning all T x ceil(H / 64) of them
   int32_t item0, nitems;
   // launched with programmatic stream serialisation: its CTAs may start while the previous
-  // kernel on the stream drains (nothing here reads what that kernel writes)
+  // kernel on the stream drains (nothing here reads what that kernel writes), and end after it
   int32_t overlap_prev;
 };
 // Largest cluster the in-kernel split merge uses (the portable cluster size).
