@@ -570,8 +570,9 @@ smla_status smla_cache_fork(const smla_cache_desc* d, int32_t* page_table, int32
  * left as it was (SMLA_DEVERR_INDEX). A request grows only if the pages that it and those before
  * it ask for are free; otherwise it stays as it was (SMLA_DEVERR_PAGE). A released entry that is
  * no page, and a release of a page beyond its holders, leave the table, set SMLA_DEVERR_PAGE and
- * do nothing else. n is at most num_requests (SMLA_ERR_SHAPE). kv_format, num_layers and layer_stride
- * are checked and not used.
+ * do nothing else. An entry of the free list that is no page leaves the list too (SMLA_DEVERR_PAGE):
+ * the request that takes it has -1 in its place, slots without a page. n is at most num_requests
+ * (SMLA_ERR_SHAPE). kv_format, num_layers and layer_stride are checked and not used.
  */
 smla_status smla_cache_resize(const smla_cache_desc* d, int32_t* page_table, int32_t* lens,
                               int32_t* refcounts, int32_t* free_list, int32_t* free_count,

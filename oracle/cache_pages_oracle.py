@@ -149,7 +149,11 @@ def resize(P, table, lens, refs, free, count, req, new):
             page = int(free[count - 1])
             free[count - 1] = -1
             count -= 1
+            if not 0 <= page < num_pages:  # no page: the slots stay without one
+                err |= ERR_PAGE
+                page = -1
+            else:
+                refs[page] = 1
             table[r, k] = page
-            refs[page] = 1
         lens[r] = m
     return err, count

@@ -444,8 +444,9 @@ __device__ __forceinline__ void pop_pages(const CachePages& c, const CacheTables
     const int64_t from = pos - (k - old_pages);
     const int32_t page = __ldcg(t.free_list + from);
     t.free_list[from] = -1;
-    row[k] = page;
-    if (page >= 0 && page < c.num_pages)
+    const bool ok = page >= 0 && page < c.num_pages;
+    row[k] = ok ? page : -1;
+    if (ok)
       t.refs[page] = 1;
     else
       flag(c.err, SMLA_DEVERR_PAGE);

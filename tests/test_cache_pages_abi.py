@@ -157,3 +157,11 @@ def test_oracle_pages_are_conserved():
         assert np.array_equal(held, refs)
         assert sorted(free[:count]) == sorted(np.flatnonzero(refs == 0)) and (free[count:] == -1).all()
     assert refused
+
+
+def test_oracle_resize_leaves_slots_without_a_page_where_the_list_holds_none():
+    table, lens, refs = np.full((2, 4), -1), np.zeros(2, dtype=int), np.zeros(6, dtype=int)
+    free = np.array([0, 77, -3, 5, -1, -1])
+    e, count = C.resize(4, table, lens, refs, free, 4, [0, 1], [9, 3])
+    assert e == C.ERR_PAGE and count == 0 and (free == -1).all()
+    assert table.tolist() == [[5, -1, -1, -1], [0, -1, -1, -1]] and lens.tolist() == [9, 3] and refs.tolist() == [1, 0, 0, 0, 0, 1]

@@ -461,3 +461,17 @@ def test_calls_behind_writes_of_what_they_read(captured, big):
     for m in marks:
         for x, y in zip(m, want):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("stride", [8, 40000])  # one launch; three
+@pytest.mark.parametrize("entry", [-1, -7, 40, 2**31 - 1, -2**31])
+def test_resize_over_a_free_list_entry_that_is_no_page(stride, entry):
+    # the request that takes it keeps -1 there, the others get their pages
+    p = Pool("fp8_tensor", 1, 4, [9, 0, 2], stride, 40, seed=13)
+    p.free[p.count - 2] = p.free[1] = entry
+    p.d_free.copy_(_dev(p.free))
+    assert p.resize([1, 2, 0], [11, 6, 20]) == C.ERR_PAGE
+    assert p.table[1, :4].tolist().count(-1) == 2 and p.lens.tolist() == [20, 11, 6]
+    p.check(C.ERR_PAGE)
+    assert p.resize([0, 1, 2], [0, 0, 0]) == C.ERR_PAGE  # the entry without a page is met again
+    p.check(C.ERR_PAGE)
