@@ -89,6 +89,10 @@ def fork(cache, fmt, P, table, lens, refs, free, count, src, dst):
         n = int(lens[s])
         got = -1
         if n % P:
+            if not 0 <= int(table[s, n // P]) < num_pages:  # nothing to copy the rows from
+                err |= ERR_PAGE
+                pages.append(-2)
+                continue
             asked += 1
             if asked > count:
                 err |= ERR_PAGE
@@ -106,8 +110,12 @@ def fork(cache, fmt, P, table, lens, refs, free, count, src, dst):
             for k in range(n % P):
                 row_set(cache, fmt, P, got, k, row_get(cache, fmt, P, old, k))
         for k in range(n // P):
-            table[d, k] = table[s, k]
-            refs[table[s, k]] += 1
+            page = int(table[s, k])
+            table[d, k] = page
+            if 0 <= page < num_pages:
+                refs[page] += 1
+            else:
+                err |= ERR_PAGE
         lens[d] = n
         pages.append(got)
     return err, count - min(asked, count), pages

@@ -264,7 +264,8 @@ __device__ __forceinline__ int64_t clamp_count(int64_t v, int64_t num_pages, int
 // First step of a fork: which forks are taken, and the page of each partly filled last page.
 // One CTA. A fork is refused (SMLA_DEVERR_INDEX) when a request is out of range, when its
 // target is listed twice as a target or at all as a source, or still holds slots; and
-// (SMLA_DEVERR_PAGE) when fewer free pages are left than it and those before it need.
+// (SMLA_DEVERR_PAGE) when its source's partly filled last page is no page, when fewer free pages are left than
+// it and those before it need, or when the one it would take is no page.
 // fork_pages[i]: the page taken, -1 where none was needed, -2 for a refused fork.
 __global__ void __launch_bounds__(kListThreads) cache_fork_plan_kernel(const CachePages c, const CacheTables t,
                                                                        const int32_t* src_req,
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kListThreads) cache_fork_plan_kernel(const Cac
   int64_t used = 0;
   for (int i0 = 0; i0 < n; i0 += kListThreads) {
     const int i = i0 + tid;
-    bool ok = false, need = false;
+    bool ok = false, need = false, lost = false;  // lost: rows to copy, and no page that holds them
     int32_t s = 0, d = 0;
     int64_t len = 0;
     if (i < n) {
@@ -304,13 +305,18 @@ __global__ void __launch_bounds__(kListThreads) cache_fork_plan_kernel(const Cac
              len <= (int64_t(c.stride) << c.log2_page);
       }
       if (!ok) flag(c.err, SMLA_DEVERR_INDEX);
-      need = ok && (len & ((1 << c.log2_page) - 1)) != 0;
+      if (ok && (len & ((1 << c.log2_page) - 1)) != 0) {
+        const int32_t last = t.page_table[int64_t(s) * c.stride + (len >> c.log2_page)];
+        need = last >= 0 && last < c.num_pages;
+        lost = !need;
+      }
     }
     int64_t total;
     const int64_t at = used + block_sum_scan(need ? 1 : 0, s_warp, total);  // needs up to this one
     used += total;
     if (i < n) {
-      int32_t got = ok ? -1 : -2;
+      int32_t got = ok && !lost ? -1 : -2;
+      if (lost) flag(c.err, SMLA_DEVERR_PAGE);
       if (need) {
         got = -2;
         if (at <= count) {
@@ -359,11 +365,7 @@ __global__ void __launch_bounds__(256) cache_fork_kernel(const CachePages c, con
     else
       flag(c.err, SMLA_DEVERR_PAGE);
   }
-  if (part == 0) return;
-  if (last < 0 || last >= c.num_pages) {
-    if (y == 0 && tid == 0) flag(c.err, SMLA_DEVERR_PAGE);
-    return;
-  }
+  if (part == 0) return;  // (a fork whose last page is no page has been refused)
   const int64_t bytes = int64_t(part) * c.row_bytes;
   const int pieces = static_cast<int>((bytes + 8191) / 8192);
   for (int w = y; w < pieces * c.L; w += ny) {

@@ -165,3 +165,18 @@ def test_oracle_resize_leaves_slots_without_a_page_where_the_list_holds_none():
     e, count = C.resize(4, table, lens, refs, free, 4, [0, 1], [9, 3])
     assert e == C.ERR_PAGE and count == 0 and (free == -1).all()
     assert table.tolist() == [[5, -1, -1, -1], [0, -1, -1, -1]] and lens.tolist() == [9, 3] and refs.tolist() == [1, 0, 0, 0, 0, 1]
+
+
+def test_oracle_fork_refuses_a_last_page_that_is_none_and_passes_full_ones_on():
+    cache = np.arange(2 * 6 * 4 * 576, dtype=np.int64).astype(np.uint8).reshape(2, 6, -1)
+    before = cache.copy()
+    table = np.array([[0, 9, -1], [1, -1, -1], [-1, -1, -1], [-1, -1, -1], [-1, -1, -1]])
+    lens, refs = np.array([7, 4, 0, 0, 0]), np.array([1, 1, 0, 0, 0, 0])
+    free = np.array([2, 3, 4, 5, -1, -1])
+    e, count, pages = C.fork(cache, "fp8_tensor", 4, table, lens, refs, free, 4, [0, 1], [2, 3])
+    assert e == C.ERR_PAGE and count == 4 and pages == [-2, -1] and free.tolist() == [2, 3, 4, 5, -1, -1]
+    assert table[2].tolist() == [-1] * 3 and table[3].tolist() == [1, -1, -1] and lens.tolist() == [7, 4, 0, 4, 0]
+    table[1, 0] = 9  # a full page that is none
+    e, count, pages = C.fork(cache, "fp8_tensor", 4, table, lens, refs, free, 4, [1], [4])
+    assert e == C.ERR_PAGE and pages == [-1] and table[4].tolist() == [9, -1, -1] and refs.tolist() == [1, 2, 0, 0, 0, 0]
+    assert np.array_equal(cache, before)

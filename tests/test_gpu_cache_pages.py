@@ -475,3 +475,18 @@ def test_resize_over_a_free_list_entry_that_is_no_page(stride, entry):
     p.check(C.ERR_PAGE)
     assert p.resize([0, 1, 2], [0, 0, 0]) == C.ERR_PAGE  # the entry without a page is met again
     p.check(C.ERR_PAGE)
+
+
+@pytest.mark.parametrize("bad", [-1, -5, 30, 2**31 - 1, -2**31])
+@pytest.mark.parametrize("fmt,page", [("bf16", 4), ("index_keys", 16)])
+def test_fork_of_a_source_whose_pages_are_none(fmt, page, bad):
+    # the last page, partly filled, is none: the fork is refused and changes nothing, those behind it take what it would have
+    # taken; a full page that is none is passed on
+    lens = [2 * page + 3, 3 * page, page + 1, 5, 0, 0, 0, 0]
+    p = Pool(fmt, 2, page, lens, 6, 30, seed=14, gap=16)
+    p.table[0, 2] = p.table[1, 1] = bad
+    p.d_table.copy_(_dev(p.table))
+    count = p.count
+    assert p.fork([0, 1, 2, 3], [4, 5, 6, 7]) == C.ERR_PAGE
+    assert p.lens.tolist()[4:] == [0, 3 * page, page + 1, 5] and p.count == count - 2 and p.table[5, 1] == bad
+    p.check(C.ERR_PAGE)
