@@ -548,11 +548,11 @@ smla_status smla_cache_compact(const smla_cache_desc* d, const int32_t* page_tab
  * it is and sets SMLA_DEVERR_PAGE). The used rows of a partly filled last page are copied, in
  * every layer, to a page off the free list (i in ascending order). lens follows.
  *   fork_pages [n] int32 receives the page taken, -1 where none was needed, -2 where the fork
- *   was refused and changed nothing: SMLA_DEVERR_INDEX for a request outside [0, B), a target
- *   that is listed twice or is also a source, a target that holds slots, or a source whose
- *   length does not fit the table; SMLA_DEVERR_PAGE for a source whose partly filled last page is
- *   no page, for a free list that is too short for this fork and those before it, or whose entry
- *   is no page.
+ *   was refused and left both requests as they were: SMLA_DEVERR_INDEX for a request outside
+ *   [0, B), a target that is listed twice or is also a source, a target that holds slots, or a
+ *   source whose length does not fit the table; SMLA_DEVERR_PAGE for a source whose partly filled
+ *   last page is no page, for a free list that is too short for this fork and those before it, or
+ *   whose entry is no page (the entry leaves the list all the same).
  * n is at most num_requests (SMLA_ERR_SHAPE).
  */
 smla_status smla_cache_fork(const smla_cache_desc* d, int32_t* page_table, int32_t* lens,

@@ -1,6 +1,7 @@
 """The tree and cache page calls refuse bad arguments on the host (CPU only), and the page
 oracle's own pins."""
 import ctypes
+import os
 
 import numpy as np
 import pytest
@@ -10,6 +11,7 @@ import sparse_mla_decode_smla_gb300 as smla
 from sparse_mla_decode_smla_gb300 import _build
 
 P = ctypes.c_void_p
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "smla.h")
 
 
 @pytest.fixture(scope="module")
@@ -180,3 +182,15 @@ def test_oracle_fork_refuses_a_last_page_that_is_none_and_passes_full_ones_on():
     e, count, pages = C.fork(cache, "fp8_tensor", 4, table, lens, refs, free, 4, [1], [4])
     assert e == C.ERR_PAGE and pages == [-1] and table[4].tolist() == [9, -1, -1] and refs.tolist() == [1, 2, 0, 0, 0, 0]
     assert np.array_equal(cache, before)
+
+
+def test_header_says_that_a_refused_fork_may_take_a_bad_entry_off_the_list():
+    # the model: an entry that is no page leaves the list with the fork that it refuses; the next fork takes the one before it
+    cache = np.zeros((1, 6, 4 * 576), dtype=np.uint8)
+    table, lens = np.array([[0], [-1], [-1], [-1]]), np.array([3, 0, 0, 0])
+    refs, free = np.array([1, 0, 0, 0, 0, 0]), np.array([1, 2, -6, 3, -1, -1])
+    e, count, pages = C.fork(cache, "fp8_tensor", 4, table, lens, refs, free, 4, [0, 0, 0], [1, 2, 3])
+    assert e == C.ERR_PAGE and count == 1 and pages == [3, -2, 2] and free.tolist() == [1, -1, -1, -1, -1, -1]
+    assert lens.tolist() == [3, 3, 0, 3] and table[2, 0] == -1
+    text = " ".join(open(HEADER).read().replace("*", " ").split())
+    assert "refused and changed nothing" not in text and "the entry leaves the list all the same" in text

@@ -490,3 +490,15 @@ def test_fork_of_a_source_whose_pages_are_none(fmt, page, bad):
     assert p.fork([0, 1, 2, 3], [4, 5, 6, 7]) == C.ERR_PAGE
     assert p.lens.tolist()[4:] == [0, 3 * page, page + 1, 5] and p.count == count - 2 and p.table[5, 1] == bad
     p.check(C.ERR_PAGE)
+
+
+@pytest.mark.parametrize("entry", [-1, -7, 12, 2**31 - 1, -2**31])
+def test_fork_over_a_free_list_entry_that_is_no_page(entry):
+    # the fork whose turn it is is refused, the entry leaves the list, and the next fork takes the one before it
+    p = Pool("fp8_ds", 2, 4, [3, 6, 0, 0, 0, 0], 3, 12, seed=15)
+    p.free[p.count - 2] = entry
+    p.d_free.copy_(_dev(p.free))
+    count, third = p.count, int(p.free[p.count - 3])
+    assert p.fork([0, 1, 0], [2, 3, 4]) == C.ERR_PAGE
+    assert p.count == count - 3 and p.lens.tolist() == [3, 6, 3, 0, 3, 0] and p.table[4, 0] == third
+    p.check(C.ERR_PAGE)
