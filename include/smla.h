@@ -79,10 +79,10 @@ enum {
   SMLA_DEVERR_INDEX = 1, /* a top-k entry other than -1 outside [0, page_table_stride*page_size) */
   SMLA_DEVERR_PAGE = 2,  /* a page-table entry used by a valid index outside [0, num_pages) */
   SMLA_DEVERR_TIMEOUT = 4, /* an internal pipeline wait gave up (bounded waits; outputs invalid) */
-  SMLA_DEVERR_RANGE = 8    /* fp8_ds with 64+ heads: a selected row holds a block scale outside
-                              the f16 window [2^-15, 2^7] ([2^-14, 2^7] for scales that are not
-                              powers of two); the outputs of that call may be inaccurate or
-                              non-finite (see smla_decode) */
+  SMLA_DEVERR_RANGE = 8    /* fp8_ds with 64+ heads (smla_tree_decode: with any number): a selected
+                              row holds a block scale outside the f16 window [2^-15, 2^7]
+                              ([2^-14, 2^7] for scales that are not powers of two); the outputs of
+                              that call may be inaccurate or non-finite (see smla_decode) */
 };
 
 typedef struct smla_desc {
@@ -461,8 +461,9 @@ smla_status smla_tree_workspace_size(const smla_tree_desc* d, size_t* bytes);
  *
  * Precision. Scores, softmax statistics and sums are fp32. With the FP8 formats q and the keys
  * enter the tensor cores as f16: q exactly, brought into range by a power of two a row, and
- * the keys within the operand range that smla_decode documents for SMLA_KV_FP8_DS
- * (SMLA_DEVERR_RANGE); probabilities enter PV as f16. With SMLA_KV_BF16 q, keys and
+ * the keys of SMLA_KV_FP8_DS within the operand range that smla_decode documents for that format with
+ * 64 or more heads, here with any number of heads: a row of a context or node whose block scale lies
+ * outside it sets SMLA_DEVERR_RANGE. Probabilities enter PV as f16. With SMLA_KV_BF16 q, keys and
  * probabilities enter as bf16.
  */
 smla_status smla_tree_decode(const smla_tree_desc* d, const void* q, const void* kv_cache,

@@ -194,3 +194,8 @@ def test_header_says_that_a_refused_fork_may_take_a_bad_entry_off_the_list():
     assert lens.tolist() == [3, 3, 0, 3] and table[2, 0] == -1
     text = " ".join(open(HEADER).read().replace("*", " ").split())
     assert "refused and changed nothing" not in text and "the entry leaves the list all the same" in text
+
+
+def test_header_says_that_tree_attention_has_the_scale_window_at_every_head_count():
+    text = " ".join(open(HEADER).read().replace("*", " ").split())
+    assert "fp8_ds with 64+ heads (smla_tree_decode: with any number)" in text and "here with any number of heads" in text

@@ -557,3 +557,56 @@ def test_row_tiles_that_start_inside_their_keys(fmt):
     b.check()
     b = Batch(fmt, 127, ctx=(190, 500), nodes=(130, 66), page=64, tree=False, seed=33)
     b.check()
+
+
+def _scale_bytes(v):
+    return torch.from_numpy(np.frombuffer(np.float32(v).tobytes(), dtype=np.uint8).copy()).cuda()
+
+
+@pytest.mark.parametrize("heads", [1, 16, 64, 128])
+def test_every_scale_outside_the_window_is_flagged(heads):
+    # fp8_ds keys enter as f16 at every head count: block scales in [2^-15, 2^7], [2^-14, 2^7] where they are no powers of two.
+    # Each of a row's four scales, in slots of every part of a key tile, of the context and of the nodes
+    b = Batch("fp8_ds", heads, ctx=(130,), nodes=(3,), page=16, seed=40)
+    b.to_gpu()
+    up, down = (lambda x: float(np.nextafter(np.float32(x), np.float32(np.inf)))), 2.0 ** -14
+    bad = [2.0 ** 8, up(2.0 ** 7), 2.0 ** -16, float(np.nextafter(np.float32(down), np.float32(0))), -2.0 ** 9, math.inf, math.nan]
+    n = 0
+    for s in (0, 5, 7, 8, 15, 16, 31, 32, 63, 64, 100, 127, 128, 129, 130, 132):
+        for block in range(4):
+            at = b.d_kv[b.slot(0, s), 512 + 4 * block:516 + 4 * block]
+            old = at.clone()
+            at.copy_(_scale_bytes(bad[n % len(bad)]))
+            n += 1
+            b.call()
+            assert smla.read_error(b.desc, b.ws) == smla.SMLA_DEVERR_RANGE, (s, block, bad[(n - 1) % len(bad)])
+            at.copy_(old)
+    for s in (133, 140):  # past the last node: not a row of the call
+        at = b.d_kv[b.slot(0, s), 512:516]
+        at.copy_(_scale_bytes(math.nan))
+    b.call()
+    assert smla.read_error(b.desc, b.ws) == 0
+
+
+@pytest.mark.parametrize("heads", [1, 16, 64])
+def test_scales_at_the_edges_of_the_window(heads):
+    # powers of two at both edges: the usual bounds
+    for v, sm in ((2.0 ** 7, SM / 1024), (2.0 ** -15, SM)):
+        b = Batch("fp8_ds", heads, ctx=(130,), nodes=(3,), page=16, seed=41, sm=float(np.float32(sm)))
+        for s in (3, 70, 131):
+            b.rows[b.slot(0, s), 512:528] = np.frombuffer(np.full(4, v, dtype=np.float32).tobytes(), dtype=np.uint8)
+        b.check()
+    # others: the scale and its product with the code are rounded to f16, 2^-11 relative each (together below 2^-10 * 1.001), and
+    # products below 2^-14 to a multiple of 2^-24: half a step of it. A score moves by that of each key value, times |q|; an
+    # output by the weights' change and by its own values'
+    for v, sm in ((float(np.nextafter(np.float32(2.0 ** -14), np.float32(1))), SM), (0.71, SM), (127.9, SM / 1024)):
+        b = Batch("fp8_ds", heads, ctx=(130,), nodes=(3,), page=16, seed=42, sm=float(np.float32(sm)))
+        for s in range(133):
+            b.rows[b.slot(0, s), 512:528] = np.frombuffer(np.full(4, v, dtype=np.float32).tobytes(), dtype=np.uint8)
+        ref, (out, lse) = b.oracle(), b.run()
+        b_out, b_lse = T.error_bounds(ref, True)
+        t = ref["terms"]
+        q1 = np.abs(O.bf16_bits_to_f64(b.q)).sum(-1)
+        ds = 2.0 ** -10 * 1.001 * t["qk"] + abs(b.sm) * 2.0 ** -25 * q1
+        assert (np.abs(lse - ref["lse"]) <= b_lse + ds).all()
+        assert (np.abs(out - ref["out"]) <= (b_out + (2 * ds + 2.0 ** -10 * 1.001)[..., None] * t["A"] + 2.0 ** -25)).all()
