@@ -460,8 +460,9 @@ smla_status smla_tree_workspace_size(const smla_tree_desc* d, size_t* bytes);
  * an infinity they are unspecified) and leaves the other nodes' as they are.
  *
  * Precision. Scores, softmax statistics and sums are fp32. With the FP8 formats q and the keys
- * enter the tensor cores as f16: q exactly, brought into range by a power of two a row, and
- * the keys of SMLA_KV_FP8_DS within the operand range that smla_decode documents for that format with
+ * enter the tensor cores as f16: q brought into range by a power of two a row, exact but for
+ * elements below 2^-17 of their row's largest, which keep 2^-25 of it in absolute error, and the
+ * keys of SMLA_KV_FP8_DS within the operand range that smla_decode documents for that format with
  * 64 or more heads, here with any number of heads: a row of a context or node whose block scale lies
  * outside it sets SMLA_DEVERR_RANGE. Probabilities enter PV as f16. With SMLA_KV_BF16 q, keys and
  * probabilities enter as bf16.

@@ -199,3 +199,9 @@ def test_header_says_that_a_refused_fork_may_take_a_bad_entry_off_the_list():
 def test_header_says_that_tree_attention_has_the_scale_window_at_every_head_count():
     text = " ".join(open(HEADER).read().replace("*", " ").split())
     assert "fp8_ds with 64+ heads (smla_tree_decode: with any number)" in text and "here with any number of heads" in text
+
+
+def test_header_gives_the_error_of_small_elements_of_a_query():
+    text = " ".join(open(HEADER).read().replace("*", " ").split())
+    tree = text[text.index("Attention of all nodes over their contexts"):]
+    assert "q exactly" not in tree and "elements below 2^-17 of their row's largest, which keep 2^-25 of it" in tree

@@ -610,3 +610,19 @@ def test_scales_at_the_edges_of_the_window(heads):
         ds = 2.0 ** -10 * 1.001 * t["qk"] + abs(b.sm) * 2.0 ** -25 * q1
         assert (np.abs(lse - ref["lse"]) <= b_lse + ds).all()
         assert (np.abs(out - ref["out"]) <= (b_out + (2 * ds + 2.0 ** -10 * 1.001)[..., None] * t["A"] + 2.0 ** -25)).all()
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_small_elements_of_a_query(fmt):
+    # one element of 1 that meets zeros, 511 of 2^-18 (1 + 2^-7) that meet the largest codes: as f16 each of them is off by 2^-25,
+    # all the same way; as bf16 (the BF16 cache) none is
+    def values(b, x):
+        x[:] = 224.0
+        x[:, 0] = x[:, 512:] = 0.0
+        return x
+    b = Batch(fmt, 16, ctx=(1,), nodes=(1,), seed=43, tree=False, values=values, sm=1.0)
+    q = np.full((1, 16, 576), 2.0 ** -18 * (1 + 2.0 ** -7))
+    q[..., 0] = 1.0
+    b.q = _bits(q)
+    assert np.array_equal(O.bf16_bits_to_f64(b.q), q)
+    b.check()
