@@ -502,3 +502,108 @@ def test_fork_over_a_free_list_entry_that_is_no_page(entry):
     assert p.fork([0, 1, 0], [2, 3, 4]) == C.ERR_PAGE
     assert p.count == count - 3 and p.lens.tolist() == [3, 6, 3, 0, 3, 0] and p.table[4, 0] == third
     p.check(C.ERR_PAGE)
+
+
+@pytest.mark.parametrize("n,short", [(1025, 1), (3000, 1300), (3000, 0), (2048, 1)])
+def test_resize_of_lists_longer_than_a_batch(n, short):
+    # the plan takes 1024 requests at a time: places, shortage and refusals carry over from one batch to the next. `short`: how
+    # many of the last requests that grow find no page left
+    g = np.random.default_rng(n + short)
+    B, stride, P = n + 50, 8, 4
+    ids = g.permutation(B)[:n]
+    new = g.integers(1, stride * P + 1, n)
+    need = -(-new // P)
+    pages = int(need[:n - short].sum()) + (int(need[n - short]) - 1 if short else 17)
+    p = Pool("fp8_tensor", 1, P, [0] * B, stride, pages, seed=16)
+    e = p.resize(ids.tolist(), new.tolist())
+    assert e == (C.ERR_PAGE if short else 0) and np.count_nonzero(p.lens) == n - short
+    p.check(e)
+    # some shrink, some grow on what those free, in another order; one twice, no such request, too long, in the second batch
+    order, new = g.permutation(ids), g.integers(0, stride * P + 1, n)
+    order[-1], order[n - 3], new[n - 4] = order[3], B, stride * P + 1
+    e = p.resize(order.tolist(), new.tolist())
+    assert e & C.ERR_INDEX
+    p.check(e)
+    assert p.resize(ids.tolist(), [0] * n) == 0 and p.count == pages
+    p.check()
+
+
+@pytest.mark.parametrize("n,short", [(1025, 1), (1025, 0), (2600, 1500), (2600, 3)])
+def test_fork_of_lists_longer_than_a_batch(n, short):
+    g = np.random.default_rng(n + short)
+    live = [9, 3, 8, 1, 14, 4, 0]
+    B, used = n + len(live) + 5, sum(-(-x // 4) for x in live)
+    src = g.integers(0, len(live), n)
+    src[-1] = 0
+    need = np.array([live[s] % 4 != 0 for s in src])
+    last = np.flatnonzero(need)
+    pages = used + len(last) - short + (0 if short else 9)
+    p = Pool("fp8_tensor", 2, 4, live + [0] * (B - len(live)), 4, pages, seed=17)
+    dst = g.permutation(np.arange(len(live), B))[:n]
+    e = p.fork(src.tolist(), dst.tolist())
+    assert e == (C.ERR_PAGE if short else 0)
+    p.check(e)
+    # refusals behind the first batch: a target twice, one that is a source, no such request; the others are taken
+    assert p.resize(dst.tolist(), [0] * n) == 0
+    src[1024], dst[n - 1] = dst[5], dst[2]
+    src[7] = -1
+    e = p.fork(src.tolist(), dst.tolist())
+    assert e & C.ERR_INDEX
+    p.check(e)
+
+
+def test_resize_refusals_in_three_launches():
+    p = Pool("bf16", 1, 4, [10, 11, 12, 0], 40000, 12, seed=2)
+    e = p.resize([0, 0, 1, 4], [0, 4, 160001, 1])       # twice; too long; no such request
+    assert e == C.ERR_INDEX
+    p.check(e)
+    e = p.resize([3, -1, 3, 2], [4, 0, 0, -1])          # twice, apart; no such request; a negative length
+    assert e == C.ERR_INDEX
+    p.check(e)
+    assert p.resize([3, 2, 0], [16, 13, 0]) == 0         # grows on what the same call frees
+    p.check()
+    e = p.resize([0, 2, 1], [16, 160000, 5])             # not enough from the second on: it stays, the last still shrinks
+    assert e == C.ERR_PAGE
+    p.check(e)
+    # a page that no request holds, and a table entry that is no page
+    p.d_refs[int(p.table[1, 0])] = 0
+    p.refs[int(p.table[1, 0])] = 0
+    p.d_table[1, 1] = 77
+    p.table[1, 1] = 77
+    assert p.resize([1, 0], [0, 3]) == C.ERR_PAGE
+    p.check(C.ERR_PAGE)
+
+
+def test_resize_random_walk_in_three_launches():
+    g = np.random.default_rng(18)
+    p = Pool("fp8_tensor", 1, 4, [0] * 40, 70000, 500, seed=1)
+    for _ in range(25):
+        n = int(g.integers(1, 41))
+        ids = g.permutation(40)[:n]
+        if g.random() < 0.3:
+            ids[-1] = ids[0]
+        new = g.integers(0, 121, n) * (g.random(n) < 0.7)
+        e = p.resize(ids.tolist(), new.tolist())
+        p.check(e)
+
+
+def test_resize_of_the_longest_list():
+    # 65,536 requests take a page each and give it back; the last ones find none
+    B = n = 65536
+    pages = B - 7
+    g = np.random.default_rng(19)
+    ids, free = g.permutation(B).astype(np.int32), g.permutation(pages).astype(np.int32)
+    d = smla.make_cache_desc(0, 1, 2, pages, B, 3)
+    dv = [_dev(x) for x in (np.full((B, 3), -1), np.zeros(B), np.zeros(pages), free, [pages])]
+    work, err = torch.empty(2 * n, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    smla.cache_resize(d, *dv, _dev(ids), _dev(np.ones(n)), work, err)
+    table, lens, refs = np.full((B, 3), -1), np.zeros(B), np.ones(pages)
+    table[ids[:pages], 0], lens[ids[:pages]] = free[::-1], 1
+    assert err.item() == C.ERR_PAGE and dv[4].item() == 0
+    for a, b in zip(dv, (table, lens, refs, np.full(pages, -1))):
+        assert np.array_equal(a.cpu().numpy(), b)
+    err.zero_()
+    smla.cache_resize(d, *dv, _dev(ids[::-1].copy()), _dev(np.zeros(n)), work, err)
+    assert err.item() == 0 and dv[4].item() == pages
+    for a, b in zip(dv, (np.full((B, 3), -1), np.zeros(B), np.zeros(pages), np.arange(pages))):
+        assert np.array_equal(a.cpu().numpy(), b)
