@@ -626,3 +626,31 @@ def test_small_elements_of_a_query(fmt):
     b.q = _bits(q)
     assert np.array_equal(O.bf16_bits_to_f64(b.q), q)
     b.check()
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("ctx,nodes,heads", [(7001, 4, 16), (9728, 1, 16), (9727, 1, 64), (20011, 2, 33)])
+def test_no_slot_is_lost_where_runs_meet(fmt, ctx, nodes, heads):
+    # the first and the last slot of every key tile in turn outweigh all others together: wherever the tile's work is cut, one
+    # that were lost or counted twice would show in full. Odd tiles' first slots and even tiles' last slots in one call, the
+    # others in the next: each marked slot has a value of its own dims
+    for part in range(2):
+        marks = [s for k in range(-(-(ctx + nodes) // 64)) for s in ((64 * k,) if (k + part) % 2 else (64 * k + 63,)) if s < ctx]
+
+        def values(b, x):
+            x *= 0.05
+            x[:, 0] = 0.0
+            for i, s in enumerate(marks):
+                row = x[b.slot(0, s)]
+                row[0] = 12.0
+                row[1 + i % 500] += 1.0 if i < 500 else -1.0
+            return x
+
+        b = Batch(fmt, heads, ctx=(ctx,), nodes=(nodes,), seed=44 + part, tree=False, values=values, sm=1.0)
+        b.q = _bits(O.bf16_bits_to_f64(b.q) * 0.02)
+        b.q[..., 0] = 0x3F80  # 1: a marked slot counts e^12 of an unmarked one
+        ref = b.oracle()
+        # one mark less, or one twice, moves the log-sum-exp by 1 / len(marks): more than twice its bound
+        b_lse = T.error_bounds(ref, fmt != "bf16")[1]
+        assert (b_lse * 2 < 1 / len(marks)).all()
+        b.check(ref)
