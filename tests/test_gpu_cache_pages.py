@@ -607,3 +607,46 @@ def test_resize_of_the_longest_list():
     assert err.item() == 0 and dv[4].item() == pages
     for a, b in zip(dv, (np.full((B, 3), -1), np.zeros(B), np.zeros(pages), np.arange(pages))):
         assert np.array_equal(a.cpu().numpy(), b)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("L", [1, 9])
+def test_compact_one_long_list_among_short_ones(fmt, L):
+    # few kept rows a request on average, the form for short lists, and one request of several chunks: on its own, and in front
+    # of and behind requests of one row and of none
+    g = np.random.default_rng(20 + L)
+    for B, at, n in ((64, 0, 1400), (64, 63, 1400), (200, 77, 4500)):
+        lens = [int(x) for x in g.integers(0, 3, B)]
+        lens[at] = n
+        p = Pool(fmt, L, 16, lens, -(-n // 16), sum(-(-x // 16) for x in lens) + 2, seed=21, gap=16)
+        keep = [list(range(x - 1, x)) if x else [] for x in lens]
+        keep[at] = sorted(g.choice(n, n * 9 // 10, replace=False).tolist())
+        flat = sum(keep, [])
+        assert 256 < len(keep[at]) and len(flat) <= 24 * B
+        cu = np.concatenate([[0], np.cumsum([len(k) for k in keep])])
+        new, want = torch.full((B,), -5, dtype=torch.int32, device="cuda"), np.full(B, -5)
+        smla.cache_compact(p.desc, p.d_table, _dev([0] * B), _dev(cu), _dev(flat), p.raw, new, p.err)
+        assert C.compact(p.cache, fmt, 16, p.table, [0] * B, cu, flat, want) == 0
+        p.check()
+        assert new.tolist() == want.tolist()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8_ds"])
+def test_compact_refusals_in_a_list_of_several_chunks(fmt):
+    # in the form for short lists and in the other one: entries that break the order, at a chunk's start too, pages that are none
+    # and slots past the table are left where they are, the others move
+    g = np.random.default_rng(22)
+    for B in (1, 120):
+        lens = [2600] + [0] * (B - 1)
+        p = Pool(fmt, 2, 16, lens, 163, 170, seed=23)
+        keep = sorted(g.choice(2599, 2300, replace=False).tolist())
+        for k in (64, 128, 255, 256, 448, 512, 1000, 1792):
+            keep[k] = keep[k - 1] if k % 3 else 0
+        keep[-1] = 5000
+        table = p.table.copy()
+        table[0, [9, 40, 100]] = [-1, 170, 2**31 - 1]
+        cu = [0] + [len(keep)] * B
+        smla.cache_compact(p.desc, _dev(table), _dev([0] * B), _dev(cu), _dev(keep), p.raw, None, p.err)
+        e = C.compact(p.cache, fmt, 16, table, [0] * B, cu, keep)
+        assert e == C.ERR_INDEX | C.ERR_PAGE
+        p.check(e)
