@@ -197,14 +197,15 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Programmatic dependent launch: the kernel queued next on the stream (launched with the
-// programmatic-serialization attribute) may start once every CTA of this grid has called
-// pdl_trigger or exited; it calls pdl_wait before touching this grid's results, which
-// returns once this grid has completed and its memory operations are visible.
 // Fetch a TMA descriptor (a kernel parameter) ahead of its first use.
 __device__ __forceinline__ void prefetch_tensormap(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
+// Programmatic dependent launch: the kernel queued next on the stream (launched with the
+// programmatic-serialization attribute) may start once every CTA of this grid has called
+// pdl_trigger or exited; it calls pdl_wait before touching this grid's results, which
+// returns once this grid has completed and its memory operations are visible. A kernel that
+// touches none of them calls it all the same before it ends: what follows waits for it alone.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

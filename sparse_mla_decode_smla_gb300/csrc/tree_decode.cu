@@ -28,9 +28,10 @@
 //
 // Bound: no unit is full. The MMAs of a unit take 2,220 clocks (18 of N 128 at 66, 8 of N 256 at 128), and shared
 // memory, at 128 bytes a clock, carries about 290 KB of it (2,270 clocks): keys in, operands, partial scores. It
-// measures 4,000-4,150 clocks with fp8_ds (3,400 us for the batch above: 701 TFLOP/s of useful work), 3,990 with
-// per-tensor FP8 and 3,690 with BF16: two key buffers and one score buffer tie the tiles' ways (scores 1,250, read
-// 800, softmax 2,000, values 1,050, the buffer's next keys about 1,000) together.
+// measures 3,990 clocks with fp8_ds (3,395 us for the batch above at 2,070 MHz: 702 TFLOP/s of useful work), 3,830 with
+// per-tensor FP8 and 3,590 with BF16; 4 requests of 8k slots, whose runs are shorter, 4,185, 4,035 and 3,720. Two key
+// buffers and one score buffer tie the tiles' ways (scores 1,250, read 800, softmax 2,000, values 1,050, the buffer's
+// next keys about 1,000) together.
 //
 // Keys come by the loads of eight warps that know a tile's rows two tiles ahead, when they are prefetched into L2. FP8
 // formats: into registers while PV still reads their place, then as f16 into the key tile (block scales applied,
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           // Warp dw loads slots [8 dw, 8 dw + 8), four of them (8 lanes of 16 bytes each) and 64 dims at a time, as soon
           // as PV has freed them; what has no row becomes zero. Copies by the threads keep pace whatever the page size,
           // where TMA boxes cost 65 clocks each, ten for every run of slots in one page: pages of 1, 8, 64 slots, 4
-          // requests x 64 nodes x 128 heads, 4k contexts, 295 us each against 2,737, 475 and 302.
+          // requests x 64 nodes x 128 heads, 4k contexts, 278 us each against 2,737, 475 and 302.
           if (!warp_wait(bar(R_ROWS + b), (gi >> 1) & 1)) { ok = false; break; }
           int32_t r[2];
 #pragma unroll
@@ -982,6 +983,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         for (int j = 0; j < 8; ++j) {
           const float2 x = f2_split(f2_add(f2(s[2 * j], s[2 * j + 1]), nb2));
           const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
+          // The weights enter PV in the keys' type, since an MMA takes both operands in one: bf16 with a BF16 cache
+          // (each off by 2^-8 at most; results 0.0018-0.0021 off 64 bits where fp32 weights give 0.0017), else f16.
           sum[j & 1] = f2_add(sum[j & 1], f2(p0, p1));
           pw2[j] = BF ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
         }

@@ -21,7 +21,7 @@ struct TreeArgs {
   const float* sink;
   void* out;
   float* lse;
-  uint8_t* ws;  // error word at 0, partials from kTreePartOff on
+  uint8_t* ws;  // error word at 0; from byte 256 on what each run leaves for joining, then the runs' parts
   int32_t T, H, B, W, stride, log2_page, kv_format;
   int64_t num_pages;
   float c2;        // sm_scale * log2(e)
