@@ -113,8 +113,8 @@ const char* smla_status_string(int32_t status);
 /* ABI version of this header (increments whenever the interface that was there changes; 2 added kv_scale,
  * 3 added SMLA_ERR_TIMEOUT, SMLA_ERR_OPERAND_RANGE, SMLA_DEVERR_RANGE,
  * smla_noalloc_read_error, the indexer calls and smla_store_kv_normed; 4 added q_format and
- * q_scale in place of two reserved words; 5 added smla_plan_launches). The tree and cache page
- * calls came later and change nothing that version 5 had: look their symbols up. */
+ * q_scale in place of two reserved words; 5 added smla_plan_launches). The tree, cache page and
+ * prompt calls came later and change nothing that version 5 had: look their symbols up. */
 int32_t smla_abi_version(void);
 
 /*
@@ -581,6 +581,109 @@ smla_status smla_cache_resize(const smla_cache_desc* d, int32_t* page_table, int
                               int32_t* refcounts, int32_t* free_list, int32_t* free_count,
                               const int32_t* requests, const int32_t* new_lens, int32_t n,
                               int32_t* work, int32_t* error_word, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * The steps around a prompt. Hidden states are normalised (smla_add_rmsnorm) before the
+ * projections that make q and the latents; a prompt's chunk reads the latents of its context back
+ * from the cache (smla_cache_read), the caller's products expand them to per-head keys and values,
+ * and smla_prompt_attention attends them; smla_token_logprobs scores the tokens of a prompt, of a
+ * draft or of an answer from their logits. The pages describe the decode that follows a prompt; the
+ * formulas here are this library's own statement of these steps.
+ * ---------------------------------------------------------------------------------------
+ */
+typedef struct smla_read_desc {
+  int32_t kv_format;         /* SMLA_KV_* */
+  int32_t page_size;         /* P: power of two, 1..4096 */
+  int64_t num_pages;         /* pages in kv_cache (1 .. 2^31 - 1) */
+  int32_t num_requests;      /* B: 1..65536 rows of page_table */
+  int32_t page_table_stride; /* entries per page_table row (>= 1) */
+  int64_t num_rows;          /* N: rows of latent and rope (0 .. 2^31 - 1) */
+  int64_t latent_stride;     /* elements from one row of latent to the next: a multiple of 8, >= 512 */
+  int64_t rope_stride;       /* of rope: a multiple of 8, >= 64 */
+  float kv_scale;            /* SMLA_KV_FP8_TENSOR: the cache's scale (finite, > 0) */
+  int32_t reserved[3];       /* must be zero */
+} smla_read_desc;
+
+/*
+ * Read cache rows back: row cu_rows[r] + k of latent [N, 512] and rope [N, 64] (bf16, 16-byte
+ * aligned) receives slot starts[r] + k of request r, k < cu_rows[r + 1] - cu_rows[r].
+ *   starts [B] int32, cu_rows [B + 1] int32, ascending; page_table as in smla_decode.
+ * Latents and per-tensor RoPE are bf16(fl32(code * scale)), bf16 values come as they are. Rows that
+ * belong to no request (before cu_rows[0], from cu_rows[B] on) are left as they were. A slot outside
+ * the page table (SMLA_DEVERR_INDEX) or whose page entry is no page (SMLA_DEVERR_PAGE) gives a row
+ * of zeros. error_word: device int32 receiving SMLA_DEVERR_* bits, or NULL.
+ * Status of this and the calls below (before any launch): SMLA_ERR_UNSUPPORTED for an unknown
+ * format or mode, SMLA_ERR_SHAPE for a size, a scale or a non-zero reserved word, SMLA_ERR_NULL or
+ * SMLA_ERR_ALIGN for a pointer (int32 and fp32 arrays 4-byte aligned); no rows launch nothing.
+ * They run on the current device, which must be the tensors', and read their lengths there: a
+ * captured call serves any batch that fits its description.
+ */
+smla_status smla_cache_read(const smla_read_desc* d, const void* kv_cache, const int32_t* page_table,
+                            const int32_t* starts, const int32_t* cu_rows, void* latent, void* rope,
+                            int32_t* error_word, void* stream);
+
+typedef struct smla_norm_desc {
+  int64_t n;          /* rows (0 .. 2^31 - 1) */
+  int64_t x_stride;   /* elements from one row of x to the next: a multiple of 8, >= dim */
+  int32_t dim;        /* D: a multiple of 8, 8..32768 */
+  int32_t group;      /* codes: 128 (a scale for 128 consecutive dims, the last block may be
+                         shorter) or 0 (a scale a row) */
+  int32_t scale_mode; /* SMLA_SCALE_* of the codes */
+  float rms_eps;      /* finite, >= 0 */
+  int32_t reserved[2]; /* must be zero */
+} smla_norm_desc;
+
+/*
+ * The residual's addition, the root-mean-square norm and its outputs: for each row
+ *   h = x + residual (x without one), residual_out = bf16(h),
+ *   y = h * r * weight, r = 1 / sqrt(mean(h^2) + rms_eps), in fp32 from the unrounded h,
+ * stored as bf16 (y_out) and as E4M3 codes with scales: a block's scale by the rule of smla_pack_kv,
+ * codes of fl32(y / scale) from the unrounded y.
+ *   x [n, D] bf16 with x_stride; residual, residual_out, y_out [n, D] bf16, weight [D] bf16, 16-byte
+ *   aligned; codes [n, D] bytes, 8-byte aligned; scales [n, ceil(D / 128)] or [n] fp32.
+ *   residual may be NULL, and so may each output, with codes and scales together; one at least is asked for
+ *   (SMLA_ERR_NULL). residual_out and y_out may be x (with x_stride = D) or residual themselves; apart
+ *   from that outputs must not overlap inputs or one another.
+ * A row with an element that is not finite gets unspecified codes and scales.
+ */
+smla_status smla_add_rmsnorm(const smla_norm_desc* d, const void* x, const void* residual,
+                             const void* weight, void* residual_out, void* y_out, void* codes,
+                             float* scales, void* stream);
+
+/* Element type of the logits (smla_logprob_desc.logits_format). */
+enum {
+  SMLA_LOGITS_BF16 = 0,
+  SMLA_LOGITS_FP32 = 1
+};
+
+typedef struct smla_logprob_desc {
+  int64_t n;             /* rows (0 .. 2^31 - 1) */
+  int64_t row_stride;    /* elements from one row of logits to the next (>= vocab) */
+  int32_t vocab;         /* V: 1..2^24 */
+  int32_t given;         /* G: given tokens a row, 0..1024 */
+  int32_t top;           /* K: alternatives a row, 0..64 */
+  int32_t logits_format; /* SMLA_LOGITS_* */
+  float scale;           /* multiplies the logits (1 / temperature): finite, > 0 */
+  int32_t reserved[3];   /* must be zero */
+} smla_logprob_desc;
+
+/*
+ * Log probabilities from rows of logits, p = softmax(scale * logits[row, 0:V]):
+ *   tokens   [n, G] int32 -> logprobs [n, G] fp32: log p of the given tokens; 0 for -1 (padding), NaN
+ *            for another token outside [0, V) (SMLA_DEVERR_INDEX).
+ *   entropy  [n] fp32 or NULL: -sum p log p, where p log p is 0 for p = 0.
+ *   top_ids  [n, K] int32 (NULL with K = 0): the tokens of the K largest logits, largest first, the
+ *            lower token at a tie (-0 and +0 are one value); -1 where V < K. top_logprobs [n, K]
+ *            fp32 or NULL: their log probabilities (-inf with -1).
+ *   logits aligned to its elements, the rest to 4 bytes. Logits of -inf are tokens that cannot be. A row
+ *   with a NaN or +inf, or with nothing but -inf, gets NaN for its log probabilities and entropy;
+ *   with a NaN its top_ids are unspecified (tokens or -1).
+ * Sums are fp32 in a fixed order.
+ */
+smla_status smla_token_logprobs(const smla_logprob_desc* d, const void* logits, const int32_t* tokens,
+                                float* logprobs, float* entropy, int32_t* top_ids,
+                                float* top_logprobs, int32_t* error_word, void* stream);
 
 /*
  * Size of the library-owned scratch array used by smla_decode_noalloc (16 MiB per device).

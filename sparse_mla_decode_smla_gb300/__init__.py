@@ -18,6 +18,8 @@ SMLA_KV_FP8_TENSOR = 2
 SMLA_CACHE_INDEX_KEYS = 3
 SMLA_SCALE_POW2 = 0
 SMLA_SCALE_FP32 = 1
+SMLA_LOGITS_BF16 = 0
+SMLA_LOGITS_FP32 = 1
 SMLA_Q_BF16 = 0
 SMLA_Q_FP8_E4M3 = 1
 SMLA_DEVERR_INDEX = 1
@@ -41,7 +43,8 @@ EXPORTS = ["smla_status_string", "smla_abi_version", "smla_workspace_size", "sml
            "smla_set_kernel_events", "smla_pack_kv_fp8_tensor", "smla_selftest_wait_timeout",
            "smla_noalloc_read_error", "smla_indexer_logits", "smla_indexer_topk", "smla_store_kv_normed",
            "smla_plan_launches", "smla_tree_workspace_size", "smla_tree_decode", "smla_cache_copy_pages",
-           "smla_cache_compact", "smla_cache_fork", "smla_cache_resize"]
+           "smla_cache_compact", "smla_cache_fork", "smla_cache_resize", "smla_cache_read", "smla_add_rmsnorm",
+           "smla_token_logprobs"]
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -98,6 +101,25 @@ class smla_cache_desc(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("num_requests", ctypes.c_int32),
                 ("page_table_stride", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("num_pages", ctypes.c_int64), ("layer_stride", ctypes.c_int64)]
+
+
+class smla_read_desc(ctypes.Structure):
+    _fields_ = [("kv_format", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+                ("num_requests", ctypes.c_int32), ("page_table_stride", ctypes.c_int32),
+                ("num_rows", ctypes.c_int64), ("latent_stride", ctypes.c_int64), ("rope_stride", ctypes.c_int64),
+                ("kv_scale", ctypes.c_float), ("reserved", ctypes.c_int32 * 3)]
+
+
+class smla_norm_desc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("dim", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("scale_mode", ctypes.c_int32), ("rms_eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32 * 2)]
+
+
+class smla_logprob_desc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("vocab", ctypes.c_int32),
+                ("given", ctypes.c_int32), ("top", ctypes.c_int32), ("logits_format", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32 * 3)]
 
 
 _lib = None
@@ -158,6 +180,12 @@ def lib() -> ctypes.CDLL:
         L.smla_cache_fork.argtypes = [CD, P, P, P, P, P, P, P, I32, P, P, P, P]
         L.smla_cache_resize.restype = I32
         L.smla_cache_resize.argtypes = [CD, P, P, P, P, P, P, P, I32, P, P, P]
+        L.smla_cache_read.restype = I32
+        L.smla_cache_read.argtypes = [ctypes.POINTER(smla_read_desc), P, P, P, P, P, P, P, P]
+        L.smla_add_rmsnorm.restype = I32
+        L.smla_add_rmsnorm.argtypes = [ctypes.POINTER(smla_norm_desc), P, P, P, P, P, P, P, P]
+        L.smla_token_logprobs.restype = I32
+        L.smla_token_logprobs.argtypes = [ctypes.POINTER(smla_logprob_desc), P, P, P, P, P, P, P, P]
         _lib = L
     return _lib
 
@@ -390,3 +418,48 @@ def cache_resize(desc, page_table, lens, refcounts, free_list, free_count, reque
     _check("smla_cache_resize", lib().smla_cache_resize(
         ctypes.byref(desc), _ptr(page_table), _ptr(lens), _ptr(refcounts), _ptr(free_list), _ptr(free_count),
         _ptr(requests), _ptr(new_lens), requests.shape[0], _ptr(work), _ptr(error_word), _stream(stream)))
+
+
+def make_read_desc(kv_format, page_size, num_pages, num_requests, page_table_stride, num_rows, kv_scale=1.0,
+                   latent_stride=512, rope_stride=64) -> smla_read_desc:
+    d = smla_read_desc()
+    d.kv_format, d.page_size, d.num_pages = kv_format, page_size, num_pages
+    d.num_requests, d.page_table_stride, d.num_rows = num_requests, page_table_stride, num_rows
+    d.latent_stride, d.rope_stride, d.kv_scale = latent_stride, rope_stride, kv_scale
+    return d
+
+
+def cache_read(desc, kv_cache, page_table, starts, cu_rows, latent, rope, error_word=None, stream=None):
+    """Cache rows of every request's slots [starts, ...) back as bf16 (smla_cache_read)."""
+    _check("smla_cache_read", lib().smla_cache_read(
+        ctypes.byref(desc), _ptr(kv_cache), _ptr(page_table), _ptr(starts), _ptr(cu_rows), _ptr(latent), _ptr(rope),
+        _ptr(error_word), _stream(stream)))
+
+
+def add_rmsnorm(x, residual, weight, eps, residual_out=None, y=None, codes=None, scales=None, group=128,
+                scale_mode=SMLA_SCALE_POW2, stream=None):
+    """x + residual, its RMS norm as bf16 and as E4M3 codes with scales (smla_add_rmsnorm); x: rows of any stride."""
+    d = smla_norm_desc()
+    d.n, d.dim = x.shape
+    d.x_stride = max(x.stride(0), d.dim) if d.n <= 1 else x.stride(0)
+    d.group, d.scale_mode, d.rms_eps = group, scale_mode, eps
+    _check("smla_add_rmsnorm", lib().smla_add_rmsnorm(
+        ctypes.byref(d), _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(codes), _ptr(scales),
+        _stream(stream)))
+
+
+def token_logprobs(logits, tokens, logprobs, entropy=None, top_ids=None, top_logprobs=None, scale=1.0, error_word=None,
+                   stream=None):
+    """Log probabilities of given tokens [n, G], entropy and top alternatives [n, K] (smla_token_logprobs).
+
+    logits: [n, V] fp32 or bf16 (any other element size is refused), rows of any stride."""
+    d = smla_logprob_desc()
+    d.n, d.vocab = logits.shape
+    d.row_stride = max(logits.stride(0), d.vocab) if d.n <= 1 else logits.stride(0)
+    d.given = 0 if tokens is None else tokens.shape[1]
+    d.top = 0 if top_ids is None else top_ids.shape[1]
+    d.logits_format = {2: SMLA_LOGITS_BF16, 4: SMLA_LOGITS_FP32}.get(logits.element_size(), -1)
+    d.scale = scale
+    _check("smla_token_logprobs", lib().smla_token_logprobs(
+        ctypes.byref(d), _ptr(logits), _ptr(tokens), _ptr(logprobs), _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs),
+        _ptr(error_word), _stream(stream)))

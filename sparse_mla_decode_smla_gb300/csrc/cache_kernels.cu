@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "quantise.cuh"
 
 namespace smla {
 
@@ -26,31 +27,6 @@ struct NormRope {
 };
 
 __device__ __forceinline__ uint32_t bf16x2_pack_rn(float lo, float hi) { return pack_bf16x2(lo, hi); }
-
-// x / scale for the E4M3 conversion. Where scale is a power of two in [2^-126, 2^126] its
-// reciprocal is exact, so x * (1 / scale) is the same real number x / scale rounded once: the
-// same fp32 value as the correctly rounded division, for every x. Otherwise divide.
-struct ScaleDiv {
-  float scale, inv;
-  bool exact;
-  __device__ __forceinline__ explicit ScaleDiv(float sc) : scale(sc) {
-    const uint32_t b = __float_as_uint(sc);
-    exact = (b & 0x007fffffu) == 0u && sc >= 0x1p-126f && sc <= 0x1p126f;
-    inv = exact ? __frcp_rn(sc) : 0.f;
-  }
-  // E4M3 codes of x[0..2n) / scale, two per 16-bit word: one branch for the whole run
-  template <int N>
-  __device__ __forceinline__ void codes(const float* x, uint16_t* out) const {
-    if (exact) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) out[i] = f32x2_to_e4m3x2(__fmul_rn(x[2 * i], inv), __fmul_rn(x[2 * i + 1], inv));
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        out[i] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
-    }
-  }
-};
 
 // One warp per row. Lane l owns latent elements [16l, 16l+16); lanes 8b..8b+7 form block b.
 // With NORM the row is first normalised (RMSNorm over the 512 latent dims: fp32 sum of
@@ -166,17 +142,7 @@ __global__ void __launch_bounds__(256, FMT == SMLA_KV_BF16 ? 5 : 6) pack_kernel(
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
-  float scale = 1.f;
-  if (amax > 0.f) {
-    const float ratio = __fdiv_rn(amax, 448.f);
-    if (scale_mode == SMLA_SCALE_POW2) {
-      int e;
-      const float m = frexpf(ratio, &e);  // ratio = m * 2^e, m in [0.5, 1)
-      scale = (m == 0.5f) ? ratio : ldexpf(1.f, e);
-    } else {
-      scale = ratio;
-    }
-  }
+  const float scale = block_scale(amax, scale_mode);
   uint16_t c[8];
   ScaleDiv(scale).codes<8>(v, c);
   uint8_t* dst = kv + slot * kFp8RowBytes;

@@ -1,0 +1,56 @@
+// Internal launchers of the operators around a prompt (not part of the C ABI).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/smla.h"
+
+namespace smla {
+
+struct ReadArgs {
+  const uint8_t* kv;
+  const int32_t* page_table;
+  const int32_t* starts;
+  const int32_t* cu;
+  void* latent;
+  void* rope;
+  int32_t* err;
+  int32_t B, stride, log2_page, kv_format;
+  int64_t num_pages, N, latent_stride, rope_stride;
+  float kv_scale;
+};
+cudaError_t launch_cache_read(const ReadArgs& a, cudaStream_t s);
+
+struct NormArgs {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  void* sum;
+  void* y;
+  uint8_t* codes;
+  float* scales;
+  int64_t n, x_stride;
+  int32_t dim, group, scale_mode;
+  float eps;
+};
+constexpr int kNormMaxDim = 32768;
+cudaError_t launch_add_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t s);
+
+struct LogprobArgs {
+  const void* x;
+  const int32_t* tokens;
+  float* logprobs;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  int32_t* err;
+  int64_t n, stride;
+  int32_t V, given, top, f32;
+  float scale;
+};
+constexpr int kLogprobMaxTop = 64, kLogprobMaxGiven = 1024, kLogprobMaxVocab = 1 << 24;
+cudaError_t launch_token_logprobs(const LogprobArgs& a, int num_sms, cudaStream_t s);
+
+}  // namespace smla

@@ -1,0 +1,44 @@
+// E4M3 codes with a scale: the rules that the cache write and the norm's 8-bit output share.
+#pragma once
+
+#include "common.cuh"
+
+namespace smla {
+
+// The scale of a block whose largest magnitude is amax: 1 for an all-zero block, else fl32(amax / 448)
+// or (SMLA_SCALE_POW2) the smallest power of two that is no less.
+__device__ __forceinline__ float block_scale(float amax, int scale_mode) {
+  if (!(amax > 0.f)) return 1.f;
+  const float ratio = __fdiv_rn(amax, 448.f);
+  if (scale_mode != SMLA_SCALE_POW2) return ratio;
+  int e;
+  const float m = frexpf(ratio, &e);  // ratio = m * 2^e, m in [0.5, 1)
+  return (m == 0.5f) ? ratio : ldexpf(1.f, e);
+}
+
+// x / scale for the E4M3 conversion. Where scale is a power of two in [2^-126, 2^126] its
+// reciprocal is exact, so x * (1 / scale) is the same real number x / scale rounded once: the
+// same fp32 value as the correctly rounded division, for every x. Otherwise divide.
+struct ScaleDiv {
+  float scale, inv;
+  bool exact;
+  __device__ __forceinline__ explicit ScaleDiv(float sc) : scale(sc) {
+    const uint32_t b = __float_as_uint(sc);
+    exact = (b & 0x007fffffu) == 0u && sc >= 0x1p-126f && sc <= 0x1p126f;
+    inv = exact ? __frcp_rn(sc) : 0.f;
+  }
+  // E4M3 codes of x[0..2n) / scale, two per 16-bit word: one branch for the whole run
+  template <int N>
+  __device__ __forceinline__ void codes(const float* x, uint16_t* out) const {
+    if (exact) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) out[i] = f32x2_to_e4m3x2(__fmul_rn(x[2 * i], inv), __fmul_rn(x[2 * i + 1], inv));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        out[i] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
+    }
+  }
+};
+
+}  // namespace smla

@@ -11,12 +11,14 @@
 #include "cache_pages.h"
 #include "indexer.h"
 #include "kernels.h"
+#include "prompt.h"
 #include "tree_decode.h"
 
 namespace {
 
 constexpr size_t kWsAlign = 256;
 constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxCount = (int64_t(1) << 31) - 1;
 
 // Per-device facts, looked up on first use. Several host threads may look them up at
 // once; they store the same values, through atomics.
@@ -692,6 +694,120 @@ smla_status smla_cache_resize(const smla_cache_desc* d, int32_t* page_table, int
   if (smla::launch_cache_resize(c, t, requests, new_lens, n, work, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return SMLA_ERR_CUDA;
   return SMLA_OK;
+}
+
+smla_status smla_cache_read(const smla_read_desc* d, const void* kv_cache, const int32_t* page_table,
+                            const int32_t* starts, const int32_t* cu_rows, void* latent, void* rope,
+                            int32_t* error_word, void* stream) {
+  if (!d) return SMLA_ERR_NULL;
+  if (d->kv_format != SMLA_KV_BF16 && d->kv_format != SMLA_KV_FP8_DS && d->kv_format != SMLA_KV_FP8_TENSOR)
+    return SMLA_ERR_UNSUPPORTED;
+  if (!is_pow2(d->page_size) || d->page_size > 4096 || d->num_pages < 1 || d->num_pages > kMaxCount || d->num_requests < 1 ||
+      d->num_requests > (1 << 16) || d->page_table_stride < 1 || d->num_rows < 0 || d->num_rows > kMaxCount)
+    return SMLA_ERR_SHAPE;
+  if (d->latent_stride < 512 || d->latent_stride % 8 || d->latent_stride > kMaxCount || d->rope_stride < 64 ||
+      d->rope_stride % 8 || d->rope_stride > kMaxCount)
+    return SMLA_ERR_SHAPE;
+  if (d->kv_format == SMLA_KV_FP8_TENSOR && !(isfinite(d->kv_scale) && d->kv_scale > 0.f)) return SMLA_ERR_SHAPE;
+  if (d->reserved[0] || d->reserved[1] || d->reserved[2]) return SMLA_ERR_SHAPE;
+  if (d->num_rows == 0) return SMLA_OK;
+  if (!kv_cache || !page_table || !starts || !cu_rows || !latent || !rope) return SMLA_ERR_NULL;
+  if (!aligned(kv_cache, 16) || !aligned(latent, 16) || !aligned(rope, 16) || !aligned(page_table, 4) ||
+      !aligned(starts, 4) || !aligned(cu_rows, 4) || !aligned(error_word, 4))
+    return SMLA_ERR_ALIGN;
+  int sms = 0;
+  const smla_status st = current_device(&sms);
+  if (st != SMLA_OK) return st;
+  smla::ReadArgs a;
+  memset(&a, 0, sizeof(a));
+  a.kv = static_cast<const uint8_t*>(kv_cache);
+  a.page_table = page_table;
+  a.starts = starts;
+  a.cu = cu_rows;
+  a.latent = latent;
+  a.rope = rope;
+  a.err = error_word;
+  a.B = d->num_requests;
+  a.stride = d->page_table_stride;
+  a.log2_page = ilog2(d->page_size);
+  a.kv_format = d->kv_format;
+  a.num_pages = d->num_pages;
+  a.N = d->num_rows;
+  a.latent_stride = d->latent_stride;
+  a.rope_stride = d->rope_stride;
+  a.kv_scale = d->kv_scale;
+  return smla::launch_cache_read(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+smla_status smla_add_rmsnorm(const smla_norm_desc* d, const void* x, const void* residual, const void* weight,
+                             void* residual_out, void* y_out, void* codes, float* scales, void* stream) {
+  if (!d) return SMLA_ERR_NULL;
+  if (d->scale_mode != SMLA_SCALE_POW2 && d->scale_mode != SMLA_SCALE_FP32) return SMLA_ERR_UNSUPPORTED;
+  if (d->group != 0 && d->group != 128) return SMLA_ERR_UNSUPPORTED;
+  if (d->n < 0 || d->n > kMaxCount || d->dim < 8 || d->dim > smla::kNormMaxDim || d->dim % 8 || d->x_stride < d->dim ||
+      d->x_stride % 8 || d->x_stride > kMaxCount || !(isfinite(d->rms_eps) && d->rms_eps >= 0.f) || d->reserved[0] ||
+      d->reserved[1])
+    return SMLA_ERR_SHAPE;
+  if (d->n == 0) return SMLA_OK;
+  if (!x || !weight || (codes != nullptr) != (scales != nullptr) || (!residual_out && !y_out && !codes)) return SMLA_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) || !aligned(y_out, 16) ||
+      !aligned(codes, 8) || !aligned(scales, 4))
+    return SMLA_ERR_ALIGN;
+  int sms = 0;
+  const smla_status st = current_device(&sms);
+  if (st != SMLA_OK) return st;
+  smla::NormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.sum = residual_out;
+  a.y = y_out;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = scales;
+  a.n = d->n;
+  a.x_stride = d->x_stride;
+  a.dim = d->dim;
+  a.group = d->group;
+  a.scale_mode = d->scale_mode;
+  a.eps = d->rms_eps;
+  return smla::launch_add_rmsnorm(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+smla_status smla_token_logprobs(const smla_logprob_desc* d, const void* logits, const int32_t* tokens, float* logprobs,
+                                float* entropy, int32_t* top_ids, float* top_logprobs, int32_t* error_word, void* stream) {
+  if (!d) return SMLA_ERR_NULL;
+  if (d->logits_format != SMLA_LOGITS_BF16 && d->logits_format != SMLA_LOGITS_FP32) return SMLA_ERR_UNSUPPORTED;
+  if (d->n < 0 || d->n > kMaxCount || d->vocab < 1 || d->vocab > smla::kLogprobMaxVocab || d->row_stride < d->vocab ||
+      d->row_stride > kMaxCount || d->given < 0 || d->given > smla::kLogprobMaxGiven || d->top < 0 ||
+      d->top > smla::kLogprobMaxTop || !(isfinite(d->scale) && d->scale > 0.f) || d->reserved[0] || d->reserved[1] ||
+      d->reserved[2])
+    return SMLA_ERR_SHAPE;
+  if (d->n == 0) return SMLA_OK;
+  if (!logits || (d->given > 0 && (!tokens || !logprobs)) || (d->top > 0 && !top_ids)) return SMLA_ERR_NULL;
+  if (!aligned(logits, d->logits_format == SMLA_LOGITS_FP32 ? 4 : 2) || !aligned(tokens, 4) || !aligned(logprobs, 4) ||
+      !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4) || !aligned(error_word, 4))
+    return SMLA_ERR_ALIGN;
+  int sms = 0;
+  const smla_status st = current_device(&sms);
+  if (st != SMLA_OK) return st;
+  smla::LogprobArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = logits;
+  a.tokens = tokens;
+  a.logprobs = logprobs;
+  a.entropy = entropy;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.err = error_word;
+  a.n = d->n;
+  a.stride = d->row_stride;
+  a.V = d->vocab;
+  a.given = d->given;
+  a.top = d->top;
+  a.f32 = d->logits_format == SMLA_LOGITS_FP32;
+  a.scale = d->scale;
+  return smla::launch_token_logprobs(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
 smla_status smla_selftest_wait_timeout(int32_t* error_word, uint32_t limit_us, void* stream) {
