@@ -651,6 +651,65 @@ smla_status smla_add_rmsnorm(const smla_norm_desc* d, const void* x, const void*
                              const void* weight, void* residual_out, void* y_out, void* codes,
                              float* scales, void* stream);
 
+typedef struct smla_prompt_desc {
+  int32_t num_tokens;   /* T: rows of q and out (0 .. 2^31 - 1, T * H < 2^31) */
+  int32_t num_keys;     /* N: rows of k, v and k_rope (>= 1) */
+  int32_t num_heads;    /* H: 1..1024 query heads */
+  int32_t num_kv_heads; /* HK: divides H; query head h attends kv head h / (H / HK) */
+  int32_t num_requests; /* B: 1..65536 */
+  int32_t rope_dim;     /* 64, or 0: no RoPE part */
+  int32_t causal;       /* 1, or 0: a token sees every key of its request */
+  float sm_scale;       /* multiplies q.k (finite, > 0) */
+  float softcap;        /* c > 0: scores become c tanh(s / c); 0: they stay as they are */
+  int32_t reserved[3];  /* must be zero */
+  /* elements from one token (row) and one head to the next: multiples of 8, at least a row's dims */
+  int64_t q_token_stride, q_head_stride;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int64_t rope_token_stride;
+} smla_prompt_desc;
+
+/*
+ * Bytes of device workspace smla_prompt_attention needs for `d` on the current device: the error word,
+ * the plan and the parts of work that several SMs share (about 80 MB, whatever the batch's size). The
+ * caller allocates it (256-byte aligned) and zeroes it once before first use (and again after a call that set
+ * SMLA_DEVERR_TIMEOUT); smla_read_error reads and clears the error word. Writes 0 into *bytes on error.
+ */
+smla_status smla_prompt_workspace_size(const smla_prompt_desc* d, size_t* bytes);
+
+/*
+ * Attention of packed prompts over per-head keys and values: a request's tokens attend its own keys only.
+ *   q      bf16, row of token t and head h at q + t * q_token_stride + h * q_head_stride: 128 dims that
+ *          pair with k, then rope_dim that pair with k_rope. 16-byte aligned, as k, v and k_rope are.
+ *   k, v   bf16, 128 dims a row and kv head, with their strides (they may be views of one
+ *          tensor [N, HK, 256], as one up-projection of the latents writes them).
+ *   k_rope [N, 64] bf16, shared by all heads, or NULL with rope_dim = 0.
+ *   cu_q, cu_k [B + 1] int32, ascending: request r has the tokens [cu_q[r], cu_q[r + 1]) and the keys
+ *          [cu_k[r], cu_k[r + 1]). Its tokens are the last of its keys: token i of nq stands at
+ *          p_i = nk - nq + i. One token a request is single-token decode.
+ *   prefix_lens [B] int32 or NULL: the first prefix_lens[r] keys are visible to every token (clamped
+ *          to [0, nk]). Causal: token i sees the keys j <= p_i and those of the prefix.
+ *   slopes [H] fp32 or NULL: the bias -slope_h |p_i - j| is added after the cap.
+ *   sink   [H] fp32 or NULL: as in smla_decode.
+ *   out    [T, H, 128] bf16, 16-byte aligned: sum_j e^{x_j} v_j / (sum_j e^{x_j} + [sink] e^{sigma_h}),
+ *          0 where a token sees nothing; lse [T, H] fp32 or NULL: the natural log of the
+ *          denominator (-inf where it is empty). Rows of no request are left as they were.
+ *   workspace smla_prompt_workspace_size(d) bytes, 256-byte aligned; calls that may overlap (two
+ *          streams, two graphs) need one each.
+ * A request whose offsets do not ascend or reach past T or N is left out (SMLA_DEVERR_INDEX): its rows are
+ * not written. What a token does not see never reaches its result, whatever the values there: a value row
+ * with a NaN or an infinity makes out (not lse) of the tokens that see it NaN or infinite and leaves the
+ * others as they are.
+ *
+ * Precision. Scores, softmax statistics and sums are fp32; q, k, v and the weights enter the tensor cores as
+ * bf16. Results do not depend on how the GPU schedules the work.
+ */
+smla_status smla_prompt_attention(const smla_prompt_desc* d, const void* q, const void* k, const void* v,
+                                  const void* k_rope, const int32_t* cu_q, const int32_t* cu_k,
+                                  const int32_t* prefix_lens, const float* slopes, const float* sink,
+                                  void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
 /* Element type of the logits (smla_logprob_desc.logits_format). */
 enum {
   SMLA_LOGITS_BF16 = 0,

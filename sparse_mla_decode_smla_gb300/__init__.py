@@ -44,7 +44,7 @@ EXPORTS = ["smla_status_string", "smla_abi_version", "smla_workspace_size", "sml
            "smla_noalloc_read_error", "smla_indexer_logits", "smla_indexer_topk", "smla_store_kv_normed",
            "smla_plan_launches", "smla_tree_workspace_size", "smla_tree_decode", "smla_cache_copy_pages",
            "smla_cache_compact", "smla_cache_fork", "smla_cache_resize", "smla_cache_read", "smla_add_rmsnorm",
-           "smla_token_logprobs"]
+           "smla_token_logprobs", "smla_prompt_workspace_size", "smla_prompt_attention"]
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -122,6 +122,14 @@ class smla_logprob_desc(ctypes.Structure):
                 ("scale", ctypes.c_float), ("reserved", ctypes.c_int32 * 3)]
 
 
+class smla_prompt_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("num_tokens", "num_keys", "num_heads", "num_kv_heads", "num_requests",
+                                               "rope_dim", "causal")] +
+                [("sm_scale", ctypes.c_float), ("softcap", ctypes.c_float), ("reserved", ctypes.c_int32 * 3)] +
+                [(n, ctypes.c_int64) for n in ("q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
+                                               "v_token_stride", "v_head_stride", "rope_token_stride")])
+
+
 _lib = None
 
 
@@ -186,6 +194,11 @@ def lib() -> ctypes.CDLL:
         L.smla_add_rmsnorm.argtypes = [ctypes.POINTER(smla_norm_desc), P, P, P, P, P, P, P, P]
         L.smla_token_logprobs.restype = I32
         L.smla_token_logprobs.argtypes = [ctypes.POINTER(smla_logprob_desc), P, P, P, P, P, P, P, P]
+        MD = ctypes.POINTER(smla_prompt_desc)
+        L.smla_prompt_workspace_size.restype = I32
+        L.smla_prompt_workspace_size.argtypes = [MD, ctypes.POINTER(SZ)]
+        L.smla_prompt_attention.restype = I32
+        L.smla_prompt_attention.argtypes = [MD, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
         _lib = L
     return _lib
 
@@ -434,6 +447,35 @@ def cache_read(desc, kv_cache, page_table, starts, cu_rows, latent, rope, error_
     _check("smla_cache_read", lib().smla_cache_read(
         ctypes.byref(desc), _ptr(kv_cache), _ptr(page_table), _ptr(starts), _ptr(cu_rows), _ptr(latent), _ptr(rope),
         _ptr(error_word), _stream(stream)))
+
+
+def make_prompt_desc(num_tokens, num_keys, num_heads, num_kv_heads, num_requests, rope_dim, sm_scale, causal=True,
+                     softcap=0.0, q_strides=None, k_strides=None, v_strides=None, rope_stride=64) -> smla_prompt_desc:
+    """Strides: (token, head) in elements; None: rows [tokens, heads, dims] that follow one another."""
+    d = smla_prompt_desc()
+    d.num_tokens, d.num_keys, d.num_heads, d.num_kv_heads = num_tokens, num_keys, num_heads, num_kv_heads
+    d.num_requests, d.rope_dim, d.causal = num_requests, rope_dim, int(causal)
+    d.sm_scale, d.softcap = sm_scale, softcap
+    dim = 128 + rope_dim
+    d.q_token_stride, d.q_head_stride = q_strides or (num_heads * dim, dim)
+    d.k_token_stride, d.k_head_stride = k_strides or (num_kv_heads * 128, 128)
+    d.v_token_stride, d.v_head_stride = v_strides or (num_kv_heads * 128, 128)
+    d.rope_token_stride = rope_stride
+    return d
+
+
+def prompt_workspace_size(desc: smla_prompt_desc) -> int:
+    n = ctypes.c_size_t(0)
+    _check("smla_prompt_workspace_size", lib().smla_prompt_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def prompt_attention(desc, q, k, v, k_rope, cu_q, cu_k, prefix_lens, slopes, sink, out, lse, workspace, stream=None):
+    """Attention of packed prompts over per-head keys and values (smla_prompt_attention)."""
+    _check("smla_prompt_attention", lib().smla_prompt_attention(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(k_rope), _ptr(cu_q), _ptr(cu_k), _ptr(prefix_lens),
+        _ptr(slopes), _ptr(sink), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def add_rmsnorm(x, residual, weight, eps, residual_out=None, y=None, codes=None, scales=None, group=128,

@@ -53,4 +53,32 @@ struct LogprobArgs {
 constexpr int kLogprobMaxTop = 64, kLogprobMaxGiven = 1024, kLogprobMaxVocab = 1 << 24;
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int num_sms, cudaStream_t s);
 
+struct PromptArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* rope;         // NULL: none
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const int32_t* prefix;    // NULL: none
+  const float* slopes;      // NULL: none
+  const float* sink;        // NULL: none
+  void* out;
+  float* lse;
+  uint8_t* ws;              // error word, counters and a line a request
+  int32_t* counts;          // [slots][row tile]: pieces that have ended, zero between calls
+  float* parts;             // [slots]
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, rope_token;  // strides in elements
+  int32_t T, N, H, HK, B, causal, log2_pack, sms, slots;
+  float c2;                 // sm_scale log2(e)
+  float cap2, cap_in;       // cap log2(e) (0: no cap); 2 sm_scale log2(e) / cap
+};
+struct PromptLayout {
+  int slots;
+  size_t counts, parts, bytes;
+};
+PromptLayout prompt_layout(int64_t requests, int num_sms);
+constexpr int kPromptMaxRequests = 1 << 16;
+cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t s);
+
 }  // namespace smla

@@ -1,0 +1,894 @@
+// Attention of packed prompts over per-head keys and values (smla_prompt_attention), on the 5th-generation tensor cores.
+//
+//   s_ij = sm_scale (<q_i[0:128], k_j> + <q_i[128:192], k_rope_j>),  x_ij = [cap tanh](s_ij) - slope |p_i - j|,
+//   out_i = sum_j e^{x_ij} v_j / (sum_j e^{x_ij} + e^{sink}) over the keys j < lim_i:
+// every mask here (the other documents, the future, a visible prefix, a shorter context) leaves a row the first lim_i
+// keys of its request, so that a number a row is all that the kernel knows of masks.
+//
+// Work. An item is 256 rows of one request and kv head, in two row tiles of 128: consecutive tokens, with as many query
+// heads of the kv head as a power of two allows beside one another (a single token's grouped heads share a tile). Its
+// keys come in tiles of 128. Items whose keys are many beside the batch's whole work are cut into pieces that leave their
+// parts in the workspace; the piece that ends last joins them, in the order of the keys. The items of a request run from
+// the last rows (most keys) to the first, some heads at a time, so that SMs that run together share keys in L2. A small
+// kernel lays the items out from the lengths on the device; the CTAs, one an SM, take them off a counter.
+//
+// A key tile on one SM: S = Q K^T (12 MMAs of 128 x 128 x 16 a row tile), the weights P = 2^(x - m) in BF16 written over
+// S in tensor memory, O += P V (8 MMAs, P from tensor memory). The two row tiles alternate: one's softmax runs while the
+// tensor cores work for the other. m moves only when a row's maximum grows by more than 2^8, so O is rescaled rarely, by
+// the softmax threads themselves; by the time S of a tile is there, PV of the tile before is complete.
+//
+// P in BF16 costs 2^-9 of each weight, independently; the sums of weights are of the fp32 values.
+//
+// What is hidden never counts: its score is replaced, and in tiles that not all rows see whole, value rows past the last
+// key become zeros and a value row with a non-finite element does too and is remembered, so that the rows that see it
+// become NaN and the others never meet it.
+//
+// Per CTA (384 threads): warps 0-3 and 4-7 softmax and epilogue of a row tile each (a thread a row), 8 MMA issue, 9 items
+// and TMA loads, 10-11 the check of value tiles. Q takes 96 KB, 16 KB units of keys and values share a ring of eight.
+// Every wait is bounded in time; one that gives up sets SMLA_DEVERR_TIMEOUT.
+#include <math_constants.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "prompt.h"
+#include "tcgen05.cuh"
+
+namespace smla {
+namespace {
+
+constexpr int kPaM = 128, kPaN = 128;      // rows of a row tile, keys of a key tile
+constexpr int kPaRows = 2 * kPaM;          // rows of an item
+constexpr int kPaUnit = 16384;             // bytes of a ring unit: 128 keys x 64 dims, or 64 values x 128 dims
+constexpr int kPaThreads = 384;
+constexpr int kPaMmaWarp = 8, kPaLoadWarp = 9, kPaGuardWarp = 10, kPaGuards = 2;
+constexpr int kPaReady = 8;                // guarded value units between the guards and the MMAs at most: 6
+constexpr float kPaRescale = 8.f;
+constexpr int kPaMinTiles = 8;             // key tiles of a piece at least
+constexpr int kPaSlotFloats = kPaRows * 128 + kPaRows * 2;  // a piece's part: O, then (m, l) of each row
+
+struct PaItem {
+  int q0;       // row of q of the request's first token
+  int nq, nk;   // tokens and keys of the request
+  int k0;       // row of k of the request's first key
+  int tok0;     // first token of the item
+  int head0;    // first query head
+  int kvh;      // kv head
+  int kt0;      // first key tile of this piece
+  int n[2];     // key tiles of this piece that each row tile sees
+  int prefix;   // keys that every token sees
+  int pieces;   // pieces of the item (1: not cut)
+  int slot;     // of the item's first piece
+  int piece;
+  int last;     // no more items
+  int pad;
+};
+
+template <int ROPE>
+struct PaLay {
+  static constexpr int qk_units = 2 + ROPE / 64;  // units of a key tile and of a row tile of q
+  static constexpr int ring = ROPE ? 8 : 10;
+  static constexpr size_t q = 0;
+  static constexpr size_t units = q + 2 * qk_units * size_t(kPaUnit);
+  static constexpr size_t item = units + ring * size_t(kPaUnit);
+  static constexpr size_t bad = item + 2 * sizeof(PaItem);
+  static constexpr size_t flag = bad + 8;
+  static constexpr size_t tmem = flag + 8;
+  static constexpr size_t bars = tmem + 16;
+  static constexpr size_t bytes = bars + 56 * 8;
+  static_assert(bytes <= 232448 && bars % 8 == 0 && units % 1024 == 0, "shared memory");
+};
+enum {
+  A_UFULL = 0,
+  A_UFREE = A_UFULL + 10,
+  A_QFULL = A_UFREE + 10,  // [row tile], and so the next ones
+  A_QFREE = A_QFULL + 2,
+  A_S = A_QFREE + 2,
+  A_P = A_S + 2,
+  A_O = A_P + 2,
+  A_ITEM = A_O + 2,        // [item parity]
+  A_TAKEN = A_ITEM + 2,
+  A_READY = A_TAKEN + 2,
+  A_GFULL = A_READY + kPaReady,
+  A_DRAIN = A_GFULL + kPaReady,
+  A_COUNT
+};
+static_assert(A_COUNT <= 56, "barriers");
+
+// ---------------------------------------------------------------- the plan
+
+struct PaReq {
+  int q0, nq, k0, nk, prefix, blocks;
+};
+
+// 1: a request with tokens, 0: without, -1: one that does not fit the description
+__device__ __forceinline__ int pa_request(const PromptArgs& p, int r, PaReq& q) {
+  const int64_t a = p.cu_q[r], b = p.cu_q[r + 1], c = p.cu_k[r], d = p.cu_k[r + 1];
+  q = PaReq{};
+  if (a < 0 || b < a || b > p.T || c < 0 || d < c || d > p.N) return -1;
+  q.q0 = static_cast<int>(a);
+  q.nq = static_cast<int>(b - a);
+  q.k0 = static_cast<int>(c);
+  q.nk = static_cast<int>(d - c);
+  q.prefix = p.prefix ? min(max(p.prefix[r], 0), q.nk) : 0;
+  const int tb = kPaRows >> p.log2_pack;
+  q.blocks = (q.nq + tb - 1) / tb;
+  return q.nq > 0;
+}
+// the keys that token i of a request sees
+__device__ __forceinline__ int pa_lim(int causal, int nq, int nk, int prefix, int i) {
+  return causal ? min(max(nk - nq + i + 1, prefix), nk) : nk;
+}
+__device__ __forceinline__ int pa_tiles(const PromptArgs& p, const PaReq& q, int token) {
+  return (max(pa_lim(p.causal, q.nq, q.nk, q.prefix, token), 0) + kPaN - 1) / kPaN;
+}
+
+struct PaHead {  // the start of the workspace
+  int32_t err, claim, total, len;  // device error word; next item; items; key tiles of a piece
+};
+struct PaTab {  // a request's line in the plan
+  int32_t item0, slot0, pieces, pad;
+};
+__device__ __forceinline__ PaTab* pa_table(const PromptArgs& p) { return reinterpret_cast<PaTab*>(p.ws + 256); }
+
+constexpr int kPlanThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ T plan_sum(T v, T* sh) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  T s = 0;
+  for (int i = 0; i < kPlanThreads / 32; ++i) s += sh[i];
+  return s;
+}
+
+// Lays out the items: a piece is as long as half of an SM's share of the key tiles, longer where the workspace asks for it.
+__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptArgs p) {
+  __shared__ int64_t sh[kPlanThreads / 32];
+  __shared__ int2 scan[kPlanThreads / 32];
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int tb = kPaRows >> p.log2_pack, G = p.H >> p.log2_pack;
+  PaHead* head = reinterpret_cast<PaHead*>(p.ws);
+  int64_t work = 0;
+  for (int r = tid; r < p.B; r += kPlanThreads) {
+    PaReq q;
+    const int ok = pa_request(p, r, q);
+    if (ok < 0) atomicOr(&head->err, SMLA_DEVERR_INDEX);
+    if (ok > 0) work += int64_t(q.blocks) * G * (pa_tiles(p, q, min(tb, q.nq) - 1) + pa_tiles(p, q, q.nq - 1) + 1) / 2;
+  }
+  work = plan_sum(work, sh);
+  int64_t len = max(int64_t(kPaMinTiles), (work + 2 * p.sms - 1) / (2 * p.sms));
+  for (;; len *= 2) {
+    int64_t slots = 0;
+    for (int r = tid; r < p.B; r += kPlanThreads) {
+      PaReq q;
+      if (pa_request(p, r, q) > 0) {
+        const int64_t n = (pa_tiles(p, q, q.nq - 1) + len - 1) / len;
+        if (n > 1) slots += int64_t(q.blocks) * G * n;
+      }
+    }
+    if (plan_sum(slots, sh) <= p.slots) break;
+  }
+  int items = 0, slots = 0;  // of the requests before this round's
+  for (int r0 = 0; r0 < p.B; r0 += kPlanThreads) {
+    const int r = r0 + tid;
+    int2 v = make_int2(0, 0);
+    int n = 1;
+    PaReq q;
+    if (r < p.B && pa_request(p, r, q) > 0) {
+      n = max(1, static_cast<int>((pa_tiles(p, q, q.nq - 1) + len - 1) / len));
+      v.x = q.blocks * G * n;
+      v.y = n > 1 ? v.x : 0;
+    }
+    int2 x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o);
+      if (lane >= o) {
+        x.x += a;
+        x.y += b;
+      }
+    }
+    __syncthreads();
+    if (lane == 31) scan[tid >> 5] = x;
+    __syncthreads();
+    int2 before = make_int2(items, slots);
+    for (int i = 0; i < kPlanThreads / 32; ++i) {
+      if (i < (tid >> 5)) {
+        before.x += scan[i].x;
+        before.y += scan[i].y;
+      }
+      items += scan[i].x;
+      slots += scan[i].y;
+    }
+    if (r < p.B) pa_table(p)[r] = PaTab{before.x + x.x - v.x, before.y + x.y - v.y, n, 0};
+  }
+  if (tid == 0) {
+    head->claim = 0;
+    head->total = items;
+    head->len = static_cast<int32_t>(min(len, int64_t(1) << 30));
+  }
+}
+
+// Item `idx` (by a whole warp); false for a piece past the end of its rows' keys.
+__device__ __forceinline__ bool pa_item(const PromptArgs& p, int idx, PaItem& it) {
+  const int lane = threadIdx.x & 31;
+  const PaTab* tab = pa_table(p);
+  int lo = 0, hi = p.B;  // the last request whose first item is not past idx
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, at < hi && __ldcg(&tab[at].item0) <= idx);
+    const int k = 31 - __clz(le);  // lane 0 holds
+    hi = min(hi, lo + (k + 1) * step);
+    lo += k * step;
+  }
+  const int4 t4 = __ldcg(reinterpret_cast<const int4*>(tab + lo));
+  const int len = __ldcg(&reinterpret_cast<const PaHead*>(p.ws)->len);
+  PaReq q;
+  pa_request(p, lo, q);
+  const int G = p.H >> p.log2_pack, g = p.H / p.HK, np = t4.z;
+  // heads at a time: their keys and values take up to 32 MB
+  const int kv_heads = max(1, min(p.HK, static_cast<int>((int64_t(32) << 20) / (int64_t(q.nk) * 512 + 1))));
+  const int gc = kv_heads * (g >> p.log2_pack);
+  int i = idx - t4.x;
+  const int64_t chunk_items = int64_t(gc) * q.blocks * np;
+  const int chunk = static_cast<int>(i / chunk_items);
+  i -= static_cast<int>(chunk * chunk_items);
+  const int wide = min(gc, G - chunk * gc);
+  const int block = q.blocks - 1 - i / (wide * np);
+  i %= wide * np;
+  const int hg = chunk * gc + i / np;
+  it.piece = i % np;
+  it.q0 = q.q0;
+  it.nq = q.nq;
+  it.nk = q.nk;
+  it.k0 = q.k0;
+  it.prefix = q.prefix;
+  it.tok0 = block * (kPaRows >> p.log2_pack);
+  it.head0 = hg << p.log2_pack;
+  it.kvh = it.head0 / g;
+  const int tt = kPaM >> p.log2_pack;  // tokens of a row tile
+  const bool two = it.tok0 + tt < q.nq;
+  const int n0 = pa_tiles(p, q, min(it.tok0 + tt, q.nq) - 1), n1 = two ? pa_tiles(p, q, min(it.tok0 + 2 * tt, q.nq) - 1) : 0;
+  const int all = max(n0, n1);
+  it.pieces = max(1, (all + len - 1) / len);
+  it.slot = t4.y + (block * G + hg) * np;
+  const int per = (all + it.pieces - 1) / it.pieces;
+  it.kt0 = it.piece * per;
+  it.n[0] = max(0, min(per, n0 - it.kt0));
+  it.n[1] = max(0, min(per, n1 - it.kt0));
+  it.last = 0;
+  return it.piece < it.pieces;
+}
+
+// ---------------------------------------------------------------- helpers
+
+__device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+}
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 f2_parts(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// 32 bytes to global memory: one whole sector
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                 "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int ROPE, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kPaThreads, 1)
+    prompt_attention_kernel(const PromptArgs p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                            const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ CUtensorMap v_map) {
+  using Y = PaLay<ROPE>;
+  constexpr int QU = Y::qk_units, R = Y::ring;
+  extern __shared__ __align__(1024) uint8_t sm[];  // all of it: the swizzle atoms need its start
+  const uint32_t sb = smem_u32(sm);
+  auto bar = [&](int k) -> uint32_t { return sb + uint32_t(Y::bars) + 8u * k; };
+  auto unit = [&](int u) -> uint32_t { return sb + uint32_t(Y::units) + uint32_t(u % R) * kPaUnit; };
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int32_t* err = reinterpret_cast<int32_t*>(p.ws);
+  PaItem* items = reinterpret_cast<PaItem*>(sm + Y::item);
+  int32_t* bad = reinterpret_cast<int32_t*>(sm + Y::bad);  // [item parity]: the first key whose values are not finite
+  if (tid == 0) {
+    for (int i = 0; i < R; ++i) {
+      mbar_init(bar(A_UFULL + i), 1);
+      mbar_init(bar(A_UFREE + i), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(A_QFULL + t), 1);
+      mbar_init(bar(A_QFREE + t), 1);
+      mbar_init(bar(A_S + t), 1);
+      mbar_init(bar(A_P + t), 4);
+      mbar_init(bar(A_O + t), 1);
+      mbar_init(bar(A_ITEM + t), 1);
+      mbar_init(bar(A_TAKEN + t), 8 + 1 + kPaGuards);
+    }
+    for (int i = 0; i < kPaReady; ++i) {
+      mbar_init(bar(A_READY + i), kPaGuards);
+      mbar_init(bar(A_GFULL + i), 1);
+    }
+    mbar_init(bar(A_DRAIN), 1);
+    tc::fence_mbarrier_init_cluster();
+  }
+  if (warp == kPaMmaWarp) tc::alloc(sb + uint32_t(Y::tmem), 512);
+  if (tid == 32 * kPaLoadWarp) {
+    prefetch_tensormap(&q_map);
+    prefetch_tensormap(&k_map);
+    prefetch_tensormap(&v_map);
+    if (ROPE) prefetch_tensormap(&rope_map);
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  pdl_wait();  // the plan is complete, and with it what came before on the stream
+  const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + Y::tmem);
+  bool ok = true;
+
+  if (warp >= kPaMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // ---------------------------------------------------------------- items and loads
+    if (warp == kPaLoadWarp) {
+      const int total = __ldcg(&reinterpret_cast<const PaHead*>(p.ws)->total);
+      int32_t* claim = &reinterpret_cast<PaHead*>(p.ws)->claim;
+      int u = 0, ng = 0, nq[2] = {0, 0}, idx = 0;
+      if (lane == 0) idx = atomicAdd(claim, 1);
+      idx = __shfl_sync(0xffffffffu, idx, 0);
+      auto room = [&](int at) { return at < R || mbar_wait(bar(A_UFREE + at % R), ((at / R) - 1) & 1); };
+      for (int k = 0; ok; ++k) {
+        PaItem it = {};
+        bool real = idx < total;
+        while (real && !pa_item(p, idx, it)) {  // a piece without keys
+          if (lane == 0) idx = atomicAdd(claim, 1);
+          idx = __shfl_sync(0xffffffffu, idx, 0);
+          real = idx < total;
+        }
+        it.last = !real;
+        if (k >= 2 && !pa_wait(bar(A_TAKEN + (k & 1)), ((k >> 1) - 1) & 1)) { ok = false; break; }
+        if (lane == 0) {
+          items[k & 1] = it;
+          bad[k & 1] = 0x7fffffff;
+          mbar_arrive(bar(A_ITEM + (k & 1)));
+        }
+        __syncwarp();
+        if (!real) break;
+        int next = 0;
+        if (lane == 0) {
+          next = atomicAdd(claim, 1);
+          const int n = max(it.n[0], it.n[1]);
+          const int seen = pa_lim(p.causal, it.nq, it.nk, it.prefix, it.tok0);
+          auto load_k = [&](int j) {
+            for (int c = 0; c < QU && ok; ++c, ++u) {
+              if (!room(u)) { ok = false; break; }
+              mbar_arrive_expect_tx(bar(A_UFULL + u % R), kPaUnit);
+              const int key = it.k0 + (it.kt0 + j) * kPaN;
+              if (c < 2) tma_load_3d(unit(u), &k_map, 64 * c, it.kvh, key, bar(A_UFULL + u % R));
+              else tma_load_2d(unit(u), &rope_map, 0, key, bar(A_UFULL + u % R));
+            }
+          };
+          auto load_v = [&](int j) {
+            for (int c = 0; c < 2 && ok; ++c, ++u) {
+              if (!room(u)) { ok = false; break; }
+              // guarded values are announced to the guards, in a ring of their own that they follow one by one
+              uint32_t full = bar(A_UFULL + u % R);
+              if ((it.kt0 + j + 1) * kPaN > seen) {
+                mbar_arrive(full);
+                full = bar(A_GFULL + ng++ % kPaReady);
+              }
+              mbar_arrive_expect_tx(full, kPaUnit);
+              const int key = it.k0 + (it.kt0 + j) * kPaN + 64 * c;
+              tma_load_3d(unit(u), &v_map, 0, it.kvh, key, full);
+              tma_load_3d(unit(u) + kPaUnit / 2, &v_map, 64, it.kvh, key, full);
+            }
+          };
+          if (n > 0) load_k(0);
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (it.n[t] == 0) continue;
+            if (nq[t] > 0 && !mbar_wait(bar(A_QFREE + t), (nq[t] - 1) & 1)) { ok = false; break; }
+            ++nq[t];
+            mbar_arrive_expect_tx(bar(A_QFULL + t), QU * kPaUnit);
+            for (int c = 0; c < QU; ++c)
+              tma_load_3d(sb + uint32_t(Y::q) + (t * QU + c) * kPaUnit, &q_map, 64 * c, it.head0,
+                          it.q0 + it.tok0 + t * (kPaM >> p.log2_pack), bar(A_QFULL + t));
+          }
+          for (int j = 0; j < n && ok; ++j) {
+            load_v(j);
+            if (j + 1 < n && ok) load_k(j + 1);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        idx = __shfl_sync(0xffffffffu, next, 0);
+      }
+      if (lane == 0) {  // copies still in flight land before shared memory goes
+        for (int at = max(0, u - R); at < u; ++at)
+          if (!mbar_wait(bar(A_UFULL + at % R), (at / R) & 1)) ok = false;
+        for (int at = max(0, ng - kPaReady); at < ng; ++at)
+          if (!mbar_wait(bar(A_GFULL + at % kPaReady), (at / kPaReady) & 1)) ok = false;
+        for (int t = 0; t < 2; ++t)
+          if (nq[t] > 0 && !mbar_wait(bar(A_QFULL + t), (nq[t] - 1) & 1)) ok = false;
+      }
+      __syncwarp();
+    }
+    // ---------------------------------------------------------------- MMA issue
+    else if (warp == kPaMmaWarp) {
+      constexpr uint32_t kIdQK = tc::idesc_bf16_f32(kPaM, kPaN, false, false), kIdPV = tc::idesc_bf16_f32(kPaM, 128, false, true);
+      int base = 0, ready = 0, nq[2] = {0, 0}, ns[2] = {0, 0};
+      for (int k = 0; ok; ++k) {
+        if (!pa_wait(bar(A_ITEM + (k & 1)), (k >> 1) & 1)) { ok = false; break; }
+        const PaItem it = items[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(A_TAKEN + (k & 1)));
+        if (it.last) break;
+        const int n = max(it.n[0], it.n[1]);
+        const int seen = pa_lim(p.causal, it.nq, it.nk, it.prefix, it.tok0);  // keys that every row of the item sees
+        if (lane == 0) {
+          // units of key tile j, and of its values
+          auto uk = [&](int j) { return j == 0 ? base : base + QU + (j - 1) * (QU + 2) + 2; };
+          auto uv = [&](int j) { return base + QU + j * (QU + 2); };
+          auto qk = [&](int t, int j) -> bool {
+            const bool last_use = t == 1 || j >= it.n[1];
+            for (int c = 0; c < QU; ++c) {
+              const int u = uk(j) + c;
+              if (!mbar_wait(bar(A_UFULL + u % R), (u / R) & 1)) return false;
+              tc::fence_after();
+              const uint32_t qa = sb + uint32_t(Y::q) + (t * QU + c) * kPaUnit, ka = unit(u);
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                tc::mma_ss(tm + 128 * t, tc::sdesc_sw128(qa + 32 * s, 16, 1024), tc::sdesc_sw128(ka + 32 * s, 16, 1024), kIdQK,
+                           c > 0 || s > 0);
+              if (last_use) tc::commit(bar(A_UFREE + u % R));
+            }
+            tc::commit(bar(A_S + t));
+            if (j + 1 == it.n[t]) tc::commit(bar(A_QFREE + t));
+            return true;
+          };
+          auto pv = [&](int t, int j) -> bool {
+            const bool last_use = t == 1 || j >= it.n[1];
+            if (!mbar_wait(bar(A_P + t), ns[t] & 1)) return false;
+            ++ns[t];
+            const bool guarded = (it.kt0 + j + 1) * kPaN > seen;
+            for (int c = 0; c < 2; ++c) {
+              const int u = uv(j) + c;
+              if (!mbar_wait(bar(A_UFULL + u % R), (u / R) & 1)) return false;
+              if (guarded && !mbar_wait(bar(A_READY + (ready + c) % kPaReady), ((ready + c) / kPaReady) & 1)) return false;
+              tc::fence_after();
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                tc::mma_ts(tm + 256 + 128 * t, tm + 128 * t + 32 * c + 8 * s, tc::sdesc_sw128(unit(u) + 2048 * s, kPaUnit / 2, 1024),
+                           kIdPV, j > 0 || c > 0 || s > 0);
+              if (last_use) tc::commit(bar(A_UFREE + u % R));
+            }
+            if (guarded && last_use) ready += 2;
+            if (j + 1 == it.n[t]) tc::commit(bar(A_O + t));
+            return true;
+          };
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (it.n[t] == 0) continue;
+            ok = mbar_wait(bar(A_QFULL + t), nq[t] & 1);
+            ++nq[t];
+            if (ok) ok = qk(t, 0);
+          }
+          for (int j = 0; j < n && ok; ++j) {
+            for (int t = 0; t < 2 && ok; ++t) {
+              if (j >= it.n[t]) continue;
+              ok = pv(t, j);
+              if (ok && j + 1 < it.n[t]) ok = qk(t, j + 1);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        base += n > 0 ? n * (QU + 2) : 0;
+      }
+      if (lane == 0 && base > 0) {  // every MMA has completed before the tensor memory is released
+        tc::commit(bar(A_DRAIN));
+        if (!mbar_wait(bar(A_DRAIN), 0)) ok = false;
+      }
+      __syncwarp();
+    }
+    // ---------------------------------------------------------------- values that not every row sees
+    else {
+      const int g = warp - kPaGuardWarp;
+      int base = 0, ready = 0;
+      for (int k = 0; ok; ++k) {
+        if (!pa_wait(bar(A_ITEM + (k & 1)), (k >> 1) & 1)) { ok = false; break; }
+        const PaItem it = items[k & 1];
+        if (it.last) break;
+        const int n = max(it.n[0], it.n[1]);
+        const int seen = pa_lim(p.causal, it.nq, it.nk, it.prefix, it.tok0);
+        for (int j = max(0, max(seen, 0) / kPaN - it.kt0); j < n && ok; ++j) {
+          for (int c = 0; c < 2; ++c, ++ready) {
+            const int u = base + QU + j * (QU + 2) + c;
+            if (!pa_wait(bar(A_GFULL + ready % kPaReady), (ready / kPaReady) & 1)) { ok = false; break; }
+            const int row = 32 * g + lane, key = (it.kt0 + j) * kPaN + 64 * c + row;
+            const uint32_t at = unit(u) + uint32_t(row) * 128;
+            bool odd = false;
+            if (key < it.nk) {
+#pragma unroll 4
+              for (int x = 0; x < 16; ++x) {
+                const uint4 y = lds128(at + (x >> 3) * (kPaUnit / 2) + (((x + lane) & 7) << 4));
+                const uint32_t w4[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) odd |= (w4[e] & 0x7f80u) == 0x7f80u || (w4[e] & 0x7f800000u) == 0x7f800000u;
+              }
+              if (odd && key >= seen) atomicMin(bad + (k & 1), key);
+            }
+            if (key >= it.nk || (odd && key >= seen)) {
+              for (int x = 0; x < 16; ++x)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at + (x >> 3) * (kPaUnit / 2) + (((x + lane) & 7) << 4)), "r"(0)
+                             : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(A_READY + ready % kPaReady));
+          }
+        }
+        base += n * (QU + 2);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(A_TAKEN + (k & 1)));
+      }
+    }
+  }
+  // ------------------------------------------------------------------ softmax and epilogue
+  else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int t = warp >> 2, row = tid & 127;
+    const uint32_t tl = tm + (uint32_t(32 * (warp & 3)) << 16), ts = tl + 128 * t, to = tl + 256 + 128 * t;
+    int32_t* flag = reinterpret_cast<int32_t*>(sm + Y::flag) + t;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+    int ns = 0, no = 0;
+    for (int k = 0; ok; ++k) {
+      if (!pa_wait(bar(A_ITEM + (k & 1)), (k >> 1) & 1)) { ok = false; break; }
+      const PaItem& it = items[k & 1];
+      if (it.last) break;
+      const int first = it.tok0 + t * (kPaM >> p.log2_pack), token = first + (row >> p.log2_pack);
+      const int hd = it.head0 + (row & ((1 << p.log2_pack) - 1));
+      const bool mine = token < it.nq;
+      const int lim = mine ? pa_lim(p.causal, it.nq, it.nk, it.prefix, token) : 0;
+      const int all_see = pa_lim(p.causal, it.nq, it.nk, it.prefix, min(first, it.nq - 1));
+      const int n = it.n[t], kt0 = it.kt0;
+      float slope = 0.f;
+      if (BIAS && mine) slope = __ldg(p.slopes + hd) * kLog2e;
+      const float pos = float(it.nk - it.nq + token);
+      float m = -CUDART_INF_F, mu = 0.f;  // mu: m where it is finite
+      uint64_t sum2 = 0;
+      for (int j = 0; j < n; ++j, ++ns) {
+        if (!pa_wait(bar(A_S + t), ns & 1)) { ok = false; break; }
+        tc::fence_after();
+        uint32_t raw[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::ld32(ts + 32 * c, raw[c]);
+        tc::wait_ld();
+        float x[128];
+#pragma unroll
+        for (int i = 0; i < 128; ++i) x[i] = __uint_as_float(raw[i >> 5][i & 31]);
+        const int key0 = (kt0 + j) * kPaN;
+        if constexpr (CAP) {  // cap tanh(u) = cap - 2 cap / (1 + e^(2u)): within 2^-22 of cap
+#pragma unroll
+          for (int i = 0; i < 128; ++i) x[i] = fmaf(-2.f * p.cap2, rcp(1.f + ex2(x[i] * p.cap_in)), p.cap2);
+        }
+        if constexpr (BIAS) {
+          const float d0 = pos - float(key0);
+#pragma unroll
+          for (int i = 0; i < 128; ++i) x[i] = fmaf(-slope, fabsf(d0 - float(i)), CAP ? x[i] : x[i] * p.c2);
+        }
+        if (key0 + kPaN > all_see) {
+          const int left = lim - key0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) x[i] = i < left ? x[i] : -CUDART_INF_F;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = x[c];
+#pragma unroll
+        for (int i = 4; i < 124; i += 8)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], x[i + c], x[i + 4 + c]);
+        float top = fmaxf(max3(mx[0], x[124], x[125]), max3(max3(mx[1], x[126], x[127]), mx[2], mx[3]));
+        if (!CAP && !BIAS) top *= p.c2;
+        const bool move = top > m + kPaRescale;
+        if (__any_sync(0xffffffffu, move)) {
+          const float f = move ? ex2(m - top) : 1.f;  // 0 from -inf
+          if (move) m = mu = top;
+          const uint64_t ff = f2(f, f);
+          sum2 = f2_fma(sum2, ff, 0);
+          if (j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tc::ld16(to + 16 * c, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tc::st16(to + 16 * c, o);
+            }
+          }
+        }
+        const uint64_t cc = CAP || BIAS ? f2(1.f, 1.f) : f2(p.c2, p.c2), mm = f2(-mu, -mu);
+        uint64_t part[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 d = f2_parts(f2_fma(f2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]), cc, mm));
+            const float a = ex2(d.x), b = ex2(d.y);
+            part[i & 1] = f2_add(part[i & 1], f2(a, b));
+            w[i] = pack_bf16x2(a, b);
+          }
+          tc::st16(ts + 16 * c, w);
+        }
+        sum2 = f2_add(sum2, f2_add(part[0], part[1]));
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(A_P + t));
+      }
+      if (!ok) break;
+      if (n > 0) {
+        if (!pa_wait(bar(A_O + t), no & 1)) { ok = false; break; }
+        ++no;
+        tc::fence_after();
+      }
+      const float2 s2 = f2_parts(sum2);
+      float l = s2.x + s2.y;
+      const bool spoilt = *reinterpret_cast<volatile int32_t*>(bad + (k & 1)) < lim;  // a value this row sees is not finite
+      const int64_t at = int64_t(it.q0 + token) * p.H + hd;
+      const float sink = p.sink && mine ? __ldg(p.sink + hd) * kLog2e : -CUDART_INF_F;
+      auto finish = [&](float& m_, float& l_) -> float {  // with the sink: the factor of O
+        const float mf = fmaxf(m_, sink), base = mf == -CUDART_INF_F ? 0.f : mf;
+        const float f = m_ == -CUDART_INF_F ? 0.f : ex2(m_ - base);
+        l_ = l_ * f + (sink == -CUDART_INF_F ? 0.f : ex2(sink - base));
+        m_ = base;
+        return l_ == 0.f ? 0.f : f / l_;
+      };
+      if (it.pieces == 1) {
+        const float f = spoilt ? CUDART_NAN_F : finish(m, l);
+        if (spoilt) finish(m, l);
+        if (mine && p.lse) p.lse[at] = (log2f(l) + m) * kLn2;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          if (n > 0) {
+            tc::ld32(to + 32 * c, o);
+            tc::wait_ld();
+          }
+          if (mine) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                w[i] = n > 0 ? pack_bf16x2(__uint_as_float(o[16 * h + 2 * i]) * f, __uint_as_float(o[16 * h + 2 * i + 1]) * f) : 0;
+              store32(static_cast<uint16_t*>(p.out) + at * 128 + 32 * c + 16 * h, w, wide);
+            }
+          }
+        }
+      } else {
+        float* slot = p.parts + int64_t(it.slot + it.piece) * kPaSlotFloats;
+        float* po = slot + (t * kPaM + row) * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          if (n > 0) {
+            tc::ld32(to + 32 * c, o);
+            tc::wait_ld();
+          }
+          if (mine) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (n > 0) v = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                         __uint_as_float(o[4 * i + 3]));
+              if (spoilt) v = make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
+              reinterpret_cast<float4*>(po + 32 * c)[i] = v;
+            }
+          }
+        }
+        if (mine) reinterpret_cast<float2*>(slot + kPaRows * 128)[t * kPaM + row] = make_float2(m, l);
+        __threadfence();
+        named_bar(1 + t, 128);
+        if (row == 0) {
+          int32_t* count = p.counts + 2 * it.slot + t;
+          const int old = atomicAdd(count, 1);
+          if (old == it.pieces - 1) *count = 0;  // the last one: nobody else looks at it in this call
+          *flag = old;
+        }
+        named_bar(1 + t, 128);
+        if (*reinterpret_cast<volatile int32_t*>(flag) == it.pieces - 1) {
+          __threadfence();
+          if (mine) {
+            const float* s0 = p.parts + int64_t(it.slot) * kPaSlotFloats;
+            float M = -CUDART_INF_F, Lsum = 0.f;
+            for (int q = 0; q < it.pieces; ++q)
+              M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(s0 + int64_t(q) * kPaSlotFloats + kPaRows * 128) + t * kPaM + row).x);
+            const float Mu = M == -CUDART_INF_F ? 0.f : M;
+            for (int q = 0; q < it.pieces; ++q) {
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(s0 + int64_t(q) * kPaSlotFloats + kPaRows * 128) + t * kPaM + row);
+              Lsum += ml.y * (ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - Mu));
+            }
+            const float f = finish(M, Lsum);
+            if (p.lse) p.lse[at] = (log2f(Lsum) + M) * kLn2;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float acc[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+              for (int q = 0; q < it.pieces; ++q) {
+                const float* s1 = s0 + int64_t(q) * kPaSlotFloats;
+                const float mq = __ldcg(reinterpret_cast<const float2*>(s1 + kPaRows * 128) + t * kPaM + row).x;
+                const float fq = mq == -CUDART_INF_F ? 0.f : ex2(mq - Mu);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float4 v = __ldcg(reinterpret_cast<const float4*>(s1 + (t * kPaM + row) * 128 + 32 * c) + i);
+                  acc[4 * i] = fmaf(v.x, fq, acc[4 * i]);
+                  acc[4 * i + 1] = fmaf(v.y, fq, acc[4 * i + 1]);
+                  acc[4 * i + 2] = fmaf(v.z, fq, acc[4 * i + 2]);
+                  acc[4 * i + 3] = fmaf(v.w, fq, acc[4 * i + 3]);
+                }
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(acc[16 * h + 2 * i] * f, acc[16 * h + 2 * i + 1] * f);
+                store32(static_cast<uint16_t*>(p.out) + at * 128 + 32 * c + 16 * h, w, wide);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(A_TAKEN + (k & 1)));
+    }
+  }
+  if (!ok && lane == 0) atomicOr(err, SMLA_DEVERR_TIMEOUT);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == kPaMmaWarp) tc::dealloc(tm, 512);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- host
+
+PromptLayout prompt_layout(int64_t requests, int num_sms) {
+  PromptLayout l;
+  l.slots = 4 * num_sms;
+  size_t at = 256 + size_t(requests) * sizeof(PaTab);
+  at = (at + 255) / 256 * 256;
+  l.counts = at;
+  at += size_t(l.slots) * 2 * sizeof(int32_t);
+  at = (at + 255) / 256 * 256;
+  l.parts = at;
+  l.bytes = at + size_t(l.slots) * kPaSlotFloats * sizeof(float);
+  return l;
+}
+
+namespace {
+
+cudaError_t map3(const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2, int b1, int b2, CUtensorMap* out) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if (tensor_map_encoder(&encode) != cudaSuccess) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {cuuint64_t(d0), cuuint64_t(d1), cuuint64_t(d2)};
+  const cuuint64_t strides[2] = {cuuint64_t(2 * s1), cuuint64_t(2 * s2)};
+  const cuuint32_t box[3] = {64, cuuint32_t(b1), cuuint32_t(b2)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int ROPE, bool CAP, bool BIAS>
+cudaError_t launch_variant(const PromptArgs& a, cudaStream_t s) {
+  CUtensorMap qm, km, rm, vm;
+  const int pack = 1 << a.log2_pack;
+  cudaError_t e = map3(a.q, 128 + ROPE, a.H, a.T, a.q_head, a.q_token, pack, kPaM / pack, &qm);
+  if (e == cudaSuccess) e = map3(a.k, 128, a.HK, a.N, a.k_head, a.k_token, 1, kPaN, &km);
+  if (e == cudaSuccess) e = map3(a.v, 128, a.HK, a.N, a.v_head, a.v_token, 1, kPaN / 2, &vm);
+  if (e != cudaSuccess) return e;
+  rm = km;
+  if (ROPE) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    e = tensor_map_encoder(&encode);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t dims[2] = {cuuint64_t(64), cuuint64_t(a.N)};
+    const cuuint64_t strides[1] = {cuuint64_t(2 * a.rope_token)};
+    const cuuint32_t box[2] = {64, kPaN}, estr[2] = {1, 1};
+    if (encode(&rm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.rope), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  // set on every device that a call runs on, once
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(prompt_attention_kernel<ROPE, CAP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(PaLay<ROPE>::bytes));
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_release);
+  }
+  prompt_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.sms));
+  cfg.blockDim = dim3(kPaThreads);
+  cfg.dynamicSmemBytes = PaLay<ROPE>::bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_attention_kernel<ROPE, CAP, BIAS>, a, qm, km, rm, vm);
+}
+
+template <int ROPE>
+cudaError_t launch_rope(const PromptArgs& a, cudaStream_t s) {
+  if (a.slopes) return a.cap2 > 0.f ? launch_variant<ROPE, true, true>(a, s) : launch_variant<ROPE, false, true>(a, s);
+  return a.cap2 > 0.f ? launch_variant<ROPE, true, false>(a, s) : launch_variant<ROPE, false, false>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t s) {
+  return a.rope ? launch_rope<64>(a, s) : launch_rope<0>(a, s);
+}
+
+}  // namespace smla

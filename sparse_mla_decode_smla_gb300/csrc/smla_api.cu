@@ -91,6 +91,29 @@ smla_status check_desc(const smla_desc* d) {
   return SMLA_OK;
 }
 
+bool prompt_stride(int64_t s, int64_t least) { return s >= least && s % 8 == 0 && s <= kMaxCount; }
+
+smla_status check_prompt_desc(const smla_prompt_desc* d) {
+  if (!d) return SMLA_ERR_NULL;
+  if (d->num_tokens < 0 || d->num_keys < 1 || d->num_heads < 1 || d->num_heads > 1024 || d->num_kv_heads < 1 ||
+      d->num_heads % d->num_kv_heads || d->num_requests < 1 || d->num_requests > smla::kPromptMaxRequests ||
+      int64_t(d->num_tokens) * d->num_heads > kMaxCount)
+    return SMLA_ERR_SHAPE;
+  if (d->rope_dim != 0 && d->rope_dim != 64) return SMLA_ERR_UNSUPPORTED;
+  if (d->causal != 0 && d->causal != 1) return SMLA_ERR_UNSUPPORTED;
+  if (!(isfinite(d->sm_scale) && d->sm_scale > 0.f) || !(isfinite(d->softcap) && d->softcap >= 0.f)) return SMLA_ERR_SHAPE;
+  if (!isfinite(d->sm_scale * 1.4426950408889634f) || !isfinite(d->softcap * 2.8853900817779268f) ||
+      (d->softcap > 0.f && !isfinite(2.f * d->sm_scale * 1.4426950408889634f / d->softcap)))
+    return SMLA_ERR_SHAPE;
+  if (!prompt_stride(d->q_token_stride, 128 + d->rope_dim) || !prompt_stride(d->q_head_stride, 128 + d->rope_dim) ||
+      !prompt_stride(d->k_token_stride, 128) || !prompt_stride(d->k_head_stride, 128) || !prompt_stride(d->v_token_stride, 128) ||
+      !prompt_stride(d->v_head_stride, 128) || (d->rope_dim && !prompt_stride(d->rope_token_stride, 64)))
+    return SMLA_ERR_SHAPE;
+  for (int i = 0; i < 3; ++i)
+    if (d->reserved[i]) return SMLA_ERR_SHAPE;
+  return SMLA_OK;
+}
+
 struct Plan {
   int num_splits;
   int split_len;
@@ -772,6 +795,76 @@ smla_status smla_add_rmsnorm(const smla_norm_desc* d, const void* x, const void*
   a.scale_mode = d->scale_mode;
   a.eps = d->rms_eps;
   return smla::launch_add_rmsnorm(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+smla_status smla_prompt_workspace_size(const smla_prompt_desc* d, size_t* bytes) {
+  if (!bytes) return SMLA_ERR_NULL;
+  *bytes = 0;
+  smla_status st = check_prompt_desc(d);
+  if (st != SMLA_OK) return st;
+  int sms = 0;
+  st = current_device(&sms);
+  if (st != SMLA_OK) return st;
+  *bytes = smla::prompt_layout(d->num_requests, sms).bytes;
+  return SMLA_OK;
+}
+
+smla_status smla_prompt_attention(const smla_prompt_desc* d, const void* q, const void* k, const void* v, const void* k_rope,
+                                  const int32_t* cu_q, const int32_t* cu_k, const int32_t* prefix_lens, const float* slopes,
+                                  const float* sink, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  smla_status st = check_prompt_desc(d);
+  if (st != SMLA_OK) return st;
+  if (d->num_tokens == 0) return SMLA_OK;
+  if (!q || !k || !v || !cu_q || !cu_k || !out || !workspace) return SMLA_ERR_NULL;
+  if ((k_rope != nullptr) != (d->rope_dim > 0)) return SMLA_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_rope, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
+      !aligned(cu_k, 4) || !aligned(prefix_lens, 4) || !aligned(slopes, 4) || !aligned(sink, 4) || !aligned(lse, 4) ||
+      !aligned(workspace, kWsAlign))
+    return SMLA_ERR_ALIGN;
+  int sms = 0;
+  st = current_device(&sms);
+  if (st != SMLA_OK) return st;
+  const smla::PromptLayout l = smla::prompt_layout(d->num_requests, sms);
+  if (workspace_bytes < l.bytes) return SMLA_ERR_WORKSPACE;
+  smla::PromptArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.rope = k_rope;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.prefix = prefix_lens;
+  a.slopes = slopes;
+  a.sink = sink;
+  a.out = out;
+  a.lse = lse;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.counts = reinterpret_cast<int32_t*>(a.ws + l.counts);
+  a.parts = reinterpret_cast<float*>(a.ws + l.parts);
+  a.slots = l.slots;
+  a.q_token = d->q_token_stride;
+  a.q_head = d->q_head_stride;
+  a.k_token = d->k_token_stride;
+  a.k_head = d->k_head_stride;
+  a.v_token = d->v_token_stride;
+  a.v_head = d->v_head_stride;
+  a.rope_token = d->rope_token_stride;
+  a.T = d->num_tokens;
+  a.N = d->num_keys;
+  a.H = d->num_heads;
+  a.HK = d->num_kv_heads;
+  a.B = d->num_requests;
+  a.causal = d->causal;
+  // the query heads of a kv head that stand beside one another in a row tile: the largest power of two, up to 128
+  const int group = d->num_heads / d->num_kv_heads;
+  while (a.log2_pack < 7 && group % (2 << a.log2_pack) == 0) ++a.log2_pack;
+  a.sms = sms;
+  a.c2 = d->sm_scale * 1.4426950408889634f;
+  a.cap2 = d->softcap * 1.4426950408889634f;
+  a.cap_in = d->softcap > 0.f ? 2.f * a.c2 / d->softcap : 0.f;
+  return smla::launch_prompt_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
 smla_status smla_token_logprobs(const smla_logprob_desc* d, const void* logits, const int32_t* tokens, float* logprobs,

@@ -22,6 +22,7 @@ def _ref(d):
 def test_layouts_match_the_header():
     assert ctypes.sizeof(smla.smla_read_desc) == 64 and smla.smla_read_desc.kv_scale.offset == 48
     assert ctypes.sizeof(smla.smla_norm_desc) == 40 and smla.smla_norm_desc.rms_eps.offset == 28
+    assert ctypes.sizeof(smla.smla_prompt_desc) == 104 and smla.smla_prompt_desc.q_token_stride.offset == 48
     assert ctypes.sizeof(smla.smla_logprob_desc) == 48 and smla.smla_logprob_desc.scale.offset == 32
 
 
@@ -59,6 +60,51 @@ def test_read_pointers(L):
     for s in (0.0, -1.0, float("nan"), float("inf")):
         assert _read(L, _read_desc(kv_format=smla.SMLA_KV_FP8_TENSOR, kv_scale=s)) == 2
     assert _read(L, _read_desc(num_rows=0), lat=0) == 0  # nothing to do
+
+
+# ---------------------------------------------------------------- attention
+
+
+def _attn(L, d, q=16, k=16, v=16, rope=16, cq=16, ck=16, prefix=None, slopes=None, sink=None, out=16, lse=None, ws=256, nbytes=1 << 40):
+    return L.smla_prompt_attention(_ref(d), P(q), P(k), P(v), P(rope), P(cq), P(ck), P(prefix), P(slopes), P(sink), P(out), P(lse),
+                                   P(ws), nbytes, None)
+
+
+def _attn_desc(**kw):
+    d = smla.make_prompt_desc(8, 16, 4, 2, 2, 64, 192 ** -0.5)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+@pytest.mark.parametrize("field,value,status", [
+    ("num_tokens", -1, 2), ("num_tokens", 1 << 30, 2), ("num_keys", 0, 2), ("num_heads", 0, 2), ("num_heads", 5, 2), ("num_heads", 2048, 2),
+    ("num_kv_heads", 0, 2), ("num_kv_heads", 3, 2), ("num_requests", 0, 2), ("num_requests", 65537, 2), ("rope_dim", 32, 4),
+    ("rope_dim", 128, 4), ("causal", 2, 4), ("sm_scale", 0.0, 2), ("sm_scale", -0.1, 2), ("sm_scale", float("nan"), 2),
+    ("sm_scale", 3e38, 2), ("softcap", -1.0, 2), ("softcap", float("inf"), 2), ("softcap", float("nan"), 2), ("softcap", 1e-40, 2),
+    ("q_token_stride", 4, 2), ("q_token_stride", 772, 2), ("q_head_stride", 128, 2), ("k_token_stride", 120, 2), ("k_head_stride", 132, 2),
+    ("v_token_stride", 0, 2), ("v_head_stride", -128, 2), ("rope_token_stride", 56, 2), ("v_token_stride", 1 << 40, 2)])
+def test_attention_rules(L, field, value, status):
+    d = _attn_desc(**{field: value})
+    assert _attn(L, d) == status
+    n = ctypes.c_size_t(7)
+    assert L.smla_prompt_workspace_size(ctypes.byref(d), ctypes.byref(n)) == status and n.value == 0
+
+
+def test_attention_pointers(L):
+    assert _attn(L, None) == 1
+    for k in ("q", "k", "v", "cq", "ck", "out", "ws"):
+        assert _attn(L, _attn_desc(), **{k: 0}) == 1, k
+        assert _attn(L, _attn_desc(), **{k: 258}) == 3, k
+    for k in ("prefix", "slopes", "sink", "lse", "rope"):
+        assert _attn(L, _attn_desc(), **{k: 18}) == 3, k
+    assert _attn(L, _attn_desc(), rope=0) == 2                     # a RoPE part without its keys
+    assert _attn(L, _attn_desc(rope_dim=0)) == 2                   # and the other way round
+    assert _attn(L, _attn_desc(num_tokens=0), q=0) == 0
+    d = _attn_desc()
+    d.reserved[2] = 1
+    assert _attn(L, d) == 2
+    assert L.smla_prompt_workspace_size(ctypes.byref(_attn_desc()), None) == 1
 
 
 # ---------------------------------------------------------------- the norm
