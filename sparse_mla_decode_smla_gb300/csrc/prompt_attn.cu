@@ -43,7 +43,7 @@ constexpr int kPaRows = 2 * kPaM;          // rows of an item
 constexpr int kPaUnit = 16384;             // bytes of a ring unit: 128 keys x 64 dims, or 64 values x 128 dims
 constexpr int kPaThreads = 384;
 constexpr int kPaMmaWarp = 8, kPaLoadWarp = 9, kPaGuardWarp = 10, kPaGuards = 2;
-constexpr int kPaReady = 8;                // guarded value units between the guards and the MMAs at most: 6
+constexpr int kPaTiles = 4;                // key (value) tiles in the ring at most: 3
 constexpr float kPaRescale = 8.f;
 constexpr int kPaMinTiles = 8;             // key tiles of a piece at least
 constexpr int kPaSlotFloats = kPaRows * 128 + kPaRows * 2;  // a piece's part: O, then (m, l) of each row
@@ -76,12 +76,11 @@ struct PaLay {
   static constexpr size_t flag = bad + 8;
   static constexpr size_t tmem = flag + 8;
   static constexpr size_t bars = tmem + 16;
-  static constexpr size_t bytes = bars + 56 * 8;
+  static constexpr size_t bytes = bars + 48 * 8;
   static_assert(bytes <= 232448 && bars % 8 == 0 && units % 1024 == 0, "shared memory");
 };
 enum {
-  A_UFULL = 0,
-  A_UFREE = A_UFULL + 10,
+  A_UFREE = 0,             // [unit]
   A_QFULL = A_UFREE + 10,  // [row tile], and so the next ones
   A_QFREE = A_QFULL + 2,
   A_S = A_QFREE + 2,
@@ -89,12 +88,14 @@ enum {
   A_O = A_P + 2,
   A_ITEM = A_O + 2,        // [item parity]
   A_TAKEN = A_ITEM + 2,
-  A_READY = A_TAKEN + 2,
-  A_GFULL = A_READY + kPaReady,
-  A_DRAIN = A_GFULL + kPaReady,
+  A_KFULL = A_TAKEN + 2,   // [tile % kPaTiles]: keys, values, values that the guards look at, those after they have
+  A_VFULL = A_KFULL + kPaTiles,
+  A_GFULL = A_VFULL + kPaTiles,
+  A_READY = A_GFULL + kPaTiles,
+  A_DRAIN = A_READY + kPaTiles,
   A_COUNT
 };
-static_assert(A_COUNT <= 56, "barriers");
+static_assert(A_COUNT <= 48, "barriers");
 
 // ---------------------------------------------------------------- the plan
 
@@ -271,6 +272,13 @@ __device__ __forceinline__ bool pa_item(const PromptArgs& p, int idx, PaItem& it
 __device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
 }
+// One lane of a converged warp. The MMA warp runs as one and elects a lane for its instructions alone: a branch on the lane
+// number around the whole loop made each MMA cost 80-200 clocks to issue (one 8191-token prompt: 837 us).
+__device__ __forceinline__ bool pa_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
@@ -336,15 +344,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   const uint32_t sb = smem_u32(sm);
   auto bar = [&](int k) -> uint32_t { return sb + uint32_t(Y::bars) + 8u * k; };
   auto unit = [&](int u) -> uint32_t { return sb + uint32_t(Y::units) + uint32_t(u % R) * kPaUnit; };
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the warp number comes from a shuffle, so that the compiler takes the warps' branches as uniform
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   int32_t* err = reinterpret_cast<int32_t*>(p.ws);
   PaItem* items = reinterpret_cast<PaItem*>(sm + Y::item);
   int32_t* bad = reinterpret_cast<int32_t*>(sm + Y::bad);  // [item parity]: the first key whose values are not finite
   if (tid == 0) {
-    for (int i = 0; i < R; ++i) {
-      mbar_init(bar(A_UFULL + i), 1);
-      mbar_init(bar(A_UFREE + i), 1);
-    }
+    for (int i = 0; i < R; ++i) mbar_init(bar(A_UFREE + i), 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(A_QFULL + t), 1);
       mbar_init(bar(A_QFREE + t), 1);
@@ -354,9 +360,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       mbar_init(bar(A_ITEM + t), 1);
       mbar_init(bar(A_TAKEN + t), 8 + 1 + kPaGuards);
     }
-    for (int i = 0; i < kPaReady; ++i) {
-      mbar_init(bar(A_READY + i), kPaGuards);
+    for (int i = 0; i < kPaTiles; ++i) {
+      mbar_init(bar(A_KFULL + i), 1);
+      mbar_init(bar(A_VFULL + i), 1);
       mbar_init(bar(A_GFULL + i), 1);
+      mbar_init(bar(A_READY + i), kPaGuards);
     }
     mbar_init(bar(A_DRAIN), 1);
     tc::fence_mbarrier_init_cluster();
@@ -372,7 +380,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   __syncthreads();
   tc::fence_after();
   pdl_wait();  // the plan is complete, and with it what came before on the stream
-  const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + Y::tmem);
+  const uint32_t tm = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(sm + Y::tmem), 0);
   bool ok = true;
 
   if (warp >= kPaMmaWarp) {
@@ -381,7 +389,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     if (warp == kPaLoadWarp) {
       const int total = __ldcg(&reinterpret_cast<const PaHead*>(p.ws)->total);
       int32_t* claim = &reinterpret_cast<PaHead*>(p.ws)->claim;
-      int u = 0, ng = 0, nq[2] = {0, 0}, idx = 0;
+      int u = 0, nk = 0, nv = 0, ng = 0, nq[2] = {0, 0}, idx = 0;
       if (lane == 0) idx = atomicAdd(claim, 1);
       idx = __shfl_sync(0xffffffffu, idx, 0);
       auto room = [&](int at) { return at < R || mbar_wait(bar(A_UFREE + at % R), ((at / R) - 1) & 1); };
@@ -407,28 +415,29 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           next = atomicAdd(claim, 1);
           const int n = max(it.n[0], it.n[1]);
           const int seen = pa_lim(p.causal, it.nq, it.nk, it.prefix, it.tok0);
+          // a key tile's units, and a value tile's, arrive at the barrier of their first one
           auto load_k = [&](int j) {
+            const uint32_t full = bar(A_KFULL + nk % kPaTiles);
+            ++nk;
+            const int key = it.k0 + (it.kt0 + j) * kPaN;
             for (int c = 0; c < QU && ok; ++c, ++u) {
               if (!room(u)) { ok = false; break; }
-              mbar_arrive_expect_tx(bar(A_UFULL + u % R), kPaUnit);
-              const int key = it.k0 + (it.kt0 + j) * kPaN;
-              if (c < 2) tma_load_3d(unit(u), &k_map, 64 * c, it.kvh, key, bar(A_UFULL + u % R));
-              else tma_load_2d(unit(u), &rope_map, 0, key, bar(A_UFULL + u % R));
+              if (c == 0) mbar_arrive_expect_tx(full, QU * kPaUnit);
+              if (c < 2) tma_load_3d(unit(u), &k_map, 64 * c, it.kvh, key, full);
+              else tma_load_2d(unit(u), &rope_map, 0, key, full);
             }
           };
           auto load_v = [&](int j) {
+            // values that not every row sees go to the guards, who pass them on
+            const bool guarded = (it.kt0 + j + 1) * kPaN > seen;
+            const uint32_t full = guarded ? bar(A_GFULL + ng % kPaTiles) : bar(A_VFULL + nv % kPaTiles);
+            ++(guarded ? ng : nv);
+            const int key = it.k0 + (it.kt0 + j) * kPaN;
             for (int c = 0; c < 2 && ok; ++c, ++u) {
               if (!room(u)) { ok = false; break; }
-              // guarded values are announced to the guards, in a ring of their own that they follow one by one
-              uint32_t full = bar(A_UFULL + u % R);
-              if ((it.kt0 + j + 1) * kPaN > seen) {
-                mbar_arrive(full);
-                full = bar(A_GFULL + ng++ % kPaReady);
-              }
-              mbar_arrive_expect_tx(full, kPaUnit);
-              const int key = it.k0 + (it.kt0 + j) * kPaN + 64 * c;
-              tma_load_3d(unit(u), &v_map, 0, it.kvh, key, full);
-              tma_load_3d(unit(u) + kPaUnit / 2, &v_map, 64, it.kvh, key, full);
+              if (c == 0) mbar_arrive_expect_tx(full, 2 * kPaUnit);
+              tma_load_3d(unit(u), &v_map, 0, it.kvh, key + 64 * c, full);
+              tma_load_3d(unit(u) + kPaUnit / 2, &v_map, 64, it.kvh, key + 64 * c, full);
             }
           };
           if (n > 0) load_k(0);
@@ -450,10 +459,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         idx = __shfl_sync(0xffffffffu, next, 0);
       }
       if (lane == 0) {  // copies still in flight land before shared memory goes
-        for (int at = max(0, u - R); at < u; ++at)
-          if (!mbar_wait(bar(A_UFULL + at % R), (at / R) & 1)) ok = false;
-        for (int at = max(0, ng - kPaReady); at < ng; ++at)
-          if (!mbar_wait(bar(A_GFULL + at % kPaReady), (at / kPaReady) & 1)) ok = false;
+        auto landed = [&](int first, int n) {
+          for (int at = max(0, n - kPaTiles); at < n; ++at)
+            if (!mbar_wait(bar(first + at % kPaTiles), (at / kPaTiles) & 1)) ok = false;
+        };
+        landed(A_KFULL, nk);
+        landed(A_VFULL, nv);
+        landed(A_GFULL, ng);
         for (int t = 0; t < 2; ++t)
           if (nq[t] > 0 && !mbar_wait(bar(A_QFULL + t), (nq[t] - 1) & 1)) ok = false;
       }
@@ -462,78 +474,98 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     // ---------------------------------------------------------------- MMA issue
     else if (warp == kPaMmaWarp) {
       constexpr uint32_t kIdQK = tc::idesc_bf16_f32(kPaM, kPaN, false, false), kIdPV = tc::idesc_bf16_f32(kPaM, 128, false, true);
-      int base = 0, ready = 0, nq[2] = {0, 0}, ns[2] = {0, 0};
+      const uint64_t dq = tc::sdesc_sw128(sb + uint32_t(Y::q), 16, 1024), dk = tc::sdesc_sw128(sb + uint32_t(Y::units), 16, 1024),
+                     dv = tc::sdesc_sw128(sb + uint32_t(Y::units), kPaUnit / 2, 1024);
+      int base = 0, nk = 0, nv = 0, ng = 0, nq[2] = {0, 0}, ns[2] = {0, 0};
       for (int k = 0; ok; ++k) {
         if (!pa_wait(bar(A_ITEM + (k & 1)), (k >> 1) & 1)) { ok = false; break; }
-        const PaItem it = items[k & 1];
+        const PaItem& item = items[k & 1];
+        auto uniform = [&](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+        const int n0 = uniform(item.n[0]), n1 = uniform(item.n[1]), kt0 = uniform(item.kt0), last_item = uniform(item.last);
+        const int seen = uniform(pa_lim(p.causal, item.nq, item.nk, item.prefix, item.tok0));  // keys that every row of the item sees
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(A_TAKEN + (k & 1)));
-        if (it.last) break;
-        const int n = max(it.n[0], it.n[1]);
-        const int seen = pa_lim(p.causal, it.nq, it.nk, it.prefix, it.tok0);  // keys that every row of the item sees
-        if (lane == 0) {
-          // units of key tile j, and of its values
-          auto uk = [&](int j) { return j == 0 ? base : base + QU + (j - 1) * (QU + 2) + 2; };
-          auto uv = [&](int j) { return base + QU + j * (QU + 2); };
-          auto qk = [&](int t, int j) -> bool {
-            const bool last_use = t == 1 || j >= it.n[1];
-            for (int c = 0; c < QU; ++c) {
-              const int u = uk(j) + c;
-              if (!mbar_wait(bar(A_UFULL + u % R), (u / R) & 1)) return false;
-              tc::fence_after();
-              const uint32_t qa = sb + uint32_t(Y::q) + (t * QU + c) * kPaUnit, ka = unit(u);
+        if (last_item) break;
+        const int n = max(n0, n1);
+        // units of key tile j, and of its values
+        auto uk = [&](int j) { return j == 0 ? base : base + QU + (j - 1) * (QU + 2) + 2; };
+        auto uv = [&](int j) { return base + QU + j * (QU + 2); };
+        auto qk = [&](int t, int j) -> bool {
+          const int nt = t ? n1 : n0;
+          const bool first_use = t == 0 || j >= n0, last_use = t == 1 || j >= n1;
+          if (first_use) {
+            if (!pa_wait(bar(A_KFULL + nk % kPaTiles), (nk / kPaTiles) & 1)) return false;
+            ++nk;
+          }
+          tc::fence_after();
+          const int u0 = uk(j);
+          if (pa_elect()) {
 #pragma unroll
-              for (int s = 0; s < 4; ++s)
-                tc::mma_ss(tm + 128 * t, tc::sdesc_sw128(qa + 32 * s, 16, 1024), tc::sdesc_sw128(ka + 32 * s, 16, 1024), kIdQK,
-                           c > 0 || s > 0);
-              if (last_use) tc::commit(bar(A_UFREE + u % R));
+            for (int c = 0; c < QU; ++c) {
+              const uint64_t qa = dq + (t * QU + c) * (kPaUnit >> 4), ka = dk + ((u0 + c) % R) * (kPaUnit >> 4);
+#pragma unroll
+              for (int s = 0; s < 4; ++s) tc::mma_ss(tm + 128 * t, qa + 2 * s, ka + 2 * s, kIdQK, c > 0 || s > 0);
+              if (last_use) tc::commit(bar(A_UFREE + (u0 + c) % R));
             }
             tc::commit(bar(A_S + t));
-            if (j + 1 == it.n[t]) tc::commit(bar(A_QFREE + t));
-            return true;
-          };
-          auto pv = [&](int t, int j) -> bool {
-            const bool last_use = t == 1 || j >= it.n[1];
-            if (!mbar_wait(bar(A_P + t), ns[t] & 1)) return false;
-            ++ns[t];
-            const bool guarded = (it.kt0 + j + 1) * kPaN > seen;
+            if (j + 1 == nt) tc::commit(bar(A_QFREE + t));
+          }
+          __syncwarp();
+          return true;
+        };
+        auto pv = [&](int t, int j) -> bool {
+          const int nt = t ? n1 : n0;
+          const bool first_use = t == 0 || j >= n0, last_use = t == 1 || j >= n1;
+          if (first_use) {
+            if ((kt0 + j + 1) * kPaN > seen) {
+              if (!pa_wait(bar(A_READY + ng % kPaTiles), (ng / kPaTiles) & 1)) return false;
+              ++ng;
+            } else {
+              if (!pa_wait(bar(A_VFULL + nv % kPaTiles), (nv / kPaTiles) & 1)) return false;
+              ++nv;
+            }
+          }
+          if (!pa_wait(bar(A_P + t), ns[t] & 1)) return false;
+          ++ns[t];
+          tc::fence_after();
+          const int u0 = uv(j);
+          if (pa_elect()) {
+#pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const int u = uv(j) + c;
-              if (!mbar_wait(bar(A_UFULL + u % R), (u / R) & 1)) return false;
-              if (guarded && !mbar_wait(bar(A_READY + (ready + c) % kPaReady), ((ready + c) / kPaReady) & 1)) return false;
-              tc::fence_after();
+              const uint64_t va = dv + ((u0 + c) % R) * (kPaUnit >> 4);
 #pragma unroll
               for (int s = 0; s < 4; ++s)
-                tc::mma_ts(tm + 256 + 128 * t, tm + 128 * t + 32 * c + 8 * s, tc::sdesc_sw128(unit(u) + 2048 * s, kPaUnit / 2, 1024),
-                           kIdPV, j > 0 || c > 0 || s > 0);
-              if (last_use) tc::commit(bar(A_UFREE + u % R));
+                tc::mma_ts(tm + 256 + 128 * t, tm + 128 * t + 32 * c + 8 * s, va + 128 * s, kIdPV, j > 0 || c > 0 || s > 0);
+              if (last_use) tc::commit(bar(A_UFREE + (u0 + c) % R));
             }
-            if (guarded && last_use) ready += 2;
-            if (j + 1 == it.n[t]) tc::commit(bar(A_O + t));
-            return true;
-          };
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (it.n[t] == 0) continue;
-            ok = mbar_wait(bar(A_QFULL + t), nq[t] & 1);
-            ++nq[t];
-            if (ok) ok = qk(t, 0);
+            if (j + 1 == nt) tc::commit(bar(A_O + t));
           }
-          for (int j = 0; j < n && ok; ++j) {
-            for (int t = 0; t < 2 && ok; ++t) {
-              if (j >= it.n[t]) continue;
-              ok = pv(t, j);
-              if (ok && j + 1 < it.n[t]) ok = qk(t, j + 1);
-            }
+          __syncwarp();
+          return true;
+        };
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || (t ? n1 : n0) == 0) continue;
+          ok = pa_wait(bar(A_QFULL + t), nq[t] & 1);
+          ++nq[t];
+          if (ok) ok = qk(t, 0);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int nt = t ? n1 : n0;
+            if (!ok || j >= nt) continue;
+            ok = pv(t, j);
+            if (ok && j + 1 < nt) ok = qk(t, j + 1);
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        base += n > 0 ? n * (QU + 2) : 0;
+        base += n * (QU + 2);
       }
-      if (lane == 0 && base > 0) {  // every MMA has completed before the tensor memory is released
-        tc::commit(bar(A_DRAIN));
-        if (!mbar_wait(bar(A_DRAIN), 0)) ok = false;
+      if (base > 0) {  // every MMA has completed before the tensor memory is released
+        if (pa_elect()) tc::commit(bar(A_DRAIN));
+        __syncwarp();
+        if (!pa_wait(bar(A_DRAIN), 0)) ok = false;
       }
-      __syncwarp();
     }
     // ---------------------------------------------------------------- values that not every row sees
     else {
@@ -546,9 +578,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const int n = max(it.n[0], it.n[1]);
         const int seen = pa_lim(p.causal, it.nq, it.nk, it.prefix, it.tok0);
         for (int j = max(0, max(seen, 0) / kPaN - it.kt0); j < n && ok; ++j) {
-          for (int c = 0; c < 2; ++c, ++ready) {
+          if (!pa_wait(bar(A_GFULL + ready % kPaTiles), (ready / kPaTiles) & 1)) { ok = false; break; }
+          for (int c = 0; c < 2; ++c) {
             const int u = base + QU + j * (QU + 2) + c;
-            if (!pa_wait(bar(A_GFULL + ready % kPaReady), (ready / kPaReady) & 1)) { ok = false; break; }
             const int row = 32 * g + lane, key = (it.kt0 + j) * kPaN + 64 * c + row;
             const uint32_t at = unit(u) + uint32_t(row) * 128;
             bool odd = false;
@@ -567,10 +599,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at + (x >> 3) * (kPaUnit / 2) + (((x + lane) & 7) << 4)), "r"(0)
                              : "memory");
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(A_READY + ready % kPaReady));
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(A_READY + ready % kPaTiles));
+          ++ready;
         }
         base += n * (QU + 2);
         __syncwarp();
