@@ -62,7 +62,7 @@ struct PaItem {
   int slot;     // of the item's first piece
   int piece;
   int last;     // no more items
-  int pad;
+  int paired;   // one row tile: the key tiles alternate between the two halves of the CTA
 };
 
 template <int ROPE>
@@ -72,7 +72,8 @@ struct PaLay {
   static constexpr size_t q = 0;
   static constexpr size_t units = q + 2 * qk_units * size_t(kPaUnit);
   static constexpr size_t item = units + ring * size_t(kPaUnit);
-  static constexpr size_t bad = item + 2 * sizeof(PaItem);
+  static constexpr size_t ml = item + 2 * sizeof(PaItem);  // (m, l) of a paired item's rows, from either half
+  static constexpr size_t bad = ml + 2 * kPaM * 8;
   static constexpr size_t flag = bad + 8;
   static constexpr size_t tmem = flag + 8;
   static constexpr size_t bars = tmem + 16;
@@ -84,15 +85,17 @@ enum {
   A_QFULL = A_UFREE + 10,  // [row tile], and so the next ones
   A_QFREE = A_QFULL + 2,
   A_S = A_QFREE + 2,
-  A_P = A_S + 2,
-  A_O = A_P + 2,
+  A_P = A_S + 2,           // [row tile][half of the keys]
+  A_O = A_P + 4,
   A_ITEM = A_O + 2,        // [item parity]
   A_TAKEN = A_ITEM + 2,
   A_KFULL = A_TAKEN + 2,   // [tile % kPaTiles]: keys, values, values that the guards look at, those after they have
   A_VFULL = A_KFULL + kPaTiles,
   A_GFULL = A_VFULL + kPaTiles,
   A_READY = A_GFULL + kPaTiles,
-  A_DRAIN = A_READY + kPaTiles,
+  A_HALF = A_READY + kPaTiles,  // [row tile]: its four warps meet, where an item is cut
+  A_PAIR = A_HALF + 2,          // the eight softmax warps meet, in paired items
+  A_DRAIN,
   A_COUNT
 };
 static_assert(A_COUNT <= 48, "barriers");
@@ -263,6 +266,12 @@ __device__ __forceinline__ bool pa_item(const PromptArgs& p, int idx, PaItem& it
   it.kt0 = it.piece * per;
   it.n[0] = max(0, min(per, n0 - it.kt0));
   it.n[1] = max(0, min(per, n1 - it.kt0));
+  // a lone row tile with several key tiles: both halves of the CTA work for it, on the even and on the odd ones
+  it.paired = n1 == 0 && all > 1;
+  if (it.paired) {
+    it.n[1] = it.n[0] / 2;
+    it.n[0] -= it.n[1];
+  }
   it.last = 0;
   return it.piece < it.pieces;
 }
@@ -302,6 +311,11 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {  // NaN if one of them is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -355,10 +369,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       mbar_init(bar(A_QFULL + t), 1);
       mbar_init(bar(A_QFREE + t), 1);
       mbar_init(bar(A_S + t), 1);
-      mbar_init(bar(A_P + t), 4);
+      mbar_init(bar(A_P + 2 * t), 4);
+      mbar_init(bar(A_P + 2 * t + 1), 4);
       mbar_init(bar(A_O + t), 1);
       mbar_init(bar(A_ITEM + t), 1);
       mbar_init(bar(A_TAKEN + t), 8 + 1 + kPaGuards);
+      mbar_init(bar(A_HALF + t), 4);
     }
     for (int i = 0; i < kPaTiles; ++i) {
       mbar_init(bar(A_KFULL + i), 1);
@@ -366,6 +382,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       mbar_init(bar(A_GFULL + i), 1);
       mbar_init(bar(A_READY + i), kPaGuards);
     }
+    mbar_init(bar(A_PAIR), 8);
     mbar_init(bar(A_DRAIN), 1);
     tc::fence_mbarrier_init_cluster();
   }
@@ -413,7 +430,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         int next = 0;
         if (lane == 0) {
           next = atomicAdd(claim, 1);
-          const int n = max(it.n[0], it.n[1]);
+          const int n = it.paired ? it.n[0] + it.n[1] : max(it.n[0], it.n[1]);
           const int seen = pa_lim(p.causal, it.nq, it.nk, it.prefix, it.tok0);
           // a key tile's units, and a value tile's, arrive at the barrier of their first one
           auto load_k = [&](int j) {
@@ -442,7 +459,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           };
           if (n > 0) load_k(0);
           for (int t = 0; t < 2 && ok; ++t) {
-            if (it.n[t] == 0) continue;
+            if (it.n[t] == 0 || (t == 1 && it.paired)) continue;
             if (nq[t] > 0 && !mbar_wait(bar(A_QFREE + t), (nq[t] - 1) & 1)) { ok = false; break; }
             ++nq[t];
             mbar_arrive_expect_tx(bar(A_QFULL + t), QU * kPaUnit);
@@ -450,9 +467,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               tma_load_3d(sb + uint32_t(Y::q) + (t * QU + c) * kPaUnit, &q_map, 64 * c, it.head0,
                           it.q0 + it.tok0 + t * (kPaM >> p.log2_pack), bar(A_QFULL + t));
           }
+          const int ahead = it.paired ? 2 : 1;
+          if (it.paired && ok && n > 1) load_k(1);
           for (int j = 0; j < n && ok; ++j) {
             load_v(j);
-            if (j + 1 < n && ok) load_k(j + 1);
+            if (j + ahead < n && ok) load_k(j + ahead);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -486,13 +505,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(A_TAKEN + (k & 1)));
         if (last_item) break;
-        const int n = max(n0, n1);
+        const int paired = uniform(item.paired), n = paired ? n0 + n1 : max(n0, n1), ahead = paired ? 2 : 1;
         // units of key tile j, and of its values
-        auto uk = [&](int j) { return j == 0 ? base : base + QU + (j - 1) * (QU + 2) + 2; };
-        auto uv = [&](int j) { return base + QU + j * (QU + 2); };
-        auto qk = [&](int t, int j) -> bool {
-          const int nt = t ? n1 : n0;
-          const bool first_use = t == 0 || j >= n0, last_use = t == 1 || j >= n1;
+        auto uk = [&](int j) { return j < ahead ? base + j * QU : base + ahead * QU + (j - ahead) * (QU + 2) + 2; };
+        auto uv = [&](int j) { return min(j + ahead, n) * QU + 2 * j + base; };
+        auto qk = [&](int t, int j, bool last) -> bool {
+          const bool first_use = paired || t == 0 || j >= n0, last_use = paired || t == 1 || j >= n1;
+          const int tq = paired ? 0 : t;  // the row tile of q
           if (first_use) {
             if (!pa_wait(bar(A_KFULL + nk % kPaTiles), (nk / kPaTiles) & 1)) return false;
             ++nk;
@@ -502,20 +521,19 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           if (pa_elect()) {
 #pragma unroll
             for (int c = 0; c < QU; ++c) {
-              const uint64_t qa = dq + (t * QU + c) * (kPaUnit >> 4), ka = dk + ((u0 + c) % R) * (kPaUnit >> 4);
+              const uint64_t qa = dq + (tq * QU + c) * (kPaUnit >> 4), ka = dk + ((u0 + c) % R) * (kPaUnit >> 4);
 #pragma unroll
               for (int s = 0; s < 4; ++s) tc::mma_ss(tm + 128 * t, qa + 2 * s, ka + 2 * s, kIdQK, c > 0 || s > 0);
               if (last_use) tc::commit(bar(A_UFREE + (u0 + c) % R));
             }
             tc::commit(bar(A_S + t));
-            if (j + 1 == nt) tc::commit(bar(A_QFREE + t));
+            if (last) tc::commit(bar(A_QFREE + tq));
           }
           __syncwarp();
           return true;
         };
-        auto pv = [&](int t, int j) -> bool {
-          const int nt = t ? n1 : n0;
-          const bool first_use = t == 0 || j >= n0, last_use = t == 1 || j >= n1;
+        auto pv = [&](int t, int j, bool first, bool last) -> bool {
+          const bool first_use = paired || t == 0 || j >= n0, last_use = paired || t == 1 || j >= n1;
           if (first_use) {
             if ((kt0 + j + 1) * kPaN > seen) {
               if (!pa_wait(bar(A_READY + ng % kPaTiles), (ng / kPaTiles) & 1)) return false;
@@ -525,38 +543,53 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               ++nv;
             }
           }
-          if (!pa_wait(bar(A_P + t), ns[t] & 1)) return false;
-          ++ns[t];
-          tc::fence_after();
           const int u0 = uv(j);
-          if (pa_elect()) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < 2; ++c) {
+            if (!pa_wait(bar(A_P + 2 * t + c), ns[t] & 1)) return false;
+            tc::fence_after();
+            if (pa_elect()) {
               const uint64_t va = dv + ((u0 + c) % R) * (kPaUnit >> 4);
 #pragma unroll
               for (int s = 0; s < 4; ++s)
-                tc::mma_ts(tm + 256 + 128 * t, tm + 128 * t + 32 * c + 8 * s, va + 128 * s, kIdPV, j > 0 || c > 0 || s > 0);
+                tc::mma_ts(tm + 256 + 128 * t, tm + 128 * t + 32 * c + 8 * s, va + 128 * s, kIdPV, !first || c > 0 || s > 0);
               if (last_use) tc::commit(bar(A_UFREE + (u0 + c) % R));
+              if (c == 1 && last) tc::commit(bar(A_O + t));
             }
-            if (j + 1 == nt) tc::commit(bar(A_O + t));
+            __syncwarp();
           }
-          __syncwarp();
+          ++ns[t];
           return true;
         };
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || (t ? n1 : n0) == 0) continue;
-          ok = pa_wait(bar(A_QFULL + t), nq[t] & 1);
-          ++nq[t];
-          if (ok) ok = qk(t, 0);
-        }
-        for (int j = 0; j < n && ok; ++j) {
+        if (paired) {
+          if (n > 0) {
+            ok = pa_wait(bar(A_QFULL), nq[0] & 1);
+            ++nq[0];
+            ok = ok && qk(0, 0, n == 1) && (n == 1 || qk(1, 1, n == 2));
+          }
+          for (int j = 0; j < n && ok; j += 2) {
+            ok = pv(0, j, j == 0, j + 2 >= n);
+            if (ok && j + 2 < n) ok = qk(0, j + 2, j + 3 == n);
+            if (ok && j + 1 < n) ok = pv(1, j + 1, j == 0, j + 3 >= n);
+            if (ok && j + 3 < n) ok = qk(1, j + 3, j + 4 == n);
+          }
+        } else {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int nt = t ? n1 : n0;
-            if (!ok || j >= nt) continue;
-            ok = pv(t, j);
-            if (ok && j + 1 < nt) ok = qk(t, j + 1);
+            if (!ok || nt == 0) continue;
+            ok = pa_wait(bar(A_QFULL + t), nq[t] & 1);
+            ++nq[t];
+            if (ok) ok = qk(t, 0, nt == 1);
+          }
+          for (int j = 0; j < n && ok; ++j) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int nt = t ? n1 : n0;
+              if (!ok || j >= nt) continue;
+              ok = pv(t, j, j == 0, j + 1 == nt);
+              if (ok && j + 1 < nt) ok = qk(t, j + 1, j + 2 == nt);
+            }
           }
         }
         base += n * (QU + 2);
@@ -575,12 +608,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (!pa_wait(bar(A_ITEM + (k & 1)), (k >> 1) & 1)) { ok = false; break; }
         const PaItem it = items[k & 1];
         if (it.last) break;
-        const int n = max(it.n[0], it.n[1]);
+        const int n = it.paired ? it.n[0] + it.n[1] : max(it.n[0], it.n[1]), ahead = it.paired ? 2 : 1;
         const int seen = pa_lim(p.causal, it.nq, it.nk, it.prefix, it.tok0);
         for (int j = max(0, max(seen, 0) / kPaN - it.kt0); j < n && ok; ++j) {
           if (!pa_wait(bar(A_GFULL + ready % kPaTiles), (ready / kPaTiles) & 1)) { ok = false; break; }
           for (int c = 0; c < 2; ++c) {
-            const int u = base + QU + j * (QU + 2) + c;
+            const int u = base + min(j + ahead, n) * QU + 2 * j + c;
             const int row = 32 * g + lane, key = (it.kt0 + j) * kPaN + 64 * c + row;
             const uint32_t at = unit(u) + uint32_t(row) * 128;
             bool odd = false;
@@ -618,12 +651,18 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const uint32_t tl = tm + (uint32_t(32 * (warp & 3)) << 16), ts = tl + 128 * t, to = tl + 256 + 128 * t;
     int32_t* flag = reinterpret_cast<int32_t*>(sm + Y::flag) + t;
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-    int ns = 0, no = 0;
+    int ns = 0, no = 0, nhalf = 0, npair = 0;
+    auto meet = [&](int b, int& count) -> bool {  // the warps of a barrier, bounded as every wait
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(b));
+      return pa_wait(bar(b), count++ & 1);
+    };
     for (int k = 0; ok; ++k) {
       if (!pa_wait(bar(A_ITEM + (k & 1)), (k >> 1) & 1)) { ok = false; break; }
       const PaItem& it = items[k & 1];
       if (it.last) break;
-      const int first = it.tok0 + t * (kPaM >> p.log2_pack), token = first + (row >> p.log2_pack);
+      const bool paired = it.paired;
+      const int first = it.tok0 + (paired ? 0 : t) * (kPaM >> p.log2_pack), token = first + (row >> p.log2_pack);
       const int hd = it.head0 + (row & ((1 << p.log2_pack) - 1));
       const bool mine = token < it.nq;
       const int lim = mine ? pa_lim(p.causal, it.nq, it.nk, it.prefix, token) : 0;
@@ -644,18 +683,40 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         float x[128];
 #pragma unroll
         for (int i = 0; i < 128; ++i) x[i] = __uint_as_float(raw[i >> 5][i & 31]);
-        const int key0 = (kt0 + j) * kPaN;
-        if constexpr (CAP) {  // cap tanh(u) = cap - 2 cap / (1 + e^(2u)): within 2^-22 of cap
+        const int key0 = (kt0 + (paired ? 2 * j + t : j)) * kPaN;
+        const bool masked = key0 + kPaN > all_see;
+        const int left = lim - key0;
+        if constexpr (CAP) {
+          if (masked) {  // four scores share a reciprocal: a hidden one that is not a number stays out of it
 #pragma unroll
-          for (int i = 0; i < 128; ++i) x[i] = fmaf(-2.f * p.cap2, rcp(1.f + ex2(x[i] * p.cap_in)), p.cap2);
+            for (int i = 0; i < 128; ++i) x[i] = i < left ? x[i] : -CUDART_INF_F;
+          }
+          float probe = -CUDART_INF_F;
+#pragma unroll
+          for (int i = 0; i < 128; i += 2) probe = max3_nan(probe, x[i], x[i + 1]);
+          if (probe != probe) sum2 = f2(CUDART_NAN_F, 0.f);
+          // cap tanh(u) = cap - 2 cap / (1 + e^(2u)), within 2^-21 of cap; four quotients from one reciprocal of the
+          // product (u is cut where tanh is 1 to 2^-29: the product stays finite)
+          const float down = -2.f * p.cap2;
+#pragma unroll
+          for (int i = 0; i < 128; i += 4) {
+            float e[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) e[c] = 1.f + ex2(fminf(x[i + c] * p.cap_in, 30.f));
+            const float ab = e[0] * e[1], cd = e[2] * e[3], r = rcp(ab * cd) * down;
+            const float rab = r * cd, rcd = r * ab;
+            x[i] = fmaf(rab, e[1], p.cap2);
+            x[i + 1] = fmaf(rab, e[0], p.cap2);
+            x[i + 2] = fmaf(rcd, e[3], p.cap2);
+            x[i + 3] = fmaf(rcd, e[2], p.cap2);
+          }
         }
         if constexpr (BIAS) {
           const float d0 = pos - float(key0);
 #pragma unroll
           for (int i = 0; i < 128; ++i) x[i] = fmaf(-slope, fabsf(d0 - float(i)), CAP ? x[i] : x[i] * p.c2);
         }
-        if (key0 + kPaN > all_see) {
-          const int left = lim - key0;
+        if (masked) {
 #pragma unroll
           for (int i = 0; i < 128; ++i) x[i] = i < left ? x[i] : -CUDART_INF_F;
         }
@@ -699,12 +760,14 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             w[i] = pack_bf16x2(a, b);
           }
           tc::st16(ts + 16 * c, w);
+          if (c & 1) {  // PV of the first half of the keys starts while the second half's weights are made
+            tc::wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(A_P + 2 * t + (c >> 1)));
+          }
         }
         sum2 = f2_add(sum2, f2_add(part[0], part[1]));
-        tc::wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(A_P + t));
       }
       if (!ok) break;
       if (n > 0) {
@@ -724,99 +787,120 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         m_ = base;
         return l_ == 0.f ? 0.f : f / l_;
       };
-      if (it.pieces == 1) {
-        const float f = spoilt ? CUDART_NAN_F : finish(m, l);
-        if (spoilt) finish(m, l);
-        if (mine && p.lse) p.lse[at] = (log2f(l) + m) * kLn2;
+      // chunks of 32 dims that this thread finishes: all four, or two of a paired item's row, out of both halves' sums
+      const int c0 = paired ? 2 * t : 0, c1 = paired ? 2 * t + 2 : 4, n_other = it.n[1 - t];
+      float fa = 1.f, fb = 0.f;
+      if (paired) {
+        float2* ml = reinterpret_cast<float2*>(sm + Y::ml);
+        ml[t * kPaM + row] = make_float2(m, l);
+        if (!meet(A_PAIR, npair)) { ok = false; break; }
+        tc::fence_after();
+        const float2 o = ml[(1 - t) * kPaM + row];
+        const float both = fmaxf(m, o.x);
+        fa = m == -CUDART_INF_F ? 0.f : ex2(m - both);
+        fb = o.x == -CUDART_INF_F ? 0.f : ex2(o.x - both);
+        l = l * fa + o.y * fb;
+        m = both;
+      }
+      auto sums = [&](int c, float (&v)[32]) {
+        uint32_t o[32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          if (n > 0) {
-            tc::ld32(to + 32 * c, o);
-            tc::wait_ld();
-          }
-          if (mine) {
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        if (n > 0) {
+          tc::ld32(to + 32 * c, o);
+          tc::wait_ld();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t w[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                w[i] = n > 0 ? pack_bf16x2(__uint_as_float(o[16 * h + 2 * i]) * f, __uint_as_float(o[16 * h + 2 * i + 1]) * f) : 0;
-              store32(static_cast<uint16_t*>(p.out) + at * 128 + 32 * c + 16 * h, w, wide);
-            }
-          }
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * fa;
         }
+        if (paired && n_other > 0) {
+          tc::ld32(tl + 256 + 128 * (1 - t) + 32 * c, o);
+          tc::wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o[i]), fb, v[i]);
+        }
+      };
+      auto write = [&](int c, const float (&v)[32], float f) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[16 * h + 2 * i] * f, v[16 * h + 2 * i + 1] * f);
+          store32(static_cast<uint16_t*>(p.out) + at * 128 + 32 * c + 16 * h, w, wide);
+        }
+      };
+      const bool writes_lse = mine && p.lse && (!paired || t == 0);
+      if (it.pieces == 1) {
+        float f = finish(m, l);
+        if (spoilt) f = CUDART_NAN_F;
+        if (writes_lse) p.lse[at] = (log2f(l) + m) * kLn2;
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
+          float v[32];
+          sums(c, v);
+          if (mine) write(c, v, f);
+        }
+        if (paired && !meet(A_PAIR, npair)) { ok = false; break; }  // both sums have been read
       } else {
         float* slot = p.parts + int64_t(it.slot + it.piece) * kPaSlotFloats;
-        float* po = slot + (t * kPaM + row) * 128;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          if (n > 0) {
-            tc::ld32(to + 32 * c, o);
-            tc::wait_ld();
-          }
+        // a part's sums: [32 pieces of 4 dims][rows], so that a warp moves whole lines; a paired row's stand in the first row tile
+        const int prow = (paired ? 0 : t * kPaM) + row;
+        float4* po = reinterpret_cast<float4*>(slot) + prow;
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
+          float v[32];
+          sums(c, v);
           if (mine) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (n > 0) v = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
-                                         __uint_as_float(o[4 * i + 3]));
-              if (spoilt) v = make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
-              reinterpret_cast<float4*>(po + 32 * c)[i] = v;
-            }
+            for (int i = 0; i < 8; ++i)
+              po[(8 * c + i) * kPaRows] = spoilt ? make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F)
+                                                 : make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
         if (mine) reinterpret_cast<float2*>(slot + kPaRows * 128)[t * kPaM + row] = make_float2(m, l);
         __threadfence();
-        named_bar(1 + t, 128);
+        if (paired && !meet(A_PAIR, npair)) { ok = false; break; }
+        if (!meet(A_HALF + t, nhalf)) { ok = false; break; }
         if (row == 0) {
           int32_t* count = p.counts + 2 * it.slot + t;
           const int old = atomicAdd(count, 1);
           if (old == it.pieces - 1) *count = 0;  // the last one: nobody else looks at it in this call
           *flag = old;
         }
-        named_bar(1 + t, 128);
-        if (*reinterpret_cast<volatile int32_t*>(flag) == it.pieces - 1) {
+        if (!meet(A_HALF + t, nhalf)) { ok = false; break; }
+        if (*reinterpret_cast<volatile int32_t*>(flag) == it.pieces - 1 && mine) {
           __threadfence();
-          if (mine) {
-            const float* s0 = p.parts + int64_t(it.slot) * kPaSlotFloats;
-            float M = -CUDART_INF_F, Lsum = 0.f;
-            for (int q = 0; q < it.pieces; ++q)
-              M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(s0 + int64_t(q) * kPaSlotFloats + kPaRows * 128) + t * kPaM + row).x);
-            const float Mu = M == -CUDART_INF_F ? 0.f : M;
-            for (int q = 0; q < it.pieces; ++q) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(s0 + int64_t(q) * kPaSlotFloats + kPaRows * 128) + t * kPaM + row);
-              Lsum += ml.y * (ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - Mu));
-            }
-            const float f = finish(M, Lsum);
-            if (p.lse) p.lse[at] = (log2f(Lsum) + M) * kLn2;
+          const float* s0 = p.parts + int64_t(it.slot) * kPaSlotFloats;
+          auto ml_of = [&](int q) {
+            return __ldcg(reinterpret_cast<const float2*>(s0 + int64_t(q) * kPaSlotFloats + kPaRows * 128) + t * kPaM + row);
+          };
+          float M = -CUDART_INF_F, Lsum = 0.f;
+          for (int q = 0; q < it.pieces; ++q) M = fmaxf(M, ml_of(q).x);
+          const float Mu = M == -CUDART_INF_F ? 0.f : M;
+          for (int q = 0; q < it.pieces; ++q) {
+            const float2 v = ml_of(q);
+            Lsum += v.y * (v.x == -CUDART_INF_F ? 0.f : ex2(v.x - Mu));
+          }
+          const float f = finish(M, Lsum);
+          // M may have moved to the sink's: the parts' factors are of Mu, f takes them there
+          if (writes_lse) p.lse[at] = (log2f(Lsum) + M) * kLn2;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              float acc[32];
+          for (int c = c0; c < c1; ++c) {
+            float acc[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-              for (int q = 0; q < it.pieces; ++q) {
-                const float* s1 = s0 + int64_t(q) * kPaSlotFloats;
-                const float mq = __ldcg(reinterpret_cast<const float2*>(s1 + kPaRows * 128) + t * kPaM + row).x;
-                const float fq = mq == -CUDART_INF_F ? 0.f : ex2(mq - Mu);
+            for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+            for (int q = 0; q < it.pieces; ++q) {
+              const float mq = ml_of(q).x, fq = mq == -CUDART_INF_F ? 0.f : ex2(mq - Mu);
+              const float4* pq = reinterpret_cast<const float4*>(s0 + int64_t(q) * kPaSlotFloats) + prow;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float4 v = __ldcg(reinterpret_cast<const float4*>(s1 + (t * kPaM + row) * 128 + 32 * c) + i);
-                  acc[4 * i] = fmaf(v.x, fq, acc[4 * i]);
-                  acc[4 * i + 1] = fmaf(v.y, fq, acc[4 * i + 1]);
-                  acc[4 * i + 2] = fmaf(v.z, fq, acc[4 * i + 2]);
-                  acc[4 * i + 3] = fmaf(v.w, fq, acc[4 * i + 3]);
-                }
-              }
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t w[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(acc[16 * h + 2 * i] * f, acc[16 * h + 2 * i + 1] * f);
-                store32(static_cast<uint16_t*>(p.out) + at * 128 + 32 * c + 16 * h, w, wide);
+              for (int i = 0; i < 8; ++i) {
+                const float4 v = __ldcg(pq + (8 * c + i) * kPaRows);
+                acc[4 * i] = fmaf(v.x, fq, acc[4 * i]);
+                acc[4 * i + 1] = fmaf(v.y, fq, acc[4 * i + 1]);
+                acc[4 * i + 2] = fmaf(v.z, fq, acc[4 * i + 2]);
+                acc[4 * i + 3] = fmaf(v.w, fq, acc[4 * i + 3]);
               }
             }
+            write(c, acc, f);
           }
         }
       }
