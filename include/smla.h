@@ -671,7 +671,7 @@ typedef struct smla_prompt_desc {
 
 /*
  * Bytes of device workspace smla_prompt_attention needs for `d` on the current device: the error word,
- * the plan and the parts of work that several SMs share (about 80 MB, whatever the batch's size). The
+ * the plan and the parts of work that several SMs share (about 40 MB, whatever the batch's size). The
  * caller allocates it (256-byte aligned) and zeroes it once before first use (and again after a call that set
  * SMLA_DEVERR_TIMEOUT); smla_read_error reads and clears the error word. Writes 0 into *bytes on error.
  */

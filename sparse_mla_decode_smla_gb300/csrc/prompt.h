@@ -66,15 +66,14 @@ struct PromptArgs {
   void* out;
   float* lse;
   uint8_t* ws;              // error word, counters and a line a request
-  int32_t* counts;          // [slots][row tile]: pieces that have ended, zero between calls
-  float* parts;             // [slots]
+  int32_t* counts;          // [SM][row tile]: pieces that have ended, zero between calls
+  float* parts;             // two an SM
   int64_t q_token, q_head, k_token, k_head, v_token, v_head, rope_token;  // strides in elements
-  int32_t T, N, H, HK, B, causal, log2_pack, sms, slots;
+  int32_t T, N, H, HK, B, causal, log2_pack, sms;
   float c2;                 // sm_scale log2(e)
   float cap2, cap_in;       // cap log2(e) (0: no cap); 2 sm_scale log2(e) / cap
 };
 struct PromptLayout {
-  int slots;
   size_t counts, parts, bytes;
 };
 PromptLayout prompt_layout(int64_t requests, int num_sms);

@@ -7,10 +7,12 @@
 //
 // Work. An item is 256 rows of one request and kv head, in two row tiles of 128: consecutive tokens, with as many query
 // heads of the kv head as a power of two allows beside one another (a single token's grouped heads share a tile). Its
-// keys come in tiles of 128. Items whose keys are many beside the batch's whole work are cut into pieces that leave their
-// parts in the workspace; the piece that ends last joins them, in the order of the keys. The items of a request run from
-// the last rows (most keys) to the first, some heads at a time, so that SMs that run together share keys in L2. A small
-// kernel lays the items out from the lengths on the device; the CTAs, one an SM, take them off a counter.
+// keys come in tiles of 128. The CTAs, one an SM, share the items in one of two ways, from the lengths on the device:
+//  * items that are short beside an SM's share are taken off a counter, a request's last rows (most keys) first, heads
+//    whose keys fit L2 together at a time;
+//  * else the key tiles of all items, in order, are cut into equal runs, one a CTA. An item that a run's end cuts leaves its
+//    parts in the workspace, two a CTA at most; the piece that ends last joins them, in the order of the keys.
+// Up to 32 requests are laid out by a warp of every CTA, more by a small kernel before.
 //
 // A key tile on one SM: S = Q K^T (12 MMAs of 128 x 128 x 16 a row tile), the weights P = 2^(x - m) in BF16 written over
 // S in tensor memory, O += P V (8 MMAs, P from tensor memory). The two row tiles alternate: one's softmax runs while the
@@ -45,7 +47,8 @@ constexpr int kPaThreads = 384;
 constexpr int kPaMmaWarp = 8, kPaLoadWarp = 9, kPaGuardWarp = 10, kPaGuards = 2;
 constexpr int kPaTiles = 4;                // key (value) tiles in the ring at most: 3
 constexpr float kPaRescale = 8.f;
-constexpr int kPaMinTiles = 8;             // key tiles of a piece at least
+constexpr int kPaMinTiles = 8;             // key tiles of a run, and of a piece but the odd one, at least
+constexpr int kPaItemCost = 3;             // an item's own work, in key tiles
 constexpr int kPaSlotFloats = kPaRows * 128 + kPaRows * 2;  // a piece's part: O, then (m, l) of each row
 
 struct PaItem {
@@ -59,7 +62,7 @@ struct PaItem {
   int n[2];     // key tiles of this piece that each row tile sees
   int prefix;   // keys that every token sees
   int pieces;   // pieces of the item (1: not cut)
-  int slot;     // of the item's first piece
+  int cta0;     // the CTA of the first one: the others follow it
   int piece;
   int last;     // no more items
   int paired;   // one row tile: the key tiles alternate between the two halves of the CTA
@@ -129,125 +132,252 @@ __device__ __forceinline__ int pa_tiles(const PromptArgs& p, const PaReq& q, int
 }
 
 struct PaHead {  // the start of the workspace
-  int32_t err, claim, total, len;  // device error word; next item; items; key tiles of a piece
+  int32_t err, claim, done, longest;  // device error word; next item; CTAs that have ended; key tiles of the longest item
 };
-struct PaTab {  // a request's line in the plan
-  int32_t item0, slot0, pieces, pad;
+struct PaTab {  // key tiles and items before a request, of all its heads; [B] holds the totals
+  int64_t tiles;
+  int32_t items, pad;
 };
 __device__ __forceinline__ PaTab* pa_table(const PromptArgs& p) { return reinterpret_cast<PaTab*>(p.ws + 256); }
 
 constexpr int kPlanThreads = 256;
+constexpr int kPlanWarp = 32;  // requests that a warp lays out itself
 
-template <typename T>
-__device__ __forceinline__ T plan_sum(T v, T* sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  T s = 0;
-  for (int i = 0; i < kPlanThreads / 32; ++i) s += sh[i];
-  return s;
+// A request's key tiles over all blocks of rows, for one group of heads beside one another.
+__device__ __forceinline__ int64_t pa_sum(const PromptArgs& p, const PaReq& q) {
+  const int tb = kPaRows >> p.log2_pack;
+  if (!p.causal) return int64_t(q.blocks) * pa_tiles(p, q, 0);
+  int64_t n = 0;
+  for (int b = 0; b < q.blocks; ++b) n += pa_tiles(p, q, min((b + 1) * tb, q.nq) - 1);
+  return n;
 }
 
-// Lays out the items: a piece is as long as half of an SM's share of the key tiles, longer where the workspace asks for it.
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptArgs p) {
-  __shared__ int64_t sh[kPlanThreads / 32];
-  __shared__ int2 scan[kPlanThreads / 32];
+  __shared__ PaTab scan[kPlanThreads / 32];
+  __shared__ int most[kPlanThreads / 32];
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int tb = kPaRows >> p.log2_pack, G = p.H >> p.log2_pack;
+  const int tid = threadIdx.x, lane = tid & 31, G = p.H >> p.log2_pack;
   PaHead* head = reinterpret_cast<PaHead*>(p.ws);
-  int64_t work = 0;
-  for (int r = tid; r < p.B; r += kPlanThreads) {
-    PaReq q;
-    const int ok = pa_request(p, r, q);
-    if (ok < 0) atomicOr(&head->err, SMLA_DEVERR_INDEX);
-    if (ok > 0) work += int64_t(q.blocks) * G * (pa_tiles(p, q, min(tb, q.nq) - 1) + pa_tiles(p, q, q.nq - 1) + 1) / 2;
-  }
-  work = plan_sum(work, sh);
-  int64_t len = max(int64_t(kPaMinTiles), (work + 2 * p.sms - 1) / (2 * p.sms));
-  for (;; len *= 2) {
-    int64_t slots = 0;
-    for (int r = tid; r < p.B; r += kPlanThreads) {
-      PaReq q;
-      if (pa_request(p, r, q) > 0) {
-        const int64_t n = (pa_tiles(p, q, q.nq - 1) + len - 1) / len;
-        if (n > 1) slots += int64_t(q.blocks) * G * n;
-      }
-    }
-    if (plan_sum(slots, sh) <= p.slots) break;
-  }
-  int items = 0, slots = 0;  // of the requests before this round's
+  PaTab before = {0, 0, 0};  // of the requests before this round's
+  int longest = 0;
   for (int r0 = 0; r0 < p.B; r0 += kPlanThreads) {
     const int r = r0 + tid;
-    int2 v = make_int2(0, 0);
-    int n = 1;
+    PaTab v = {0, 0, 0};
     PaReq q;
-    if (r < p.B && pa_request(p, r, q) > 0) {
-      n = max(1, static_cast<int>((pa_tiles(p, q, q.nq - 1) + len - 1) / len));
-      v.x = q.blocks * G * n;
-      v.y = n > 1 ? v.x : 0;
+    const int ok = r < p.B ? pa_request(p, r, q) : 0;
+    if (ok < 0) atomicOr(&head->err, SMLA_DEVERR_INDEX);
+    if (ok > 0) {
+      v.tiles = pa_sum(p, q) * G;
+      v.items = q.blocks * G;
+      longest = max(longest, pa_tiles(p, q, q.nq - 1));
     }
-    int2 x = v;
+    PaTab x = v;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const int a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o);
+      const int64_t a = __shfl_up_sync(0xffffffffu, x.tiles, o);
+      const int b = __shfl_up_sync(0xffffffffu, x.items, o);
       if (lane >= o) {
-        x.x += a;
-        x.y += b;
+        x.tiles += a;
+        x.items += b;
       }
     }
     __syncthreads();
     if (lane == 31) scan[tid >> 5] = x;
     __syncthreads();
-    int2 before = make_int2(items, slots);
+    PaTab mine = before;
     for (int i = 0; i < kPlanThreads / 32; ++i) {
       if (i < (tid >> 5)) {
-        before.x += scan[i].x;
-        before.y += scan[i].y;
+        mine.tiles += scan[i].tiles;
+        mine.items += scan[i].items;
       }
-      items += scan[i].x;
-      slots += scan[i].y;
+      before.tiles += scan[i].tiles;
+      before.items += scan[i].items;
     }
-    if (r < p.B) pa_table(p)[r] = PaTab{before.x + x.x - v.x, before.y + x.y - v.y, n, 0};
+    if (r < p.B) pa_table(p)[r] = PaTab{mine.tiles + x.tiles - v.tiles, mine.items + x.items - v.items, 0};
   }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) most[tid >> 5] = longest;
+  __syncthreads();
   if (tid == 0) {
-    head->claim = 0;
-    head->total = items;
-    head->len = static_cast<int32_t>(min(len, int64_t(1) << 30));
+    for (int i = 1; i < kPlanThreads / 32; ++i) longest = max(longest, most[i]);
+    head->longest = longest;
+    pa_table(p)[p.B] = before;
   }
 }
 
-// Item `idx` (by a whole warp); false for a piece past the end of its rows' keys.
-__device__ __forceinline__ bool pa_item(const PromptArgs& p, int idx, PaItem& it) {
+// What a warp knows of the batch, and its CTA's way through it. Lane r holds request r's line where there are few.
+struct PaWalk {
+  PaTab tab;       // few requests: this lane's line
+  PaTab total;
+  int64_t per;     // runs: their length; 0: items come off the counter
+  int cost;        // an item's own, in key tiles
+  // runs: the next item, how much of it is done, and where the run ends
+  int64_t x;       // the item's start
+  int r, hg, block, from;
+  int64_t x_end;   // start of the item that the run ends in
+  int end;         // key tiles of that item that belong to the run
+  int cta;
+};
+constexpr int kPaAll = 0x7fffffff;
+
+__device__ __forceinline__ PaTab pa_line(const PromptArgs& p, const PaWalk& w, int r) {
+  PaTab t;
+  if (p.B <= kPlanWarp) {
+    t.tiles = __shfl_sync(0xffffffffu, w.tab.tiles, r);
+    t.items = __shfl_sync(0xffffffffu, w.tab.items, r);
+  } else {
+    const int4 v = __ldcg(reinterpret_cast<const int4*>(pa_table(p) + r));
+    t.tiles = int64_t(uint32_t(v.x)) | int64_t(v.y) << 32;
+    t.items = v.z;
+  }
+  return t;
+}
+// The last request whose tiles * a + items * b before it are no more than x.
+__device__ __forceinline__ int pa_find(const PromptArgs& p, const PaWalk& w, int a, int b, int64_t x) {
   const int lane = threadIdx.x & 31;
-  const PaTab* tab = pa_table(p);
-  int lo = 0, hi = p.B;  // the last request whose first item is not past idx
+  if (p.B <= kPlanWarp) {
+    const uint32_t le = __ballot_sync(0xffffffffu, lane < p.B && w.tab.tiles * a + int64_t(w.tab.items) * b <= x);
+    return 31 - __clz(le);
+  }
+  int lo = 0, hi = p.B;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const uint32_t le = __ballot_sync(0xffffffffu, at < hi && __ldcg(&tab[at].item0) <= idx);
-    const int k = 31 - __clz(le);  // lane 0 holds
+    bool ok = false;
+    if (at < hi) {
+      const int4 v = __ldcg(reinterpret_cast<const int4*>(pa_table(p) + at));
+      ok = (int64_t(uint32_t(v.x)) | int64_t(v.y) << 32) * a + int64_t(v.z) * b <= x;
+    }
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, ok));  // lane 0 holds
     hi = min(hi, lo + (k + 1) * step);
     lo += k * step;
   }
-  const int4 t4 = __ldcg(reinterpret_cast<const int4*>(tab + lo));
-  const int len = __ldcg(&reinterpret_cast<const PaHead*>(p.ws)->len);
+  return lo;
+}
+// How many of an item's n key tiles lie before a cut at offset o of its n + cost: short pieces at the ends are avoided.
+__device__ __forceinline__ int pa_cut(int n, int cost, int o) {
+  if (n < 2 * kPaMinTiles) return 2 * o < n + cost ? 0 : kPaAll;
+  if (o < kPaMinTiles) return o < kPaMinTiles / 2 ? 0 : kPaMinTiles;
+  if (o > n - kPaMinTiles) return o > n - kPaMinTiles / 2 ? kPaAll : n - kPaMinTiles;
+  return o;
+}
+__device__ __forceinline__ int pa_block_tiles(const PromptArgs& p, const PaReq& q, int block) {
+  return pa_tiles(p, q, min((block + 1) * (kPaRows >> p.log2_pack), q.nq) - 1);
+}
+// The item that x lies in (its request, heads and block), its start, and the cut there.
+__device__ __forceinline__ int pa_locate(const PromptArgs& p, const PaWalk& w, int64_t x, int& r, int& hg, int& block, int64_t& start) {
+  const int lane = threadIdx.x & 31, G = p.H >> p.log2_pack;
+  r = pa_find(p, w, 1, w.cost, x);
+  const PaTab t = pa_line(p, w, r);
+  const PaTab next = r + 1 < p.B ? pa_line(p, w, r + 1) : w.total;
   PaReq q;
-  pa_request(p, lo, q);
-  const int G = p.H >> p.log2_pack, g = p.H / p.HK, np = t4.z;
-  // heads at a time: their keys and values take up to 32 MB
-  const int kv_heads = max(1, min(p.HK, static_cast<int>((int64_t(32) << 20) / (int64_t(q.nk) * 512 + 1))));
-  const int gc = kv_heads * (g >> p.log2_pack);
-  int i = idx - t4.x;
-  const int64_t chunk_items = int64_t(gc) * q.blocks * np;
-  const int chunk = static_cast<int>(i / chunk_items);
-  i -= static_cast<int>(chunk * chunk_items);
-  const int wide = min(gc, G - chunk * gc);
-  const int block = q.blocks - 1 - i / (wide * np);
-  i %= wide * np;
-  const int hg = chunk * gc + i / np;
-  it.piece = i % np;
+  pa_request(p, r, q);
+  const int64_t head = (next.tiles - t.tiles + int64_t(next.items - t.items) * w.cost) / G;  // one group of heads
+  int64_t at = x - t.tiles - int64_t(t.items) * w.cost;
+  hg = static_cast<int>(at / head);
+  at -= hg * head;
+  start = x - at;
+  for (int b0 = 0;; b0 += 32) {  // blocks, 32 at a time
+    const int b = b0 + lane, v = b < q.blocks ? pa_block_tiles(p, q, b) + w.cost : 0;
+    int sum = v;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const int all = __shfl_sync(0xffffffffu, sum, 31);
+    if (at < all) {
+      const int k = __ffs(__ballot_sync(0xffffffffu, sum > at)) - 1;
+      const int mine = __shfl_sync(0xffffffffu, sum - v, k), n = __shfl_sync(0xffffffffu, v, k) - w.cost;
+      block = b0 + k;
+      start += mine;
+      return pa_cut(n, w.cost, static_cast<int>(at) - mine);
+    }
+    at -= all;
+    start += all;
+    if (b0 + 32 >= q.blocks) break;  // not reached
+  }
+  block = 0;
+  return kPaAll;
+}
+__device__ __forceinline__ void pa_next(const PromptArgs& p, PaWalk& w, const PaReq& q) {  // the item behind this one
+  w.x += pa_block_tiles(p, q, w.block) + w.cost;
+  w.from = 0;
+  if (++w.block < q.blocks) return;
+  w.block = 0;
+  if (++w.hg < (p.H >> p.log2_pack)) return;
+  w.hg = 0;
+  PaReq n;
+  do ++w.r;
+  while (w.r < p.B && pa_request(p, w.r, n) <= 0);
+}
+
+// Lays the batch out: by a whole warp.
+__device__ __forceinline__ void pa_plan(const PromptArgs& p, PaWalk& w) {
+  const int lane = threadIdx.x & 31, G = p.H >> p.log2_pack;
+  PaHead* head = reinterpret_cast<PaHead*>(p.ws);
+  int longest = 0;
+  if (p.B <= kPlanWarp) {
+    PaReq q;
+    const int ok = lane < p.B ? pa_request(p, lane, q) : 0;
+    if (ok < 0 && blockIdx.x == 0) atomicOr(&head->err, SMLA_DEVERR_INDEX);
+    PaTab v = {0, 0, 0};
+    if (ok > 0) {
+      v.tiles = pa_sum(p, q) * G;
+      v.items = q.blocks * G;
+      longest = pa_tiles(p, q, q.nq - 1);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    w.tab = v;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t a = __shfl_up_sync(0xffffffffu, w.tab.tiles, o);
+      const int b = __shfl_up_sync(0xffffffffu, w.tab.items, o);
+      if (lane >= o) {
+        w.tab.tiles += a;
+        w.tab.items += b;
+      }
+    }
+    w.total.tiles = __shfl_sync(0xffffffffu, w.tab.tiles, 31);
+    w.total.items = __shfl_sync(0xffffffffu, w.tab.items, 31);
+    w.tab.tiles -= v.tiles;
+    w.tab.items -= v.items;
+  } else {
+    w.total = pa_line(p, w, p.B);
+    longest = __ldcg(&head->longest);
+  }
+  w.per = 0;
+  w.cost = kPaItemCost;
+  // Runs where the longest item is over a third of an SM's share (8191 tokens of 32 heads, 0.29 of it, take 2 % longer in
+  // runs; chunks of 2 x 1024 over 12k keys, 16 heads, 20 % longer off the counter).
+  if (int64_t(longest) * 3 * gridDim.x <= w.total.tiles || w.total.items == 0) return;
+  // an SM for every item, and none long enough to be cut: nothing to lay out
+  if (w.total.items <= static_cast<int>(gridDim.x) && longest < 2 * kPaMinTiles) return;
+  int64_t all = w.total.tiles + int64_t(w.total.items) * w.cost;
+  if (all < int64_t(kPaMinTiles) * gridDim.x) {  // less than a run each: items count as one, so that every one gets an SM
+    w.cost = kPaMinTiles;
+    all = w.total.tiles + int64_t(w.total.items) * w.cost;
+  }
+  w.per = max(int64_t(kPaMinTiles), (all + gridDim.x - 1) / gridDim.x);
+  w.cta = blockIdx.x;
+  const int64_t x0 = w.cta * w.per, x1 = x0 + w.per;
+  w.r = p.B;
+  w.x = w.x_end = 0;
+  w.end = 0;
+  if (x0 >= all) return;
+  w.from = pa_locate(p, w, x0, w.r, w.hg, w.block, w.x);
+  if (w.from == kPaAll) {
+    PaReq q;
+    pa_request(p, w.r, q);
+    pa_next(p, w, q);
+  }
+  w.x_end = all;
+  if (x1 < all) {
+    int r, hg, block;
+    w.end = pa_locate(p, w, x1, r, hg, block, w.x_end);
+  }
+}
+
+__device__ __forceinline__ void pa_fill(const PromptArgs& p, const PaReq& q, int hg, int block, PaItem& it) {
   it.q0 = q.q0;
   it.nq = q.nq;
   it.nk = q.nk;
@@ -255,26 +385,68 @@ __device__ __forceinline__ bool pa_item(const PromptArgs& p, int idx, PaItem& it
   it.prefix = q.prefix;
   it.tok0 = block * (kPaRows >> p.log2_pack);
   it.head0 = hg << p.log2_pack;
-  it.kvh = it.head0 / g;
+  it.kvh = it.head0 / (p.H / p.HK);
+  it.pieces = 1;
+  it.cta0 = it.piece = 0;
+  it.last = 0;
+}
+// key tiles [from, to) of an item
+__device__ __forceinline__ void pa_range(const PromptArgs& p, const PaReq& q, int from, int to, PaItem& it) {
   const int tt = kPaM >> p.log2_pack;  // tokens of a row tile
   const bool two = it.tok0 + tt < q.nq;
   const int n0 = pa_tiles(p, q, min(it.tok0 + tt, q.nq) - 1), n1 = two ? pa_tiles(p, q, min(it.tok0 + 2 * tt, q.nq) - 1) : 0;
-  const int all = max(n0, n1);
-  it.pieces = max(1, (all + len - 1) / len);
-  it.slot = t4.y + (block * G + hg) * np;
-  const int per = (all + it.pieces - 1) / it.pieces;
-  it.kt0 = it.piece * per;
-  it.n[0] = max(0, min(per, n0 - it.kt0));
-  it.n[1] = max(0, min(per, n1 - it.kt0));
+  it.kt0 = from;
+  it.n[0] = max(0, min(to, n0) - from);
+  it.n[1] = max(0, min(to, n1) - from);
   // a lone row tile with several key tiles: both halves of the CTA work for it, on the even and on the odd ones
-  it.paired = n1 == 0 && all > 1;
+  it.paired = !two && n0 > 1;
   if (it.paired) {
     it.n[1] = it.n[0] / 2;
     it.n[0] -= it.n[1];
   }
-  it.last = 0;
-  return it.piece < it.pieces;
 }
+
+// The next item of this CTA (by a whole warp); false when there are no more. idx: the item off the counter, without runs.
+__device__ __forceinline__ bool pa_item(const PromptArgs& p, PaWalk& w, int idx, PaItem& it) {
+  const int G = p.H >> p.log2_pack;
+  PaReq q;
+  if (w.per == 0) {
+    if (idx >= w.total.items) return false;
+    const int r = pa_find(p, w, 0, 1, idx);
+    int i = idx - pa_line(p, w, r).items;
+    pa_request(p, r, q);
+    // heads at a time: their keys and values take up to 128 MB
+    const int g = p.H / p.HK;
+    const int kv_heads = max(1, min(p.HK, static_cast<int>((int64_t(128) << 20) / (int64_t(q.nk) * 512 + 1))));
+    const int gc = kv_heads * (g >> p.log2_pack);
+    const int64_t chunk_items = int64_t(gc) * q.blocks;
+    const int chunk = static_cast<int>(i / chunk_items);
+    i -= static_cast<int>(chunk * chunk_items);
+    const int wide = min(gc, G - chunk * gc), block = q.blocks - 1 - i / wide;
+    pa_fill(p, q, chunk * gc + i % wide, block, it);
+    pa_range(p, q, 0, kPaAll, it);
+    return true;
+  }
+  if (w.r >= p.B || w.x > w.x_end || (w.x == w.x_end && w.end == 0)) return false;
+  pa_request(p, w.r, q);
+  pa_fill(p, q, w.hg, w.block, it);
+  const int n = pa_block_tiles(p, q, w.block);
+  const int to = w.x == w.x_end ? min(w.end, n) : n;
+  if (w.from > 0 || to < n) {  // the cuts of this item: runs' starts in it, in order
+    const int64_t k0 = (w.x + w.per - 1) / w.per;
+    int64_t lo = k0, hi = (w.x + n + w.cost - 1) / w.per;
+    while (lo <= hi && pa_cut(n, w.cost, static_cast<int>(lo * w.per - w.x)) == 0) ++lo;
+    while (hi >= lo && pa_cut(n, w.cost, static_cast<int>(hi * w.per - w.x)) == kPaAll) --hi;
+    it.pieces = static_cast<int>(hi - lo + 2);
+    it.cta0 = static_cast<int>(lo - 1);
+    it.piece = w.cta - it.cta0;
+  }
+  pa_range(p, q, w.from, to, it);
+  pa_next(p, w, q);
+  return true;
+}
+// A part's place: a CTA leaves one of an item that it starts, and one of an item that another CTA started.
+__device__ __forceinline__ int pa_slot(int cta0, int piece) { return 2 * (cta0 + piece) + (piece == 0); }
 
 // ---------------------------------------------------------------- helpers
 
@@ -396,7 +568,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  pdl_wait();  // the plan is complete, and with it what came before on the stream
+  pdl_wait();  // the plan, where there is one, is complete, and with it what came before on the stream
   const uint32_t tm = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(sm + Y::tmem), 0);
   bool ok = true;
 
@@ -404,20 +576,15 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---------------------------------------------------------------- items and loads
     if (warp == kPaLoadWarp) {
-      const int total = __ldcg(&reinterpret_cast<const PaHead*>(p.ws)->total);
       int32_t* claim = &reinterpret_cast<PaHead*>(p.ws)->claim;
-      int u = 0, nk = 0, nv = 0, ng = 0, nq[2] = {0, 0}, idx = 0;
-      if (lane == 0) idx = atomicAdd(claim, 1);
-      idx = __shfl_sync(0xffffffffu, idx, 0);
+      int u = 0, nk = 0, nv = 0, ng = 0, nq[2] = {0, 0}, idx = blockIdx.x;  // a CTA's first item is its own
+      PaWalk walk;
+      pa_plan(p, walk);
+      const bool counted = walk.per == 0 && walk.total.items > static_cast<int>(gridDim.x);
       auto room = [&](int at) { return at < R || mbar_wait(bar(A_UFREE + at % R), ((at / R) - 1) & 1); };
       for (int k = 0; ok; ++k) {
         PaItem it = {};
-        bool real = idx < total;
-        while (real && !pa_item(p, idx, it)) {  // a piece without keys
-          if (lane == 0) idx = atomicAdd(claim, 1);
-          idx = __shfl_sync(0xffffffffu, idx, 0);
-          real = idx < total;
-        }
+        const bool real = pa_item(p, walk, idx, it);
         it.last = !real;
         if (k >= 2 && !pa_wait(bar(A_TAKEN + (k & 1)), ((k >> 1) - 1) & 1)) { ok = false; break; }
         if (lane == 0) {
@@ -427,9 +594,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         }
         __syncwarp();
         if (!real) break;
-        int next = 0;
+        int next = kPaAll;
         if (lane == 0) {
-          next = atomicAdd(claim, 1);
+          if (counted) next = gridDim.x + atomicAdd(claim, 1);
           const int n = it.paired ? it.n[0] + it.n[1] : max(it.n[0], it.n[1]);
           const int seen = pa_lim(p.causal, it.nq, it.nk, it.prefix, it.tok0);
           // a key tile's units, and a value tile's, arrive at the barrier of their first one
@@ -477,6 +644,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         idx = __shfl_sync(0xffffffffu, next, 0);
       }
+      if (lane == 0 && counted) {  // the last CTA to come here resets the counter for the next call: no other one takes items any more
+        int32_t* done = &reinterpret_cast<PaHead*>(p.ws)->done;
+        __threadfence();
+        if (atomicAdd(done, 1) == static_cast<int>(gridDim.x) - 1) *claim = *done = 0;
+      }
       if (lane == 0) {  // copies still in flight land before shared memory goes
         auto landed = [&](int first, int n) {
           for (int at = max(0, n - kPaTiles); at < n; ++at)
@@ -502,10 +674,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         auto uniform = [&](int v) { return __shfl_sync(0xffffffffu, v, 0); };
         const int n0 = uniform(item.n[0]), n1 = uniform(item.n[1]), kt0 = uniform(item.kt0), last_item = uniform(item.last);
         const int seen = uniform(pa_lim(p.causal, item.nq, item.nk, item.prefix, item.tok0));  // keys that every row of the item sees
+        const int paired = uniform(item.paired);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(A_TAKEN + (k & 1)));
         if (last_item) break;
-        const int paired = uniform(item.paired), n = paired ? n0 + n1 : max(n0, n1), ahead = paired ? 2 : 1;
+        const int n = paired ? n0 + n1 : max(n0, n1), ahead = paired ? 2 : 1;
         // units of key tile j, and of its values
         auto uk = [&](int j) { return j < ahead ? base + j * QU : base + ahead * QU + (j - ahead) * (QU + 2) + 2; };
         auto uv = [&](int j) { return min(j + ahead, n) * QU + 2 * j + base; };
@@ -616,18 +789,19 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             const int u = base + min(j + ahead, n) * QU + 2 * j + c;
             const int row = 32 * g + lane, key = (it.kt0 + j) * kPaN + 64 * c + row;
             const uint32_t at = unit(u) + uint32_t(row) * 128;
-            bool odd = false;
-            if (key < it.nk) {
-#pragma unroll 4
+            bool zero = key >= it.nk;
+            if (!zero && key >= seen) {
+              uint32_t top = 0;  // the larger exponents of both halves of the words
+#pragma unroll
               for (int x = 0; x < 16; ++x) {
                 const uint4 y = lds128(at + (x >> 3) * (kPaUnit / 2) + (((x + lane) & 7) << 4));
-                const uint32_t w4[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) odd |= (w4[e] & 0x7f80u) == 0x7f80u || (w4[e] & 0x7f800000u) == 0x7f800000u;
+                top = __vmaxu2(__vmaxu2(top, __vmaxu2(y.x & 0x7f807f80u, y.y & 0x7f807f80u)),
+                               __vmaxu2(y.z & 0x7f807f80u, y.w & 0x7f807f80u));
               }
-              if (odd && key >= seen) atomicMin(bad + (k & 1), key);
+              zero = (top & 0xffffu) == 0x7f80u || (top >> 16) == 0x7f80u;
+              if (zero) atomicMin(bad + (k & 1), key);
             }
-            if (key >= it.nk || (odd && key >= seen)) {
+            if (zero) {
               for (int x = 0; x < 16; ++x)
                 asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at + (x >> 3) * (kPaUnit / 2) + (((x + lane) & 7) << 4)), "r"(0)
                              : "memory");
@@ -841,7 +1015,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         }
         if (paired && !meet(A_PAIR, npair)) { ok = false; break; }  // both sums have been read
       } else {
-        float* slot = p.parts + int64_t(it.slot + it.piece) * kPaSlotFloats;
+        float* slot = p.parts + int64_t(pa_slot(it.cta0, it.piece)) * kPaSlotFloats;
         // a part's sums: [32 pieces of 4 dims][rows], so that a warp moves whole lines; a paired row's stand in the first row tile
         const int prow = (paired ? 0 : t * kPaM) + row;
         float4* po = reinterpret_cast<float4*>(slot) + prow;
@@ -861,7 +1035,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (paired && !meet(A_PAIR, npair)) { ok = false; break; }
         if (!meet(A_HALF + t, nhalf)) { ok = false; break; }
         if (row == 0) {
-          int32_t* count = p.counts + 2 * it.slot + t;
+          int32_t* count = p.counts + 2 * it.cta0 + t;
           const int old = atomicAdd(count, 1);
           if (old == it.pieces - 1) *count = 0;  // the last one: nobody else looks at it in this call
           *flag = old;
@@ -869,9 +1043,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (!meet(A_HALF + t, nhalf)) { ok = false; break; }
         if (*reinterpret_cast<volatile int32_t*>(flag) == it.pieces - 1 && mine) {
           __threadfence();
-          const float* s0 = p.parts + int64_t(it.slot) * kPaSlotFloats;
+          auto part_of = [&](int q) { return p.parts + int64_t(pa_slot(it.cta0, q)) * kPaSlotFloats; };
           auto ml_of = [&](int q) {
-            return __ldcg(reinterpret_cast<const float2*>(s0 + int64_t(q) * kPaSlotFloats + kPaRows * 128) + t * kPaM + row);
+            return __ldcg(reinterpret_cast<const float2*>(part_of(q) + kPaRows * 128) + t * kPaM + row);
           };
           float M = -CUDART_INF_F, Lsum = 0.f;
           for (int q = 0; q < it.pieces; ++q) M = fmaxf(M, ml_of(q).x);
@@ -890,7 +1064,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             for (int i = 0; i < 32; ++i) acc[i] = 0.f;
             for (int q = 0; q < it.pieces; ++q) {
               const float mq = ml_of(q).x, fq = mq == -CUDART_INF_F ? 0.f : ex2(mq - Mu);
-              const float4* pq = reinterpret_cast<const float4*>(s0 + int64_t(q) * kPaSlotFloats) + prow;
+              const float4* pq = reinterpret_cast<const float4*>(part_of(q)) + prow;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const float4 v = __ldcg(pq + (8 * c + i) * kPaRows);
@@ -921,14 +1095,14 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 
 PromptLayout prompt_layout(int64_t requests, int num_sms) {
   PromptLayout l;
-  l.slots = 4 * num_sms;
-  size_t at = 256 + size_t(requests) * sizeof(PaTab);
+  const size_t slots = 2 * size_t(num_sms);
+  size_t at = 256 + size_t(requests + 1) * sizeof(PaTab);
   at = (at + 255) / 256 * 256;
   l.counts = at;
-  at += size_t(l.slots) * 2 * sizeof(int32_t);
+  at += slots * sizeof(int32_t);
   at = (at + 255) / 256 * 256;
   l.parts = at;
-  l.bytes = at + size_t(l.slots) * kPaSlotFloats * sizeof(float);
+  l.bytes = at + slots * kPaSlotFloats * sizeof(float);
   return l;
 }
 
@@ -980,9 +1154,11 @@ cudaError_t launch_variant(const PromptArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_release);
   }
-  prompt_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (a.B > kPlanWarp) {
+    prompt_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.sms));
   cfg.blockDim = dim3(kPaThreads);

@@ -843,7 +843,6 @@ smla_status smla_prompt_attention(const smla_prompt_desc* d, const void* q, cons
   a.ws = static_cast<uint8_t*>(workspace);
   a.counts = reinterpret_cast<int32_t*>(a.ws + l.counts);
   a.parts = reinterpret_cast<float*>(a.ws + l.parts);
-  a.slots = l.slots;
   a.q_token = d->q_token_stride;
   a.q_head = d->q_head_stride;
   a.k_token = d->k_token_stride;
