@@ -8,6 +8,7 @@ importing fails loudly when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from ._build import LIB as LIB_PATH
@@ -211,13 +212,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()  # the argtypes make it a pointer
 
 
+_raw_stream = None  # torch's call for a device's current stream as a number, where it has one
+
+
 def _stream(stream):
+    global _raw_stream
     if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of current_stream()'s time
-        if raw is not None:
-            return raw(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            import torch
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of current_stream()'s time
+            dev = torch.cuda.current_device
+            _raw_stream = (lambda: raw(dev())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+        return _raw_stream()
     return int(getattr(stream, "cuda_stream", stream))  # a torch stream or a handle
 
 
@@ -481,13 +487,30 @@ def prompt_attention(desc, q, k, v, k_rope, cu_q, cu_k, prefix_lens, slopes, sin
 def add_rmsnorm(x, residual, weight, eps, residual_out=None, y=None, codes=None, scales=None, group=128,
                 scale_mode=SMLA_SCALE_POW2, stream=None):
     """x + residual, its RMS norm as bf16 and as E4M3 codes with scales (smla_add_rmsnorm); x: rows of any stride."""
-    d = smla_norm_desc()
-    d.n, d.dim = x.shape
-    d.x_stride = max(x.stride(0), d.dim) if d.n <= 1 else x.stride(0)
-    d.group, d.scale_mode, d.rms_eps = group, scale_mode, eps
+    n, dim = x.shape
+    d = _norm_desc(n, dim, x.stride(0) if n > 1 else dim, group, scale_mode, eps)
     _check("smla_add_rmsnorm", lib().smla_add_rmsnorm(
-        ctypes.byref(d), _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(codes), _ptr(scales),
-        _stream(stream)))
+        d, _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+# Descriptions of the calls that take none, by their numbers: filling one in takes longer than a small call's kernel.
+@functools.lru_cache(maxsize=256)
+def _norm_desc(n, dim, x_stride, group, scale_mode, eps):
+    d = smla_norm_desc()
+    d.n, d.dim, d.x_stride = n, dim, x_stride
+    d.group, d.scale_mode, d.rms_eps = group, scale_mode, eps
+    return ctypes.pointer(d)
+
+
+@functools.lru_cache(maxsize=256)
+def _logprob_desc(n, vocab, row_stride, given, top, logits_format, scale):
+    d = smla_logprob_desc()
+    d.n, d.vocab, d.row_stride = n, vocab, row_stride
+    d.given, d.top, d.logits_format, d.scale = given, top, logits_format, scale
+    return ctypes.pointer(d)
+
+
+_LOGITS_FORMAT = {2: SMLA_LOGITS_BF16, 4: SMLA_LOGITS_FP32}
 
 
 def token_logprobs(logits, tokens, logprobs, entropy=None, top_ids=None, top_logprobs=None, scale=1.0, error_word=None,
@@ -495,13 +518,9 @@ def token_logprobs(logits, tokens, logprobs, entropy=None, top_ids=None, top_log
     """Log probabilities of given tokens [n, G], entropy and top alternatives [n, K] (smla_token_logprobs).
 
     logits: [n, V] fp32 or bf16 (any other element size is refused), rows of any stride."""
-    d = smla_logprob_desc()
-    d.n, d.vocab = logits.shape
-    d.row_stride = max(logits.stride(0), d.vocab) if d.n <= 1 else logits.stride(0)
-    d.given = 0 if tokens is None else tokens.shape[1]
-    d.top = 0 if top_ids is None else top_ids.shape[1]
-    d.logits_format = {2: SMLA_LOGITS_BF16, 4: SMLA_LOGITS_FP32}.get(logits.element_size(), -1)
-    d.scale = scale
+    n, vocab = logits.shape
+    d = _logprob_desc(n, vocab, logits.stride(0) if n > 1 else vocab, 0 if tokens is None else tokens.shape[1],
+                      0 if top_ids is None else top_ids.shape[1], _LOGITS_FORMAT.get(logits.element_size(), -1), scale)
     _check("smla_token_logprobs", lib().smla_token_logprobs(
-        ctypes.byref(d), _ptr(logits), _ptr(tokens), _ptr(logprobs), _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs),
+        d, _ptr(logits), _ptr(tokens), _ptr(logprobs), _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs),
         _ptr(error_word), _stream(stream)))
