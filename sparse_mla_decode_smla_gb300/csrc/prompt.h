@@ -72,6 +72,8 @@ struct PromptArgs {
   int32_t T, N, H, HK, B, causal, log2_pack, sms;
   float c2;                 // sm_scale log2(e)
   float cap2, cap_in;       // cap log2(e) (0: no cap); 2 sm_scale log2(e) / cap
+  float tanh_max;           // scores q.k up to this are capped by the polynomial
+  float tanh_c[5];          // its coefficients, of odd powers of q.k
 };
 struct PromptLayout {
   size_t counts, parts, bytes;

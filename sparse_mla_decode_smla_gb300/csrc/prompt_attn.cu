@@ -475,6 +475,11 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -863,11 +868,28 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if constexpr (CAP) {
           if (masked) {  // four scores share a reciprocal: a hidden one that is not a number stays out of it
 #pragma unroll
-            for (int i = 0; i < 128; ++i) x[i] = i < left ? x[i] : -CUDART_INF_F;
+            for (int i = 0; i < 128; ++i) x[i] = i < left ? x[i] : 0.f;
           }
-          float probe = -CUDART_INF_F;
+          float probe = 0.f;
 #pragma unroll
-          for (int i = 0; i < 128; i += 2) probe = max3_nan(probe, x[i], x[i + 1]);
+          for (int i = 0; i < 128; i += 2) probe = max3_nan(probe, fabsf(x[i]), fabsf(x[i + 1]));
+          if (__all_sync(0xffffffffu, probe <= p.tanh_max)) {
+            // all |u| <= 0.625: cap tanh(u) as u times a polynomial in u^2 (least maximum error: 2^-25 of cap), without the
+            // special functions that the weights need too
+            uint64_t cf[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) cf[i] = f2(p.tanh_c[i], p.tanh_c[i]);
+#pragma unroll
+            for (int i = 0; i < 128; i += 2) {
+              const uint64_t v = f2(x[i], x[i + 1]), t2 = f2_mul(v, v);
+              uint64_t q = f2_fma(t2, cf[4], cf[3]);
+#pragma unroll
+              for (int c = 2; c >= 0; --c) q = f2_fma(t2, q, cf[c]);
+              const float2 f = f2_parts(f2_mul(v, q));
+              x[i] = f.x;
+              x[i + 1] = f.y;
+            }
+          } else {
           if (probe != probe) sum2 = f2(CUDART_NAN_F, 0.f);
           // cap tanh(u) = cap - 2 cap / (1 + e^(2u)), within 2^-21 of cap; four quotients from one reciprocal of the
           // product (u is cut where tanh is 1 to 2^-29: the product stays finite)
@@ -883,6 +905,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             x[i + 1] = fmaf(rab, e[0], p.cap2);
             x[i + 2] = fmaf(rcd, e[3], p.cap2);
             x[i + 3] = fmaf(rcd, e[2], p.cap2);
+          }
           }
         }
         if constexpr (BIAS) {

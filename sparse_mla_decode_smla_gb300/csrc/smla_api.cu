@@ -863,6 +863,14 @@ smla_status smla_prompt_attention(const smla_prompt_desc* d, const void* q, cons
   a.c2 = d->sm_scale * 1.4426950408889634f;
   a.cap2 = d->softcap * 1.4426950408889634f;
   a.cap_in = d->softcap > 0.f ? 2.f * a.c2 / d->softcap : 0.f;
+  if (d->softcap > 0.f) {
+    // tanh(u) / u on |u| <= 0.625 by powers of u^2, of least maximum error in tanh(u): 3.0e-8
+    const double tanh_fit[5] = {0.9999994588, -0.3333048274, 0.1329103148, -0.0513628633, 0.0145300620};
+    const double in = double(d->sm_scale) / d->softcap;
+    double power = a.c2;
+    for (int i = 0; i < 5; ++i, power *= in * in) a.tanh_c[i] = static_cast<float>(tanh_fit[i] * power);
+    a.tanh_max = static_cast<float>(0.625 / in);
+  }
   return smla::launch_prompt_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
