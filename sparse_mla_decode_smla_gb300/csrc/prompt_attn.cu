@@ -16,7 +16,7 @@
 //
 // A key tile on one SM: S = Q K^T (12 MMAs of 128 x 128 x 16 a row tile), the weights P = 2^(x - m) in BF16 written over
 // S in tensor memory, O += P V (8 MMAs, P from tensor memory). The two row tiles alternate: one's softmax runs while the
-// tensor cores work for the other. m moves only when a row's maximum grows by more than 2^8, so O is rescaled rarely, by
+// tensor cores work for the other. m moves only when a row's maximum grows by more than 2^16, so O is rescaled rarely, by
 // the softmax threads themselves; by the time S of a tile is there, PV of the tile before is complete.
 //
 // P in BF16 costs 2^-9 of each weight, independently; the sums of weights are of the fp32 values.
@@ -46,7 +46,9 @@ constexpr int kPaUnit = 16384;             // bytes of a ring unit: 128 keys x 6
 constexpr int kPaThreads = 384;
 constexpr int kPaMmaWarp = 8, kPaLoadWarp = 9, kPaGuardWarp = 10, kPaGuards = 2;
 constexpr int kPaTiles = 4;                // key (value) tiles in the ring at most: 3
-constexpr float kPaRescale = 8.f;
+// m moves when a row's maximum exceeds it by more than this (log2 units): weights stay below 2^16, which neither BF16 nor the
+// fp32 sums notice, and with a bias, where scores grow from tile to tile, it moves less often than with 2^8
+constexpr float kPaRescale = 16.f;
 constexpr int kPaMinTiles = 8;             // key tiles of a run, and of a piece but the odd one, at least
 constexpr int kPaItemCost = 3;             // an item's own work, in key tiles
 constexpr int kPaSlotFloats = kPaRows * 128 + kPaRows * 2;  // a piece's part: O, then (m, l) of each row
@@ -143,12 +145,27 @@ __device__ __forceinline__ PaTab* pa_table(const PromptArgs& p) { return reinter
 constexpr int kPlanThreads = 256;
 constexpr int kPlanWarp = 32;  // requests that a warp lays out itself
 
-// A request's key tiles over all blocks of rows, for one group of heads beside one another.
-__device__ __forceinline__ int64_t pa_sum(const PromptArgs& p, const PaReq& q) {
-  const int tb = kPaRows >> p.log2_pack;
-  if (!p.causal) return int64_t(q.blocks) * pa_tiles(p, q, 0);
+// The key tiles of every lane's request over all its blocks of rows, for one group of heads beside one another (by a whole
+// warp; a request without tokens has no blocks). Requests of many blocks are added up by all lanes together.
+__device__ __forceinline__ int64_t pa_sum(const PromptArgs& p, const PaReq& mine) {
+  const int tb = kPaRows >> p.log2_pack, lane = threadIdx.x & 31;
   int64_t n = 0;
-  for (int b = 0; b < q.blocks; ++b) n += pa_tiles(p, q, min((b + 1) * tb, q.nq) - 1);
+  const bool many = mine.blocks > 32;
+  if (!many)
+    for (int b = 0; b < mine.blocks; ++b) n += pa_tiles(p, mine, min((b + 1) * tb, mine.nq) - 1);
+  for (uint32_t left = __ballot_sync(0xffffffffu, many); left; left &= left - 1) {
+    const int r = __ffs(left) - 1;
+    PaReq q = {};
+    q.nq = __shfl_sync(0xffffffffu, mine.nq, r);
+    q.nk = __shfl_sync(0xffffffffu, mine.nk, r);
+    q.prefix = __shfl_sync(0xffffffffu, mine.prefix, r);
+    q.blocks = __shfl_sync(0xffffffffu, mine.blocks, r);
+    int64_t sum = 0;
+    for (int b = lane; b < q.blocks; b += 32) sum += pa_tiles(p, q, static_cast<int>(min(int64_t(b + 1) * tb, int64_t(q.nq))) - 1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == r) n = sum;
+  }
   return n;
 }
 
@@ -163,11 +180,12 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptA
   for (int r0 = 0; r0 < p.B; r0 += kPlanThreads) {
     const int r = r0 + tid;
     PaTab v = {0, 0, 0};
-    PaReq q;
+    PaReq q = {};
     const int ok = r < p.B ? pa_request(p, r, q) : 0;
     if (ok < 0) atomicOr(&head->err, SMLA_DEVERR_INDEX);
+    const int64_t tiles = pa_sum(p, q);
     if (ok > 0) {
-      v.tiles = pa_sum(p, q) * G;
+      v.tiles = tiles * G;
       v.items = q.blocks * G;
       longest = max(longest, pa_tiles(p, q, q.nq - 1));
     }
@@ -317,12 +335,13 @@ __device__ __forceinline__ void pa_plan(const PromptArgs& p, PaWalk& w) {
   PaHead* head = reinterpret_cast<PaHead*>(p.ws);
   int longest = 0;
   if (p.B <= kPlanWarp) {
-    PaReq q;
+    PaReq q = {};
     const int ok = lane < p.B ? pa_request(p, lane, q) : 0;
     if (ok < 0 && blockIdx.x == 0) atomicOr(&head->err, SMLA_DEVERR_INDEX);
     PaTab v = {0, 0, 0};
+    const int64_t tiles = pa_sum(p, q);
     if (ok > 0) {
-      v.tiles = pa_sum(p, q) * G;
+      v.tiles = tiles * G;
       v.items = q.blocks * G;
       longest = pa_tiles(p, q, q.nq - 1);
     }

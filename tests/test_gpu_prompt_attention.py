@@ -114,6 +114,9 @@ CASES = [
     dict(nq=[40], nk=[40], heads=256, kv_heads=2, rope=0),         # a group of 128 heads
     dict(nq=[40], nk=[41], heads=96, kv_heads=2),                  # of 48: sixteen beside one another
     dict(nq=[600], nk=[5000], heads=2, kv_heads=2, causal=False),
+    dict(nq=[260], nk=[900], heads=2, kv_heads=2, cap=300.0),      # small beside the cap: by the polynomial
+    dict(nq=[260], nk=[900], heads=2, kv_heads=2, cap=0.5, rope=0),  # and all but cut off
+    dict(nq=[1, 130], nk=[2600, 131], heads=2, kv_heads=2, prefix=[5, 131], bias=True),
 ]
 
 
@@ -128,6 +131,48 @@ def test_many_small_requests(smla):
     nq = r.integers(0, 4, 700)
     nk = nq + r.integers(0, 200, 700)
     Prompt(smla, nq.tolist(), nk.tolist(), 2, 1, rope=64, seed=4).run().check()
+
+
+def test_a_long_request_among_many(smla):
+    """More requests than a warp lays out, one of them over many SMs."""
+    r = np.random.default_rng(6)
+    nq = r.integers(0, 3, 60)
+    nk = nq + r.integers(0, 90, 60)
+    nq[[17, 41]], nk[[17, 41]] = [1, 150], [9000, 2000]
+    Prompt(smla, nq.tolist(), nk.tolist(), 4, 2, rope=0, seed=18).run().check()
+
+
+def test_single_head_group_of_many_blocks(smla):
+    """128 query heads on one kv head: two tokens a row tile pair, more blocks than a warp has lanes."""
+    Prompt(smla, [300, 7], [310, 500], 128, 1, rope=64, seed=19).run().check()
+
+
+@pytest.mark.parametrize("heads,requests", [(256, 1), (128, 35)])
+def test_items_off_the_counter(smla, heads, requests):
+    """More short items than SMs: a few heads of the result against float64."""
+    torch = _torch()
+    nq = [1500] if requests == 1 else [300] * requests
+    p = Prompt(smla, nq, nq, heads, heads, seed=20, sink=True).run()
+    sel = [0, 1, heads // 2, heads - 1]
+    p.q, p.k, p.v, p.sink = p.q[:, sel], p.k[:, sel], p.v[:, sel], p.sink[sel]
+    p.out, p.lse, p.H, p.HK = p.out[:, sel], p.lse[:, sel], 4, 4
+    p.check()
+    assert torch.isfinite(p.out.float()).all()
+
+
+@pytest.mark.parametrize("case", [dict(nq=[1, 1], nk=[3000, 777], heads=4, kv_heads=4), dict(nq=[700], nk=[1500], heads=2, kv_heads=2),
+                                  dict(nq=[1], nk=[20000], heads=2, kv_heads=1, cap=30.0)])
+def test_the_first_call_on_a_workspace_is_as_good_as_any(smla, case):
+    """Parts of cut items that are read before they are written would be zeros here, and right ones in later calls."""
+    torch = _torch()
+    first = Prompt(smla, **case, seed=22).run()
+    again = first.out.clone()
+    first.run()
+    real = slice(int(first.cu_q[0]), int(first.cu_q[-1]))
+    assert torch.equal(first.out[real], again[real])
+    for _ in range(8):
+        p = Prompt(smla, **case, seed=22).run()
+        assert torch.equal(p.out[real], again[real]) and torch.equal(p.lse, first.lse)
 
 
 def test_large_scores_and_equal_ones(smla):
