@@ -133,104 +133,154 @@ __global__ void __launch_bounds__(kRdThreads) cache_read_kernel(const ReadArgs a
 
 // ---------------------------------------------------------------- residual + RMS norm
 
-// h = x + residual; y = h r w with r = 1 / sqrt(mean(h^2) + eps), in fp32 from the unrounded sum. A thread holds
-// VPT pieces of eight consecutive dims of its row in registers: the row is read once. Sixteen lanes share a block of 128.
-// WARP: a warp takes a row (of up to 1024 dims), else a CTA does.
-constexpr int kNormVpt = 4, kNormWarpRows = 8;
+// h = x + residual; y = h r w with r = 1 / sqrt(mean(h^2) + eps), in fp32 from the unrounded sum. A thread holds VPT pieces of
+// eight consecutive dims of its row in registers: the row is read once. Sixteen lanes share a block of 128.
+//
+// A row's work on its VPT pieces, by LANES lanes of a warp (LANES <= 32), or by a CTA of T threads that meet in `part`
+// (LANES = 0).
+template <int LANES, int VPT>
+struct NormRow {
+  float h[VPT][8];
 
-template <bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kNormWarpRows : 1024, 1) add_rmsnorm_kernel(const NormArgs a) {
+  // x and the residual -> h, its bf16 sum stored; the sum of squares
+  __device__ __forceinline__ float add(const NormArgs& a, int64_t row, int t, int T, const uint4 (&xv)[VPT], const uint4 (&rv)[VPT]) {
+    const int nv = a.dim >> 3;
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const uint32_t xw[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w}, rw[4] = {rv[k].x, rv[k].y, rv[k].z, rv[k].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[k][2 * i] = __fadd_rn(bf16_lo(xw[i]), bf16_lo(rw[i]));
+        h[k][2 * i + 1] = __fadd_rn(bf16_hi(xw[i]), bf16_hi(rw[i]));
+        o[i] = pack_bf16x2(h[k][2 * i], h[k][2 * i + 1]);
+        ss = fmaf(h[k][2 * i + 1], h[k][2 * i + 1], fmaf(h[k][2 * i], h[k][2 * i], ss));
+      }
+      if (a.sum && k * T + t < nv)
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.sum) + row * a.dim)[k * T + t] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    return ss;
+  }
+  // the value that every lane of the row (part: of the CTA) gets
+  template <typename F>
+  __device__ __forceinline__ static float all(float v, int T, float* part, F f) {
+#pragma unroll
+    for (int o = (LANES ? LANES : 32) / 2; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (LANES) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < (T >> 5) ? part[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+  // h -> y and its outputs
+  __device__ __forceinline__ void finish(const NormArgs& a, int64_t row, int t, int T, float ss, const uint4 (&wv)[VPT], float* part) {
+    const int nv = a.dim >> 3;
+    const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, float(a.dim)), a.eps)));
+    float amax[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const uint32_t ww[4] = {wv[k].x, wv[k].y, wv[k].z, wv[k].w};
+      uint32_t o[4];
+      amax[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[k][2 * i] = __fmul_rn(__fmul_rn(h[k][2 * i], r), bf16_lo(ww[i]));
+        h[k][2 * i + 1] = __fmul_rn(__fmul_rn(h[k][2 * i + 1], r), bf16_hi(ww[i]));
+        o[i] = pack_bf16x2(h[k][2 * i], h[k][2 * i + 1]);
+        amax[k] = fmaxf(amax[k], fmaxf(fabsf(h[k][2 * i]), fabsf(h[k][2 * i + 1])));
+      }
+      if (a.y && k * T + t < nv)
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + row * a.dim)[k * T + t] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (!a.codes) return;
+    if (a.group) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], o));
+    } else {
+      float m = amax[0];
+#pragma unroll
+      for (int k = 1; k < VPT; ++k) m = fmaxf(m, amax[k]);
+      m = all(m, T, part, [](float x, float y) { return fmaxf(x, y); });
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) amax[k] = m;
+    }
+    const int groups = a.group ? (a.dim + 127) >> 7 : 1;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int v = k * T + t;
+      if (v >= nv) continue;
+      const float scale = block_scale(amax[k], a.scale_mode);
+      uint16_t c[4];
+      ScaleDiv(scale).codes_by_reciprocal<4>(h[k], c);
+      reinterpret_cast<uint2*>(a.codes + row * a.dim)[v] = make_uint2(c[0] | (uint32_t(c[1]) << 16), c[2] | (uint32_t(c[3]) << 16));
+      if (a.group ? (v & 15) == 0 : v == 0) a.scales[row * groups + (a.group ? v >> 4 : 0)] = scale;
+    }
+  }
+};
+__device__ __forceinline__ float norm_sum(float x, float y) { return x + y; }
+
+__device__ __forceinline__ const uint4* norm_x(const NormArgs& a, int64_t row) {
+  return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + row * a.x_stride);
+}
+__device__ __forceinline__ const uint4* norm_res(const NormArgs& a, int64_t row) {
+  return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + row * a.dim);
+}
+
+// Short rows, of up to 8 LANES VPT dims: LANES lanes of a warp a row.
+constexpr int kNormSmallThreads = 256;
+template <int LANES, int VPT>
+__global__ void __launch_bounds__(kNormSmallThreads) add_rmsnorm_small_kernel(const NormArgs a) {
+  const int t = threadIdx.x & (LANES - 1), nv = a.dim >> 3;
+  const int64_t row = int64_t(blockIdx.x) * (kNormSmallThreads / LANES) + threadIdx.x / LANES;
+  const bool real = row < a.n;  // (lanes of rows past the end go along: the warp shuffles together)
+  uint4 xv[VPT], rv[VPT], wv[VPT];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int v = k * LANES + t;
+    xv[k] = rv[k] = wv[k] = make_uint4(0, 0, 0, 0);
+    if (real && v < nv) {
+      xv[k] = norm_x(a, row)[v];
+      if (a.residual) rv[k] = norm_res(a, row)[v];
+      wv[k] = __ldg(static_cast<const uint4*>(a.weight) + v);
+    }
+  }
+  NormArgs b = a;
+  if (!real) b.dim = 0;  // nothing of it is stored
+  NormRow<LANES, VPT> r;
+  const float ss = r.all(r.add(b, row, t, LANES, xv, rv), LANES, nullptr, norm_sum);
+  r.finish(b, row, t, LANES, ss, wv, nullptr);
+}
+
+// Long rows: a CTA each, four or five an SM, whose loads, sums and stores overlap. (A CTA that goes from row to row with the
+// next ones on their way to shared memory holds fewer rows an SM and is slower: 206 us for 16384 x 7168 with the residual where
+// this takes 171, 91 % of the measured bandwidth.)
+constexpr int kNormVpt = 4;
+
+template <int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) add_rmsnorm_kernel(const NormArgs a) {
   __shared__ float part[2][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int T = WARP ? 32 : blockDim.x, t = WARP ? lane : threadIdx.x;
-  const int64_t row = WARP ? int64_t(blockIdx.x) * kNormWarpRows + warp : blockIdx.x;
-  if (WARP && row >= a.n) return;
-  const int nv = a.dim >> 3;
-  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + row * a.x_stride);
-  const uint4* res = a.residual ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + row * a.dim) : nullptr;
+  const int t = threadIdx.x, T = blockDim.x, nv = a.dim >> 3;
+  const int64_t row = blockIdx.x;
   uint4 xv[kNormVpt], rv[kNormVpt], wv[kNormVpt];
 #pragma unroll
   for (int k = 0; k < kNormVpt; ++k) {
     const int v = k * T + t;
     xv[k] = rv[k] = wv[k] = make_uint4(0, 0, 0, 0);
     if (v < nv) {
-      xv[k] = x[v];
-      if (res) rv[k] = res[v];
+      xv[k] = norm_x(a, row)[v];
+      if (a.residual) rv[k] = norm_res(a, row)[v];
       wv[k] = __ldg(static_cast<const uint4*>(a.weight) + v);
     }
   }
-  float h[kNormVpt][8], ss = 0.f;
-#pragma unroll
-  for (int k = 0; k < kNormVpt; ++k) {
-    const uint32_t xw[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w}, rw[4] = {rv[k].x, rv[k].y, rv[k].z, rv[k].w};
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[k][2 * i] = __fadd_rn(bf16_lo(xw[i]), bf16_lo(rw[i]));
-      h[k][2 * i + 1] = __fadd_rn(bf16_hi(xw[i]), bf16_hi(rw[i]));
-      o[i] = pack_bf16x2(h[k][2 * i], h[k][2 * i + 1]);
-      ss = fmaf(h[k][2 * i + 1], h[k][2 * i + 1], fmaf(h[k][2 * i], h[k][2 * i], ss));
-    }
-    if (a.sum && k * T + t < nv)
-      reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.sum) + row * a.dim)[k * T + t] = make_uint4(o[0], o[1], o[2], o[3]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (!WARP) {
-    if (lane == 0) part[0][warp] = ss;
-    __syncthreads();
-    ss = lane < (T >> 5) ? part[0][lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  }
-  const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, float(a.dim)), a.eps)));
-  float amax[kNormVpt];
-#pragma unroll
-  for (int k = 0; k < kNormVpt; ++k) {
-    const uint32_t ww[4] = {wv[k].x, wv[k].y, wv[k].z, wv[k].w};
-    uint32_t o[4];
-    amax[k] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[k][2 * i] = __fmul_rn(__fmul_rn(h[k][2 * i], r), bf16_lo(ww[i]));
-      h[k][2 * i + 1] = __fmul_rn(__fmul_rn(h[k][2 * i + 1], r), bf16_hi(ww[i]));
-      o[i] = pack_bf16x2(h[k][2 * i], h[k][2 * i + 1]);
-      amax[k] = fmaxf(amax[k], fmaxf(fabsf(h[k][2 * i]), fabsf(h[k][2 * i + 1])));
-    }
-    if (a.y && k * T + t < nv)
-      reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + row * a.dim)[k * T + t] = make_uint4(o[0], o[1], o[2], o[3]);
-  }
-  if (!a.codes) return;
-  if (a.group) {
-#pragma unroll
-    for (int k = 0; k < kNormVpt; ++k)
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], o));
-  } else {
-    float m = fmaxf(fmaxf(amax[0], amax[1]), fmaxf(amax[2], amax[3]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (!WARP) {
-      if (lane == 0) part[1][warp] = m;
-      __syncthreads();
-      m = lane < (T >> 5) ? part[1][lane] : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    }
-#pragma unroll
-    for (int k = 0; k < kNormVpt; ++k) amax[k] = m;
-  }
-  const int groups = a.group ? (a.dim + 127) >> 7 : 1;
-#pragma unroll
-  for (int k = 0; k < kNormVpt; ++k) {
-    const int v = k * T + t;
-    if (v >= nv) continue;
-    const float scale = block_scale(amax[k], a.scale_mode);
-    uint16_t c[4];
-    ScaleDiv(scale).codes<4>(h[k], c);
-    reinterpret_cast<uint2*>(a.codes + row * a.dim)[v] = make_uint2(c[0] | (uint32_t(c[1]) << 16), c[2] | (uint32_t(c[3]) << 16));
-    if (a.group ? (v & 15) == 0 : v == 0) a.scales[row * groups + (a.group ? v >> 4 : 0)] = scale;
-  }
+  NormRow<0, kNormVpt> r;
+  const float ss = r.all(r.add(a, row, t, T, xv, rv), T, part[0], norm_sum);
+  r.finish(a, row, t, T, ss, wv, part[1]);
 }
 
 }  // namespace
@@ -244,13 +294,16 @@ cudaError_t launch_cache_read(const ReadArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_add_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t s) {
-  (void)num_sms;
   const int nv = a.dim >> 3;
-  if (nv <= 32 * kNormVpt) {
-    add_rmsnorm_kernel<true><<<static_cast<unsigned>((a.n + kNormWarpRows - 1) / kNormWarpRows), 32 * kNormWarpRows, 0, s>>>(a);
+  auto ctas = [&](int lanes) { return static_cast<unsigned>((a.n * lanes + kNormSmallThreads - 1) / kNormSmallThreads); };
+  if (nv <= 32) {
+    add_rmsnorm_small_kernel<16, 2><<<ctas(16), kNormSmallThreads, 0, s>>>(a);
+  } else if (nv <= 128) {
+    add_rmsnorm_small_kernel<32, 4><<<ctas(32), kNormSmallThreads, 0, s>>>(a);
   } else {
     const int threads = ((nv + kNormVpt - 1) / kNormVpt + 31) & ~31;
-    add_rmsnorm_kernel<false><<<static_cast<unsigned>(a.n), threads, 0, s>>>(a);
+    if (threads <= 256) add_rmsnorm_kernel<256><<<static_cast<unsigned>(a.n), threads, 0, s>>>(a);
+    else add_rmsnorm_kernel<1024><<<static_cast<unsigned>(a.n), threads, 0, s>>>(a);
   }
   return cudaGetLastError();
 }

@@ -24,8 +24,7 @@
 namespace smla {
 namespace {
 
-constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
-constexpr int kLpCand = 1024;     // candidates a CTA keeps
+constexpr int kLpWide = 256, kLpNarrow = 64;  // threads of a CTA: for long rows, and for short ones
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpUnroll = 4;      // 16-byte pieces a thread loads together
 static_assert(kLpUnroll == 4, "pick");
@@ -92,14 +91,16 @@ __device__ __forceinline__ void join(LpSums& a, const LpSums& b, float c) {
   a.m = m;
 }
 
+template <int TH>
 struct __align__(16) LpShared {
-  uint64_t cand[kLpCand];
-  uint64_t best[kLpMaxCluster * kLogprobMaxTop];  // the CTAs' first k, in the cluster's first CTA
-  alignas(16) float maxima[kLpThreads];
+  static constexpr int kCand = TH == kLpWide ? 1024 : 512;  // candidates a CTA keeps
+  uint64_t cand[kCand];
+  uint64_t best[(TH == kLpWide ? kLpMaxCluster : 1) * kLogprobMaxTop];  // the CTAs' first k, in the cluster's first CTA
+  float maxima[TH];
   uint32_t hist[256];
-  float quarter[4 * kLpThreads];  // the threads' maxima of each quarter of their pieces
-  int32_t hot[4 * kLpThreads];    // the quarters whose maximum reaches the bound
-  LpSums part[kLpWarps];
+  float quarter[4 * TH];  // the threads' maxima of each quarter of their pieces
+  int32_t hot[4 * TH];    // the quarters whose maximum reaches the bound
+  LpSums part[TH / 32];
   LpSums all[kLpMaxCluster];  // the CTAs' sums, in the first CTA
   LpSums total;
   uint32_t count, hot_count, pick, need;
@@ -115,18 +116,19 @@ __device__ __forceinline__ float lp_load(const LogprobArgs& a, const void* row, 
 // A value that at least k of the threads' maxima reach -> sh.bound: the k-th largest one's upper 16 bits, found from the top
 // by the first warp, eight maxima a lane (all of a BF16 value's bits; the few more that reach it in fp32 cost less than 16
 // more steps).
-__device__ __forceinline__ void find_bound(LpShared& sh, float mine, int k) {
+template <int TH>
+__device__ __forceinline__ void find_bound(LpShared<TH>& sh, float mine, int k) {
   sh.maxima[threadIdx.x] = mine;
   __syncthreads();
   if (threadIdx.x < 32) {
-    uint32_t key[kLpThreads / 32], found = 0;
+    uint32_t key[TH / 32], found = 0;
 #pragma unroll
-    for (int i = 0; i < kLpThreads / 32; ++i) key[i] = ordered(sh.maxima[32 * i + threadIdx.x]);
+    for (int i = 0; i < TH / 32; ++i) key[i] = ordered(sh.maxima[32 * i + threadIdx.x]);
     for (int b = 31; b >= 16; --b) {
       const uint32_t next = found | 1u << b;
       int n = 0;
 #pragma unroll
-      for (int i = 0; i < kLpThreads / 32; ++i) n += key[i] >= next ? 1 : 0;
+      for (int i = 0; i < TH / 32; ++i) n += key[i] >= next ? 1 : 0;
       if (__reduce_add_sync(0xffffffffu, n) >= k) found = next;
     }
     if (threadIdx.x == 0) sh.bound = found;
@@ -136,15 +138,15 @@ __device__ __forceinline__ void find_bound(LpShared& sh, float mine, int k) {
 
 // The k first keys of [v0, v1) by a radix search over the row: for parts with more candidates than the buffer holds.
 // Eight bits of the 64-bit key a pass, from the top; then the keys from the k-th on are collected.
-template <bool F32>
-__device__ __noinline__ void radix_top(const LogprobArgs& a, const void* row, int v0, int v1, int k, LpShared& sh) {
+template <bool F32, int TH>
+__device__ __noinline__ void radix_top(const LogprobArgs& a, const void* row, int v0, int v1, int k, LpShared<TH>& sh) {
   uint64_t prefix = 0;
   const int want = min(k, v1 - v0);
   if (threadIdx.x == 0) sh.need = want;
   for (int shift = 56; shift >= 0; shift -= 8) {
-    sh.hist[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < 256; i += TH) sh.hist[i] = 0;
     __syncthreads();
-    for (int i = v0 + threadIdx.x; i < v1; i += kLpThreads) {
+    for (int i = v0 + threadIdx.x; i < v1; i += TH) {
       const uint64_t key = key_of(lp_load<F32>(a, row, i), i);
       if (shift == 56 || (key >> (shift + 8)) == prefix) atomicAdd(&sh.hist[(key >> shift) & 255], 1u);
     }
@@ -163,7 +165,7 @@ __device__ __noinline__ void radix_top(const LogprobArgs& a, const void* row, in
   if (threadIdx.x == 0) sh.count = 0;
   __syncthreads();
   if (want > 0) {
-    for (int i = v0 + threadIdx.x; i < v1; i += kLpThreads) {
+    for (int i = v0 + threadIdx.x; i < v1; i += TH) {
       const uint64_t key = key_of(lp_load<F32>(a, row, i), i);
       if (key >= prefix) sh.cand[atomicAdd(&sh.count, 1u)] = key;  // exactly `want` keys: they are distinct
     }
@@ -172,8 +174,9 @@ __device__ __noinline__ void radix_top(const LogprobArgs& a, const void* row, in
 }
 
 // the k first of n distinct keys, in order, to dst (shared memory of this CTA or, by its cluster address, another's)
+template <int TH>
 __device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int k, uint32_t dst) {
-  for (int t = threadIdx.x; t < n; t += kLpThreads) {
+  for (int t = threadIdx.x; t < n; t += TH) {
     const uint64_t me = keys[t];
     int above = 0;
     for (int u = 0; u < n; ++u) above += keys[u] > me ? 1 : 0;
@@ -181,10 +184,11 @@ __device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int k, ui
   }
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const LogprobArgs a, int cluster) {
+template <bool F32, int TH>
+__global__ void __launch_bounds__(TH, 1024 / TH) token_logprobs_kernel(const LogprobArgs a, int cluster) {
   extern __shared__ __align__(16) uint8_t lp_smem[];
-  LpShared& sh = *reinterpret_cast<LpShared*>(lp_smem);
+  using Shared = LpShared<TH>;
+  Shared& sh = *reinterpret_cast<Shared*>(lp_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = cluster > 1 ? blockIdx.x % cluster : 0;
   constexpr int es = F32 ? 4 : 2, kPer = 16 / es;  // elements of a 16-byte piece
@@ -203,17 +207,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const Log
     q.p1 = static_cast<int>(int64_t(q.pieces) * (rank + 1) / cluster);
     return q;
   };
-  constexpr int step = kLpThreads * kLpUnroll;
+  constexpr int step = TH * kLpUnroll;
   uint4 next[kLpUnroll];
   auto load = [&](const uint4* from, int left) {  // left: pieces from there on; one past the end is nothing but lowest values
     if (left >= step) {
 #pragma unroll
-      for (int j = 0; j < kLpUnroll; ++j) next[j] = __ldg(from + j * kLpThreads);
+      for (int j = 0; j < kLpUnroll; ++j) next[j] = __ldg(from + j * TH);
     } else {
       const uint32_t none = F32 ? 0xff800000u : 0xff80ff80u;
 #pragma unroll
       for (int j = 0; j < kLpUnroll; ++j)
-        next[j] = j * kLpThreads + tid < left ? __ldg(from + j * kLpThreads) : make_uint4(none, none, none, none);
+        next[j] = j * TH + tid < left ? __ldg(from + j * TH) : make_uint4(none, none, none, none);
     }
   };
   auto first_load = [&](const Part& q) { load(reinterpret_cast<const uint4*>(q.row + size_t(q.head) * es) + q.p0 + tid, q.p1 - q.p0); };
@@ -234,7 +238,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const Log
   __syncthreads();  // the row before is done with shared memory
   if (tid == 0) sh.count = sh.hot_count = 0;
   if (k > 0)
-    for (int i = tid; i < (cluster > 1 ? kLpMaxCluster * kLogprobMaxTop : k); i += kLpThreads) sh.best[i] = 0;
+    for (int i = tid; i < (cluster > 1 ? kLpMaxCluster * kLogprobMaxTop : k); i += TH) sh.best[i] = 0;
   __syncthreads();
   if (cluster > 1) tc::cluster_arrive();
   float m = -CUDART_INF_F, mu = 0.f, s = 0.f, w = 0.f, big = -CUDART_INF_F;  // mu: m where it is finite; big: the largest x of the pieces
@@ -274,7 +278,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const Log
   float here = -CUDART_INF_F;
   auto end_part = [&] {
     while (in_part < 4 && round == part_end) {
-      sh.quarter[in_part * kLpThreads + tid] = here;
+      sh.quarter[in_part * TH + tid] = here;
       here = -CUDART_INF_F;
       ++in_part;
       part_end = (in_part + 1) * rounds >> 2;
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const Log
     auto keep = [&](float x, int i) {
       if (ordered(x) >= bound) {
         const uint32_t to = atomicAdd(&sh.count, 1u);
-        if (to < kLpCand) sh.cand[to] = key_of(x, i);
+        if (to < Shared::kCand) sh.cand[to] = key_of(x, i);
       }
     };
 #pragma unroll
@@ -407,22 +411,22 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const Log
     if (short_row) {
 #pragma unroll 1
       for (int j = 0; j < kLpUnroll; ++j)
-        if (p0 + j * kLpThreads + tid < p1) look(pick(next, j), p0 + j * kLpThreads + tid);
+        if (p0 + j * TH + tid < p1) look(pick(next, j), p0 + j * TH + tid);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (ordered(sh.quarter[i * kLpThreads + tid]) >= bound) sh.hot[atomicAdd(&sh.hot_count, 1u)] = i * kLpThreads + tid;
+        if (ordered(sh.quarter[i * TH + tid]) >= bound) sh.hot[atomicAdd(&sh.hot_count, 1u)] = i * TH + tid;
       __syncthreads();
       const int hot = sh.hot_count, each = ((rounds + 3) >> 2) * kLpUnroll;
-      for (int i = tid; i < hot * each && sh.count <= kLpCand; i += kLpThreads) {
-        const int q = sh.hot[i % hot], in = i / hot, first = (q / kLpThreads) * rounds >> 2, end = (q / kLpThreads + 1) * rounds >> 2;
+      for (int i = tid; i < hot * each && sh.count <= Shared::kCand; i += TH) {
+        const int q = sh.hot[i % hot], in = i / hot, first = (q / TH) * rounds >> 2, end = (q / TH + 1) * rounds >> 2;
         if (first + in / kLpUnroll >= end) continue;
-        const int piece = p0 + (first * kLpUnroll + in) * kLpThreads + q % kLpThreads;
+        const int piece = p0 + (first * kLpUnroll + in) * TH + q % TH;
         if (piece < p1) look(__ldg(body + piece), piece);
       }
     }
     __syncthreads();
-    if (sh.count > kLpCand) radix_top<F32>(a, row, v0, v1, k, sh);
+    if (sh.count > Shared::kCand) radix_top<F32, TH>(a, row, v0, v1, k, sh);
   }
   if (short_row && r + rows_apart < a.n) first_load(part_of(r + rows_apart));
   const uint32_t base = smem_u32(lp_smem);
@@ -430,20 +434,20 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const Log
   const uint32_t first = cluster > 1 ? tc::mapa(base, 0) : base;
   if (warp == 0) {
     LpSums t = {-CUDART_INF_F, 0.f, 0.f};
-    if (lane < kLpWarps) t = sh.part[lane];
+    if (lane < (TH / 32)) t = sh.part[lane];
 #pragma unroll
-    for (int o = 1; o < kLpWarps; o *= 2) {  // lane 0: the warps' sums in order
+    for (int o = 1; o < (TH / 32); o *= 2) {  // lane 0: the warps' sums in order
       const LpSums other = {__shfl_down_sync(0xffffffffu, t.m, o), __shfl_down_sync(0xffffffffu, t.s, o), __shfl_down_sync(0xffffffffu, t.w, o)};
       join(t, other, c);
     }
     if (lane == 0) {
-      const uint32_t to = first + uint32_t(offsetof(LpShared, all)) + uint32_t(sizeof(LpSums)) * rank;
+      const uint32_t to = first + uint32_t(offsetof(Shared, all)) + uint32_t(sizeof(LpSums)) * rank;
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(t.m) : "memory");
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4), "f"(t.s) : "memory");
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 8), "f"(t.w) : "memory");
     }
   }
-  if (k > 0) rank_keys(sh.cand, min(int(sh.count), kLpCand), k, first + uint32_t(offsetof(LpShared, best)) + 8u * k * rank);
+  if (k > 0) rank_keys<TH>(sh.cand, min(int(sh.count), Shared::kCand), k, first + uint32_t(offsetof(Shared, best)) + 8u * k * rank);
   if (cluster > 1) {
     tc::cluster_arrive();
     tc::cluster_wait();
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const Log
   const float log2_s = log2f(t.s);
   auto logprob = [&](float x) { return fmaf(x - t.m, a.scale, -log2_s * kLn2); };
   if (tid == 0 && a.entropy) a.entropy[r] = (log2_s - t.w / t.s) * kLn2;
-  for (int g = tid; g < a.given; g += kLpThreads) {
+  for (int g = tid; g < a.given; g += TH) {
     const int id = g == tid ? given_id : a.tokens[r * a.given + g];
     float v = 0.f;
     if (id >= 0 && id < a.V) {
@@ -471,7 +475,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const Log
     if (cluster > 1) {
       // zeros (a part with fewer than k values) rank last among themselves by place
       const int n = cluster * k;
-      for (int i = tid; i < n; i += kLpThreads) {
+      for (int i = tid; i < n; i += TH) {
         const uint64_t me = sh.best[i];
         int above = 0;
         for (int u = 0; u < n; ++u) above += sh.best[u] > me || (sh.best[u] == me && u < i) ? 1 : 0;
@@ -480,7 +484,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const Log
       __syncthreads();
       keys = sh.cand;
     }
-    for (int i = tid; i < k; i += kLpThreads) {
+    for (int i = tid; i < k; i += TH) {
       const uint64_t key = keys[i];
       const float x = of_ordered(uint32_t(key >> 32));
       a.top_ids[r * k + i] = key ? int32_t(0xffffffffu - uint32_t(key)) : -1;
@@ -490,16 +494,12 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const Log
   }
 }
 
-template <bool F32>
-cudaError_t launch(const LogprobArgs& a, int num_sms, cudaStream_t s) {
-  // a row over one CTA, or over up to eight while that leaves SMs without work and every thread a piece or two
-  int cluster = 1;
-  while (cluster < kLpMaxCluster && a.n * cluster * 2 <= num_sms && a.V / (cluster * 2) >= kLpThreads * 8) cluster *= 2;
+template <bool F32, int TH>
+cudaError_t launch(const LogprobArgs& a, int cluster, int ctas, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  // four CTAs an SM go from row to row
-  cfg.gridDim = dim3(static_cast<unsigned>(cluster > 1 ? a.n * cluster : a.n < 4 * num_sms ? a.n : 4 * num_sms));
-  cfg.blockDim = dim3(kLpThreads);
-  cfg.dynamicSmemBytes = sizeof(LpShared);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(TH);
+  cfg.dynamicSmemBytes = sizeof(LpShared<TH>);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -507,13 +507,26 @@ cudaError_t launch(const LogprobArgs& a, int num_sms, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<F32>, a, cluster);
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<F32, TH>, a, cluster);
+}
+
+template <bool F32>
+cudaError_t launch_rows(const LogprobArgs& a, int num_sms, cudaStream_t s) {
+  // Four wide CTAs an SM go from row to row, or a row is split over up to eight of them while that leaves places without
+  // work and every thread a piece or two. Many short rows take narrow CTAs, sixteen an SM: a row's fixed steps are most of its time
+  // (2134 rows of 1862 fp32 logits, nothing in L2: 21 us, 31 with wide ones).
+  const int64_t places = 4 * int64_t(num_sms);
+  const int64_t bytes = int64_t(a.V) * (F32 ? 4 : 2);
+  if (a.n > places && bytes <= kLpNarrow * 16 * 16) return launch<F32, kLpNarrow>(a, 1, static_cast<int>(a.n < 4 * places ? a.n : 4 * places), s);
+  int cluster = 1;
+  while (cluster < kLpMaxCluster && a.n * cluster * 2 <= places && bytes / (cluster * 2) >= kLpWide * 32) cluster *= 2;
+  return launch<F32, kLpWide>(a, cluster, static_cast<int>(cluster > 1 ? a.n * cluster : a.n < places ? a.n : places), s);
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int num_sms, cudaStream_t s) {
-  return a.f32 ? launch<true>(a, num_sms, s) : launch<false>(a, num_sms, s);
+  return a.f32 ? launch_rows<true>(a, num_sms, s) : launch_rows<false>(a, num_sms, s);
 }
 
 }  // namespace smla

@@ -146,7 +146,7 @@ def _check_norm(smla, n, dim, residual, group, mode, eps=1e-6, x_stride=None, ze
 
 
 @pytest.mark.parametrize("n,dim", [(1, 8), (5, 64), (9, 136), (17, 512), (3, 1024), (2, 1032), (33, 1536), (4, 7168), (2, 16384),
-                                   (1, 32768), (2, 10008)])
+                                   (1, 32768), (2, 10008), (300, 128), (1001, 248)])
 @pytest.mark.parametrize("residual,group,mode", [(True, 128, 0), (False, 0, 1), (True, 0, 0), (False, 128, 1)])
 def test_norm(smla, n, dim, residual, group, mode):
     _check_norm(smla, n, dim, residual, group, mode, seed=n + dim)
@@ -158,6 +158,31 @@ def test_norm_of_a_slice_zero_rows_and_in_place(smla):
     _check_norm(smla, 6, 2048, True, 128, 0, zero_row=True)
     _check_norm(smla, 6, 256, True, 0, 0, zero_row=True, eps=1e-3)
     _check_norm(smla, 40, 7168, True, 128, 0, alias=True)
+
+
+@pytest.mark.parametrize("dim", [96, 1024, 7168])
+@pytest.mark.parametrize("group", [128, 0])
+@pytest.mark.parametrize("mode", [0, 1])
+def test_codes_are_those_of_the_rounded_quotient(smla, dim, group, mode):
+    """Rows of +-1 have the norm 1, so y is the weight exactly: scales and codes bit for bit."""
+    torch = _torch()
+    g = torch.Generator().manual_seed(dim + group)
+    x = torch.where(torch.rand((6, dim), generator=g) < 0.5, -1.0, 1.0).to(torch.bfloat16)
+    w = torch.randn((dim,), generator=g) * torch.exp2(torch.randint(-30, 12, (dim,), generator=g).float())
+    w = w.to(torch.bfloat16)
+    codes = torch.empty((6, dim), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((6, -(-dim // 128) if group else 1), device="cuda")
+    smla.add_rmsnorm(x.cuda(), None, w.cuda(), 0.0, codes=codes, scales=scales, group=group, scale_mode=mode)
+    y = (x.float() * w.float()).numpy()
+    width = group or dim
+    for b in range(0, dim, width):
+        part = y[:, b:b + width]
+        ratio = np.abs(part).max(1) / np.float32(448)
+        scale = ratio if mode == smla.SMLA_SCALE_FP32 else O.pow2_ceil_f32(ratio).astype(np.float32)
+        assert np.array_equal(scales[:, b // width].cpu().numpy(), scale.astype(np.float32))
+        want = O.e4m3_encode_rne_satfinite((part / scale[:, None].astype(np.float32)).astype(np.float32))
+        got = codes[:, b:b + width].cpu().numpy()
+        assert np.array_equal(O.e4m3_decode(got), O.e4m3_decode(want))
 
 
 def test_norm_single_outputs(smla):
@@ -218,7 +243,8 @@ def _check_logprobs(smla, x, tokens, top, scale=1.0, ids_too=True):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("n,v,g,k", [(1, 1, 1, 1), (2, 7, 2, 20), (1, 129280, 1, 20), (3, 32003, 1, 5), (40, 5001, 7, 64), (200, 999, 1, 33),
-                                     (5, 2049, 0, 3), (4, 70001, 3, 0), (170, 16384, 1, 1)])
+                                     (5, 2049, 0, 3), (4, 70001, 3, 0), (170, 16384, 1, 1),
+                                     (700, 1862, 2, 20), (900, 4096, 1, 64), (64, 40001, 7, 20), (11, 70001, 1, 33)])
 def test_logprobs(smla, dtype, n, v, g, k):
     torch = _torch()
     gen = torch.Generator().manual_seed(n * 1000 + v)
