@@ -142,6 +142,36 @@ def test_a_long_request_among_many(smla):
     Prompt(smla, nq.tolist(), nk.tolist(), 4, 2, rope=0, seed=18).run().check()
 
 
+@pytest.mark.parametrize("heads,kv_heads,rope", [(7, 7, 64), (8, 8, 0), (10, 5, 64), (9, 3, 0)])
+@pytest.mark.parametrize("requests", [30, 90])
+def test_requests_of_one_row_tile(smla, heads, kv_heads, rope, requests):
+    """More of them than SMs, each of a few tokens over a few key tiles, and a value that spoils one head of one of them."""
+    r = np.random.default_rng(heads)
+    nq = r.integers(0, 65 if heads == kv_heads else 30, requests)
+    nk = nq + r.integers(0, 400, requests)
+    nq[3], nk[3], nq[4], nk[4] = 1, 1, 3, 2
+    p = Prompt(smla, nq.tolist(), nk.tolist(), heads, kv_heads, rope=rope, seed=23, sink=heads == 8, cap=20.0 if heads == 10 else 0.0,
+               bias=heads == 9).run()
+    p.check()
+    # a value that one head's later tokens alone see
+    torch = _torch()
+    out, lse = p.out.clone(), p.lse.clone()
+    big = int(np.argmax(nq))
+    j, h = int(nk[big]) - 1 - int(nq[big]) // 2, kv_heads // 2
+    p.v[int(p.cu_k[big]) + j, h, 9] = float("nan")
+    p.run()
+    first, g = int(p.cu_q[big]) + j - int(nk[big] - nq[big]), heads // kv_heads
+    same = torch.ones((p.T, heads), dtype=torch.bool, device="cuda")
+    same[first:int(p.cu_q[big + 1]), h * g:h * g + g] = False
+    assert torch.equal(p.out[same], out[same]) and torch.equal(p.lse, lse)
+    assert torch.isnan(p.out[first:int(p.cu_q[big + 1]), h * g].float()).any(-1).all()
+
+
+def test_single_tokens_of_many_heads_over_long_contexts(smla):
+    """More heads than SMs, and items that several SMs share."""
+    Prompt(smla, [1, 2, 1], [9000, 5000, 700], 60, 60, seed=24).run().check()
+
+
 def test_single_head_group_of_many_blocks(smla):
     """128 query heads on one kv head: two tokens a row tile pair, more blocks than a warp has lanes."""
     Prompt(smla, [300, 7], [310, 500], 128, 1, rope=64, seed=19).run().check()
