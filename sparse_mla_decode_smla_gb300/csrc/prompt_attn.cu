@@ -19,7 +19,7 @@
 // tensor cores work for the other. m moves only when a row's maximum grows by more than 2^16, so O is rescaled rarely, by
 // the softmax threads themselves; by the time S of a tile is there, PV of the tile before is complete.
 //
-// P in BF16 costs 2^-9 of each weight, independently; the sums of weights are of the fp32 values.
+// P in BF16 is off by 2^-8 of each weight at most, independently of the others; the sums of weights are of the fp32 values.
 //
 // What is hidden never counts: its score is replaced, and in tiles that not all rows see whole, value rows past the last
 // key become zeros and a value row with a non-finite element does too and is remembered, so that the rows that see it

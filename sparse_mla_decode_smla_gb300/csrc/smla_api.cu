@@ -870,6 +870,8 @@ smla_status smla_prompt_attention(const smla_prompt_desc* d, const void* q, cons
     double power = a.c2;
     for (int i = 0; i < 5; ++i, power *= in * in) a.tanh_c[i] = static_cast<float>(tanh_fit[i] * power);
     a.tanh_max = static_cast<float>(0.625 / in);
+    for (int i = 0; i < 5; ++i)
+      if (!isfinite(a.tanh_c[i])) a.tanh_max = -1.f;  // a cap so small that the powers leave fp32: not by the polynomial
   }
   return smla::launch_prompt_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }

@@ -117,6 +117,8 @@ CASES = [
     dict(nq=[260], nk=[900], heads=2, kv_heads=2, cap=300.0),      # small beside the cap: by the polynomial
     dict(nq=[260], nk=[900], heads=2, kv_heads=2, cap=0.5, rope=0),  # and all but cut off
     dict(nq=[1, 130], nk=[2600, 131], heads=2, kv_heads=2, prefix=[5, 131], bias=True),
+    dict(nq=[130], nk=[300], heads=2, kv_heads=2, cap=1e-7),       # whose polynomial's powers would leave fp32
+    dict(nq=[130], nk=[300], heads=2, kv_heads=2, cap=1e30),
 ]
 
 
@@ -205,11 +207,25 @@ def test_the_first_call_on_a_workspace_is_as_good_as_any(smla, case):
         assert torch.equal(p.out[real], again[real]) and torch.equal(p.lse, first.lse)
 
 
+def test_output_on_a_border_of_sixteen_bytes_and_no_lse(smla):
+    torch = _torch()
+    p = Prompt(smla, [70, 300], [400, 300], 3, 3, seed=25, sink=True).run()
+    want = p.out.clone()
+    room = torch.full((p.out.numel() + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+    p.out, lse, p.lse = room[8:].view(want.shape), p.lse, None
+    assert p.out.data_ptr() % 32 == 16
+    p.run()
+    assert torch.equal(p.out, want)
+    p.lse = lse
+    p.check()
+
+
 def test_large_scores_and_equal_ones(smla):
     Prompt(smla, [90], [400], 2, 2, seed=8, spread=40.0).run().check()
-    p = Prompt(smla, [90], [400], 2, 2, seed=9)
-    p.q.zero_()
-    p.run().check()
+    for cap in (0.0, 1e-7, 30.0):
+        p = Prompt(smla, [90], [400], 2, 2, seed=9, cap=cap)
+        p.q.zero_()
+        p.run().check()
     # the maximum grows from key tile to key tile: the sums are rescaled every time
     p = Prompt(smla, [130], [1300], 2, 2, seed=10)
     p.q.fill_(1.0)
