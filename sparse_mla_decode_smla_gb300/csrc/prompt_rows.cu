@@ -24,6 +24,8 @@ __device__ __forceinline__ uint4 bf16x8_of_e4m3(uint2 w, float scale) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Bound by HBM: 24 contexts of 4k to 32k fp8_ds slots (796 MB in and out) take 123 us, 96 % of the measured copy bandwidth.
+//
 // Output row i belongs to the request r with cu[r] <= i < cu[r + 1] and receives its slot starts[r] + i - cu[r].
 // A CTA finds the cache rows of its 64 output rows with one thread each (a binary search over cu, then the page
 // table), so that the eight rows of a warp are loaded together: one memory round trip for all of them.
@@ -257,9 +259,9 @@ __global__ void __launch_bounds__(kNormSmallThreads) add_rmsnorm_small_kernel(co
   r.finish(b, row, t, LANES, ss, wv, nullptr);
 }
 
-// Long rows: a CTA each, four or five an SM, whose loads, sums and stores overlap. (A CTA that goes from row to row with the
-// next ones on their way to shared memory holds fewer rows an SM and is slower: 206 us for 16384 x 7168 with the residual where
-// this takes 171, 91 % of the measured bandwidth.)
+// Long rows: a CTA each, four or five an SM, whose loads, sums and stores overlap: 16384 x 7168 with the residual, y and a
+// scale a row take 155 us, the measured copy bandwidth (6.8 TB/s). (A CTA that goes from row to row with the next ones on their
+// way to shared memory holds fewer rows an SM and is slower: 206 us.)
 constexpr int kNormVpt = 4;
 
 template <int MAXT>
@@ -271,15 +273,18 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) add_rmsnorm_kernel(
 #pragma unroll
   for (int k = 0; k < kNormVpt; ++k) {
     const int v = k * T + t;
-    xv[k] = rv[k] = wv[k] = make_uint4(0, 0, 0, 0);
+    xv[k] = rv[k] = make_uint4(0, 0, 0, 0);
     if (v < nv) {
       xv[k] = norm_x(a, row)[v];
       if (a.residual) rv[k] = norm_res(a, row)[v];
-      wv[k] = __ldg(static_cast<const uint4*>(a.weight) + v);
     }
   }
   NormRow<0, kNormVpt> r;
-  const float ss = r.all(r.add(a, row, t, T, xv, rv), T, part[0], norm_sum);
+  const float mine = r.add(a, row, t, T, xv, rv);
+#pragma unroll
+  for (int k = 0; k < kNormVpt; ++k)  // on their way while the threads meet (loaded with the row: 100 bytes of spills, 171 us)
+    wv[k] = k * T + t < nv ? __ldg(static_cast<const uint4*>(a.weight) + k * T + t) : make_uint4(0, 0, 0, 0);
+  const float ss = r.all(mine, T, part[0], norm_sum);
   r.finish(a, row, t, T, ss, wv, part[1]);
 }
 
