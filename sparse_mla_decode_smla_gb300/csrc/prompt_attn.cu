@@ -19,6 +19,12 @@
 // tensor cores work for the other. m moves only when a row's maximum grows by more than 2^16, so O is rescaled rarely, by
 // the softmax threads themselves; by the time S of a tile is there, PV of the tile before is complete.
 //
+// What bounds it: one 8191-token prompt of 32 heads takes 470 us, 1,460 TFLOP/s and 77 % of the measured matrix rate, the tensor
+// pipe busy for 67 % of the time. A row tile's chain is scores, softmax, P, then PV and the next scores; tensor memory (two S,
+// two O) has no room for a third row tile's, so a tile's softmax, about 2,500 clocks, is longer than the 1,280 that the other's
+// MMAs cover. With a cap the softmax is longer still (2 x 1024 tokens over 12k keys, 16 heads: 182 us where the MMAs' rate
+// would allow 96). Single tokens are bound by memory: 32 of them over 0.7k to 16k keys, 8 kv heads: 159 us, 90 % of the bandwidth.
+//
 // P in BF16 is off by 2^-8 of each weight at most, independently of the others; the sums of weights are of the fp32 values.
 //
 // What is hidden never counts: its score is replaced, and in tiles that not all rows see whole, value rows past the last
@@ -367,7 +373,7 @@ __device__ __forceinline__ void pa_plan(const PromptArgs& p, PaWalk& w) {
   w.per = 0;
   w.cost = kPaItemCost;
   // Runs where the longest item is over a third of an SM's share (8191 tokens of 32 heads, 0.29 of it, take 2 % longer in
-  // runs; chunks of 2 x 1024 over 12k keys, 16 heads, 20 % longer off the counter).
+  // runs than their 470 us off the counter; chunks of 2 x 1024 over 12k keys, 16 heads, 20 % longer off it than their 182 in runs).
   if (int64_t(longest) * 3 * gridDim.x <= w.total.tiles || w.total.items == 0) return;
   // an SM for every item, and none long enough to be cut: nothing to lay out
   if (w.total.items <= static_cast<int>(gridDim.x) && longest < 2 * kPaMinTiles) return;
@@ -473,7 +479,7 @@ __device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
 }
 // One lane of a converged warp. The MMA warp runs as one and elects a lane for its instructions alone: a branch on the lane
-// number around the whole loop made each MMA cost 80-200 clocks to issue (one 8191-token prompt: 837 us).
+// number around the whole loop made each MMA cost 80-200 clocks to issue (one 8191-token prompt: 837 us, 637 without it, then).
 __device__ __forceinline__ bool pa_elect() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
