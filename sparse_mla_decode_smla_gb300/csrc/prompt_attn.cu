@@ -55,6 +55,9 @@ constexpr int kPaTiles = 4;                // key (value) tiles in the ring at m
 // m moves when a row's maximum exceeds it by more than this (log2 units): weights stay below 2^16, which neither BF16 nor the
 // fp32 sums notice, and with a bias, where scores grow from tile to tile, it moves less often than with 2^8
 constexpr float kPaRescale = 16.f;
+// With a bias m moves this far beyond the maximum, so that it moves less often (8191 tokens of 32 heads: 513 us, 522 with 0);
+// weights around 2^-40 are as exact as others.
+constexpr float kPaAhead = 40.f;
 constexpr int kPaMinTiles = 8;             // key tiles of a run, and of a piece but the odd one, at least
 constexpr int kPaItemCost = 3;             // an item's own work, in key tiles
 constexpr int kPaSlotFloats = kPaRows * 128 + kPaRows * 2;  // a piece's part: O, then (m, l) of each row
@@ -953,8 +956,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (!CAP && !BIAS) top *= p.c2;
         const bool move = top > m + kPaRescale;
         if (__any_sync(0xffffffffu, move)) {
-          const float f = move ? ex2(m - top) : 1.f;  // 0 from -inf
-          if (move) m = mu = top;
+          const float to_m = BIAS ? top + kPaAhead : top;
+          const float f = move ? ex2(m - to_m) : 1.f;  // 0 from -inf
+          if (move) m = mu = to_m;
           const uint64_t ff = f2(f, f);
           sum2 = f2_fma(sum2, ff, 0);
           if (j > 0) {
