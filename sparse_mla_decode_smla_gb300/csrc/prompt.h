@@ -36,7 +36,7 @@ struct NormArgs {
   float eps;
 };
 constexpr int kNormMaxDim = 32768;
-cudaError_t launch_add_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s);
 
 struct LogprobArgs {
   const void* x;

@@ -24,7 +24,7 @@ __device__ __forceinline__ uint4 bf16x8_of_e4m3(uint2 w, float scale) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Bound by HBM: 24 contexts of 4k to 32k fp8_ds slots (796 MB in and out) take 123 us, 96 % of the measured copy bandwidth.
+// Bound by HBM: 24 contexts of 4k to 32k fp8_ds slots (796 MB in and out) take 120 us, 98 % of the measured copy bandwidth.
 //
 // Output row i belongs to the request r with cu[r] <= i < cu[r + 1] and receives its slot starts[r] + i - cu[r].
 // A CTA finds the cache rows of its 64 output rows with one thread each (a binary search over cu, then the page
@@ -32,6 +32,7 @@ __device__ __forceinline__ uint4 bf16x8_of_e4m3(uint2 w, float scale) {
 template <int FMT>
 __global__ void __launch_bounds__(kRdThreads) cache_read_kernel(const ReadArgs a) {
   __shared__ int64_t slots[kRdRows];  // -1: zeros, -2: no request's row
+  pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row0 = int64_t(blockIdx.x) * kRdRows;
   if (tid < kRdRows) {
@@ -62,6 +63,7 @@ __global__ void __launch_bounds__(kRdThreads) cache_read_kernel(const ReadArgs a
     slots[tid] = slot;
   }
   __syncthreads();
+  pdl_trigger();
   constexpr bool BF = FMT == SMLA_KV_BF16, tens = FMT == SMLA_KV_FP8_TENSOR;
   constexpr int R = BF ? kBf16RowBytes : tens ? kFp8TensorRowBytes : kFp8RowBytes;
   const uint4 none = make_uint4(0, 0, 0, 0);
@@ -241,6 +243,7 @@ __global__ void __launch_bounds__(kNormSmallThreads) add_rmsnorm_small_kernel(co
   const int t = threadIdx.x & (LANES - 1), nv = a.dim >> 3;
   const int64_t row = int64_t(blockIdx.x) * (kNormSmallThreads / LANES) + threadIdx.x / LANES;
   const bool real = row < a.n;  // (lanes of rows past the end go along: the warp shuffles together)
+  pdl_wait();
   uint4 xv[VPT], rv[VPT], wv[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
@@ -252,6 +255,7 @@ __global__ void __launch_bounds__(kNormSmallThreads) add_rmsnorm_small_kernel(co
       wv[k] = __ldg(static_cast<const uint4*>(a.weight) + v);
     }
   }
+  pdl_trigger();
   NormArgs b = a;
   if (!real) b.dim = 0;  // nothing of it is stored
   NormRow<LANES, VPT> r;
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(kNormSmallThreads) add_rmsnorm_small_kernel(co
 }
 
 // Long rows: a CTA each, four or five an SM, whose loads, sums and stores overlap: 16384 x 7168 with the residual, y and a
-// scale a row take 155 us, the measured copy bandwidth (6.8 TB/s). (A CTA that goes from row to row with the next ones on their
+// scale a row take 153 us, the measured copy bandwidth (6.9 TB/s). (A CTA that goes from row to row with the next ones on their
 // way to shared memory holds fewer rows an SM and is slower: 206 us.)
 constexpr int kNormVpt = 4;
 
@@ -270,6 +274,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) add_rmsnorm_kernel(
   const int t = threadIdx.x, T = blockDim.x, nv = a.dim >> 3;
   const int64_t row = blockIdx.x;
   uint4 xv[kNormVpt], rv[kNormVpt], wv[kNormVpt];
+  pdl_wait();
 #pragma unroll
   for (int k = 0; k < kNormVpt; ++k) {
     const int v = k * T + t;
@@ -280,6 +285,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) add_rmsnorm_kernel(
     }
   }
   NormRow<0, kNormVpt> r;
+  pdl_trigger();
   const float mine = r.add(a, row, t, T, xv, rv);
 #pragma unroll
   for (int k = 0; k < kNormVpt; ++k)  // on their way while the threads meet (loaded with the row: 100 bytes of spills, 171 us)
@@ -288,29 +294,38 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) add_rmsnorm_kernel(
   r.finish(a, row, t, T, ss, wv, part[1]);
 }
 
+// A kernel that starts up while the one before it on the stream ends, and waits for it before it touches memory (pdl_wait).
+template <typename A>
+cudaError_t launch_early(void (*kernel)(A), int64_t ctas, int threads, const A& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_read(const ReadArgs& a, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((a.N + kRdRows - 1) / kRdRows);
-  if (a.kv_format == SMLA_KV_BF16) cache_read_kernel<SMLA_KV_BF16><<<grid, kRdThreads, 0, s>>>(a);
-  else if (a.kv_format == SMLA_KV_FP8_DS) cache_read_kernel<SMLA_KV_FP8_DS><<<grid, kRdThreads, 0, s>>>(a);
-  else cache_read_kernel<SMLA_KV_FP8_TENSOR><<<grid, kRdThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  const int64_t ctas = (a.N + kRdRows - 1) / kRdRows;
+  if (a.kv_format == SMLA_KV_BF16) return launch_early(cache_read_kernel<SMLA_KV_BF16>, ctas, kRdThreads, a, s);
+  if (a.kv_format == SMLA_KV_FP8_DS) return launch_early(cache_read_kernel<SMLA_KV_FP8_DS>, ctas, kRdThreads, a, s);
+  return launch_early(cache_read_kernel<SMLA_KV_FP8_TENSOR>, ctas, kRdThreads, a, s);
 }
 
-cudaError_t launch_add_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
   const int nv = a.dim >> 3;
-  auto ctas = [&](int lanes) { return static_cast<unsigned>((a.n * lanes + kNormSmallThreads - 1) / kNormSmallThreads); };
-  if (nv <= 32) {
-    add_rmsnorm_small_kernel<16, 2><<<ctas(16), kNormSmallThreads, 0, s>>>(a);
-  } else if (nv <= 128) {
-    add_rmsnorm_small_kernel<32, 4><<<ctas(32), kNormSmallThreads, 0, s>>>(a);
-  } else {
-    const int threads = ((nv + kNormVpt - 1) / kNormVpt + 31) & ~31;
-    if (threads <= 256) add_rmsnorm_kernel<256><<<static_cast<unsigned>(a.n), threads, 0, s>>>(a);
-    else add_rmsnorm_kernel<1024><<<static_cast<unsigned>(a.n), threads, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  auto ctas = [&](int lanes) { return (a.n * lanes + kNormSmallThreads - 1) / kNormSmallThreads; };
+  if (nv <= 32) return launch_early(add_rmsnorm_small_kernel<16, 2>, ctas(16), kNormSmallThreads, a, s);
+  if (nv <= 128) return launch_early(add_rmsnorm_small_kernel<32, 4>, ctas(32), kNormSmallThreads, a, s);
+  const int threads = ((nv + kNormVpt - 1) / kNormVpt + 31) & ~31;
+  return threads <= 256 ? launch_early(add_rmsnorm_kernel<256>, a.n, threads, a, s)
+                        : launch_early(add_rmsnorm_kernel<1024>, a.n, threads, a, s);
 }
 
 }  // namespace smla

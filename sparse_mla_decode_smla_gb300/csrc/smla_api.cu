@@ -794,7 +794,7 @@ smla_status smla_add_rmsnorm(const smla_norm_desc* d, const void* x, const void*
   a.group = d->group;
   a.scale_mode = d->scale_mode;
   a.eps = d->rms_eps;
-  return smla::launch_add_rmsnorm(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+  return smla::launch_add_rmsnorm(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
 smla_status smla_prompt_workspace_size(const smla_prompt_desc* d, size_t* bytes) {

@@ -13,7 +13,7 @@
 // (rows of equal values) are found by a radix search over the part instead. Keys are distinct, so the order in which they
 // came does not matter.
 //
-// 1024 rows of 129,280 bf16 logits take 58 us with 20 alternatives, 48 with none (265 MB: 39 us at the measured copy
+// 1024 rows of 129,280 bf16 logits take 55 us with 20 alternatives, 8 more than with none (265 MB: 39 us at the measured copy
 // bandwidth). The reading and the ends of rows bound it, where a CTA's threads meet, all CTAs at nearly the same time: without
 // the exponentials it takes as long, and so it does with twice as much on its way (by asynchronous copies to shared memory).
 // Bounds raised on the way and candidates kept in the first reading: 82 us.
@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) token_logprobs_kernel(const Log
   auto first_load = [&](const Part& q) { load(reinterpret_cast<const uint4*>(q.row + size_t(q.head) * es) + q.p0 + tid, q.p1 - q.p0); };
   const int64_t rows_apart = gridDim.x / cluster;
   int64_t r = blockIdx.x / cluster;
+  pdl_wait();  // what came before on the stream is complete
   first_load(part_of(r));
   for (; r < a.n; r += rows_apart) {  // (one row where it is shared by a cluster)
   const Part part = part_of(r);
@@ -364,6 +365,8 @@ __global__ void __launch_bounds__(TH, 1024 / TH) token_logprobs_kernel(const Log
   // the next row's first pieces, while this one's end is worked out
   const bool short_row = rounds <= 1;  // its pieces are all still in `next`
   if (!short_row && r + rows_apart < a.n) first_load(part_of(r + rows_apart));
+  // (CTAs of the next kernel that come where some have two rows and some one take places unevenly: 1024 rows of 129,280 then take 59.7 us, 55 without)
+  if (a.n <= rows_apart) pdl_trigger();
   float edge[2] = {-CUDART_INF_F, -CUDART_INF_F};  // a value before the first and one behind the last piece
   const int edge_at[2] = {rank == 0 && tid < head ? tid : -1,
                           rank == cluster - 1 && head + pieces * kPer + tid < a.V ? head + pieces * kPer + tid : -1};
@@ -505,12 +508,14 @@ cudaError_t launch(const LogprobArgs& a, int cluster, int ctas, cudaStream_t s) 
   cfg.blockDim = dim3(TH);
   cfg.dynamicSmemBytes = sizeof(LpShared<TH>);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<F32, TH>, a, cluster);
 }
 
