@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptA
   __shared__ PaTab scan[kPlanThreads / 32];
   __shared__ int most[kPlanThreads / 32];
   pdl_trigger();
+  pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, G = p.H >> p.log2_pack;
   PaHead* head = reinterpret_cast<PaHead*>(p.ws);
   PaTab before = {0, 0, 0};  // of the requests before this round's
@@ -1206,21 +1207,22 @@ cudaError_t launch_variant(const PromptArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_release);
   }
-  if (a.B > kPlanWarp) {
-    prompt_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.sms));
-  cfg.blockDim = dim3(kPaThreads);
-  cfg.dynamicSmemBytes = PaLay<ROPE>::bytes;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (a.B > kPlanWarp) {
+    e = cudaLaunchKernelEx(&cfg, prompt_plan_kernel, a);
+    if (e != cudaSuccess) return e;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(a.sms));
+  cfg.blockDim = dim3(kPaThreads);
+  cfg.dynamicSmemBytes = PaLay<ROPE>::bytes;
   return cudaLaunchKernelEx(&cfg, prompt_attention_kernel<ROPE, CAP, BIAS>, a, qm, km, rm, vm);
 }
 
