@@ -19,7 +19,7 @@
 // tensor cores work for the other. m moves only when a row's maximum grows by more than 2^16, so O is rescaled rarely, by
 // the softmax threads themselves; by the time S of a tile is there, PV of the tile before is complete.
 //
-// What bounds it: one 8191-token prompt of 32 heads takes 470 us, 1,460 TFLOP/s and 77 % of the measured matrix rate, the tensor
+// What bounds it: one 8191-token prompt of 32 heads takes 473 us, 1,450 TFLOP/s and 76 % of the measured matrix rate, the tensor
 // pipe busy for 67 % of the time. A row tile's chain is scores, softmax, P, then PV and the next scores; tensor memory (two S,
 // two O) has no room for a third row tile's, so a tile's softmax, about 2,500 clocks, is longer than the 1,280 that the other's
 // MMAs cover. With a cap the softmax is longer still (2 x 1024 tokens over 12k keys, 16 heads: 182 us where the MMAs' rate
@@ -377,7 +377,7 @@ __device__ __forceinline__ void pa_plan(const PromptArgs& p, PaWalk& w) {
   w.per = 0;
   w.cost = kPaItemCost;
   // Runs where the longest item is over a third of an SM's share (8191 tokens of 32 heads, 0.29 of it, take 2 % longer in
-  // runs than their 470 us off the counter; chunks of 2 x 1024 over 12k keys, 16 heads, 20 % longer off it than their 182 in runs).
+  // runs than their 473 us off the counter; chunks of 2 x 1024 over 12k keys, 16 heads, 20 % longer off it than their 182 in runs).
   if (int64_t(longest) * 3 * gridDim.x <= w.total.tiles || w.total.items == 0) return;
   // an SM for every item, and none long enough to be cut: nothing to lay out
   if (w.total.items <= static_cast<int>(gridDim.x) && longest < 2 * kPaMinTiles) return;
