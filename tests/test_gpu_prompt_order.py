@@ -85,3 +85,40 @@ def test_calls_on_one_stream_take_effect_in_order(smla, rows, vocab):
         torch.cuda.synchronize()
         for i, (a, b) in enumerate(zip(want, got)):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (captured, i)
+
+
+@pytest.mark.parametrize("requests", [33, 700])
+def test_many_requests_behind_the_kernels_that_write_their_inputs(smla, requests):
+    """More requests than a warp lays out: lengths, keys and queries are written right in front of each call, and the output is
+    overwritten right behind it."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(5)
+    n, H = 7 * requests, 4
+    xs = [torch.randn((n, 1024), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    w = torch.ones(1024, device="cuda").to(torch.bfloat16)
+    w128 = torch.ones(H * 128, device="cuda").to(torch.bfloat16)
+    cus = [torch.arange(0, n + 1, 7, dtype=torch.int32, device="cuda"),
+           torch.cat([torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((requests,), n, dtype=torch.int32, device="cuda")])]
+    y, cu = torch.zeros_like(xs[0]), torch.zeros(requests + 1, dtype=torch.int32, device="cuda")
+    q, k, v = y[:, :512].view(n, H, 128), y[:, 512:768].view(n, 2, 128), y[:, 768:].view(n, 2, 128)
+    d = smla.make_prompt_desc(n, n, H, 2, requests, 0, 128 ** -0.5, q_strides=q.stride()[:2], k_strides=k.stride()[:2], v_strides=v.stride()[:2])
+    ws = torch.zeros(smla.prompt_workspace_size(d), dtype=torch.uint8, device="cuda")
+    out, lse = torch.zeros((n, H, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros((n, H), device="cuda")
+
+    def once(i, wait):
+        keep = torch.zeros_like(out)
+        for f in (lambda: cu.copy_(cus[i % 2]), lambda: smla.add_rmsnorm(xs[i % 3], None, w, 1e-6, y=y),
+                  lambda: smla.prompt_attention(d, q, k, v, None, cu, cu, None, None, None, out, lse, ws),
+                  lambda: smla.add_rmsnorm(out.view(n, H * 128), None, w128, 1e-6, y=keep.view(n, H * 128)),
+                  lambda: smla.add_rmsnorm(y[:, :512], None, w128, 1e-6, y=out.view(n, H * 128))):
+            f()
+            if wait:
+                torch.cuda.synchronize()
+        return keep
+
+    want = [once(i, True) for i in range(6)]
+    got = [once(i, False) for i in range(6)]
+    torch.cuda.synchronize()
+    assert smla.read_error(None, ws) == 0
+    for a, b in zip(want, got):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
