@@ -671,9 +671,12 @@ typedef struct smla_prompt_desc {
 
 /*
  * Bytes of device workspace smla_prompt_attention needs for `d` on the current device: the error word,
- * the plan and the parts of work that several SMs share (about 40 MB, whatever the batch's size). The
+ * the plan and the parts of work that several SMs share (about 40 MB, and 16 bytes a request). The
  * caller allocates it (256-byte aligned) and zeroes it once before first use (and again after a call that set
- * SMLA_DEVERR_TIMEOUT); smla_read_error reads and clears the error word. Writes 0 into *bytes on error.
+ * SMLA_DEVERR_TIMEOUT); smla_read_error reads and clears the error word. One workspace serves calls of any
+ * descriptions that it is large enough for, one after another: counters in it have to be zero between calls,
+ * and each call leaves them so. Nothing else may write there: smla_decode and smla_tree_decode take a
+ * workspace of their own. Writes 0 into *bytes on error.
  */
 smla_status smla_prompt_workspace_size(const smla_prompt_desc* d, size_t* bytes);
 

@@ -65,8 +65,9 @@ struct PromptArgs {
   const float* sink;        // NULL: none
   void* out;
   float* lse;
-  uint8_t* ws;              // error word, counters and a line a request
+  uint8_t* ws;              // error word and item counters
   int32_t* counts;          // [SM][row tile]: pieces that have ended, zero between calls
+  uint8_t* table;           // a line a request
   float* parts;             // two an SM
   int64_t q_token, q_head, k_token, k_head, v_token, v_head, rope_token;  // strides in elements
   int32_t T, N, H, HK, B, causal, log2_pack, sms;
@@ -76,7 +77,7 @@ struct PromptArgs {
   float tanh_c[5];          // its coefficients, of odd powers of q.k
 };
 struct PromptLayout {
-  size_t counts, parts, bytes;
+  size_t counts, table, parts, bytes;
 };
 PromptLayout prompt_layout(int64_t requests, int num_sms);
 constexpr int kPromptMaxRequests = 1 << 16;

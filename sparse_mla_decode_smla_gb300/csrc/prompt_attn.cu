@@ -149,7 +149,7 @@ struct PaTab {  // key tiles and items before a request, of all its heads; [B] h
   int64_t tiles;
   int32_t items, pad;
 };
-__device__ __forceinline__ PaTab* pa_table(const PromptArgs& p) { return reinterpret_cast<PaTab*>(p.ws + 256); }
+__device__ __forceinline__ PaTab* pa_table(const PromptArgs& p) { return reinterpret_cast<PaTab*>(p.table); }
 
 constexpr int kPlanThreads = 256;
 constexpr int kPlanWarp = 32;  // requests that a warp lays out itself
@@ -1149,10 +1149,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 PromptLayout prompt_layout(int64_t requests, int num_sms) {
   PromptLayout l;
   const size_t slots = 2 * size_t(num_sms);
-  size_t at = 256 + size_t(requests + 1) * sizeof(PaTab);
+  // What lasts from call to call, the head and the counters, comes first: where it is depends on the device alone, so that
+  // calls of other descriptions on the same workspace find it as they left it and write nothing else there.
+  l.counts = 256;
+  size_t at = l.counts + slots * sizeof(int32_t);
   at = (at + 255) / 256 * 256;
-  l.counts = at;
-  at += slots * sizeof(int32_t);
+  l.table = at;
+  at += size_t(requests + 1) * sizeof(PaTab);
   at = (at + 255) / 256 * 256;
   l.parts = at;
   l.bytes = at + slots * kPaSlotFloats * sizeof(float);

@@ -842,6 +842,7 @@ smla_status smla_prompt_attention(const smla_prompt_desc* d, const void* q, cons
   a.lse = lse;
   a.ws = static_cast<uint8_t*>(workspace);
   a.counts = reinterpret_cast<int32_t*>(a.ws + l.counts);
+  a.table = a.ws + l.table;
   a.parts = reinterpret_cast<float*>(a.ws + l.parts);
   a.q_token = d->q_token_stride;
   a.q_head = d->q_head_stride;
