@@ -701,8 +701,8 @@ smla_status smla_prompt_workspace_size(const smla_prompt_desc* d, size_t* bytes)
  *          streams, two graphs) need one each.
  * A request whose offsets do not ascend or reach past T or N is left out (SMLA_DEVERR_INDEX): its rows are
  * not written. What a token does not see never reaches its result, whatever the values there: a value row
- * with a NaN or an infinity makes out (not lse) of the tokens that see it NaN or infinite and leaves the
- * others as they are.
+ * with a NaN or an infinity makes out (not lse) of the tokens that see it NaN or infinite, in that dim or in
+ * all, and leaves the others as they are.
  *
  * Precision. Scores, softmax statistics and sums are fp32; q, k, v and the weights enter the tensor cores as
  * bf16. Results do not depend on how the GPU schedules the work.

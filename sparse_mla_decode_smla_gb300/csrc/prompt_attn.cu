@@ -1004,7 +1004,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
       const float2 s2 = f2_parts(sum2);
       float l = s2.x + s2.y;
-      const bool spoilt = *reinterpret_cast<volatile int32_t*>(bad + (k & 1)) < lim;  // a value this row sees is not finite
       const int64_t at = int64_t(it.q0 + token) * p.H + hd;
       const float sink = p.sink && mine ? __ldg(p.sink + hd) * kLog2e : -CUDART_INF_F;
       auto finish = [&](float& m_, float& l_) -> float {  // with the sink: the factor of O
@@ -1029,6 +1028,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         l = l * fa + o.y * fb;
         m = both;
       }
+      // A value this row sees is not finite. The guards have looked at the tiles of this half's own sums when those are there,
+      // and at the other half's of a paired item once the halves have met.
+      const bool spoilt = *reinterpret_cast<volatile int32_t*>(bad + (k & 1)) < lim;
       auto sums = [&](int c, float (&v)[32]) {
         uint32_t o[32];
 #pragma unroll
