@@ -699,8 +699,9 @@ smla_status smla_prompt_workspace_size(const smla_prompt_desc* d, size_t* bytes)
  *          denominator (-inf where it is empty). Rows of no request are left as they were.
  *   workspace smla_prompt_workspace_size(d) bytes, 256-byte aligned; calls that may overlap (two
  *          streams, two graphs) need one each.
- * A request whose offsets do not ascend or reach past T or N is left out (SMLA_DEVERR_INDEX): its rows are
- * not written. What a token does not see never reaches its result, whatever the values there: a value row
+ * A request whose offsets do not ascend or reach past T or N, or which starts before the end of an earlier
+ * request that fits, is left out (SMLA_DEVERR_INDEX): its rows, but for those of other requests, are not
+ * written. What a token does not see never reaches its result, whatever the values there: a value row
  * with a NaN or an infinity makes out (not lse) of the tokens that see it NaN or infinite, in that dim or in
  * all, and leaves the others as they are.
  *

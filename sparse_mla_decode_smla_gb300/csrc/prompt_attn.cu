@@ -178,20 +178,48 @@ __device__ __forceinline__ int64_t pa_sum(const PromptArgs& p, const PaReq& mine
   return n;
 }
 
+// A request that starts before the last token of an earlier one would write its rows too, in no order (and offsets that go to and fro
+// would ask for work without bound): it is left out. By a whole warp, a request with its `ok` of pa_request a lane: the largest end of
+// the requests with tokens before the lane's, and of all of them.
+__device__ __forceinline__ int pa_ends(const PaReq& q, int ok, int& all) {
+  int x = ok > 0 ? q.q0 + q.nq : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int a = __shfl_up_sync(0xffffffffu, x, o);
+    if ((threadIdx.x & 31) >= o) x = max(x, a);
+  }
+  all = __shfl_sync(0xffffffffu, x, 31);
+  x = __shfl_up_sync(0xffffffffu, x, 1);
+  return threadIdx.x & 31 ? x : 0;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptArgs p) {
   __shared__ PaTab scan[kPlanThreads / 32];
+  __shared__ int ends[kPlanThreads / 32];
   __shared__ int most[kPlanThreads / 32];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, G = p.H >> p.log2_pack;
   PaHead* head = reinterpret_cast<PaHead*>(p.ws);
   PaTab before = {0, 0, 0};  // of the requests before this round's
-  int longest = 0;
+  int longest = 0, end = 0;
   for (int r0 = 0; r0 < p.B; r0 += kPlanThreads) {
     const int r = r0 + tid;
     PaTab v = {0, 0, 0};
     PaReq q = {};
-    const int ok = r < p.B ? pa_request(p, r, q) : 0;
+    int ok = r < p.B ? pa_request(p, r, q) : 0, all;
+    const int in_warp = pa_ends(q, ok, all);
+    if (lane == 0) ends[tid >> 5] = all;
+    __syncthreads();
+    int taken = end;
+    for (int i = 0; i < kPlanThreads / 32; ++i) {
+      if (i < (tid >> 5)) taken = max(taken, ends[i]);
+      end = max(end, ends[i]);
+    }
+    if (ok > 0 && q.q0 < max(taken, in_warp)) {
+      ok = -1;
+      q = PaReq{};
+    }
     if (ok < 0) atomicOr(&head->err, SMLA_DEVERR_INDEX);
     const int64_t tiles = pa_sum(p, q);
     if (ok > 0) {
@@ -334,9 +362,8 @@ __device__ __forceinline__ void pa_next(const PromptArgs& p, PaWalk& w, const Pa
   w.block = 0;
   if (++w.hg < (p.H >> p.log2_pack)) return;
   w.hg = 0;
-  PaReq n;
-  do ++w.r;
-  while (w.r < p.B && pa_request(p, w.r, n) <= 0);
+  do ++w.r;  // past requests without items
+  while (w.r < p.B && pa_line(p, w, w.r).items == (w.r + 1 < p.B ? pa_line(p, w, w.r + 1) : w.total).items);
 }
 
 // Lays the batch out: by a whole warp.
@@ -346,7 +373,14 @@ __device__ __forceinline__ void pa_plan(const PromptArgs& p, PaWalk& w) {
   int longest = 0;
   if (p.B <= kPlanWarp) {
     PaReq q = {};
-    const int ok = lane < p.B ? pa_request(p, lane, q) : 0;
+    int ok = lane < p.B ? pa_request(p, lane, q) : 0;
+    if (__any_sync(0xffffffffu, ok < 0)) {  // (requests overlap only where an offset goes back)
+      int all;
+      if (q.q0 < pa_ends(q, ok, all) && ok > 0) {
+        ok = -1;
+        q = PaReq{};
+      }
+    }
     if (ok < 0 && blockIdx.x == 0) atomicOr(&head->err, SMLA_DEVERR_INDEX);
     PaTab v = {0, 0, 0};
     const int64_t tiles = pa_sum(p, q);
