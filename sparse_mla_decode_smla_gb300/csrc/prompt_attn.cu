@@ -936,7 +936,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           float probe = 0.f;
 #pragma unroll
           for (int i = 0; i < 128; i += 2) probe = max3_nan(probe, fabsf(x[i]), fabsf(x[i + 1]));
-          if (__all_sync(0xffffffffu, probe <= p.tanh_max)) {
+          // Each row goes by its own scores of this tile, so that no other row's change a bit of it; rows that are no token's go
+          // along with the quick way. 2 x 1024 tokens over 12k keys, 16 heads, cap 30: 176 us where no score of a tile is large beside
+          // the cap, 276 where every row has some, 303 where a warp has rows of both kinds and takes both ways (queries five
+          // times as large; 274 with one way a warp, by vote).
+          if (!mine || probe <= p.tanh_max) {
             // all |u| <= 0.625: cap tanh(u) as u times a polynomial in u^2 (least maximum error: 2^-25 of cap), without the
             // special functions that the weights need too
             uint64_t cf[5];
@@ -970,6 +974,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             x[i + 3] = fmaf(rcd, e[2], p.cap2);
           }
           }
+          __syncwarp();
         }
         if constexpr (BIAS) {
           const float d0 = pos - float(key0);

@@ -1,0 +1,55 @@
+"""A token's attention is its own: other rows, other requests and far positions leave it as it is, on the GPU."""
+import numpy as np
+import pytest
+
+from test_gpu_prompt_attention import Prompt
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def smla():
+    import sparse_mla_decode_smla_gb300 as m
+    m.lib()
+    return m
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _same(a, b):
+    """Bit for bit."""
+    return _torch().equal(a.contiguous().view(_torch().uint8), b.contiguous().view(_torch().uint8))
+
+
+@pytest.mark.parametrize("rope,bias", [(64, False), (0, False), (0, True)])
+@pytest.mark.parametrize("value", [200.0, float("nan"), float("inf")])
+def test_a_capped_token_does_not_depend_on_other_queries(smla, rope, bias, value):
+    """The first 40 tokens, whose scores are small beside the cap, in front of large queries: later ones of their own request
+    and another request's, over key tiles that all of them see."""
+    p = Prompt(smla, [70, 90], [600, 300], 2, 2, rope=rope, cap=20.0, bias=bias, seed=31, sink=True, spread=0.3).run()
+    out, lse = p.out.clone(), p.lse.clone()
+    first = int(p.cu_q[0]) + 40
+    p.q[first:].copy_(p.q[first:] * value if np.isfinite(value) else _torch().full_like(p.q[first:], value))
+    p.run()
+    assert _same(p.out[:first], out[:first]) and _same(p.lse[:first], lse[:first])
+
+
+@pytest.mark.parametrize("value", [200.0, float("nan")])
+def test_a_capped_token_does_not_depend_on_other_heads(smla, value):
+    """Grouped heads of one token stand beside one another in a row tile."""
+    p = Prompt(smla, [30], [700], 8, 2, cap=20.0, seed=32, spread=0.3).run()
+    out, lse = p.out.clone(), p.lse.clone()
+    p.q[:, 1].copy_(p.q[:, 1] * value if np.isfinite(value) else _torch().full_like(p.q[:, 1], value))
+    p.run()
+    others = [h for h in range(8) if h != 1]
+    assert _same(p.out[:, others], out[:, others]) and _same(p.lse[:, others], lse[:, others])
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_small_and_large_scores_beside_one_another(smla, bias):
+    p = Prompt(smla, [150, 33], [400, 150], 4, 2, cap=20.0, bias=bias, seed=33, sink=True)
+    p.q.copy_(p.q * _torch().where(_torch().arange(p.T, device="cuda") % 3 == 0, 15.0, 0.2)[:, None, None])
+    p.run().check()
