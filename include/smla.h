@@ -706,7 +706,8 @@ smla_status smla_prompt_workspace_size(const smla_prompt_desc* d, size_t* bytes)
  * all, and leaves the others as they are.
  *
  * Precision. Scores, softmax statistics and sums are fp32; q, k, v and the weights enter the tensor cores as
- * bf16. Results do not depend on how the GPU schedules the work.
+ * bf16; a capped score is within 2^-20 of the cap. Results do not depend on how the GPU schedules the work, and
+ * a token's do not depend on the values of other queries.
  */
 smla_status smla_prompt_attention(const smla_prompt_desc* d, const void* q, const void* k, const void* v,
                                   const void* k_rope, const int32_t* cu_q, const int32_t* cu_k,

@@ -870,9 +870,15 @@ smla_status smla_prompt_attention(const smla_prompt_desc* d, const void* q, cons
     const double in = double(d->sm_scale) / d->softcap;
     double power = a.c2;
     for (int i = 0; i < 5; ++i, power *= in * in) a.tanh_c[i] = static_cast<float>(tanh_fit[i] * power);
-    a.tanh_max = static_cast<float>(0.625 / in);
+    // Powers of in leave fp32 at both ends. A cap so small that they are not finite: not by the polynomial. One so large that the
+    // last ones lose digits or vanish (1,700 and more at a scale of 0.07): as far as each of those stays below 2^-25 of tanh(u) / u,
+    // c u^2i <= 2^-25 with tanh(u) / u >= 0.88; and squares of scores stay finite.
+    double most = 0.625;
+    for (int i = 1; i < 5; ++i)
+      if (fabsf(a.tanh_c[i]) < 1.17549435e-38f) most = fmin(most, pow(0.88 * 0x1p-25 / fabs(tanh_fit[i]), 0.5 / i));
+    a.tanh_max = static_cast<float>(fmin(most / in, 1e18));
     for (int i = 0; i < 5; ++i)
-      if (!isfinite(a.tanh_c[i])) a.tanh_max = -1.f;  // a cap so small that the powers leave fp32: not by the polynomial
+      if (!isfinite(a.tanh_c[i])) a.tanh_max = -1.f;
   }
   return smla::launch_prompt_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }

@@ -53,3 +53,19 @@ def test_small_and_large_scores_beside_one_another(smla, bias):
     p = Prompt(smla, [150, 33], [400, 150], 4, 2, cap=20.0, bias=bias, seed=33, sink=True)
     p.q.copy_(p.q * _torch().where(_torch().arange(p.T, device="cuda") % 3 == 0, 15.0, 0.2)[:, None, None])
     p.run().check()
+
+
+def test_scores_up_to_a_cap_that_is_large_beside_the_scale(smla):
+    """Powers of scale / cap that leave fp32: scores from next to nothing up to 0.63 of the cap."""
+    torch = _torch()
+    for cap in (2e3, 5e4, 1e6, 1e9):
+        p = Prompt(smla, [130], [130], 2, 2, cap=cap, seed=34)
+        # s = scale * 192 a b, up to 0.63 cap: a in whole numbers up to 85, b a power of two or 27 / 16 of one, exact in bf16
+        b = 2.0 ** np.floor(np.log2(0.63 * cap / (p.scale * 192 * 85)))
+        p.q.copy_((1 + torch.arange(p.T, device="cuda") * 84 // p.T)[:, None, None].to(p.q.dtype).expand_as(p.q))
+        p.k.fill_(b)
+        p.rope.fill_(b)
+        p.run().check()
+        p.k.fill_(b * 1.6875)
+        p.rope.fill_(b * 1.6875)
+        p.run().check()
