@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       const int n = it.n[t], kt0 = it.kt0;
       float slope = 0.f;
       if (BIAS && mine) slope = __ldg(p.slopes + hd) * kLog2e;
-      const float pos = float(it.nk - it.nq + token);
+      const int pos = it.nk - it.nq + token;
       float m = -CUDART_INF_F, mu = 0.f;  // mu: m where it is finite
       uint64_t sum2 = 0;
       for (int j = 0; j < n; ++j, ++ns) {
@@ -977,7 +977,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           __syncwarp();
         }
         if constexpr (BIAS) {
-          const float d0 = pos - float(key0);
+          const float d0 = float(pos - key0);  // the difference first: positions past 2^24 are not fp32 numbers
 #pragma unroll
           for (int i = 0; i < 128; ++i) x[i] = fmaf(-slope, fabsf(d0 - float(i)), CAP ? x[i] : x[i] * p.c2);
         }

@@ -2,7 +2,8 @@
 import numpy as np
 import pytest
 
-from test_gpu_prompt_attention import Prompt
+import oracle.prompt_oracle as PO
+from test_gpu_prompt_attention import Prompt, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +70,25 @@ def test_scores_up_to_a_cap_that_is_large_beside_the_scale(smla):
         p.k.fill_(b * 1.6875)
         p.rope.fill_(b * 1.6875)
         p.run().check()
+
+
+def test_a_bias_by_distance_past_two_to_the_24_keys(smla):
+    """Positions that fp32 does not hold: all but the nearest keys weigh nothing, so the last 300 are the reference."""
+    torch = _torch()
+    n, near, slope = (1 << 24) + 130, 300, 1.0
+    g = torch.Generator(device="cuda").manual_seed(35)
+    q = torch.randn((3, 1, 128), generator=g, device="cuda").to(torch.bfloat16)
+    k, v = (torch.zeros((n, 1, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for t in (k, v):
+        t[-near:] = torch.randn((near, 1, 128), generator=g, device="cuda").to(torch.bfloat16)
+    out, lse = torch.zeros((3, 1, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros((3, 1), device="cuda")
+    d = smla.make_prompt_desc(3, n, 1, 1, 1, 0, 128 ** -0.5)
+    ws = torch.zeros(smla.prompt_workspace_size(d), dtype=torch.uint8, device="cuda")
+    smla.prompt_attention(d, q, k, v, None, _i32([0, 3]), _i32([0, n]), None, torch.full((1,), slope, device="cuda"), None, out, lse, ws)
+    assert smla.read_error(None, ws) == 0
+    f = lambda t: t.double().cpu().numpy()  # noqa: E731
+    ref, rl, size, big = PO.prompt_attention(f(q), f(k[-near:]), f(v[-near:]), None, [0, 3], [0, near], 128 ** -0.5, slopes=[slope])
+    # keys 40 steps away weigh e^-40: the others' scores are of size 40 + 8 at most, in fp32 as elsewhere
+    e = 48 * 200 * 2.0 ** -24
+    assert (np.abs(f(lse) - rl) <= e).all(), np.abs(f(lse) - rl).max()
+    assert (np.abs(f(out) - ref) <= size * (2.0 ** -8 + 2 * e) + np.abs(ref) * 2.0 ** -8).all()
