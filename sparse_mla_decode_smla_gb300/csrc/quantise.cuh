@@ -42,13 +42,14 @@ struct ScaleDiv {
   // The same codes, with three instructions a value in place of a division: with y the correctly rounded reciprocal of the
   // scale, q = x y and r = x - q scale (exact in one fused multiply-add), q + r y rounds to the correctly rounded quotient
   // (Markstein, IBM Journal of Research and Development 34, 1990). Quotients too small for that round to code 0 all the same.
+  // The remainder is taken as -r: with it zeros of either sign come out as they are, as from the division.
   template <int N>
   __device__ __forceinline__ void codes_by_reciprocal(const float* x, uint16_t* out) const {
     if (!exact && scale >= 0x1p-60f && scale <= 0x1p60f) {
       const float y = __frcp_rn(scale);
       auto quotient = [&](float v) {
         const float q = __fmul_rn(v, y);
-        return __fmaf_rn(__fmaf_rn(-q, scale, v), y, q);
+        return __fmaf_rn(-__fmaf_rn(q, scale, -v), y, q);
       };
 #pragma unroll
       for (int i = 0; i < N; ++i) out[i] = f32x2_to_e4m3x2(quotient(x[2 * i]), quotient(x[2 * i + 1]));
