@@ -232,6 +232,11 @@ __device__ __forceinline__ float norm_sum(float x, float y) { return x + y; }
 __device__ __forceinline__ const uint4* norm_x(const NormArgs& a, int64_t row) {
   return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + row * a.x_stride);
 }
+// Without a residual -0 is added, which leaves every x as it is, zeros of both signs among them.
+__device__ __forceinline__ uint4 norm_no_res(const NormArgs& a) {
+  const uint32_t z = a.residual ? 0u : 0x80008000u;
+  return make_uint4(z, z, z, z);
+}
 __device__ __forceinline__ const uint4* norm_res(const NormArgs& a, int64_t row) {
   return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + row * a.dim);
 }
@@ -248,7 +253,8 @@ __global__ void __launch_bounds__(kNormSmallThreads) add_rmsnorm_small_kernel(co
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int v = k * LANES + t;
-    xv[k] = rv[k] = wv[k] = make_uint4(0, 0, 0, 0);
+    xv[k] = wv[k] = make_uint4(0, 0, 0, 0);
+    rv[k] = norm_no_res(a);
     if (real && v < nv) {
       xv[k] = norm_x(a, row)[v];
       if (a.residual) rv[k] = norm_res(a, row)[v];
@@ -278,7 +284,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) add_rmsnorm_kernel(
 #pragma unroll
   for (int k = 0; k < kNormVpt; ++k) {
     const int v = k * T + t;
-    xv[k] = rv[k] = make_uint4(0, 0, 0, 0);
+    xv[k] = make_uint4(0, 0, 0, 0);
+    rv[k] = norm_no_res(a);
     if (v < nv) {
       xv[k] = norm_x(a, row)[v];
       if (a.residual) rv[k] = norm_res(a, row)[v];

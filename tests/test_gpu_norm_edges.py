@@ -41,3 +41,15 @@ def test_code_bytes_are_those_of_the_rounded_quotient(smla, dim, group, mode):
         scale = ratio if mode == smla.SMLA_SCALE_FP32 else O.pow2_ceil_f32(ratio).astype(np.float32)
         want = O.e4m3_encode_rne_satfinite((part / scale[:, None].astype(np.float32)).astype(np.float32))
         assert np.array_equal(codes[:, b:b + width].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dim", [64, 1024, 7168])
+def test_zeros_keep_their_sign_without_a_residual(smla, dim):
+    torch = _torch()
+    x = torch.randn((5, dim), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    x[:, ::3], x[:, 1::7] = -0.0, 0.0
+    x, w = x.cuda(), torch.ones(dim, device="cuda").to(torch.bfloat16)
+    total, y = torch.empty_like(x), torch.empty_like(x)
+    smla.add_rmsnorm(x, None, w, 1e-6, residual_out=total, y=y)
+    assert torch.equal(total.view(torch.int16), x.view(torch.int16))
+    assert torch.equal(torch.signbit(y), torch.signbit(x))
