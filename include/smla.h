@@ -638,8 +638,9 @@ typedef struct smla_norm_desc {
  * The residual's addition, the root-mean-square norm and its outputs: for each row
  *   h = x + residual (x without one), residual_out = bf16(h),
  *   y = h * r * weight, r = 1 / sqrt(mean(h^2) + rms_eps), in fp32 from the unrounded h,
- * stored as bf16 (y_out) and as E4M3 codes with scales: a block's scale by the rule of smla_pack_kv,
- * codes of fl32(y / scale) from the unrounded y.
+ * stored as bf16 (y_out) and as E4M3 codes with scales: a block's scale by the rule of smla_pack_kv (2^-149
+ * where amax / 448 rounds to 0), codes of fl32(y / scale) from the unrounded y. A row whose sum of squares
+ * leaves fp32 (elements around 2^64 and more) has r = 0.
  *   x [n, D] bf16 with x_stride; residual, residual_out, y_out [n, D] bf16, weight [D] bf16, 16-byte
  *   aligned; codes [n, D] bytes, 8-byte aligned; scales [n, ceil(D / 128)] or [n] fp32.
  *   residual may be NULL, and so may each output, with codes and scales together; one at least is asked for

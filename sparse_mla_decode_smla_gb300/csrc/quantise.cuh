@@ -6,10 +6,11 @@
 namespace smla {
 
 // The scale of a block whose largest magnitude is amax: 1 for an all-zero block, else fl32(amax / 448)
-// or (SMLA_SCALE_POW2) the smallest power of two that is no less.
+// or (SMLA_SCALE_POW2) the smallest power of two that is no less. A quotient that rounds to 0 (below 2^-150, of the norm's fp32
+// values only: bf16 ones start at 2^-133) counts as fp32's smallest number, so that no scale is 0.
 __device__ __forceinline__ float block_scale(float amax, int scale_mode) {
   if (!(amax > 0.f)) return 1.f;
-  const float ratio = __fdiv_rn(amax, 448.f);
+  const float ratio = fmaxf(__fdiv_rn(amax, 448.f), 0x1p-149f);
   if (scale_mode != SMLA_SCALE_POW2) return ratio;
   int e;
   const float m = frexpf(ratio, &e);  // ratio = m * 2^e, m in [0.5, 1)

@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+import oracle.prompt_oracle as PO
 import oracle.smla_oracle as O
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +54,25 @@ def test_zeros_keep_their_sign_without_a_residual(smla, dim):
     smla.add_rmsnorm(x, None, w, 1e-6, residual_out=total, y=y)
     assert torch.equal(total.view(torch.int16), x.view(torch.int16))
     assert torch.equal(torch.signbit(y), torch.signbit(x))
+
+
+@pytest.mark.parametrize("group", [128, 0])
+@pytest.mark.parametrize("mode", [0, 1])
+def test_values_whose_scale_would_round_to_zero(smla, group, mode):
+    """y of some 2^-142.5 where it is not 0: a 448th of that is below fp32's smallest number, 2^-149, which is the scale then."""
+    torch = _torch()
+    x = torch.cat([torch.ones(3, 128), torch.full((3, 128), 2.0 ** -10)], 1).to(torch.bfloat16)
+    w = torch.zeros(256)
+    w[128::2] = 2.0 ** -133  # bf16's smallest number
+    w = w.to(torch.bfloat16)
+    codes = torch.empty((3, 256), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((3, 2 if group else 1), device="cuda")
+    smla.add_rmsnorm(x.cuda(), None, w.cuda(), 0.0, codes=codes, scales=scales, group=group, scale_mode=mode)
+    s = scales.double().cpu().numpy()
+    assert (s[:, -1] == 2.0 ** -149).all()
+    if group:
+        assert (s[:, 0] == 1).all()
+    _, ref, _ = PO.add_rmsnorm(x.double().numpy(), None, w.double().numpy(), 0.0, group)
+    value = O.e4m3_decode(codes.cpu().numpy()) * np.repeat(s, group or 256, 1)
+    # y itself is a whole number of 2^-149, off by a few roundings to such; a code is off by 2^-4 of it at most
+    assert (np.abs(value - ref) <= np.abs(ref) * 2.0 ** -4 + 2 * 2.0 ** -149).all()
