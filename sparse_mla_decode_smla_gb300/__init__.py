@@ -34,6 +34,8 @@ SMLA_MERGE_NONE = 0
 SMLA_MERGE_CLUSTER = 1
 SMLA_MERGE_KERNEL = 2
 
+SMLA_ERR_SHAPE = 2
+SMLA_ERR_UNSUPPORTED = 4
 STATUS = {0: "SMLA_OK", 1: "SMLA_ERR_NULL", 2: "SMLA_ERR_SHAPE", 3: "SMLA_ERR_ALIGN",
           4: "SMLA_ERR_UNSUPPORTED", 5: "SMLA_ERR_WORKSPACE", 6: "SMLA_ERR_CUDA",
           7: "SMLA_ERR_INDEX_RANGE", 8: "SMLA_ERR_DEVICE", 9: "SMLA_ERR_TIMEOUT",
@@ -484,13 +486,47 @@ def prompt_attention(desc, q, k, v, k_rope, cu_q, cu_k, prefix_lens, slopes, sin
         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
+# torch's types, put here by the first call that needs them: importing this package does not import torch
+_BF16 = _F32 = _I32 = _LOGITS_FORMAT = None
+
+
+def _types():
+    global _BF16, _F32, _I32, _LOGITS_FORMAT
+    import torch
+    _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+    _LOGITS_FORMAT = {_BF16: SMLA_LOGITS_BF16, _F32: SMLA_LOGITS_FP32}
+
+
+def _whole(fn, t, dtype):
+    """The pointer of a tensor that a call takes without strides: refused unless it has that type and its elements follow one another."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise SmlaError(fn, SMLA_ERR_UNSUPPORTED)
+    if not t.is_contiguous():
+        raise SmlaError(fn, SMLA_ERR_SHAPE)
+    return t.data_ptr()
+
+
 def add_rmsnorm(x, residual, weight, eps, residual_out=None, y=None, codes=None, scales=None, group=128,
                 scale_mode=SMLA_SCALE_POW2, stream=None):
-    """x + residual, its RMS norm as bf16 and as E4M3 codes with scales (smla_add_rmsnorm); x: rows of any stride."""
+    """x + residual, its RMS norm as bf16 and as E4M3 codes with scales (smla_add_rmsnorm).
+
+    x, residual, weight, residual_out and y: bf16; codes: one byte an element; scales: fp32. x: rows of any stride. Other types
+    are refused (SMLA_ERR_UNSUPPORTED), and so are elements that do not follow one another (SMLA_ERR_SHAPE)."""
     n, dim = x.shape
-    d = _norm_desc(n, dim, x.stride(0) if n > 1 else dim, group, scale_mode, eps)
-    _check("smla_add_rmsnorm", lib().smla_add_rmsnorm(
-        d, _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(codes), _ptr(scales), _stream(stream)))
+    stride, step = x.stride()
+    if _BF16 is None:
+        _types()
+    fn = "smla_add_rmsnorm"
+    if x.dtype is not _BF16 or (codes is not None and codes.itemsize != 1):
+        raise SmlaError(fn, SMLA_ERR_UNSUPPORTED)
+    if step != 1:
+        raise SmlaError(fn, SMLA_ERR_SHAPE)
+    d = _norm_desc(n, dim, stride if n > 1 else dim, group, scale_mode, eps)
+    _check(fn, lib().smla_add_rmsnorm(
+        d, x.data_ptr(), _whole(fn, residual, _BF16), _whole(fn, weight, _BF16), _whole(fn, residual_out, _BF16), _whole(fn, y, _BF16),
+        None if codes is None else _whole(fn, codes, codes.dtype), _whole(fn, scales, _F32), _stream(stream)))
 
 
 # Descriptions of the calls that take none, by their numbers: filling one in takes longer than a small call's kernel.
@@ -510,17 +546,24 @@ def _logprob_desc(n, vocab, row_stride, given, top, logits_format, scale):
     return ctypes.pointer(d)
 
 
-_LOGITS_FORMAT = {2: SMLA_LOGITS_BF16, 4: SMLA_LOGITS_FP32}
-
-
 def token_logprobs(logits, tokens, logprobs, entropy=None, top_ids=None, top_logprobs=None, scale=1.0, error_word=None,
                    stream=None):
     """Log probabilities of given tokens [n, G], entropy and top alternatives [n, K] (smla_token_logprobs).
 
-    logits: [n, V] fp32 or bf16 (any other element size is refused), rows of any stride."""
+    logits: [n, V] fp32 or bf16, rows of any stride; tokens and top_ids: int32; the rest: fp32. Other types are refused
+    (SMLA_ERR_UNSUPPORTED), and so are elements that do not follow one another (SMLA_ERR_SHAPE)."""
     n, vocab = logits.shape
-    d = _logprob_desc(n, vocab, logits.stride(0) if n > 1 else vocab, 0 if tokens is None else tokens.shape[1],
-                      0 if top_ids is None else top_ids.shape[1], _LOGITS_FORMAT.get(logits.element_size(), -1), scale)
-    _check("smla_token_logprobs", lib().smla_token_logprobs(
-        d, _ptr(logits), _ptr(tokens), _ptr(logprobs), _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs),
-        _ptr(error_word), _stream(stream)))
+    stride, step = logits.stride()
+    if _BF16 is None:
+        _types()
+    fn = "smla_token_logprobs"
+    fmt = _LOGITS_FORMAT.get(logits.dtype)
+    if fmt is None:
+        raise SmlaError(fn, SMLA_ERR_UNSUPPORTED)
+    if step != 1 and vocab > 1:
+        raise SmlaError(fn, SMLA_ERR_SHAPE)
+    d = _logprob_desc(n, vocab, stride if n > 1 else vocab, 0 if tokens is None else tokens.shape[1],
+                      0 if top_ids is None else top_ids.shape[1], fmt, scale)
+    _check(fn, lib().smla_token_logprobs(
+        d, logits.data_ptr(), _whole(fn, tokens, _I32), _whole(fn, logprobs, _F32), _whole(fn, entropy, _F32),
+        _whole(fn, top_ids, _I32), _whole(fn, top_logprobs, _F32), _ptr(error_word), _stream(stream)))
