@@ -729,7 +729,7 @@ typedef struct smla_logprob_desc {
   int32_t given;         /* G: given tokens a row, 0..1024 */
   int32_t top;           /* K: alternatives a row, 0..64 */
   int32_t logits_format; /* SMLA_LOGITS_* */
-  float scale;           /* multiplies the logits (1 / temperature): finite, > 0 */
+  float scale;           /* multiplies the logits (1 / temperature): > 0 and no more than 2.35e38 (scale * log2(e) finite) */
   int32_t reserved[3];   /* must be zero */
 } smla_logprob_desc;
 

@@ -889,8 +889,8 @@ smla_status smla_token_logprobs(const smla_logprob_desc* d, const void* logits, 
   if (d->logits_format != SMLA_LOGITS_BF16 && d->logits_format != SMLA_LOGITS_FP32) return SMLA_ERR_UNSUPPORTED;
   if (d->n < 0 || d->n > kMaxCount || d->vocab < 1 || d->vocab > smla::kLogprobMaxVocab || d->row_stride < d->vocab ||
       d->row_stride > kMaxCount || d->given < 0 || d->given > smla::kLogprobMaxGiven || d->top < 0 ||
-      d->top > smla::kLogprobMaxTop || !(isfinite(d->scale) && d->scale > 0.f) || d->reserved[0] || d->reserved[1] ||
-      d->reserved[2])
+      d->top > smla::kLogprobMaxTop || !(isfinite(d->scale * 1.4426950408889634f) && d->scale > 0.f) || d->reserved[0] ||
+      d->reserved[1] || d->reserved[2])
     return SMLA_ERR_SHAPE;
   if (d->n == 0) return SMLA_OK;
   if (!logits || (d->given > 0 && (!tokens || !logprobs)) || (d->top > 0 && !top_ids)) return SMLA_ERR_NULL;

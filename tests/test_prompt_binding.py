@@ -62,3 +62,8 @@ def test_the_norm(name):
     _refused(2, smla.add_rmsnorm, **_norm(**{name: wide[tuple(slice(0, 2 * n, 2) for n in t.shape)]}))
     if t.dim() == 2:
         _refused(2, smla.add_rmsnorm, **_norm(**{name: torch.zeros(t.shape[::-1], dtype=t.dtype).t()}))
+
+
+def test_a_scale_whose_product_with_log2_e_is_not_finite():
+    for scale in (2.4e38, 3e38, 3.4e38):
+        _refused(2, smla.token_logprobs, **_lp(scale=scale), stream=0)
