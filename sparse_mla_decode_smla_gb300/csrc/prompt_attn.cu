@@ -16,8 +16,9 @@
 //
 // A key tile on one SM: S = Q K^T (12 MMAs of 128 x 128 x 16 a row tile), the weights P = 2^(x - m) in BF16 written over
 // S in tensor memory, O += P V (8 MMAs, P from tensor memory). The two row tiles alternate: one's softmax runs while the
-// tensor cores work for the other. m moves only when a row's maximum grows by more than 2^16, so O is rescaled rarely, by
-// the softmax threads themselves; by the time S of a tile is there, PV of the tile before is complete.
+// tensor cores work for the other. m moves only when a row's maximum grows by more than 2^16 (in a lone row tile whenever it
+// grows), so O is rescaled rarely, by the softmax threads themselves; by the time S of a tile is there, PV of the tile before
+// is complete.
 //
 // What bounds it: one 8191-token prompt of 32 heads takes 473 us, 1,450 TFLOP/s and 76 % of the measured matrix rate, the tensor
 // pipe busy for 67 % of the time. A row tile's chain is scores, softmax, P, then PV and the next scores; tensor memory (two S,
@@ -913,6 +914,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       float slope = 0.f;
       if (BIAS && mine) slope = __ldg(p.slopes + hd) * kLog2e;
       const int pos = it.nk - it.nq + token;
+      // A lone row tile's m is the row's maximum itself: the largest weight is 1 then, which BF16 holds exactly, and a token whose
+      // weight lies on few of many keys is as near as fp32 weights would make it (one over 50k keys: out is 0.0016 off 64 bits, 0.0035
+      // with a stale m). Its rows are few, so that O is still rescaled rarely: no time lost.
+      const float stale = paired && !BIAS ? 0.f : kPaRescale;
       float m = -CUDART_INF_F, mu = 0.f;  // mu: m where it is finite
       uint64_t sum2 = 0;
       for (int j = 0; j < n; ++j, ++ns) {
@@ -994,7 +999,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], x[i + c], x[i + 4 + c]);
         float top = fmaxf(max3(mx[0], x[124], x[125]), max3(max3(mx[1], x[126], x[127]), mx[2], mx[3]));
         if (!CAP && !BIAS) top *= p.c2;
-        const bool move = top > m + kPaRescale;
+        const bool move = mine && top > m + stale;
         if (__any_sync(0xffffffffu, move)) {
           const float to_m = BIAS ? top + kPaAhead : top;
           const float f = move ? ex2(m - to_m) : 1.f;  // 0 from -inf

@@ -67,3 +67,32 @@ def test_with_a_prefix_that_reaches_past_a_token(smla):
         p.out.fill_(7.0)
         p.run()
         assert torch.isnan(p.out[int(p.cu_q[0]):int(p.cu_q[1]), 0, 70].float()).all() and torch.equal(p.lse, lse)
+
+
+@pytest.mark.parametrize("nk", [400, 9000])
+@pytest.mark.parametrize("cap", [0.0, 60.0])
+def test_one_key_that_has_nearly_all_the_weight(smla, nk, cap):
+    """A late key some 2^15 above the ones before: its weight's rounding would be all of the result's, in one direction."""
+    import numpy as np
+    import torch
+    H = 64
+    p = Prompt(smla, [1], [nk], H, H, rope=0, seed=53, cap=cap)
+    g = torch.Generator(device="cuda").manual_seed(54)
+    sign = torch.where(torch.rand((H, 128), generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    top = 7
+    p.q[int(p.cu_q[0])] = sign.to(torch.bfloat16)
+    p.k.mul_(0.01)
+    # s = 128^0.5 c: 14.4 to 16 in log2 of the ones before, which are about 0 (10.2 to 11 of a cap of 60 stays as it is but for 1 %)
+    p.k[int(p.cu_k[1]) - top] = (sign * torch.linspace(0.885, 0.97, H, device="cuda")[:, None]).to(torch.bfloat16)
+    p.run()
+    out, lse = p.check()
+    f = lambda t: t.double().cpu().numpy()  # noqa: E731
+    q, k, v = f(p.q[int(p.cu_q[0])]), f(p.k[int(p.cu_k[0]):int(p.cu_k[1])]), f(p.v[int(p.cu_k[0]):int(p.cu_k[1])])
+    s = np.einsum("hd,nhd->hn", q, k) * p.scale
+    s = cap * np.tanh(s / cap) if cap else s
+    w = np.exp(s - s.max(1, keepdims=True))
+    rest = np.einsum("hn,nhd->hd", np.delete(w, nk - top, 1), np.abs(np.delete(v, nk - top, 0))) / w.sum(1)[:, None]
+    want, got = out[int(p.cu_q[0])], f(p.out)[int(p.cu_q[0])]
+    # the result's rounding, the other weights', and scores of 11 in fp32 as elsewhere
+    e = 11 * 200 * 2.0 ** -24 + cap * 2.0 ** -20 + nk * 2.0 ** -24
+    assert (np.abs(got - want) <= np.abs(want) * 2.0 ** -8 + rest * 2.0 ** -8 + e * (np.abs(want) + rest)).all()
