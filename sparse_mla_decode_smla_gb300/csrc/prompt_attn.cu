@@ -916,8 +916,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       const int pos = it.nk - it.nq + token;
       // A lone row tile's m is the row's maximum itself: the largest weight is 1 then, which BF16 holds exactly, and a token whose
       // weight lies on few of many keys is as near as fp32 weights would make it (one over 50k keys: out is 0.0016 off 64 bits, 0.0035
-      // with a stale m). Its rows are few, so that O is still rescaled rarely: no time lost.
-      const float stale = paired && !BIAS ? 0.f : kPaRescale;
+      // with a stale m). Its rows are few, so that O is still rescaled rarely: no time lost. Rows that are no token's never move theirs
+      // (-inf + inf is no number, which nothing exceeds).
+      const float stale = !mine ? CUDART_INF_F : paired && !BIAS ? 0.f : kPaRescale;
       float m = -CUDART_INF_F, mu = 0.f;  // mu: m where it is finite
       uint64_t sum2 = 0;
       for (int j = 0; j < n; ++j, ++ns) {
@@ -999,7 +1000,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], x[i + c], x[i + 4 + c]);
         float top = fmaxf(max3(mx[0], x[124], x[125]), max3(max3(mx[1], x[126], x[127]), mx[2], mx[3]));
         if (!CAP && !BIAS) top *= p.c2;
-        const bool move = mine && top > m + stale;
+        const bool move = top > m + stale;
         if (__any_sync(0xffffffffu, move)) {
           const float to_m = BIAS ? top + kPaAhead : top;
           const float f = move ? ex2(m - to_m) : 1.f;  // 0 from -inf
