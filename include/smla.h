@@ -744,7 +744,7 @@ typedef struct smla_logprob_desc {
  *   logits aligned to its elements, the rest to 4 bytes. Logits of -inf are tokens that cannot be. A row
  *   with a NaN or +inf, or with nothing but -inf, gets NaN for its log probabilities and entropy;
  *   with a NaN its top_ids are unspecified (tokens or -1).
- * Sums are fp32 in a fixed order.
+ * Sums are fp32 in a fixed order; a log probability that leaves fp32 is -inf.
  */
 smla_status smla_token_logprobs(const smla_logprob_desc* d, const void* logits, const int32_t* tokens,
                                 float* logprobs, float* entropy, int32_t* top_ids,

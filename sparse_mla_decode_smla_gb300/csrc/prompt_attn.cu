@@ -20,11 +20,13 @@
 // grows), so O is rescaled rarely, by the softmax threads themselves; by the time S of a tile is there, PV of the tile before
 // is complete.
 //
-// What bounds it: one 8191-token prompt of 32 heads takes 473 us, 1,450 TFLOP/s and 76 % of the measured matrix rate, the tensor
-// pipe busy for 67 % of the time. A row tile's chain is scores, softmax, P, then PV and the next scores; tensor memory (two S,
-// two O) has no room for a third row tile's, so a tile's softmax, about 2,500 clocks, is longer than the 1,280 that the other's
-// MMAs cover. With a cap the softmax is longer still (2 x 1024 tokens over 12k keys, 16 heads: 182 us where the MMAs' rate
-// would allow 96). Single tokens are bound by memory: 32 of them over 0.7k to 16k keys, 8 kv heads: 159 us, 90 % of the bandwidth.
+// What bounds it: one 8191-token prompt of 32 heads takes 468 to 483 us from GPU to GPU, 1,420 to 1,470 TFLOP/s and 75 to 77 % of
+// the measured matrix rate, the tensor pipe busy for 67 % of the time. A row tile's chain is scores, softmax, P, then PV and the next
+// scores; tensor memory (two S, two O) has no room for a third row tile's, so a tile's softmax, about 2,500 clocks, is longer than
+// the 1,280 that the other's MMAs cover. With a cap the chain is longer still (2 x 1024 tokens over 12k keys, 16 heads, where the
+// MMAs' rate would allow 96 us: 183 us with scores small beside the cap, 303 with ones on both sides of 0.6 of it), and no pipe
+// is full either: issue slots 40 %, FMA 36 %, XU 17 %, tensor 43 %. Single tokens are bound by memory: 32 of them over 0.7k to
+// 16k keys, 8 kv heads: 159 us, 90 % of the bandwidth; 250 to 265 us with scores past 0.6 of a cap.
 //
 // P in BF16 is off by 2^-8 of each weight at most, independently of the others; the sums of weights are of the fp32 values.
 //
@@ -56,7 +58,7 @@ constexpr int kPaTiles = 4;                // key (value) tiles in the ring at m
 // m moves when a row's maximum exceeds it by more than this (log2 units): weights stay below 2^16, which neither BF16 nor the
 // fp32 sums notice, and with a bias, where scores grow from tile to tile, it moves less often than with 2^8
 constexpr float kPaRescale = 16.f;
-// With a bias m moves this far beyond the maximum, so that it moves less often (8191 tokens of 32 heads: 513 us, 522 with 0);
+// With a bias m moves this far beyond the maximum, so that it moves less often (8191 tokens of 32 heads: 1.7 % less than with 0);
 // weights around 2^-40 are as exact as others.
 constexpr float kPaAhead = 40.f;
 constexpr int kPaMinTiles = 8;             // key tiles of a run, and of a piece but the odd one, at least
@@ -412,7 +414,7 @@ __device__ __forceinline__ void pa_plan(const PromptArgs& p, PaWalk& w) {
   w.per = 0;
   w.cost = kPaItemCost;
   // Runs where the longest item is over a third of an SM's share (8191 tokens of 32 heads, 0.29 of it, take 2 % longer in
-  // runs than their 473 us off the counter; chunks of 2 x 1024 over 12k keys, 16 heads, 20 % longer off it than their 182 in runs).
+  // runs than off the counter; chunks of 2 x 1024 over 12k keys, 16 heads, 20 % longer off it than in runs).
   if (int64_t(longest) * 3 * gridDim.x <= w.total.tiles || w.total.items == 0) return;
   // an SM for every item, and none long enough to be cut: nothing to lay out
   if (w.total.items <= static_cast<int>(gridDim.x) && longest < 2 * kPaMinTiles) return;
